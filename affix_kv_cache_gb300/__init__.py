@@ -12,5 +12,7 @@ from ._lib import (AcacheError, AttnDesc, attn_desc, acache_build_slot_maps,  # 
                    acache_slot_attention, acache_slot_attention_dropna, acache_slot_attention_path,
                    acache_slot_attention_varlen,
                    acache_rerotate_keys, acache_store_attend, acache_store_attend_layers, acache_topk_anchors, Pool,
-                   acache_wait_budget, acache_write_slots, lib,
+                   acache_wait_budget, acache_write_slots,
+                   acache_write_slots_q8, acache_gather_slots_q8, acache_slot_attention_q8,
+                   acache_slot_attention_varlen_q8, acache_store_attend_q8, lib,
                    status_string, version)

@@ -31,6 +31,7 @@ ACACHE_PATH_RECOMPUTE_PERSISTENT = 3
 SLOT_NONE = -1
 DEV_BAD_SLOT, DEV_SHARED_WRITE, DEV_BAD_ROW, DEV_BAD_ANCHOR, DEV_NAN, DEV_TIMEOUT = 1, 2, 4, 8, 16, 32
 DEV_BAD_LENGTH = 64
+DEV_BAD_VALUE = 128
 
 EXPORTS = ("acache_status_string", "acache_version", "acache_wait_budget", "acache_probe_workspace_bytes",
            "acache_probe_scores", "acache_probe_scores_layers", "acache_probe_scores_noalloc", "acache_topk_anchors", "acache_build_slot_maps",
@@ -40,7 +41,9 @@ EXPORTS = ("acache_status_string", "acache_version", "acache_wait_budget", "acac
            "acache_store_attend", "acache_store_attend_layers", "acache_rerotate_keys", "acache_pool_create",
            "acache_pool_destroy",
            "acache_pool_register_affix", "acache_pool_release_affix", "acache_pool_alloc_private",
-           "acache_pool_free_private", "acache_pool_stats")
+           "acache_pool_free_private", "acache_pool_stats",
+           "acache_write_slots_q8", "acache_gather_slots_q8", "acache_slot_attention_q8",
+           "acache_slot_attention_varlen_q8", "acache_store_attend_q8")
 
 
 class AcacheError(RuntimeError):
@@ -96,6 +99,11 @@ def lib() -> ctypes.CDLL:
             "acache_store_attend": (I, [D, I, I, P, P, P, P, P, I64, I64, I, P, I, P, P, P, P]),
             "acache_store_attend_layers": (I, [D, I, I, I, P, P, P, P, P, I64, I64, I, P, I, P, P, P, P]),
             "acache_rerotate_keys": (I, [D, I64, P, P, ctypes.c_int32, ctypes.c_double, I, P]),
+            "acache_write_slots_q8": (I, [D, I, I, P, P, P, P, P, P, I64, I64, P, P]),
+            "acache_gather_slots_q8": (I, [D, I, I, P, P, P, P, I64, P, P, P, P]),
+            "acache_slot_attention_q8": (I, [D, I, I, P, I, P, P, P, P, I64, P, I, P, P]),
+            "acache_slot_attention_varlen_q8": (I, [D, I, P, I, I, P, P, I, P, P, P, P, I64, P, I, P, P]),
+            "acache_store_attend_q8": (I, [D, I, I, P, P, P, P, P, P, I64, I64, I, P, I, P, P, I, P, P]),
             "acache_pool_create": (I, [I64, I64, ctypes.c_int32, ctypes.POINTER(P)]),
             "acache_pool_destroy": (None, [P]),
             "acache_pool_register_affix": (I, [P, ctypes.c_uint64, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
@@ -315,6 +323,58 @@ def acache_rerotate_keys(desc, rows, k_in, k_out, delta_pos, rope_theta, interle
     st = lib().acache_rerotate_keys(ctypes.byref(desc), rows, _p(k_in), _p(k_out), int(delta_pos),
                                     float(rope_theta), int(bool(interleaved)), _stream(stream))
     return _check("acache_rerotate_keys", st) if check else st
+
+
+# ---- the 8-bit KV pool (see include/acache.h): k_cache / v_cache [num_slots][Hkv][d] e4m3 codes
+# (torch.float8_e4m3fn or uint8), kv_scale [num_slots][Hkv][2] uint8 exponents
+def acache_write_slots_q8(desc, batch, rows, write_slot, k_new, v_new, k_cache, v_cache, kv_scale, num_slots,
+                          private_begin, dev_status=None, stream=None, check=True):
+    """The store step into an 8-bit pool: quantises as it writes."""
+    st = lib().acache_write_slots_q8(ctypes.byref(desc), batch, rows, _p(write_slot), _p(k_new), _p(v_new),
+                                     _p(k_cache), _p(v_cache), _p(kv_scale), num_slots, private_begin,
+                                     _p(dev_status), _stream(stream))
+    return _check("acache_write_slots_q8", st) if check else st
+
+
+def acache_gather_slots_q8(desc, batch, seq_len, read_slot, k_cache, v_cache, kv_scale, num_slots, k_out, v_out,
+                           dev_status=None, stream=None, check=True):
+    """The logical K/V view of an 8-bit pool, in the descriptor's dtype."""
+    st = lib().acache_gather_slots_q8(ctypes.byref(desc), batch, seq_len, _p(read_slot), _p(k_cache), _p(v_cache),
+                                      _p(kv_scale), num_slots, _p(k_out), _p(v_out), _p(dev_status),
+                                      _stream(stream))
+    return _check("acache_gather_slots_q8", st) if check else st
+
+
+def acache_slot_attention_q8(desc, batch, n_q, q, seq_len, read_slot, k_cache, v_cache, kv_scale, num_slots, out,
+                             drop_none=False, dev_status=None, stream=None, check=True):
+    """Read-slot attention over an 8-bit pool; with drop_none, SLOT_NONE entries are discarded keys."""
+    st = lib().acache_slot_attention_q8(ctypes.byref(desc), batch, n_q, _p(q), seq_len, _p(read_slot), _p(k_cache),
+                                        _p(v_cache), _p(kv_scale), num_slots, _p(out), int(bool(drop_none)),
+                                        _p(dev_status), _stream(stream))
+    return _check("acache_slot_attention_q8", st) if check else st
+
+
+def acache_slot_attention_varlen_q8(desc, batch, q_start, max_q_rows, total_q_rows, q, kv_start, max_seq_len,
+                                    read_slot, k_cache, v_cache, kv_scale, num_slots, out, drop_none=False,
+                                    dev_status=None, stream=None, check=True):
+    """Read-slot attention over a ragged batch and an 8-bit pool (offsets as in
+    acache_slot_attention_varlen)."""
+    st = lib().acache_slot_attention_varlen_q8(ctypes.byref(desc), batch, _p(q_start), max_q_rows, total_q_rows,
+                                               _p(q), _p(kv_start), max_seq_len, _p(read_slot), _p(k_cache),
+                                               _p(v_cache), _p(kv_scale), num_slots, _p(out), int(bool(drop_none)),
+                                               _p(dev_status), _stream(stream))
+    return _check("acache_slot_attention_varlen_q8", st) if check else st
+
+
+def acache_store_attend_q8(desc, batch, rows, write_slot, k_new, v_new, k_cache, v_cache, kv_scale, num_slots,
+                           private_begin, n_q, q, seq_len, read_slot, out, drop_none=False, dev_status=None,
+                           stream=None, check=True):
+    """Store step into an 8-bit pool, then read-slot attention over it, in one call."""
+    st = lib().acache_store_attend_q8(ctypes.byref(desc), batch, rows, _p(write_slot), _p(k_new), _p(v_new),
+                                      _p(k_cache), _p(v_cache), _p(kv_scale), num_slots, private_begin, n_q, _p(q),
+                                      seq_len, _p(read_slot), _p(out), int(bool(drop_none)), _p(dev_status),
+                                      _stream(stream))
+    return _check("acache_store_attend_q8", st) if check else st
 
 
 class Pool:

@@ -36,14 +36,6 @@ std::atomic<long long> g_wait_budget{kDefaultWaitBudget};
 
 long long wait_budget() { return g_wait_budget.load(std::memory_order_relaxed); }
 
-namespace {
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Validates the attention descriptor; fills `out`.
 int check_desc(const acache_attn_desc* a, AttnArgs* out) {
     if (!a) return ACACHE_ERR_INVALID_ARG;
     if (a->num_q_heads <= 0 || a->num_kv_heads <= 0 || a->num_q_heads % a->num_kv_heads)
@@ -54,6 +46,13 @@ int check_desc(const acache_attn_desc* a, AttnArgs* out) {
     *out = AttnArgs{a->num_q_heads, a->num_kv_heads, a->head_dim, a->dtype, a->scale};
     return ACACHE_OK;
 }
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 size_t elem_bytes(int dtype) { return dtype == ACACHE_F32 ? 4 : 2; }
 

@@ -10,6 +10,9 @@ struct AttnArgs {
     float scale;
 };
 
+// Validates the attention descriptor of a call and fills `out` (errors as the header states).
+int check_desc(const acache_attn_desc* a, AttnArgs* out);
+
 // Keys of the read-slot attention: logical key t of request b lives in physical slot
 // read_slot[b][t] of the layer's pool (Sec. 4.1, App. C.1).  An out-of-range slot reads
 // as a zero row and is flagged.  With drop_none, an entry equal to ACACHE_SLOT_NONE is a

@@ -1,0 +1,327 @@
+// q8_simt.cu -- read-slot attention over an 8-bit pool on CUDA cores: float32 queries and outputs
+// (tensor cores have no float32 mode that keeps them) and shapes the tensor-core kernel does not
+// cover.
+//
+// One CTA per 64 packed rows -- (query, query head of the KV head's group), so the heads of a
+// group share one pass over the keys -- and per part of the key range: 64-key tiles are decoded to
+// float32 in shared memory, S = Q K^T and O += P V run as 4 x 4 and 4 x d/16 register tiles, and
+// the softmax keeps a running maximum and sum per row in base 2.  Bound by FFMA issue and the
+// shared-memory reads that feed it; two CTAs per SM.  When there are few blocks the key range is
+// split over a cluster of up to 8 CTAs, which merge their partial (maximum, sum, O) through
+// distributed shared memory in rank order.
+#include "q8.cuh"
+#include "ptx.cuh"
+
+namespace acache {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBM = 64, kBN = 64;
+constexpr int kMaxCluster = 8;
+
+struct SimtParams {
+    const void* q;
+    const uint8_t *k_cache, *v_cache, *kv_scale;
+    const int32_t *read_slot, *q_start, *kv_start;
+    void* out;
+    int32_t* dev_status;
+    int64_t num_slots;
+    int n_q, T_len, Hq, Hkv, g, cs;
+    bool drop_none;
+    float scale_log2;
+};
+
+template <int D>
+struct SimtSmem {
+    float q[D][kBM];          // transposed; the partial O of a split key range afterwards
+    float k[D][kBN];          // transposed
+    float v[kBN][D];
+    float p[kBN][kBM];        // transposed
+    float ks[kBN], vs[kBN];
+    int64_t row[kBN];         // pool row, or -1 (zero row), or -2 (no key)
+    float m[kBM], l[kBM];
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+q8_simt_kernel(const SimtParams p) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
+    constexpr int NC = D / 64;                          // 4-column chunks of O per thread
+    const int cr = (int)(blockIdx.x % (unsigned)p.cs), hk = (int)(blockIdx.x / (unsigned)p.cs);
+    const int b = (int)blockIdx.y;
+    int n_q = p.n_q, T_len = p.T_len;
+    int64_t qbase = (int64_t)b * p.n_q, kbase = (int64_t)b * p.T_len;
+    if (p.q_start) {
+        qbase = p.q_start[b];
+        kbase = p.kv_start[b];
+        n_q = (int)(p.q_start[b + 1] - qbase);
+        T_len = (int)(p.kv_start[b + 1] - kbase);
+        if (n_q != 0 && (n_q < 0 || n_q > p.n_q || T_len < 1 || T_len > p.T_len)) {
+            if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) flag(p.dev_status, ACACHE_DEV_BAD_LENGTH);
+            return;
+        }
+    }
+    const int64_t r0 = (int64_t)blockIdx.z * kBM, n_rows = (int64_t)n_q * p.g;
+    if (r0 >= n_rows) return;
+    const int rows = (int)min((int64_t)kBM, n_rows - r0);
+    const int n_all = (T_len + kBN - 1) / kBN;
+    const int cs = min(p.cs, n_all);                    // ranks past the tiles have nothing to do
+    if (cr >= cs) return;
+    const int j0 = (int)((int64_t)cr * n_all / cs), j1 = (int)((int64_t)(cr + 1) * n_all / cs);
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    auto q_off = [&](int r) {                           // element offset of packed row r0 + r
+        const int64_t i = (r0 + r) / p.g;
+        return ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r0 + r - i * p.g)) * D;
+    };
+    for (int x = tid; x < kBM * D; x += kThreads) {
+        const int r = x / D, c = x % D;
+        sm.q[c][r] = r < rows ? to_f32(((const T*)p.q)[q_off(r) + c]) : 0.f;
+    }
+    float m[4], l[4], acc[4][NC * 4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        m[y] = -INFINITY;
+        l[y] = 0.f;
+#pragma unroll
+        for (int x = 0; x < NC * 4; ++x) acc[y][x] = 0.f;
+    }
+    for (int j = j0; j < j1; ++j) {
+        __syncthreads();                                // the last tile has been read
+        if (tid < kBN) {
+            const int t = j * kBN + tid;
+            int64_t row = -2;
+            float ks = 0.f, vs = 0.f;
+            if (t < T_len) {
+                const int64_t s = p.read_slot[kbase + t];
+                if (s >= 0 && s < p.num_slots) {
+                    row = s * p.Hkv + hk;
+                    const uint32_t two = reinterpret_cast<const uint16_t*>(p.kv_scale)[row];
+                    ks = q8_factor(two & 0xffu);
+                    vs = q8_factor(two >> 8);
+                } else if (!(p.drop_none && s == ACACHE_SLOT_NONE)) {
+                    row = -1;
+                    flag(p.dev_status, ACACHE_DEV_BAD_SLOT);
+                }
+            }
+            sm.row[tid] = row;
+            sm.ks[tid] = ks;
+            sm.vs[tid] = vs;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int it = 0; it < kBN * D / 16 / kThreads; ++it) {
+            const int x = it * kThreads + tid;
+            {   // K: consecutive lanes take consecutive keys, so the transposed stores do not conflict
+                const int key = x & (kBN - 1), c = x / kBN;
+                const int64_t row = sm.row[key];
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (row >= 0) w = *reinterpret_cast<const uint4*>(p.k_cache + row * D + c * 16);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                const float f = sm.ks[key];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 e = q8_decode2((ww[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                    sm.k[c * 16 + 2 * i][key] = e.x * f;
+                    sm.k[c * 16 + 2 * i + 1][key] = e.y * f;
+                }
+            }
+            {   // V
+                const int key = x / (D / 16), c = x % (D / 16);
+                const int64_t row = sm.row[key];
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (row >= 0) w = *reinterpret_cast<const uint4*>(p.v_cache + row * D + c * 16);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                const float f = row >= 0 ? sm.vs[key] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 e = q8_decode2(ww[i] & 0xffffu), h = q8_decode2(ww[i] >> 16);
+                    *reinterpret_cast<float4*>(&sm.v[key][c * 16 + 4 * i]) =
+                        make_float4(e.x * f, e.y * f, h.x * f, h.y * f);
+                }
+            }
+        }
+        __syncthreads();
+        float s[4][4] = {};
+#pragma unroll 8
+        for (int c = 0; c < D; ++c) {
+            const float4 qv = *reinterpret_cast<const float4*>(&sm.q[c][4 * ty]);
+            const float4 kv = *reinterpret_cast<const float4*>(&sm.k[c][4 * tx]);
+            const float qa[4] = {qv.x, qv.y, qv.z, qv.w}, ka[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[y][x] = fmaf(qa[y], ka[x], s[y][x]);
+        }
+        bool gone[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) gone[x] = sm.row[4 * tx + x] == -2;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            float mt = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                s[y][x] = gone[x] ? -INFINITY : s[y][x] * p.scale_log2;
+                mt = fmaxf(mt, s[y][x]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+            const float mn = fmaxf(m[y], mt);
+            const float ref = mn == -INFINITY ? 0.f : mn;      // no key so far: exponentiate against 0
+            const float alpha = fast_exp2(m[y] - ref);
+            m[y] = mn;
+            float lt = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                s[y][x] = fast_exp2(s[y][x] - ref);
+                lt += s[y][x];
+            }
+            l[y] = l[y] * alpha + lt;                           // this lane's share of the row's sum
+#pragma unroll
+            for (int x = 0; x < NC * 4; ++x) acc[y][x] *= alpha;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<float4*>(&sm.p[4 * tx + x][4 * ty]) = make_float4(s[0][x], s[1][x], s[2][x], s[3][x]);
+        __syncwarp();                                           // a warp reads only rows it wrote
+#pragma unroll 4
+        for (int t = 0; t < kBN; ++t) {
+            const float4 pv = *reinterpret_cast<const float4*>(&sm.p[t][4 * ty]);
+            const float pa[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                const float4 vv = *reinterpret_cast<const float4*>(&sm.v[t][n * 64 + 4 * tx]);
+                const float va[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[y][n * 4 + x] = fmaf(pa[y], va[x], acc[y][n * 4 + x]);
+            }
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) l[y] += __shfl_xor_sync(0xffffffffu, l[y], o);
+    if (cs == 1) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int r = 4 * ty + y;
+            if (r >= rows) continue;
+            T* o = (T*)p.out + q_off(r);
+            // a row without keys gives zeros (a NaN sum is carried into the output)
+            const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[n * 64 + 4 * tx + x] = from_f32<T>(acc[y][n * 4 + x] * inv);
+        }
+        return;
+    }
+    // merge the parts: rank w finalises rows w, w + cs, ...
+    __syncthreads();
+    float* part = &sm.q[0][0];                                  // [row][D]
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const int r = 4 * ty + y;
+        if (tx == 0) {
+            sm.m[r] = m[y];
+            sm.l[r] = l[y];
+        }
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+            *reinterpret_cast<float4*>(part + r * D + n * 64 + 4 * tx) =
+                make_float4(acc[y][n * 4], acc[y][n * 4 + 1], acc[y][n * 4 + 2], acc[y][n * 4 + 3]);
+    }
+    ptx::cluster_sync();
+    const uint32_t m_a = ptx::smem_u32(&sm.m[0]), l_a = ptx::smem_u32(&sm.l[0]), o_a = ptx::smem_u32(part);
+    for (int x = tid; x < ((rows - cr + cs - 1) / cs) * (D / 4); x += kThreads) {
+        const int r = cr + (x / (D / 4)) * cs, c = x % (D / 4);
+        float M = -INFINITY;
+        for (int w = 0; w < cs; ++w) M = fmaxf(M, ptx::ld_cluster_f32(ptx::mapa_shared(m_a + 4u * r, w)));
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < cs; ++w) {
+            const float e = fast_exp2(ptx::ld_cluster_f32(ptx::mapa_shared(m_a + 4u * r, w)) - ref);
+            const float4 o = ptx::ld_cluster_v4(ptx::mapa_shared(o_a + (uint32_t)(r * D + 4 * c) * 4u, w));
+            L = fmaf(e, ptx::ld_cluster_f32(ptx::mapa_shared(l_a + 4u * r, w)), L);
+            O.x = fmaf(e, o.x, O.x);
+            O.y = fmaf(e, o.y, O.y);
+            O.z = fmaf(e, o.z, O.z);
+            O.w = fmaf(e, o.w, O.w);
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        T* o = (T*)p.out + q_off(r) + 4 * c;
+        o[0] = from_f32<T>(O.x * inv);
+        o[1] = from_f32<T>(O.y * inv);
+        o[2] = from_f32<T>(O.z * inv);
+        o[3] = from_f32<T>(O.w * inv);
+    }
+    ptx::cluster_sync();       // no CTA may leave while another still reads its shared memory
+}
+
+template <typename T, int D>
+int launch(const SimtParams& prm, dim3 grid, cudaStream_t stream) {
+    auto kern = q8_simt_kernel<T, D>;
+    constexpr int smem = (int)sizeof(SimtSmem<D>);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ACACHE_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)prm.cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = prm.cs > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, prm) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ACACHE_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+int launch_q8_simt_attention(const Q8Attn& c) {
+    const int g = c.a.hq / c.a.hkv;
+    const int64_t n_rb = ((int64_t)c.n_q * g + kBM - 1) / kBM;
+    if (c.B > 65535 || n_rb > 65535) return ACACHE_ERR_INVALID_ARG;
+    SimtParams prm{};
+    prm.q = c.q;
+    prm.k_cache = c.k_cache;
+    prm.v_cache = c.v_cache;
+    prm.kv_scale = c.kv_scale;
+    prm.read_slot = c.read_slot;
+    prm.q_start = c.q_start;
+    prm.kv_start = c.kv_start;
+    prm.out = c.out;
+    prm.dev_status = c.dev_status;
+    prm.num_slots = c.num_slots;
+    prm.n_q = c.n_q;
+    prm.T_len = c.T_len;
+    prm.Hq = c.a.hq;
+    prm.Hkv = c.a.hkv;
+    prm.g = g;
+    prm.drop_none = c.drop_none;
+    prm.scale_log2 = c.a.scale * kLog2e;
+    // split the keys while the parts still fit in one wave (two CTAs per SM) and have two tiles each
+    const int64_t units = (int64_t)c.B * c.a.hkv * n_rb, tiles = (c.T_len + kBN - 1) / kBN;
+    prm.cs = 1;
+    while (prm.cs < kMaxCluster && units * prm.cs * 2 <= 2 * (int64_t)sm_count() && tiles >= 4 * prm.cs) prm.cs *= 2;
+    if ((int64_t)c.a.hkv * prm.cs > 0x7fffffff) return ACACHE_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)(c.a.hkv * prm.cs), (unsigned)c.B, (unsigned)n_rb);
+    if (c.a.dtype == ACACHE_F32)
+        return c.a.d == 64 ? launch<float, 64>(prm, grid, c.stream) : launch<float, 128>(prm, grid, c.stream);
+    return c.a.d == 64 ? launch<__nv_bfloat16, 64>(prm, grid, c.stream)
+                       : launch<__nv_bfloat16, 128>(prm, grid, c.stream);
+}
+
+}  // namespace acache

@@ -66,7 +66,8 @@ enum {
     ACACHE_DEV_BAD_ANCHOR = 8,    /* anchors not strictly ascending offsets in [0, L)      */
     ACACHE_DEV_NAN = 16,          /* a NaN importance score reached Top-K                  */
     ACACHE_DEV_TIMEOUT = 32,      /* a bounded wait inside a kernel gave up                */
-    ACACHE_DEV_BAD_LENGTH = 64    /* a ragged-batch request length outside its bounds     */
+    ACACHE_DEV_BAD_LENGTH = 64,   /* a ragged-batch request length outside its bounds     */
+    ACACHE_DEV_BAD_VALUE = 128    /* a K or V value an 8-bit pool cannot hold was stored  */
 };
 
 /* Read-slot map entry of a logical position whose K/V was discarded (the page's DropNA
@@ -374,6 +375,67 @@ ACACHE_API int acache_gather_slots(const acache_attn_desc* a, int batch, int seq
                         const int32_t* read_slot, const void* k_cache, const void* v_cache,
                         int64_t num_slots, void* k_out, void* v_out, int32_t* dev_status,
                         void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * The 8-bit KV pool.  The page keeps its cache in 16 bits; here a layer's pool may instead be
+ * held at half the bytes, with the same slots, maps and ownership:
+ *   k_cache, v_cache  [num_slots][Hkv][d] e4m3 codes, 16-byte aligned
+ *   kv_scale          [num_slots][Hkv][2] uint8: the biased exponents of the slot's K row and V
+ *                     row of that head, 2-byte aligned.  Element = code * 2^(byte - 127).
+ * The block of tokens that shares a scale is one slot: a store writes single slots anywhere in the
+ * pool, and a wider block would have it rewrite rows other requests are reading.  The exponent
+ * is the smallest e in [-50, 38] with max |x| <= 448 * 2^e; codes are rounded to nearest, ties to
+ * even, so an element is off by at most 2^-4 of itself (2^-10 * 2^e where that is more), reading back
+ * is exact, and storing a read-back row again keeps its values.  A row with a NaN, an infinity or a
+ * value above 448 * 2^38 is stored as scale byte 255 and zero codes and flags ACACHE_DEV_BAD_VALUE: it
+ * reads as NaN, and so does every query row that attends to it.  Bytes of 166 to 254 read as NaN too; a
+ * pool set to zero bytes reads as zeros.
+ * The descriptor's dtype is that of the fresh K/V, the queries and the outputs.
+ * ------------------------------------------------------------------------------- */
+
+/* (4a) Store step of one layer: acache_write_slots into an 8-bit pool, quantising as it writes.
+ * Arguments and errors as there.  The slots of one call must differ from one another (as they do
+ * in a write-side map): a slot named twice ends up with a mix of the two rows. */
+ACACHE_API int acache_write_slots_q8(const acache_attn_desc* a, int batch, int rows,
+                          const int32_t* write_slot, const void* k_new, const void* v_new,
+                          void* k_cache, void* v_cache, uint8_t* kv_scale, int64_t num_slots,
+                          int64_t private_begin, int32_t* dev_status, void* stream);
+
+/* Logical KV view: acache_gather_slots from an 8-bit pool, in the descriptor's dtype (exact in
+ * both).  This is how a shared affix held in 8 bits is handed to acache_probe_scores.  Bad slots
+ * are skipped (the output row is left untouched) and flag ACACHE_DEV_BAD_SLOT. */
+ACACHE_API int acache_gather_slots_q8(const acache_attn_desc* a, int batch, int seq_len,
+                          const int32_t* read_slot, const void* k_cache, const void* v_cache,
+                          const uint8_t* kv_scale, int64_t num_slots, void* k_out, void* v_out,
+                          int32_t* dev_status, void* stream);
+
+/* (4b) Read-slot attention of one layer over an 8-bit pool: acache_slot_attention (recompute
+ * points, block decoding and single tokens alike), and with drop_none != 0
+ * acache_slot_attention_dropna.  Arguments and errors as there; a query row whose keys are all
+ * discarded outputs zeros.  float32 queries and outputs run on CUDA cores. */
+ACACHE_API int acache_slot_attention_q8(const acache_attn_desc* a, int batch, int n_q, const void* q,
+                          int seq_len, const int32_t* read_slot, const void* k_cache,
+                          const void* v_cache, const uint8_t* kv_scale, int64_t num_slots, void* out,
+                          int drop_none, int32_t* dev_status, void* stream);
+
+/* (4b'') The same over a ragged batch: acache_slot_attention_varlen on an 8-bit pool (a serving
+ * batch of single tokens, prompts, or both).  Arguments and errors as there. */
+ACACHE_API int acache_slot_attention_varlen_q8(const acache_attn_desc* a, int batch,
+                          const int32_t* q_start, int max_q_rows, int total_q_rows, const void* q,
+                          const int32_t* kv_start, int max_seq_len, const int32_t* read_slot,
+                          const void* k_cache, const void* v_cache, const uint8_t* kv_scale,
+                          int64_t num_slots, void* out, int drop_none, int32_t* dev_status,
+                          void* stream);
+
+/* (4a+4b) Store-then-attend of one layer in one call: acache_write_slots_q8(rows, write_slot, ...)
+ * followed by acache_slot_attention_q8(n_q, q, ...) on the same pool; every argument is checked
+ * before anything is launched.  rows = 0 attends only; n_q = 0 stores only. */
+ACACHE_API int acache_store_attend_q8(const acache_attn_desc* a, int batch, int rows,
+                          const int32_t* write_slot, const void* k_new, const void* v_new,
+                          void* k_cache, void* v_cache, uint8_t* kv_scale, int64_t num_slots,
+                          int64_t private_begin, int n_q, const void* q, int seq_len,
+                          const int32_t* read_slot, void* out, int drop_none, int32_t* dev_status,
+                          void* stream);
 
 /* ---------------------------------------------------------------------------------
  * Position-aware affix registration.  Page: Sec. 4 (opening) and Limitations -- the cache

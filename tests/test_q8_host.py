@@ -1,0 +1,108 @@
+"""The 8-bit pool's entry points on a host without a GPU: refusals and no-ops (nothing reaches a
+launch), and the reference the GPU tests compare with."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import affix_kv_cache_gb300 as ac
+from affix_kv_cache_gb300 import _lib
+
+from q8_reference import VALUES, quantise, values
+
+BOGUS = 1 << 40
+E, U = _lib.ACACHE_ERR_INVALID_ARG, _lib.ACACHE_ERR_UNSUPPORTED
+
+
+def _desc(hq=4, hkv=2, d=128, dtype="bf16"):
+    return ac.attn_desc(hq, hkv, d, 0.088, dtype)
+
+
+def _write(dsc, batch=1, rows=4, slot=BOGUS, kn=BOGUS, vn=BOGUS, kc=BOGUS, vc=BOGUS, sc=BOGUS, ns=10, pb=0):
+    return ac.lib().acache_write_slots_q8(ctypes.byref(dsc) if dsc else None, batch, rows, slot, kn, vn, kc, vc, sc, ns, pb, None, None)
+
+
+def _gather(dsc, batch=1, T=4, rs=BOGUS, kc=BOGUS, vc=BOGUS, sc=BOGUS, ns=10, ko=BOGUS, vo=BOGUS):
+    return ac.lib().acache_gather_slots_q8(ctypes.byref(dsc), batch, T, rs, kc, vc, sc, ns, ko, vo, None, None)
+
+
+def _attend(dsc, batch=1, n_q=4, q=BOGUS, T=4, rs=BOGUS, kc=BOGUS, vc=BOGUS, sc=BOGUS, ns=10, out=BOGUS, drop=0):
+    return ac.lib().acache_slot_attention_q8(ctypes.byref(dsc), batch, n_q, q, T, rs, kc, vc, sc, ns, out, drop, None, None)
+
+
+def _varlen(dsc, batch=1, qs=BOGUS, mq=4, tq=4, q=BOGUS, ks=BOGUS, mt=4, rs=BOGUS, kc=BOGUS, vc=BOGUS, sc=BOGUS, ns=10, out=BOGUS):
+    return ac.lib().acache_slot_attention_varlen_q8(ctypes.byref(dsc), batch, qs, mq, tq, q, ks, mt, rs, kc, vc, sc, ns, out, 0, None, None)
+
+
+def _both(dsc, batch=1, rows=4, slot=BOGUS, kn=BOGUS, vn=BOGUS, kc=BOGUS, vc=BOGUS, sc=BOGUS, ns=10, pb=0, n_q=4, q=BOGUS,
+          T=4, rs=BOGUS, out=BOGUS):
+    return ac.lib().acache_store_attend_q8(ctypes.byref(dsc), batch, rows, slot, kn, vn, kc, vc, sc, ns, pb, n_q, q, T, rs,
+                                           out, 0, None, None)
+
+
+@pytest.mark.parametrize("call", [_write, _gather, _attend, _varlen, _both])
+def test_descriptor_refusals(call):
+    for bad, want in ((ac.attn_desc(3, 2, 128, 0.1, "bf16"), E), (ac.attn_desc(0, 1, 128, 0.1, "bf16"), E),
+                      (ac.attn_desc(4, 2, 96, 0.1, "bf16"), U), (_lib.AttnDesc(4, 2, 128, 0.1, 7), U),
+                      (ac.attn_desc(4, 2, 128, float("inf"), "bf16"), E)):
+        assert call(bad) == want
+
+
+@pytest.mark.parametrize("call,pointers", [
+    (_write, ("slot", "kn", "vn", "kc", "vc", "sc")), (_gather, ("rs", "kc", "vc", "sc", "ko", "vo")),
+    (_attend, ("q", "rs", "kc", "vc", "sc", "out")), (_varlen, ("qs", "q", "ks", "rs", "kc", "vc", "sc", "out")),
+    (_both, ("slot", "kn", "vn", "kc", "vc", "sc", "q", "rs", "out"))])
+def test_pointer_refusals(call, pointers):
+    for name in pointers:
+        assert call(_desc(), **{name: None}) == E, name
+        if name not in ("slot", "rs", "qs", "ks", "sc"):
+            assert call(_desc(), **{name: BOGUS + 8}) == E, name        # 16-byte alignment
+    assert call(_desc(), sc=BOGUS + 1) == E                             # scale pairs are 2-byte words
+
+
+def test_scalar_refusals_and_noops():
+    d = _desc()
+    assert _write(None) == E
+    assert _write(d, rows=-1) == E and _write(d, batch=-1) == E and _write(d, ns=-1) == E
+    assert _write(d, pb=11) == E and _write(d, pb=-1) == E
+    assert _attend(d, T=0) == E and _attend(d, n_q=-1) == E and _attend(d, T=-1) == E
+    assert _varlen(d, mt=0) == E and _varlen(d, mq=-1) == E and _varlen(d, tq=-1) == E
+    assert _both(d, T=0) == E and _both(d, pb=11) == E
+    assert _gather(d, T=-1) == E
+    none = dict(kc=None, vc=None, sc=None)
+    assert _write(d, rows=0, slot=None, kn=None, vn=None, **none) == 0
+    assert _gather(d, T=0, rs=None, ko=None, vo=None, **none) == 0
+    assert _attend(d, n_q=0, q=None, rs=None, out=None, **none) == 0
+    assert _attend(d, batch=0, q=None, rs=None, out=None, **none) == 0
+    assert _varlen(d, tq=0, qs=None, ks=None, q=None, rs=None, out=None, **none) == 0
+    assert _both(d, batch=0, slot=None, kn=None, vn=None, q=None, rs=None, out=None, **none) == 0
+    assert _both(d, rows=0, n_q=0, slot=None, kn=None, vn=None, q=None, rs=None, out=None, **none) == 0
+
+
+def test_binding_raises():
+    with pytest.raises(ac.AcacheError) as e:
+        ac.acache_slot_attention_q8(_desc(), 1, 4, None, 4, None, None, None, None, 8, None)
+    assert e.value.status == E
+
+
+def test_reference_matches_the_torch_format():
+    codes = torch.arange(256, dtype=torch.uint8)
+    t = codes.view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(VALUES, t, equal_nan=True)
+    # rows whose exponent is known: torch's own conversion is the rounding
+    g = torch.Generator().manual_seed(0)
+    x = torch.rand((200, 64), generator=g) * 400
+    x[:, 0] = 448.0
+    c, s, bad = quantise(x)
+    assert (s == 127).all() and not bad.any()
+    assert np.array_equal(c, x.to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+def test_reference_scales_at_their_borders():
+    top = torch.tensor([448.0, float(np.nextafter(np.float32(448), np.float32(500))), 1.75, 0.0, 1e-30, 2.0 ** 46,
+                        448 * 2.0 ** 38, 2.0 ** 47, float("inf"), float("nan")])
+    c, s, bad = quantise(top[:, None])
+    assert s.tolist() == [127, 128, 119, 77, 77, 165, 165, 255, 255, 255]
+    assert bad.tolist() == [False] * 7 + [True] * 3
+    assert np.isnan(values(c, s)[-1]).all()

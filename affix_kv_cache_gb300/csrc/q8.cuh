@@ -70,5 +70,8 @@ int launch_q8_gather(int dtype, int batch, int seq_len, int hkv, int d, const in
                      const uint8_t* k_cache, const uint8_t* v_cache, const uint8_t* kv_scale, int64_t num_slots,
                      void* k_out, void* v_out, int32_t* dev_status, cudaStream_t stream);
 int launch_q8_simt_attention(const Q8Attn& c);
+// True when the tcgen05 kernel covers the call: bf16 and a positive softmax scale.
+bool q8_tc_supported(const AttnArgs& a);
+int launch_q8_tc_attention(const Q8Attn& c);
 
 }  // namespace acache

@@ -18,7 +18,7 @@ int attend(const Q8Attn& c) {
     if (!c.q || !c.read_slot || !c.out || !aligned16(c.q) || !aligned16(c.out) ||
         !pool_ok(c.k_cache, c.v_cache, c.kv_scale))
         return ACACHE_ERR_INVALID_ARG;
-    return launch_q8_simt_attention(c);
+    return q8_tc_supported(c.a) ? launch_q8_tc_attention(c) : launch_q8_simt_attention(c);
 }
 
 Q8Attn call(const AttnArgs& a, int batch, int n_q, const void* q, int seq_len, const int32_t* read_slot,

@@ -1,0 +1,974 @@
+// q8_tc.cu -- read-slot attention over an 8-bit pool on the tensor cores (tcgen05 + TMEM): bf16
+// queries and outputs, head dim 64 or 128.
+//
+// Page: "Affix Cache for Diffusion Large Language Models", Sec. 4.3 and App. C.1 (attention that
+// reads every logical key through the per-request read-slot map); the 8-bit pool is this
+// library's.
+//
+// Mathematics.  out = softmax(scale q . k) v with k = 2^ek kc, v = 2^ev vc, codes kc and vc in e4m3.
+//   * S: the keys' codes are an operand as they lie in the pool.  A bf16 query row has 8
+//     significant bits, twice e4m3's 4: scaled by a power of two so that its largest element lies in
+//     [128, 256), q' = hi + lo with hi = e4m3(q') and lo = e4m3(q' - hi) is exact for elements within
+//     2^-10 of the largest and off by at most 2^-17 of the largest below.  S = hi kc + lo kc: two
+//     8-bit MMA passes at twice the bf16 rate, so no key is ever converted and the K ring takes
+//     half the shared memory.  2^ek multiplies S per key (float32), the row's power of two joins the
+//     softmax scale.
+//   * O: bf16 P (as in the 16-bit kernels) times V in bf16: 2^(ev - 32) vc has 4 significant bits, so
+//     the conversion is exact; the factor 2^32 goes into the final 1/l.
+//
+// Work.  Rows are (query, query head of the KV head's group) pairs, packed, so a group shares one
+// pass over the keys; a CTA takes up to 256 of them (two 128-row tiles A and B) and the keys of one
+// (request, KV head).  512 threads, one CTA per SM:
+//   WG0, WG1  softmax + epilogue of chain A / B, thread r owns row r (= TMEM lane r): first it turns
+//             its query row into hi and lo; then per key tile it reads S from TMEM, multiplies by the
+//             keys' factors, exponentiates in base 2 against a lazily raised maximum and writes P
+//             over S.  The two chains take turns.  It fetches one key's scale a tile ahead.
+//   WG2       warps 8 and 9 issue the MMAs of chain A / B; warps 10 and 11 fill the K ring by TMA (a
+//             tile of consecutive slots as one box, any other as 32 gather4 loads).
+//   WG3       V: each thread reads 16-byte pieces of pool rows into registers two tiles ahead,
+//             converts them to bf16 and writes the V ring.  Through registers instead of a raw ring:
+//             the converted tile is the only copy in shared memory.
+//   A CTA with one row tile (few rows: decoding) splits its keys between the chains and merges
+//   them at the end.  When there are few blocks the key range is also split over a cluster of cs
+//   CTAs, whose partial (maximum, sum, O) are merged through distributed shared memory, in rank order.
+//
+// Every mbarrier wait is bounded; a wait that gives up raises a CTA-wide abort flag and
+// ACACHE_DEV_TIMEOUT, roles leave their loops, MMAs in flight are drained, TMA loads issued before
+// it are waited for (bounded), TMEM is freed, the cluster barriers are reached on every path, and
+// no output of the block is written.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "q8.cuh"
+#include "ptx.cuh"
+#include "tc_attn.cuh"
+
+namespace acache {
+namespace {
+
+using namespace ptx;
+using bf16 = __nv_bfloat16;
+
+constexpr int kBM = 128;                    // rows per tile (TMEM lanes)
+constexpr int kQT = 2;                      // row tiles per CTA
+constexpr int kBN = 128;                    // keys per tile
+constexpr int kMmaWarp = 8;
+constexpr int kProdWarp = 10, kProd = 2;    // K producer warps
+constexpr int kConvWarp = 12, kConv = 4;    // V converter warps
+constexpr int kThreads = 512;
+// Registers: 512 x 128 at launch = 65536; 2 x 128 x 168 + 128 x 56 + 128 x 120 = 65536.
+constexpr int kRegSoftmax = 168, kRegIssue = 56, kRegConv = 120;
+static_assert(2 * 128 * kRegSoftmax + 128 * kRegIssue + 128 * kRegConv <= kThreads * 128, "register split");
+constexpr uint32_t kTmemCols = 512;         // S_A, S_B, O_A, O_B
+__host__ __device__ constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
+__host__ __device__ constexpr uint32_t col_o(int t) { return 256u + (uint32_t)t * 128u; }
+constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
+constexpr int kVShift = 32;                 // V is carried times 2^-32
+constexpr int kMaxCluster = 8;
+constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles, abort path
+
+template <int D>
+struct Geo {
+    static constexpr uint32_t kQPart = kBM * D;            // one term of a query tile
+    static constexpr uint32_t kKTile = kBN * D;            // e4m3
+    static constexpr uint32_t kVTile = kBN * D * 2;        // bf16
+    static constexpr uint32_t kRegion = kBN * 128;         // 64 bf16 columns of a V tile
+    static constexpr int kKSt = D == 128 ? 3 : 4, kVSt = D == 128 ? 3 : 4;
+    static constexpr uint32_t kRing = 2 * kQT * kQPart;    // offset of the K ring
+    static constexpr uint32_t kBytes = kRing + kKSt * kKTile + kVSt * kVTile + 1024;
+    static_assert(kKSt * kKTile + kVSt * kVTile >= kQT * kBM * D * 4u, "partial O reuses the rings");
+};
+
+struct Q8Params {
+    CUtensorMap tm_k;      // 2-D pool rows [num_slots*Hkv][d], box {d, 1} (gather4)
+    CUtensorMap tm_kbox;   // 3-D pool [num_slots][Hkv][d], box {d, 1, 128} (consecutive slots)
+    const bf16* q;
+    const uint8_t* v_cache;
+    const uint8_t* kv_scale;
+    const int32_t *read_slot, *q_start, *kv_start;
+    bf16* out;
+    int32_t* dev_status;
+    int64_t num_slots;
+    int oob_row;           // a pool row outside the tensor (reads zeros)
+    int n_q, T_len, Hq, Hkv, g;
+    int cs, part;          // CTAs per cluster; key tiles per part
+    float scale_log2;
+    long long budget;      // cycles a pipeline wait may take before it gives up
+};
+
+template <int D>
+struct Ctl {
+    uint64_t q_full;
+    uint64_t k_full[Geo<D>::kKSt], k_empty[Geo<D>::kKSt];
+    uint64_t v_full[Geo<D>::kVSt], v_empty[Geo<D>::kVSt];
+    uint64_t s_full[kQT], p_half[kQT], p_full[kQT], drain[kQT], turn[kQT];
+    uint64_t f_full[kQT];              // the keys' factors of chain t's tile are in `factor`
+    uint32_t tmem_base;
+    int abort, unlanded;
+    uint32_t drop[kQT][2][4];          // discarded keys, 32 per word
+    float part_m[kQT * kBM], part_l[kQT * kBM];
+    float failed;                      // this CTA gave up (read by the other ranks)
+    __align__(16) float factor[kQT][2][kBN];
+};
+
+// Chain t's i-th key tile comes through ring entry entry(t, i).  One row tile: chain 0 reads
+// tiles [0, n0), chain 1 the rest, entries alternating.
+struct Schedule {
+    bool split;
+    int n_kv, n0;
+    ACACHE_DEVFN int n_tiles(int t) const { return split ? (t == 0 ? n0 : n_kv - n0) : n_kv; }
+    ACACHE_DEVFN int tile(int t, int i) const { return (split && t == 1) ? n0 + i : i; }
+    ACACHE_DEVFN int entry(int t, int i) const {
+        if (!split) return i;
+        const int n1 = n_kv - n0;
+        return i < n1 ? 2 * i + t : n1 + i;
+    }
+    ACACHE_DEVFN int entry_tile(int e) const {
+        if (!split) return e;
+        const int n1 = n_kv - n0;
+        if (e < 2 * n1) return (e & 1) ? n0 + (e >> 1) : (e >> 1);
+        return e - n1;
+    }
+};
+
+ACACHE_DEVFN bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_status,
+                           long long budget) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > budget) {
+            *abort_flag = 1;
+            flag(dev_status, ACACHE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+ACACHE_DEVFN uint64_t f2mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit float inputs, fp32 accumulate
+ACACHE_DEVFN void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// e4m3 A and B (format 0), fp32 D, K-major operands
+constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// K-major descriptor of a tile whose rows are D bytes (one swizzle span of 128 or 64 bytes)
+template <int D>
+ACACHE_DEVFN uint64_t sdesc_rows(uint32_t addr) {
+    uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16;
+    d |= (uint64_t)((8u * D) >> 4) << 32;                    // next 8 rows
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;                 // 128- or 64-byte swizzle
+    return d;
+}
+// byte offset of 16-byte chunk c of row r in such a tile
+template <int D>
+ACACHE_DEVFN uint32_t row_chunk(uint32_t r, uint32_t c) {
+    return r * D + ((D == 128 ? c ^ (r & 7u) : c ^ ((r >> 1) & 3u)) << 4);
+}
+// float4 slot q of row r in the partial-O area
+template <int D>
+ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (uint32_t)((q ^ (r & (D / 4 - 1))) << 4); }
+
+// Four e4m3 codes -> bf16 pairs times f2.  A code's exponent and significand bits moved into a
+// bf16's lowest exponent bits make code * 2^-120 (subnormal codes included: bf16 subnormals); f2
+// holds 2^(120 + ev - 32) twice.
+ACACHE_DEVFN void codes_to_bf16(uint32_t w, uint32_t f2, uint32_t& lo, uint32_t& hi) {
+    const uint32_t x = __byte_perm(w, 0u, 0x1404), y = __byte_perm(w, 0u, 0x3424);
+    const uint32_t a = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+    const uint32_t b = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(f2));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(f2));
+}
+
+template <int D, bool kDrop>
+__global__ void __launch_bounds__(kThreads, 1)
+q8_attn_kernel(const __grid_constant__ Q8Params p) {
+    using G = Geo<D>;
+    extern __shared__ uint8_t dsm[];
+    __shared__ Ctl<D> ctl;
+    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+    uint8_t* base_ptr = dsm + (base - smem_u32(dsm));
+    auto sQ = [&](int t) { return base + 2u * G::kQPart * (uint32_t)t; };          // hi, then lo
+    auto sK = [&](int s) { return base + G::kRing + G::kKTile * (uint32_t)s; };
+    auto sV = [&](int s) { return base + G::kRing + G::kKTile * G::kKSt + G::kVTile * (uint32_t)s; };
+    const int cr = p.cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)p.cs);
+    const int hk = p.cs == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)p.cs);
+    const int b = (int)blockIdx.y;
+    int n_q = p.n_q, T_len = p.T_len;
+    int64_t qbase = (int64_t)b * p.n_q, kbase = (int64_t)b * p.T_len;
+    if (p.q_start) {
+        qbase = p.q_start[b];
+        kbase = p.kv_start[b];
+        n_q = (int)(p.q_start[b + 1] - qbase);
+        T_len = (int)(p.kv_start[b + 1] - kbase);
+        if (n_q != 0 && (n_q < 0 || n_q > p.n_q || T_len < 1 || T_len > p.T_len)) {
+            if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) flag(p.dev_status, ACACHE_DEV_BAD_LENGTH);
+            return;
+        }
+    }
+    const int64_t row0 = (int64_t)blockIdx.z * (kQT * kBM), all_rows = (int64_t)n_q * p.g;
+    if (row0 >= all_rows) return;
+    const int n_rows = (int)min((int64_t)(kQT * kBM), all_rows - row0);
+    const int n_qt = n_rows > kBM ? 2 : 1;
+    const int n_all = (T_len + kBN - 1) / kBN;
+    const int cs = (n_all + p.part - 1) / p.part;              // parts of this request's keys (<= p.cs)
+    if (cr >= cs) return;
+    const int kt0 = (int)((int64_t)cr * n_all / cs);
+    const int n_kv = (int)((int64_t)(cr + 1) * n_all / cs) - kt0;      // >= 1
+    const bool split = n_qt == 1 && n_kv >= 2;
+    const int n_ch = split ? 2 : n_qt;
+    const Schedule sch{split, n_kv, split ? (n_kv + 1) / 2 : n_kv};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
+    volatile int* abort_flag = &ctl.abort;
+    int32_t* dev_status = p.dev_status;
+    const long long budget = p.budget;
+
+    if (threadIdx.x == 0) {
+        const int readers = split ? 1 : n_qt;
+        mbar_init(&ctl.q_full, 4u * n_qt);
+        for (int s = 0; s < G::kKSt; ++s) {
+            mbar_init(&ctl.k_full[s], kProd);
+            mbar_init(&ctl.k_empty[s], readers);
+        }
+        for (int s = 0; s < G::kVSt; ++s) {
+            mbar_init(&ctl.v_full[s], kConv);
+            mbar_init(&ctl.v_empty[s], readers);
+        }
+        for (int t = 0; t < kQT; ++t) {
+            mbar_init(&ctl.s_full[t], 1);
+            mbar_init(&ctl.p_half[t], 128);
+            mbar_init(&ctl.p_full[t], 128);
+            mbar_init(&ctl.drain[t], 1);
+            mbar_init(&ctl.turn[t], 128);
+            mbar_init(&ctl.f_full[t], 4);
+        }
+        ctl.abort = 0;
+        ctl.unlanded = 0;
+        ctl.failed = 0.f;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ctl.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+
+    if (wg == 3) {
+        setmaxnreg_dec<kRegConv>();
+        // ------------------------------------------------------------------ V converters
+        constexpr int CPR = D / 16;                  // 16-byte pieces per pool row
+        constexpr int RPI = 32 / CPR;                // rows per warp load
+        constexpr int NI = 32 / RPI;                 // loads per tile and lane
+        const int w = warp - kConvWarp;
+        const int c = lane % CPR, rr = lane / CPR;
+        auto slot_of = [&](int e) -> int {           // slot of this lane's key (32 w + lane) of entry e, or -1
+            if (e >= n_kv) return -1;
+            const int t = (kt0 + sch.entry_tile(e)) * kBN + 32 * w + lane;
+            if (t >= T_len) return -1;
+            const int s = p.read_slot[kbase + t];
+            return (s >= 0 && s < p.num_slots) ? s : -1;
+        };
+        uint4 dat[2][NI];
+        uint32_t fac[2];
+        auto issue = [&](int sl, uint4 (&d)[NI], uint32_t& f) {
+            // 2^(120 + ev - 32) as bf16; a byte above the largest is NaN, no key has factor 0
+            f = 0u;
+            if (sl >= 0) {
+                const uint32_t s = p.kv_scale[((int64_t)sl * p.Hkv + hk) * 2 + 1];
+                f = s > kQ8MaxByte ? 0x7fffu : (s + 120u - kVShift) << 7;
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int s = __shfl_sync(0xffffffffu, sl, i * RPI + rr);
+                d[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (s >= 0) {
+                    const uint8_t* src = p.v_cache + ((int64_t)s * p.Hkv + hk) * D + c * 16;
+                    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(d[i].x), "=r"(d[i].y), "=r"(d[i].z), "=r"(d[i].w)
+                                 : "l"(src));
+                }
+            }
+        };
+        auto convert = [&](uint32_t dst, const uint4 (&d)[NI], uint32_t f) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const uint32_t r = (uint32_t)(32 * w + i * RPI + rr);
+                uint32_t f2 = __shfl_sync(0xffffffffu, f, i * RPI + rr);
+                f2 |= f2 << 16;
+                uint32_t o[8];
+                codes_to_bf16(d[i].x, f2, o[0], o[1]);
+                codes_to_bf16(d[i].y, f2, o[2], o[3]);
+                codes_to_bf16(d[i].z, f2, o[4], o[5]);
+                codes_to_bf16(d[i].w, f2, o[6], o[7]);
+                // chunks 2c and 2c + 1 of the row; lanes of the second region write them in the
+                // other order, so the eight lanes of a row never meet in a bank
+                const uint32_t flip = (uint32_t)c >> 2;
+                const uint32_t ch0 = 2u * c + flip, ch1 = 2u * c + 1u - flip;
+                const uint32_t row = dst + r * 128u;
+                const uint32_t a0 = row + (ch0 >> 3) * G::kRegion + (((ch0 & 7u) ^ (r & 7u)) << 4);
+                const uint32_t a1 = row + (ch1 >> 3) * G::kRegion + (((ch1 & 7u) ^ (r & 7u)) << 4);
+                if (flip) {
+                    st_shared_v4(a0, o[4], o[5], o[6], o[7]);
+                    st_shared_v4(a1, o[0], o[1], o[2], o[3]);
+                } else {
+                    st_shared_v4(a0, o[0], o[1], o[2], o[3]);
+                    st_shared_v4(a1, o[4], o[5], o[6], o[7]);
+                }
+            }
+        };
+        const int s0 = slot_of(0), s1 = slot_of(1);
+        int s_next = slot_of(2);
+        grid_dependency_wait();                      // store-then-attend: the pool is written now
+        issue(s0, dat[0], fac[0]);
+        issue(s1, dat[1], fac[1]);
+        bool ok = true;
+        for (int e0 = 0; ok && e0 < n_kv; e0 += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int e = e0 + u;
+                if (!ok || e >= n_kv) break;
+                const int s = e % G::kVSt;
+                if (e >= G::kVSt)
+                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.v_empty[s], ((e / G::kVSt) - 1) & 1, abort_flag,
+                                                          dev_status, budget));
+                if (!ok) break;
+                convert(sV(s), dat[u], fac[u]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.v_full[s]);
+                issue(s_next, dat[u], fac[u]);
+                s_next = slot_of(e + 3);
+            }
+        }
+        __syncwarp();
+        if (cs > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+    } else if (wg == 2) {
+        setmaxnreg_dec<kRegIssue>();
+        if (warp >= kProdWarp) {
+            // -------------------------------------------------------------- K producers
+            const int pi = warp - kProdWarp;
+            const bool leader = pi == 0 && lane == 0, flagger = pi == 0;
+            if (leader) {
+                tma_prefetch_desc(&p.tm_k);
+                tma_prefetch_desc(&p.tm_kbox);
+            }
+            // lane l reads the slots of keys 4l .. 4l+3; lanes below 16 gather keys 4x .. 4x+3 with
+            // x = 16 pi + lane.  128 consecutive slots are one box load.
+            auto resolve = [&](int e, int (&rows)[4], int& slot0) -> bool {
+                int sl[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    sl[u] = -1;
+                    if (e < n_kv) {
+                        const int t = (kt0 + sch.entry_tile(e)) * kBN + 4 * lane + u;
+                        if (t < T_len) {
+                            const int s = p.read_slot[kbase + t];
+                            if (s >= 0 && s < p.num_slots) sl[u] = s;
+                            else if (flagger && !(kDrop && s == ACACHE_SLOT_NONE)) flag(dev_status, ACACHE_DEV_BAD_SLOT);
+                        }
+                    }
+                }
+                bool run = sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
+                const int after = __shfl_down_sync(0xffffffffu, sl[0], 1);
+                if (lane < 31) run = run && after == sl[0] + 4;
+                slot0 = __shfl_sync(0xffffffffu, sl[0], 0);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int s = __shfl_sync(0xffffffffu, sl[u], (16 * pi + lane) & 31);
+                    rows[u] = s >= 0 ? s * p.Hkv + hk : p.oob_row;
+                }
+                return __all_sync(0xffffffffu, run);
+            };
+            int next[4], next_slot0;
+            bool next_box = resolve(0, next, next_slot0);
+            grid_dependency_wait();
+            int armed = -1;
+            for (int e = 0; e < n_kv; ++e) {
+                const int s = e % G::kKSt;
+                int rows[4] = {next[0], next[1], next[2], next[3]};
+                const int slot0 = next_slot0;
+                const bool box = next_box;
+                next_box = resolve(e + 1, next, next_slot0);
+                if (e >= G::kKSt && !__all_sync(0xffffffffu, wait_bar(&ctl.k_empty[s], ((e / G::kKSt) - 1) & 1,
+                                                                       abort_flag, dev_status, budget)))
+                    break;
+                // both warps arrive for every entry, so neither can get a phase ahead of the other
+                if (leader) mbar_arrive_expect_tx(&ctl.k_full[s], G::kKTile);
+                else if (lane == 0) mbar_arrive(&ctl.k_full[s]);
+                armed = e;
+                __syncwarp();
+                if (box) {
+                    if (leader) tma_load_3d(sK(s), &p.tm_kbox, 0, hk, slot0, &ctl.k_full[s]);
+                } else if (lane < 16) {
+                    tma_gather4(sK(s) + (uint32_t)(16 * pi + lane) * (4u * D), &p.tm_k, 0, rows[0], rows[1], rows[2],
+                                rows[3], &ctl.k_full[s]);
+                }
+            }
+            // Abort: the loads this warp issued land before the CTA exits (see tc_attn.cu)
+            if (*abort_flag && armed >= 0) {
+                bool landed = true;
+                for (int e = max(0, armed - G::kKSt + 1); e <= armed; ++e)
+                    landed = mbar_wait(&ctl.k_full[e % G::kKSt], (uint32_t)(e / G::kKSt) & 1u, kLandBudget) && landed;
+                if (!__all_sync(0xffffffffu, landed) && lane == 0) ctl.unlanded = 1;
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------------ MMA issuers
+            const int t = warp - kMmaWarp;
+            if (t < n_ch && lane == 0) {
+                constexpr uint32_t idS = idesc_e4m3(kBM, kBN);
+                const uint32_t idO = idesc_bf16(kBM, D, false, true);
+                const uint32_t d_s = tmem + col_s(t), d_o = tmem + col_o(t);
+                const uint64_t dq = sdesc_rows<D>(sQ(split ? 0 : t));
+                const int nt = sch.n_tiles(t);
+                auto issue_s = [&](int e) {
+                    const uint64_t dk = sdesc_rows<D>(sK(e % G::kKSt));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)                    // hi, lo
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            umma_ss_f8(d_s, dq + (uint64_t)((h * G::kQPart + k * 32) >> 4), dk + (uint64_t)(k * 32 >> 4),
+                                       idS, h > 0 || k > 0);
+                    umma_commit(&ctl.s_full[t]);
+                    umma_commit(&ctl.k_empty[e % G::kKSt]);
+                };
+                auto issue_pv_half = [&](int e, bool acc, int h) {
+                    const uint64_t dv = sdesc_sw128(sV(e % G::kVSt), G::kRegion, 1024);
+#pragma unroll
+                    for (int k = 4 * h; k < 4 * h + 4; ++k)
+                        umma_ts(d_o, d_s + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (acc || k > 0));
+                };
+                const int e0 = sch.entry(t, 0);
+                bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget) &&
+                          wait_bar(&ctl.k_full[e0 % G::kKSt], (e0 / G::kKSt) & 1, abort_flag, dev_status, budget);
+                if (ok) {
+                    tc_fence_after();
+                    issue_s(e0);
+                }
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int e = sch.entry(t, i);
+                    ok = wait_bar(&ctl.v_full[e % G::kVSt], (e / G::kVSt) & 1, abort_flag, dev_status, budget) &&
+                         wait_bar(&ctl.p_half[t], i & 1, abort_flag, dev_status, budget);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv_half(e, i > 0, 0);
+                    ok = wait_bar(&ctl.p_full[t], i & 1, abort_flag, dev_status, budget);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv_half(e, i > 0, 1);
+                    umma_commit(&ctl.v_empty[e % G::kVSt]);
+                    if (i + 1 < nt) {
+                        const int en = sch.entry(t, i + 1);
+                        ok = wait_bar(&ctl.k_full[en % G::kKSt], (en / G::kKSt) & 1, abort_flag, dev_status, budget);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(en);
+                    }
+                }
+                // no MMA may still run when TMEM is released
+                umma_commit(&ctl.drain[t]);
+                mbar_wait(&ctl.drain[t], 0, kDrainBudget);
+            }
+            __syncwarp();
+        }
+        if (cs > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+    } else {
+        setmaxnreg_inc<kRegSoftmax>();
+        const int t = wg;                                  // chain
+        const int r = threadIdx.x - t * 128;               // row of the tile = TMEM lane
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int row_of = split ? r : t * kBM + r;        // row of the block this thread works on
+        const bool live = row_of < n_rows && t < n_ch;
+        // element offset of this thread's row in q and out
+        int64_t off = 0;
+        if (row_of < n_rows) {
+            const int64_t i = (row0 + row_of) / p.g;
+            off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (row0 + row_of - i * p.g)) * D;
+        }
+        float c_row = p.scale_log2;
+        if (t < n_ch) {
+            // ---------------------------------------------------------------- query row -> hi + lo
+            // (a split block's chain B only needs the row's power of two)
+            uint4 raw[D / 8];
+            uint32_t top2 = 0;
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x) {
+                raw[x] = live ? __ldg(reinterpret_cast<const uint4*>(p.q + off) + x) : make_uint4(0u, 0u, 0u, 0u);
+                top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(raw[x].x & 0x7fff7fffu, raw[x].y & 0x7fff7fffu),
+                                               __vmaxu2(raw[x].z & 0x7fff7fffu, raw[x].w & 0x7fff7fffu)));
+            }
+            const uint32_t E = max(max(top2 & 0xffffu, top2 >> 16) >> 7, 8u);      // exponent of the largest
+            const bool finite = E != 255u;
+            const float up = finite ? __uint_as_float((261u - E) << 23) : 0.f;      // 2^(134 - E)
+            c_row = finite ? p.scale_log2 * __uint_as_float((E - 7u) << 23) : __uint_as_float(0x7fffffffu);   // 2^(E - 134)
+            if (!(split && t == 1)) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {                                  // 16 elements: one chunk of hi, one of lo
+                    const uint32_t w[8] = {raw[2 * x].x, raw[2 * x].y, raw[2 * x].z, raw[2 * x].w,
+                                           raw[2 * x + 1].x, raw[2 * x + 1].y, raw[2 * x + 1].z, raw[2 * x + 1].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        // a row that is not finite is carried as zeros (c_row is NaN)
+                        const float a = finite ? __uint_as_float(w[y] << 16) * up : 0.f;
+                        const float d = finite ? __uint_as_float(w[y] & 0xffff0000u) * up : 0.f;
+                        const uint32_t h = q8_encode2(a, d);
+                        const float2 hf = q8_decode2(h);
+                        const uint32_t l = q8_encode2(a - hf.x, d - hf.y);
+                        if (y & 1) {
+                            hi[y >> 1] |= h << 16;
+                            lo[y >> 1] |= l << 16;
+                        } else {
+                            hi[y >> 1] = h;
+                            lo[y >> 1] = l;
+                        }
+                    }
+                    const uint32_t o = row_chunk<D>((uint32_t)r, (uint32_t)x);
+                    st_shared_v4(sQ(t) + o, hi[0], hi[1], hi[2], hi[3]);
+                    st_shared_v4(sQ(t) + G::kQPart + o, lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.q_full);
+            }
+        }
+        bool ok = t < n_ch;
+        float m_used = -INFINITY, l_sum = 0.f;
+        if (t < n_ch) {
+            // ---------------------------------------------------------------- softmax
+            const bool pingpong = n_ch > 1;
+            const int nt = sch.n_tiles(t);
+            // this thread looks after key r of each tile: its slot two tiles ahead, its factor one
+            auto slot_of = [&](int i) -> int {
+                if (i >= nt) return -2;
+                const int tk = (kt0 + sch.tile(t, i)) * kBN + r;
+                return tk < T_len ? p.read_slot[kbase + tk] : -2;
+            };
+            auto scale_of = [&](int s) -> uint32_t {
+                return (s >= 0 && s < p.num_slots) ? p.kv_scale[((int64_t)s * p.Hkv + hk) * 2] : 127u;
+            };
+            int s_cur = slot_of(0), s_next = slot_of(1);
+            grid_dependency_wait();
+            uint32_t sc = scale_of(s_cur);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            for (int i = 0; i < nt; ++i) {
+                const int buf = i & 1;
+                ctl.factor[t][buf][r] = q8_factor(sc);
+                if constexpr (kDrop) {
+                    const uint32_t gone = __ballot_sync(0xffffffffu, s_cur == ACACHE_SLOT_NONE);
+                    if (lane == 0) ctl.drop[t][buf][warp & 3] = gone;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.f_full[t]);
+                s_cur = s_next;
+                sc = scale_of(s_cur);
+                s_next = slot_of(i + 2);
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.s_full[t], i & 1, abort_flag, dev_status, budget));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t v[4][32];
+                if (warp_live) {
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) tmem_ld32(lane_base + col_s(t) + cc * 32, v[cc]);
+                    tmem_ld_wait();
+                }
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.f_full[t], i & 1, abort_flag, dev_status, budget));
+                if (!ok) break;
+                if (pingpong && (t == 1 || i > 0))
+                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.turn[t], (t == 0 ? i - 1 : i) & 1, abort_flag,
+                                                          dev_status, budget));
+                if (!ok) break;
+                if (!warp_live) {
+                    // rows past the block: whatever P holds only reaches rows that are never read
+                    mbar_arrive(&ctl.p_half[t]);
+                    mbar_arrive(&ctl.p_full[t]);
+                    if (pingpong) mbar_arrive(&ctl.turn[t ^ 1]);
+                    continue;
+                }
+                // logits in units of c_row: S times the key's factor
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&ctl.factor[t][buf][cc * 32 + x]);
+                        float a, bb;
+                        f2unpack(f2mul(f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1])), f2pack(f.x, f.y)), a, bb);
+                        v[cc][x] = __float_as_uint(a);
+                        v[cc][x + 1] = __float_as_uint(bb);
+                        f2unpack(f2mul(f2pack(__uint_as_float(v[cc][x + 2]), __uint_as_float(v[cc][x + 3])), f2pack(f.z, f.w)), a, bb);
+                        v[cc][x + 2] = __float_as_uint(a);
+                        v[cc][x + 3] = __float_as_uint(bb);
+                    }
+                const int valid = min(kBN, T_len - (kt0 + sch.tile(t, i)) * kBN);
+                if (valid < kBN) {
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (cc * 32 + x >= valid) v[cc][x] = __float_as_uint(-INFINITY);
+                }
+                if constexpr (kDrop) {
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) {
+                        const uint32_t gone = ctl.drop[t][buf][cc];
+                        if (gone) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                if ((gone >> x) & 1u) v[cc][x] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                }
+                float mx[4];
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    mx[cc] = max3f(__uint_as_float(v[cc][0]), __uint_as_float(v[cc][1]), __uint_as_float(v[cc][2]));
+#pragma unroll
+                    for (int x = 3; x < 31; x += 2)
+                        mx[cc] = max3f(mx[cc], __uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
+                    mx[cc] = fmaxf(mx[cc], __uint_as_float(v[cc][31]));
+                }
+                const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c_row;
+                float alpha = 1.f;
+                bool resc = false;
+                if (i == 0) {
+                    m_used = mt;
+                } else if (mt > m_used + kRescaleThreshold) {
+                    alpha = fast_exp2(m_used - mt);
+                    m_used = mt;
+                    resc = true;
+                }
+                if (__any_sync(0xffffffffu, resc)) {
+                    // S of this tile completed after PV of the last: O is final up to there
+#pragma unroll 1
+                    for (int q = 0; q < D / 8; ++q) {
+                        uint32_t o[8];
+                        tmem_ld8(lane_base + col_o(t) + q * 8, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                        tmem_st8(lane_base + col_o(t) + q * 8, o);
+                    }
+                    tmem_st_wait();
+                }
+                // a row whose keys so far were all discarded exponentiates against 0
+                const float ms = (kDrop && m_used == -INFINITY) ? 0.f : m_used;
+                const uint64_t c2 = f2pack(c_row, c_row), nm2 = f2pack(-ms, -ms);
+                uint64_t ls2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        float x0, x1;
+                        f2unpack(f2fma(f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1])), c2, nm2), x0, x1);
+                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                        ls2[(x >> 1) & 1] = f2add(ls2[(x >> 1) & 1], f2pack(p0, p1));
+                        __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
+                        pk[x >> 1] = *reinterpret_cast<uint32_t*>(&two);
+                    }
+                    tmem_st16(lane_base + col_s(t) + cc * 16, pk);
+                    if (cc == 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&ctl.p_half[t]);
+                    }
+                }
+                float l0, l1, l2, l3;
+                f2unpack(ls2[0], l0, l1);
+                f2unpack(ls2[1], l2, l3);
+                l_sum = l_sum * alpha + ((l0 + l1) + (l2 + l3));
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&ctl.p_full[t]);
+                if (pingpong) mbar_arrive(&ctl.turn[t ^ 1]);
+            }
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget));
+        }
+        // Split keys: chain A merges the two partial states (weight 0 for a chain without keys)
+        float w_a = 1.f, w_b = 0.f;
+        if (split) {
+            if (t == 1) {
+                ctl.part_m[kBM + r] = m_used;
+                ctl.part_l[kBM + r] = l_sum;
+            }
+            if (!ok) ctl.failed = 1.f;
+            named_barrier_sync<1>(2 * kBM);
+            ok = ok && ctl.failed == 0.f;
+            if (t == 1) {
+                ok = false;                                // chain A carries the rows from here
+            } else if (ok) {
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[1], 0, abort_flag, dev_status, budget));
+                const float mb = ctl.part_m[kBM + r], lb = ctl.part_l[kBM + r];
+                const float m = fmaxf(m_used, mb);
+                w_a = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m);
+                w_b = mb == -INFINITY ? 0.f : fast_exp2(mb - m);
+                l_sum = l_sum * w_a + lb * w_b;
+                m_used = m;
+            }
+        }
+        auto load_o = [&](int cc, uint32_t (&o)[32]) {
+            tmem_ld32(lane_base + col_o(t) + cc * 32, o);
+            tmem_ld_wait();
+            if (split) {
+                uint32_t ob[32];
+                tmem_ld32(lane_base + col_o(1) + cc * 32, ob);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    o[x] = __float_as_uint(fmaf(__uint_as_float(o[x]), w_a, __uint_as_float(ob[x]) * w_b));
+            }
+        };
+        constexpr float kUnshift = 4294967296.f;           // 2^kVShift
+        if (cs == 1) {
+            if (ok) {
+                tc_fence_after();
+                // rows go through this chain's query buffer so that a warp writes whole rows
+                const float inv = l_sum == 0.f ? 0.f : kUnshift / l_sum;
+                const uint32_t stage = sQ(t) + (uint32_t)r * (2u * D);
+                constexpr uint32_t kCh = D / 8;            // 16-byte chunks per output row
+#pragma unroll
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[32];
+                    load_o(cc, o);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t k[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float a = __uint_as_float(o[8 * x + 2 * y]) * inv, d = __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
+                            __nv_bfloat162 two = __floats2bfloat162_rn(a, d);
+                            k[y] = *reinterpret_cast<uint32_t*>(&two);
+                        }
+                        const uint32_t ch = (uint32_t)(4 * cc + x);
+                        st_shared_v4(stage + ((ch ^ ((uint32_t)r & (kCh - 1u))) << 4), k[0], k[1], k[2], k[3]);
+                    }
+                }
+                __syncwarp();
+                constexpr int kRows = 32 / (int)kCh;       // rows per warp store
+#pragma unroll 4
+                for (int it = 0; it < 32 / kRows; ++it) {
+                    const int lr = it * kRows + lane / (int)kCh, ch = lane % (int)kCh;
+                    const int64_t o = __shfl_sync(0xffffffffu, off, lr);
+                    const int rr = (warp & 3) * 32 + lr;
+                    if ((split ? 0 : t * kBM) + rr < n_rows) {
+                        const uint4 val = *reinterpret_cast<const uint4*>(
+                            base_ptr + (sQ(t) - base) + (uint32_t)rr * (2u * D) + (((uint32_t)ch ^ ((uint32_t)rr & (kCh - 1u))) << 4));
+                        *(reinterpret_cast<uint4*>(p.out + o) + ch) = val;
+                    }
+                }
+            }
+        } else {
+            // partial of this part: the rings are free once both chains' MMAs are complete
+            if (!split && n_ch == 2 && ok)
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t ^ 1], 0, abort_flag, dev_status, budget));
+            if (t < n_qt) {
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[32];
+                        load_o(cc, o);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            *reinterpret_cast<uint4*>(base_ptr + G::kRing + part_off<D>(t * kBM + r, cc * 8 + x)) =
+                                make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    }
+                    ctl.part_m[t * kBM + r] = m_used;
+                    ctl.part_l[t * kBM + r] = l_sum;
+                } else {
+                    ctl.failed = 1.f;
+                }
+            }
+            cluster_sync();
+            // rank w finalises the (row, 32-column) items w, w + cs, ...
+            const uint32_t m_a = smem_u32(&ctl.part_m[0]), l_a = smem_u32(&ctl.part_l[0]), f_a = smem_u32(&ctl.failed);
+            bool all = true;
+            for (int w = 0; w < cs; ++w) all = all && ld_cluster_f32(mapa_shared(f_a, w)) == 0.f;
+            if (all)
+                for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 32); it += cs * 2 * kBM) {
+                    const int rr = it / (D / 32), c4 = it % (D / 32);
+                    float M = -INFINITY;
+                    for (int w = 0; w < cs; ++w) M = fmaxf(M, ld_cluster_f32(mapa_shared(m_a + 4u * rr, w)));
+                    float acc[32], L = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) acc[x] = 0.f;
+                    for (int w = 0; w < cs; ++w) {
+                        const float mw = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
+                        if (mw == -INFINITY) continue;       // no key in this part
+                        const float e = fast_exp2(mw - M);
+                        L = fmaf(e, ld_cluster_f32(mapa_shared(l_a + 4u * rr, w)), L);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const float4 f = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, c4 * 8 + x), w));
+                            acc[4 * x] = fmaf(e, f.x, acc[4 * x]);
+                            acc[4 * x + 1] = fmaf(e, f.y, acc[4 * x + 1]);
+                            acc[4 * x + 2] = fmaf(e, f.z, acc[4 * x + 2]);
+                            acc[4 * x + 3] = fmaf(e, f.w, acc[4 * x + 3]);
+                        }
+                    }
+                    const float inv = L == 0.f ? 0.f : kUnshift / L;
+                    const int64_t i = (row0 + rr) / p.g;
+                    bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (row0 + rr - i * p.g)) * D + c4 * 32;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t k[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            __nv_bfloat162 two = __floats2bfloat162_rn(acc[8 * x + 2 * y] * inv, acc[8 * x + 2 * y + 1] * inv);
+                            k[y] = *reinterpret_cast<uint32_t*>(&two);
+                        }
+                        reinterpret_cast<uint4*>(o)[x] = make_uint4(k[0], k[1], k[2], k[3]);
+                    }
+                }
+            __syncwarp();
+            cluster_sync();        // no CTA may leave while another still reads its shared memory
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag) settle_after_abort(ctl.unlanded != 0);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Per device and variant: 0 = not prepared yet, 1 = ready, otherwise the status to return.
+// Preparing twice is harmless, so a race between threads only repeats the work.
+std::atomic<int> g_prepared[4][64];
+
+template <int D, bool kDrop>
+int prepare() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return ACACHE_ERR_CUDA;
+    }
+    std::atomic<int>& st = g_prepared[(D == 128 ? 2 : 0) + (kDrop ? 1 : 0)][dev];
+    const int known = st.load(std::memory_order_acquire);
+    if (known) return known == 1 ? ACACHE_OK : known;
+    auto kern = q8_attn_kernel<D, kDrop>;
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kBytes) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, kern) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ACACHE_ERR_CUDA;   // not cached: a later call may succeed
+    }
+    // the register split assumes the launch allocation; refuse to launch otherwise
+    const int rc = fa.numRegs * kThreads < 2 * 128 * kRegSoftmax + 128 * kRegIssue + 128 * kRegConv ? ACACHE_ERR_UNSUPPORTED
+                                                                                                 : ACACHE_OK;
+    st.store(rc == ACACHE_OK ? 1 : rc, std::memory_order_release);
+    return rc;
+}
+
+template <int D, bool kDrop>
+int launch(const Q8Params& prm, dim3 grid, cudaStream_t stream, bool pdl) {
+    auto kern = q8_attn_kernel<D, kDrop>;
+    if (int rc = prepare<D, kDrop>()) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Geo<D>::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    if (prm.cs > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = (unsigned)prm.cs;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    if (pdl) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    if (cudaLaunchKernelEx(&cfg, kern, prm) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ACACHE_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+bool q8_tc_supported(const AttnArgs& a) {
+    return a.dtype == ACACHE_BF16 && a.scale > 0.f;
+}
+
+int launch_q8_tc_attention(const Q8Attn& c) {
+    const int d = c.a.d, hkv = c.a.hkv, g = c.a.hq / hkv;
+    if (c.num_slots * hkv >= 0x7fffffffLL) return ACACHE_ERR_INVALID_ARG;
+    const int64_t n_rb = ((int64_t)c.n_q * g + kQT * kBM - 1) / (kQT * kBM);
+    if (c.B > 65535 || n_rb > 65535 || (int64_t)hkv * kMaxCluster > 0x7fffffff) return ACACHE_ERR_INVALID_ARG;
+    Q8Params prm{};
+    const uint64_t rows[2] = {(uint64_t)d, (uint64_t)(c.num_slots * hkv)};
+    const uint64_t pool[3] = {(uint64_t)d, (uint64_t)hkv, (uint64_t)c.num_slots};
+    const uint32_t one[2] = {(uint32_t)d, 1}, box[3] = {(uint32_t)d, 1, kBN};
+    if (!make_map_u8(&prm.tm_k, c.k_cache, 2, rows, one) || !make_map_u8(&prm.tm_kbox, c.k_cache, 3, pool, box))
+        return ACACHE_ERR_CUDA;
+    prm.q = (const bf16*)c.q;
+    prm.v_cache = c.v_cache;
+    prm.kv_scale = c.kv_scale;
+    prm.read_slot = c.read_slot;
+    prm.q_start = c.q_start;
+    prm.kv_start = c.kv_start;
+    prm.out = (bf16*)c.out;
+    prm.dev_status = c.dev_status;
+    prm.num_slots = c.num_slots;
+    prm.oob_row = (int)(c.num_slots * hkv) + (c.num_slots == 0);
+    prm.n_q = c.n_q;
+    prm.T_len = c.T_len;
+    prm.Hq = c.a.hq;
+    prm.Hkv = hkv;
+    prm.g = g;
+    prm.scale_log2 = c.a.scale * kLog2e;
+    prm.budget = wait_budget();
+    // Parts of the key range: waves x (tiles per part + the fixed cost of a CTA, about 4 tiles, and
+    // of a merge, about 2).
+    const int n_all = (c.T_len + kBN - 1) / kBN;
+    const int64_t units = (int64_t)c.B * hkv * n_rb, nsm = sm_count();
+    prm.cs = 1;
+    int64_t best = 0;
+    for (int cs = 1; cs <= kMaxCluster && cs <= n_all; cs *= 2) {
+        const int64_t est = ((units * cs + nsm - 1) / nsm) * ((n_all + cs - 1) / cs + 4 + (cs > 1 ? 2 : 0));
+        if (cs == 1 || est < best) {
+            best = est;
+            prm.cs = cs;
+        }
+    }
+    prm.part = (n_all + prm.cs - 1) / prm.cs;
+    const dim3 grid((unsigned)(hkv * prm.cs), (unsigned)c.B, (unsigned)n_rb);
+    if (d == 128)
+        return c.drop_none ? launch<128, true>(prm, grid, c.stream, c.after_store)
+                           : launch<128, false>(prm, grid, c.stream, c.after_store);
+    return c.drop_none ? launch<64, true>(prm, grid, c.stream, c.after_store)
+                       : launch<64, false>(prm, grid, c.stream, c.after_store);
+}
+
+}  // namespace acache

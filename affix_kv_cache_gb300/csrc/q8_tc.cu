@@ -22,9 +22,11 @@
 //   WG0, WG1  softmax + epilogue of chain A / B, thread r owns row r (= TMEM lane r): first it turns
 //             its query row into hi and lo; then per key tile it reads S from TMEM, multiplies by the
 //             keys' factors, exponentiates in base 2 against a lazily raised maximum and writes P
-//             over S.  The two chains take turns.  It fetches one key's scale a tile ahead.
+//             over S, 64 keys a step.  A chain has two S buffers of 64 keys: the MMA of the next step
+//             runs under the softmax of this one.
 //   WG2       warps 8 and 9 issue the MMAs of chain A / B; warps 10 and 11 fill the K ring by TMA (a
-//             tile of consecutive slots as one box, any other as 32 gather4 loads).
+//             tile of consecutive slots as one box, any other as 32 gather4 loads) and the ring of the
+//             keys' factors.
 //   WG3       V: each thread reads 16-byte pieces of pool rows into registers two tiles ahead,
 //             converts them to bf16 and writes the V ring.  Through registers instead of a raw ring:
 //             the converted tile is the only copy in shared memory.
@@ -41,19 +43,17 @@
 #include <algorithm>
 #include <atomic>
 
-#include "q8.cuh"
-#include "ptx.cuh"
-#include "tc_attn.cuh"
+#include "q8_tc.cuh"
 
 namespace acache {
 namespace {
 
-using namespace ptx;
-using bf16 = __nv_bfloat16;
+using namespace q8;
 
 constexpr int kBM = 128;                    // rows per tile (TMEM lanes)
 constexpr int kQT = 2;                      // row tiles per CTA
-constexpr int kBN = 128;                    // keys per tile
+constexpr int kBN = 128;                    // keys per tile (ring entry)
+constexpr int kStep = 64;                   // keys per step (half a tile): one S buffer of a chain
 constexpr int kMmaWarp = 8;
 constexpr int kProdWarp = 10, kProd = 2;    // K producer warps
 constexpr int kConvWarp = 12, kConv = 4;    // V converter warps
@@ -61,13 +61,15 @@ constexpr int kThreads = 512;
 // Registers: 512 x 128 at launch = 65536; 2 x 128 x 168 + 128 x 56 + 128 x 120 = 65536.
 constexpr int kRegSoftmax = 168, kRegIssue = 56, kRegConv = 120;
 static_assert(2 * 128 * kRegSoftmax + 128 * kRegIssue + 128 * kRegConv <= kThreads * 128, "register split");
-constexpr uint32_t kTmemCols = 512;         // S_A, S_B, O_A, O_B
+constexpr uint32_t kTmemCols = 512;         // two S buffers of 64 columns per chain, O_A, O_B
 __host__ __device__ constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + (uint32_t)t * 128u; }
-constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
+// log2 units a row's maximum may grow before O and the sum are rescaled.  bf16 and float32 have the
+// same exponents, so P up to 2^40 costs no precision, and the sums stay far inside float32.
+constexpr float kRescaleThreshold = 40.0f;
 constexpr int kVShift = 32;                 // V is carried times 2^-32
+constexpr int kFSt = 8;                     // ring of the keys' factors (see the K producers)
 constexpr int kMaxCluster = 8;
-constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles, abort path
 
 template <int D>
 struct Geo {
@@ -103,14 +105,16 @@ struct Ctl {
     uint64_t q_full;
     uint64_t k_full[Geo<D>::kKSt], k_empty[Geo<D>::kKSt];
     uint64_t v_full[Geo<D>::kVSt], v_empty[Geo<D>::kVSt];
-    uint64_t s_full[kQT], p_half[kQT], p_full[kQT], drain[kQT], turn[kQT];
-    uint64_t f_full[kQT];              // the keys' factors of chain t's tile are in `factor`
+    uint64_t s_full[kQT][2], p_full[kQT][2];   // by step parity
+    uint64_t pv_done[kQT];             // phase u: PV of step u is complete
+    uint64_t drain[kQT];
+    uint64_t f_full[kFSt];             // the keys' factors of a ring entry are in `factor`
     uint32_t tmem_base;
     int abort, unlanded;
-    uint32_t drop[kQT][2][4];          // discarded keys, 32 per word
+    uint32_t drop[kFSt][4];            // discarded keys, 32 per word
     float part_m[kQT * kBM], part_l[kQT * kBM];
     float failed;                      // this CTA gave up (read by the other ranks)
-    __align__(16) float factor[kQT][2][kBN];
+    __align__(16) float factor[kFSt][kBN];
 };
 
 // Chain t's i-th key tile comes through ring entry entry(t, i).  One row tile: chain 0 reads
@@ -119,6 +123,11 @@ struct Schedule {
     bool split;
     int n_kv, n0;
     ACACHE_DEVFN int n_tiles(int t) const { return split ? (t == 0 ? n0 : n_kv - n0) : n_kv; }
+    // steps (half tiles) of chain t; `last` = keys of the part's last tile: 64 or fewer leave its
+    // second half out
+    ACACHE_DEVFN int n_steps(int t, int last) const {
+        return 2 * n_tiles(t) - (last <= kStep && (!split || t == 1) ? 1 : 0);
+    }
     ACACHE_DEVFN int tile(int t, int i) const { return (split && t == 1) ? n0 + i : i; }
     ACACHE_DEVFN int entry(int t, int i) const {
         if (!split) return i;
@@ -132,57 +141,6 @@ struct Schedule {
         return e - n1;
     }
 };
-
-ACACHE_DEVFN bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_status,
-                           long long budget) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (clock64() - t0 > budget) {
-            *abort_flag = 1;
-            flag(dev_status, ACACHE_DEV_TIMEOUT);
-            return false;
-        }
-    }
-}
-
-ACACHE_DEVFN uint64_t f2mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-// D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit float inputs, fp32 accumulate
-ACACHE_DEVFN void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// e4m3 A and B (format 0), fp32 D, K-major operands
-constexpr uint32_t idesc_e4m3(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// K-major descriptor of a tile whose rows are D bytes (one swizzle span of 128 or 64 bytes)
-template <int D>
-ACACHE_DEVFN uint64_t sdesc_rows(uint32_t addr) {
-    uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16;
-    d |= (uint64_t)((8u * D) >> 4) << 32;                    // next 8 rows
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;                 // 128- or 64-byte swizzle
-    return d;
-}
-// byte offset of 16-byte chunk c of row r in such a tile
-template <int D>
-ACACHE_DEVFN uint32_t row_chunk(uint32_t r, uint32_t c) {
-    return r * D + ((D == 128 ? c ^ (r & 7u) : c ^ ((r >> 1) & 3u)) << 4);
-}
-// float4 slot q of row r in the partial-O area
-template <int D>
-ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (uint32_t)((q ^ (r & (D / 4 - 1))) << 4); }
 
 // Four e4m3 codes -> bf16 pairs times f2.  A code's exponent and significand bits moved into a
 // bf16's lowest exponent bits make code * 2^-120 (subnormal codes included: bf16 subnormals); f2
@@ -233,6 +191,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
     const bool split = n_qt == 1 && n_kv >= 2;
     const int n_ch = split ? 2 : n_qt;
     const Schedule sch{split, n_kv, split ? (n_kv + 1) / 2 : n_kv};
+    const int last_keys = min(kBN, T_len - (kt0 + n_kv - 1) * kBN);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
     volatile int* abort_flag = &ctl.abort;
     int32_t* dev_status = p.dev_status;
@@ -250,13 +209,14 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             mbar_init(&ctl.v_empty[s], readers);
         }
         for (int t = 0; t < kQT; ++t) {
-            mbar_init(&ctl.s_full[t], 1);
-            mbar_init(&ctl.p_half[t], 128);
-            mbar_init(&ctl.p_full[t], 128);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&ctl.s_full[t][h], 1);
+                mbar_init(&ctl.p_full[t][h], 128);
+            }
+            mbar_init(&ctl.pv_done[t], 1);
             mbar_init(&ctl.drain[t], 1);
-            mbar_init(&ctl.turn[t], 128);
-            mbar_init(&ctl.f_full[t], 4);
         }
+        for (int s = 0; s < kFSt; ++s) mbar_init(&ctl.f_full[s], kProd);
         ctl.abort = 0;
         ctl.unlanded = 0;
         ctl.failed = 0.f;
@@ -278,67 +238,64 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         constexpr int RPI = 32 / CPR;                // rows per warp load
         constexpr int NI = 32 / RPI;                 // loads per tile and lane
         const int w = warp - kConvWarp;
-        const int c = lane % CPR, rr = lane / CPR;
-        auto slot_of = [&](int e) -> int {           // slot of this lane's key (32 w + lane) of entry e, or -1
-            if (e >= n_kv) return -1;
-            const int t = (kt0 + sch.entry_tile(e)) * kBN + 32 * w + lane;
-            if (t >= T_len) return -1;
-            const int s = p.read_slot[kbase + t];
-            return (s >= 0 && s < p.num_slots) ? s : -1;
+        // Lane -> piece c of row rr of a load.  The eight lanes of a shared-memory phase hold four
+        // pieces of one 64-column region in two neighbouring rows: their swizzled chunks differ.
+        const int c = (lane & 3) | (D == 128 ? (lane >> 4) << 2 : 0), rr = (lane >> 2) & (RPI - 1);
+        // Loads are issued a tile or two before their values are looked at: nothing is computed from
+        // a value in the step that loads it.
+        auto slot_of = [&](int e) -> int {           // slot of this lane's key (32 w + lane) of entry e
+            int s = -1;
+            if (e < n_kv) {
+                const int t = (kt0 + sch.entry_tile(e)) * kBN + 32 * w + lane;
+                if (t < T_len) s = p.read_slot[kbase + t];
+            }
+            return s;
         };
         uint4 dat[2][NI];
-        uint32_t fac[2];
-        auto issue = [&](int sl, uint4 (&d)[NI], uint32_t& f) {
-            // 2^(120 + ev - 32) as bf16; a byte above the largest is NaN, no key has factor 0
-            f = 0u;
-            if (sl >= 0) {
-                const uint32_t s = p.kv_scale[((int64_t)sl * p.Hkv + hk) * 2 + 1];
-                f = s > kQ8MaxByte ? 0x7fffu : (s + 120u - kVShift) << 7;
-            }
+        uint32_t sc[2];                              // V's scale byte of this lane's key; 256: no row
+        // All shuffles before all loads: between two loads, a shuffle would wait for the first one.
+        // A key without a row reads the pool's first row, with factor 0.
+        const uint8_t* v_lane = p.v_cache + (int64_t)hk * D + c * 16;
+        auto issue = [&](int slot, uint4 (&d)[NI], uint32_t& f) {
+            const bool in = slot >= 0 && slot < p.num_slots;
+            const int sl = in ? slot : 0;
+            int s[NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int s = __shfl_sync(0xffffffffu, sl, i * RPI + rr);
-                d[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (s >= 0) {
-                    const uint8_t* src = p.v_cache + ((int64_t)s * p.Hkv + hk) * D + c * 16;
-                    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(d[i].x), "=r"(d[i].y), "=r"(d[i].z), "=r"(d[i].w)
-                                 : "l"(src));
-                }
-            }
+            for (int i = 0; i < NI; ++i) s[i] = __shfl_sync(0xffffffffu, sl, i * RPI + rr);
+            f = 256u;
+            if (in) f = p.kv_scale[((int64_t)sl * p.Hkv + hk) * 2 + 1];
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(d[i].x), "=r"(d[i].y), "=r"(d[i].z), "=r"(d[i].w)
+                             : "l"(v_lane + (int64_t)s[i] * ((int64_t)p.Hkv * D)));
         };
         auto convert = [&](uint32_t dst, const uint4 (&d)[NI], uint32_t f) {
+            // 2^(120 + ev - 32) as bf16, twice; a byte above the largest is NaN
+            uint32_t g2 = f > 255u ? 0u : f > kQ8MaxByte ? 0x7fffu : (f + 120u - kVShift) << 7;
+            g2 |= g2 << 16;
+            const uint32_t at = dst + (uint32_t)(32 * w + rr) * 128u + ((uint32_t)c >> 2) * G::kRegion;
+            uint32_t f2[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) f2[i] = __shfl_sync(0xffffffffu, g2, i * RPI + rr);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const uint32_t r = (uint32_t)(32 * w + i * RPI + rr);
-                uint32_t f2 = __shfl_sync(0xffffffffu, f, i * RPI + rr);
-                f2 |= f2 << 16;
                 uint32_t o[8];
-                codes_to_bf16(d[i].x, f2, o[0], o[1]);
-                codes_to_bf16(d[i].y, f2, o[2], o[3]);
-                codes_to_bf16(d[i].z, f2, o[4], o[5]);
-                codes_to_bf16(d[i].w, f2, o[6], o[7]);
-                // chunks 2c and 2c + 1 of the row; lanes of the second region write them in the
-                // other order, so the eight lanes of a row never meet in a bank
-                const uint32_t flip = (uint32_t)c >> 2;
-                const uint32_t ch0 = 2u * c + flip, ch1 = 2u * c + 1u - flip;
-                const uint32_t row = dst + r * 128u;
-                const uint32_t a0 = row + (ch0 >> 3) * G::kRegion + (((ch0 & 7u) ^ (r & 7u)) << 4);
-                const uint32_t a1 = row + (ch1 >> 3) * G::kRegion + (((ch1 & 7u) ^ (r & 7u)) << 4);
-                if (flip) {
-                    st_shared_v4(a0, o[4], o[5], o[6], o[7]);
-                    st_shared_v4(a1, o[0], o[1], o[2], o[3]);
-                } else {
-                    st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-                    st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-                }
+                codes_to_bf16(d[i].x, f2[i], o[0], o[1]);
+                codes_to_bf16(d[i].y, f2[i], o[2], o[3]);
+                codes_to_bf16(d[i].z, f2[i], o[4], o[5]);
+                codes_to_bf16(d[i].w, f2[i], o[6], o[7]);
+                // chunks 2c and 2c + 1 (of the region) of the row
+                const uint32_t a0 = at + i * RPI * 128u + (((2u * c & 7u) ^ ((uint32_t)(i * RPI + rr) & 7u)) << 4);
+                st_shared_v4(a0, o[0], o[1], o[2], o[3]);
+                st_shared_v4(a0 ^ 16u, o[4], o[5], o[6], o[7]);
             }
         };
         const int s0 = slot_of(0), s1 = slot_of(1);
         int s_next = slot_of(2);
         grid_dependency_wait();                      // store-then-attend: the pool is written now
-        issue(s0, dat[0], fac[0]);
-        issue(s1, dat[1], fac[1]);
+        issue(s0, dat[0], sc[0]);
+        issue(s1, dat[1], sc[1]);
         bool ok = true;
         for (int e0 = 0; ok && e0 < n_kv; e0 += 2) {
 #pragma unroll
@@ -350,11 +307,11 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                     ok = __all_sync(0xffffffffu, wait_bar(&ctl.v_empty[s], ((e / G::kVSt) - 1) & 1, abort_flag,
                                                           dev_status, budget));
                 if (!ok) break;
-                convert(sV(s), dat[u], fac[u]);
+                convert(sV(s), dat[u], sc[u]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.v_full[s]);
-                issue(s_next, dat[u], fac[u]);
+                if (e + 2 < n_kv) issue(s_next, dat[u], sc[u]);
                 s_next = slot_of(e + 3);
             }
         }
@@ -368,26 +325,34 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         if (warp >= kProdWarp) {
             // -------------------------------------------------------------- K producers
             const int pi = warp - kProdWarp;
-            const bool leader = pi == 0 && lane == 0, flagger = pi == 0;
+            const bool leader = pi == 0 && lane == 0;
             if (leader) {
                 tma_prefetch_desc(&p.tm_k);
                 tma_prefetch_desc(&p.tm_kbox);
             }
-            // lane l reads the slots of keys 4l .. 4l+3; lanes below 16 gather keys 4x .. 4x+3 with
-            // x = 16 pi + lane.  128 consecutive slots are one box load.
-            auto resolve = [&](int e, int (&rows)[4], int& slot0) -> bool {
-                int sl[4];
+            // Lane l reads the slots of keys 4l .. 4l+3; lanes below 16 gather keys 4x .. 4x+3 with
+            // x = 16 pi + lane and look up their factors.  128 consecutive slots are one box load.
+            // Slots are loaded two entries ahead and scales one.
+            const int x = 16 * pi + (lane & 15);
+            auto load_slots = [&](int e, int (&raw)[4]) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    sl[u] = -1;
+                    raw[u] = kNoKey;
                     if (e < n_kv) {
                         const int t = (kt0 + sch.entry_tile(e)) * kBN + 4 * lane + u;
-                        if (t < T_len) {
-                            const int s = p.read_slot[kbase + t];
-                            if (s >= 0 && s < p.num_slots) sl[u] = s;
-                            else if (flagger && !(kDrop && s == ACACHE_SLOT_NONE)) flag(dev_status, ACACHE_DEV_BAD_SLOT);
-                        }
+                        if (t < T_len) raw[u] = p.read_slot[kbase + t];
                     }
+                }
+            };
+            auto resolve = [&](const int (&raw)[4], int (&rows)[4], int& slot0, uint32_t& gone) -> bool {
+                int sl[4];
+                gone = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const bool in = raw[u] >= 0 && raw[u] < p.num_slots;
+                    sl[u] = in ? raw[u] : -1;
+                    if (kDrop && raw[u] == ACACHE_SLOT_NONE) gone |= 1u << u;
+                    else if (!in && raw[u] != kNoKey && pi == 0) flag(dev_status, ACACHE_DEV_BAD_SLOT);
                 }
                 bool run = sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
                 const int after = __shfl_down_sync(0xffffffffu, sl[0], 1);
@@ -395,21 +360,33 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 slot0 = __shfl_sync(0xffffffffu, sl[0], 0);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int s = __shfl_sync(0xffffffffu, sl[u], (16 * pi + lane) & 31);
+                    const int s = __shfl_sync(0xffffffffu, sl[u], x);
                     rows[u] = s >= 0 ? s * p.Hkv + hk : p.oob_row;
+                }
+                if constexpr (kDrop) {                 // eight lanes' keys make a word
+                    gone <<= 4 * (lane & 7);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) gone |= __shfl_xor_sync(0xffffffffu, gone, o);
                 }
                 return __all_sync(0xffffffffu, run);
             };
-            int next[4], next_slot0;
-            bool next_box = resolve(0, next, next_slot0);
+            auto load_scales = [&](const int (&rows)[4], uint32_t (&sc)[4]) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    sc[u] = 127u;                      // a zero row: any finite factor
+                    if (rows[u] != p.oob_row) sc[u] = p.kv_scale[(int64_t)rows[u] * 2];
+                }
+            };
+            int raw[4], rows[4], slot0;
+            uint32_t sc[4], gone;
+            load_slots(0, raw);
+            bool box = resolve(raw, rows, slot0, gone);
+            load_slots(1, raw);
             grid_dependency_wait();
+            load_scales(rows, sc);
             int armed = -1;
             for (int e = 0; e < n_kv; ++e) {
-                const int s = e % G::kKSt;
-                int rows[4] = {next[0], next[1], next[2], next[3]};
-                const int slot0 = next_slot0;
-                const bool box = next_box;
-                next_box = resolve(e + 1, next, next_slot0);
+                const int s = e % G::kKSt, fs = e % kFSt;
                 if (e >= G::kKSt && !__all_sync(0xffffffffu, wait_bar(&ctl.k_empty[s], ((e / G::kKSt) - 1) & 1,
                                                                        abort_flag, dev_status, budget)))
                     break;
@@ -421,8 +398,23 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 if (box) {
                     if (leader) tma_load_3d(sK(s), &p.tm_kbox, 0, hk, slot0, &ctl.k_full[s]);
                 } else if (lane < 16) {
-                    tma_gather4(sK(s) + (uint32_t)(16 * pi + lane) * (4u * D), &p.tm_k, 0, rows[0], rows[1], rows[2],
-                                rows[3], &ctl.k_full[s]);
+                    tma_gather4(sK(s) + (uint32_t)x * (4u * D), &p.tm_k, 0, rows[0], rows[1], rows[2], rows[3],
+                                &ctl.k_full[s]);
+                }
+                // The factors' ring: a chain's S of a step is issued only after its softmax has written
+                // the P two steps before; so once entry e - kKSt is free (the wait above), the
+                // factors of that chain's entries before it have been read, and with split keys those
+                // of the other chain's up to two entries earlier: kFSt > kKSt + 3 entries suffice.
+                if (lane < 16)
+                    *reinterpret_cast<float4*>(&ctl.factor[fs][4 * x]) =
+                        make_float4(q8_factor(sc[0]), q8_factor(sc[1]), q8_factor(sc[2]), q8_factor(sc[3]));
+                if (kDrop && pi == 0 && (lane & 7) == 0) ctl.drop[fs][lane >> 3] = gone;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.f_full[fs]);
+                if (e + 1 < n_kv) {
+                    box = resolve(raw, rows, slot0, gone);
+                    load_scales(rows, sc);
+                    load_slots(e + 2, raw);
                 }
             }
             // Abort: the loads this warp issued land before the CTA exits (see tc_attn.cu)
@@ -437,54 +429,46 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             // ------------------------------------------------------------------ MMA issuers
             const int t = warp - kMmaWarp;
             if (t < n_ch && lane == 0) {
-                constexpr uint32_t idS = idesc_e4m3(kBM, kBN);
+                constexpr uint32_t idS = idesc_e4m3(kBM, kStep);
                 const uint32_t idO = idesc_bf16(kBM, D, false, true);
                 const uint32_t d_s = tmem + col_s(t), d_o = tmem + col_o(t);
                 const uint64_t dq = sdesc_rows<D>(sQ(split ? 0 : t));
-                const int nt = sch.n_tiles(t);
-                auto issue_s = [&](int e) {
-                    const uint64_t dk = sdesc_rows<D>(sK(e % G::kKSt));
+                const int n_st = sch.n_steps(t, last_keys);
+                // step u: half u & 1 of the chain's tile u / 2, into S buffer u & 1
+                auto issue_s = [&](int u) -> bool {
+                    const int e = sch.entry(t, u >> 1), h = u & 1;
+                    if (h == 0 && !wait_bar(&ctl.k_full[e % G::kKSt], (e / G::kKSt) & 1, abort_flag, dev_status, budget))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t dk = sdesc_rows<D>(sK(e % G::kKSt) + (uint32_t)(h * kStep * D));
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)                    // hi, lo
+                    for (int x = 0; x < 2; ++x)                    // hi, lo
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k)
-                            umma_ss_f8(d_s, dq + (uint64_t)((h * G::kQPart + k * 32) >> 4), dk + (uint64_t)(k * 32 >> 4),
-                                       idS, h > 0 || k > 0);
-                    umma_commit(&ctl.s_full[t]);
-                    umma_commit(&ctl.k_empty[e % G::kKSt]);
+                            umma_ss_f8(d_s + h * kStep, dq + (uint64_t)((x * G::kQPart + k * 32) >> 4),
+                                       dk + (uint64_t)(k * 32 >> 4), idS, x > 0 || k > 0);
+                    umma_commit(&ctl.s_full[t][h]);
+                    if (h == 1 || u + 1 == n_st) umma_commit(&ctl.k_empty[e % G::kKSt]);
+                    return true;
                 };
-                auto issue_pv_half = [&](int e, bool acc, int h) {
-                    const uint64_t dv = sdesc_sw128(sV(e % G::kVSt), G::kRegion, 1024);
+                bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget);
+                for (int u = 0; ok && u < 2 && u < n_st; ++u) ok = issue_s(u);
+                // PV of step u once its P is in TMEM, then S of step u + 2 into the buffer P came from
+                // (MMAs of one thread run in issue order); S of step u + 1 is there already, so the
+                // softmax never waits for it.
+                for (int u = 0; ok && u < n_st; ++u) {
+                    const int e = sch.entry(t, u >> 1), h = u & 1;
+                    ok = (h == 1 || wait_bar(&ctl.v_full[e % G::kVSt], (e / G::kVSt) & 1, abort_flag, dev_status, budget)) &&
+                         wait_bar(&ctl.p_full[t][h], (u >> 1) & 1, abort_flag, dev_status, budget);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dv = sdesc_sw128(sV(e % G::kVSt) + (uint32_t)(h * kStep * 128), G::kRegion, 1024);
 #pragma unroll
-                    for (int k = 4 * h; k < 4 * h + 4; ++k)
-                        umma_ts(d_o, d_s + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (acc || k > 0));
-                };
-                const int e0 = sch.entry(t, 0);
-                bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget) &&
-                          wait_bar(&ctl.k_full[e0 % G::kKSt], (e0 / G::kKSt) & 1, abort_flag, dev_status, budget);
-                if (ok) {
-                    tc_fence_after();
-                    issue_s(e0);
-                }
-                for (int i = 0; ok && i < nt; ++i) {
-                    const int e = sch.entry(t, i);
-                    ok = wait_bar(&ctl.v_full[e % G::kVSt], (e / G::kVSt) & 1, abort_flag, dev_status, budget) &&
-                         wait_bar(&ctl.p_half[t], i & 1, abort_flag, dev_status, budget);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv_half(e, i > 0, 0);
-                    ok = wait_bar(&ctl.p_full[t], i & 1, abort_flag, dev_status, budget);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv_half(e, i > 0, 1);
-                    umma_commit(&ctl.v_empty[e % G::kVSt]);
-                    if (i + 1 < nt) {
-                        const int en = sch.entry(t, i + 1);
-                        ok = wait_bar(&ctl.k_full[en % G::kKSt], (en / G::kKSt) & 1, abort_flag, dev_status, budget);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_s(en);
-                    }
+                    for (int k = 0; k < kStep / 16; ++k)
+                        umma_ts(d_o, d_s + h * kStep + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (u > 0 || k > 0));
+                    umma_commit(&ctl.pv_done[t]);
+                    if (h == 1 || u + 1 == n_st) umma_commit(&ctl.v_empty[e % G::kVSt]);
+                    if (u + 2 < n_st) ok = issue_s(u + 2);
                 }
                 // no MMA may still run when TMEM is released
                 umma_commit(&ctl.drain[t]);
@@ -504,53 +488,22 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         const int row_of = split ? r : t * kBM + r;        // row of the block this thread works on
         const bool live = row_of < n_rows && t < n_ch;
         // element offset of this thread's row in q and out
-        int64_t off = 0;
-        if (row_of < n_rows) {
-            const int64_t i = (row0 + row_of) / p.g;
-            off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (row0 + row_of - i * p.g)) * D;
-        }
+        const int64_t off = [&] {
+            const int64_t pr = row0 + (row_of < n_rows ? row_of : 0), i = pr / p.g;
+            return ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
+        }();
+        const bool warp_live = __any_sync(0xffffffffu, live);
         float c_row = p.scale_log2;
         if (t < n_ch) {
-            // ---------------------------------------------------------------- query row -> hi + lo
-            // (a split block's chain B only needs the row's power of two)
-            uint4 raw[D / 8];
-            uint32_t top2 = 0;
-#pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
-                raw[x] = live ? __ldg(reinterpret_cast<const uint4*>(p.q + off) + x) : make_uint4(0u, 0u, 0u, 0u);
-                top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(raw[x].x & 0x7fff7fffu, raw[x].y & 0x7fff7fffu),
-                                               __vmaxu2(raw[x].z & 0x7fff7fffu, raw[x].w & 0x7fff7fffu)));
+            // ---------------------------------------------------------------- query rows -> hi + lo
+            // (rows past the block read the block's first row; warps past it leave theirs unwritten:
+            // what they hold only reaches output rows that are never read)
+            if (warp_live) {
+                const uint32_t at = sQ(t) + (uint32_t)((warp & 3) * 32 * D);
+                c_row = query_terms<D>(p.q, off, at, at + G::kQPart, lane, p.scale_log2);
             }
-            const uint32_t E = max(max(top2 & 0xffffu, top2 >> 16) >> 7, 8u);      // exponent of the largest
-            const bool finite = E != 255u;
-            const float up = finite ? __uint_as_float((261u - E) << 23) : 0.f;      // 2^(134 - E)
-            c_row = finite ? p.scale_log2 * __uint_as_float((E - 7u) << 23) : __uint_as_float(0x7fffffffu);   // 2^(E - 134)
+            // a split block's chain B converts into the free query buffer: it needs the rows' powers of two
             if (!(split && t == 1)) {
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) {                                  // 16 elements: one chunk of hi, one of lo
-                    const uint32_t w[8] = {raw[2 * x].x, raw[2 * x].y, raw[2 * x].z, raw[2 * x].w,
-                                           raw[2 * x + 1].x, raw[2 * x + 1].y, raw[2 * x + 1].z, raw[2 * x + 1].w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        // a row that is not finite is carried as zeros (c_row is NaN)
-                        const float a = finite ? __uint_as_float(w[y] << 16) * up : 0.f;
-                        const float d = finite ? __uint_as_float(w[y] & 0xffff0000u) * up : 0.f;
-                        const uint32_t h = q8_encode2(a, d);
-                        const float2 hf = q8_decode2(h);
-                        const uint32_t l = q8_encode2(a - hf.x, d - hf.y);
-                        if (y & 1) {
-                            hi[y >> 1] |= h << 16;
-                            lo[y >> 1] |= l << 16;
-                        } else {
-                            hi[y >> 1] = h;
-                            lo[y >> 1] = l;
-                        }
-                    }
-                    const uint32_t o = row_chunk<D>((uint32_t)r, (uint32_t)x);
-                    st_shared_v4(sQ(t) + o, hi[0], hi[1], hi[2], hi[3]);
-                    st_shared_v4(sQ(t) + G::kQPart + o, lo[0], lo[1], lo[2], lo[3]);
-                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.q_full);
@@ -560,81 +513,50 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         float m_used = -INFINITY, l_sum = 0.f;
         if (t < n_ch) {
             // ---------------------------------------------------------------- softmax
-            const bool pingpong = n_ch > 1;
-            const int nt = sch.n_tiles(t);
-            // this thread looks after key r of each tile: its slot two tiles ahead, its factor one
-            auto slot_of = [&](int i) -> int {
-                if (i >= nt) return -2;
-                const int tk = (kt0 + sch.tile(t, i)) * kBN + r;
-                return tk < T_len ? p.read_slot[kbase + tk] : -2;
-            };
-            auto scale_of = [&](int s) -> uint32_t {
-                return (s >= 0 && s < p.num_slots) ? p.kv_scale[((int64_t)s * p.Hkv + hk) * 2] : 127u;
-            };
-            int s_cur = slot_of(0), s_next = slot_of(1);
-            grid_dependency_wait();
-            uint32_t sc = scale_of(s_cur);
-            const bool warp_live = __any_sync(0xffffffffu, live);
-            for (int i = 0; i < nt; ++i) {
-                const int buf = i & 1;
-                ctl.factor[t][buf][r] = q8_factor(sc);
-                if constexpr (kDrop) {
-                    const uint32_t gone = __ballot_sync(0xffffffffu, s_cur == ACACHE_SLOT_NONE);
-                    if (lane == 0) ctl.drop[t][buf][warp & 3] = gone;
+            const int n_st = sch.n_steps(t, last_keys);
+            for (int u = 0; u < n_st; ++u) {
+                const int e = sch.entry(t, u >> 1), h = u & 1, fs = e % kFSt;
+                if (h == 0) {
+                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.f_full[fs], (e / kFSt) & 1, abort_flag, dev_status, budget));
+                    if (!ok) break;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.f_full[t]);
-                s_cur = s_next;
-                sc = scale_of(s_cur);
-                s_next = slot_of(i + 2);
-                ok = __all_sync(0xffffffffu, wait_bar(&ctl.s_full[t], i & 1, abort_flag, dev_status, budget));
+                // the keys' factors, on their way while S is waited for
+                uint32_t f[kStep / 4][4];
+#pragma unroll
+                for (int x = 0; x < kStep / 4; ++x)
+                    ld_shared_v4(smem_u32(&ctl.factor[fs][0]) + (uint32_t)(h * kStep + 4 * x) * 4u, f[x]);
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.s_full[t][h], (u >> 1) & 1, abort_flag, dev_status, budget));
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t v[4][32];
-                if (warp_live) {
-#pragma unroll
-                    for (int cc = 0; cc < 4; ++cc) tmem_ld32(lane_base + col_s(t) + cc * 32, v[cc]);
-                    tmem_ld_wait();
-                }
-                ok = __all_sync(0xffffffffu, wait_bar(&ctl.f_full[t], i & 1, abort_flag, dev_status, budget));
-                if (!ok) break;
-                if (pingpong && (t == 1 || i > 0))
-                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.turn[t], (t == 0 ? i - 1 : i) & 1, abort_flag,
-                                                          dev_status, budget));
-                if (!ok) break;
                 if (!warp_live) {
                     // rows past the block: whatever P holds only reaches rows that are never read
-                    mbar_arrive(&ctl.p_half[t]);
-                    mbar_arrive(&ctl.p_full[t]);
-                    if (pingpong) mbar_arrive(&ctl.turn[t ^ 1]);
+                    mbar_arrive(&ctl.p_full[t][h]);
                     continue;
                 }
-                // logits in units of c_row: S times the key's factor
+                const uint32_t s_at = lane_base + col_s(t) + (uint32_t)(h * kStep);
+                uint32_t v[2][32];
+                tmem_ld32(s_at, v[0]);
+                tmem_ld32(s_at + 32, v[1]);
+                tmem_ld_wait();
+                // logits in units of c_row: S times the keys' factors
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc)
+                for (int x = 0; x < kStep; x += 2) {
+                    float a, bb;
+                    f2unpack(f2mul(f2pack(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1])),
+                                   f2pack(__uint_as_float(f[x >> 2][x & 3]), __uint_as_float(f[x >> 2][(x & 3) + 1]))), a, bb);
+                    v[x >> 5][x & 31] = __float_as_uint(a);
+                    v[x >> 5][(x & 31) + 1] = __float_as_uint(bb);
+                }
+                const int valid = T_len - (kt0 + sch.tile(t, u >> 1)) * kBN - h * kStep;
+                if (valid < kStep) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&ctl.factor[t][buf][cc * 32 + x]);
-                        float a, bb;
-                        f2unpack(f2mul(f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1])), f2pack(f.x, f.y)), a, bb);
-                        v[cc][x] = __float_as_uint(a);
-                        v[cc][x + 1] = __float_as_uint(bb);
-                        f2unpack(f2mul(f2pack(__uint_as_float(v[cc][x + 2]), __uint_as_float(v[cc][x + 3])), f2pack(f.z, f.w)), a, bb);
-                        v[cc][x + 2] = __float_as_uint(a);
-                        v[cc][x + 3] = __float_as_uint(bb);
-                    }
-                const int valid = min(kBN, T_len - (kt0 + sch.tile(t, i)) * kBN);
-                if (valid < kBN) {
-#pragma unroll
-                    for (int cc = 0; cc < 4; ++cc)
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (cc * 32 + x >= valid) v[cc][x] = __float_as_uint(-INFINITY);
+                    for (int x = 0; x < kStep; ++x)
+                        if (x >= valid) v[x >> 5][x & 31] = __float_as_uint(-INFINITY);
                 }
                 if constexpr (kDrop) {
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc) {
-                        const uint32_t gone = ctl.drop[t][buf][cc];
+                    for (int cc = 0; cc < 2; ++cc) {
+                        const uint32_t gone = ctl.drop[fs][2 * h + cc];
                         if (gone) {
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
@@ -644,17 +566,17 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 }
                 float mx[4];
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    mx[cc] = max3f(__uint_as_float(v[cc][0]), __uint_as_float(v[cc][1]), __uint_as_float(v[cc][2]));
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t* y = &v[q >> 1][(q & 1) * 16];
+                    mx[q] = max3f(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
 #pragma unroll
-                    for (int x = 3; x < 31; x += 2)
-                        mx[cc] = max3f(mx[cc], __uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
-                    mx[cc] = fmaxf(mx[cc], __uint_as_float(v[cc][31]));
+                    for (int x = 3; x < 15; x += 2) mx[q] = max3f(mx[q], __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
+                    mx[q] = fmaxf(mx[q], __uint_as_float(y[15]));
                 }
                 const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c_row;
                 float alpha = 1.f;
                 bool resc = false;
-                if (i == 0) {
+                if (u == 0) {
                     m_used = mt;
                 } else if (mt > m_used + kRescaleThreshold) {
                     alpha = fast_exp2(m_used - mt);
@@ -662,7 +584,10 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                     resc = true;
                 }
                 if (__any_sync(0xffffffffu, resc)) {
-                    // S of this tile completed after PV of the last: O is final up to there
+                    // O holds the steps before this one once PV of the last is complete
+                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.pv_done[t], (u - 1) & 1, abort_flag, dev_status, budget));
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int q = 0; q < D / 8; ++q) {
                         uint32_t o[8];
@@ -679,7 +604,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 const uint64_t c2 = f2pack(c_row, c_row), nm2 = f2pack(-ms, -ms);
                 uint64_t ls2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
+                for (int cc = 0; cc < 2; ++cc) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) {
@@ -690,12 +615,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                         __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
                         pk[x >> 1] = *reinterpret_cast<uint32_t*>(&two);
                     }
-                    tmem_st16(lane_base + col_s(t) + cc * 16, pk);
-                    if (cc == 1) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        mbar_arrive(&ctl.p_half[t]);
-                    }
+                    tmem_st16(s_at + cc * 16, pk);
                 }
                 float l0, l1, l2, l3;
                 f2unpack(ls2[0], l0, l1);
@@ -703,8 +623,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 l_sum = l_sum * alpha + ((l0 + l1) + (l2 + l3));
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&ctl.p_full[t]);
-                if (pingpong) mbar_arrive(&ctl.turn[t ^ 1]);
+                mbar_arrive(&ctl.p_full[t][h]);
             }
             if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget));
         }

@@ -73,5 +73,8 @@ int launch_q8_simt_attention(const Q8Attn& c);
 // True when the tcgen05 kernel covers the call: bf16 and a positive softmax scale.
 bool q8_tc_supported(const AttnArgs& a);
 int launch_q8_tc_attention(const Q8Attn& c);
+// ... and the one for few rows per (request, KV head): at most 64 packed rows (queries x group).
+bool q8_decode_supported(const AttnArgs& a, int n_q);
+int launch_q8_decode_attention(const Q8Attn& c);
 
 }  // namespace acache

@@ -18,8 +18,9 @@ int attend(const Q8Attn& c) {
     if (!c.q || !c.read_slot || !c.out || !aligned16(c.q) || !aligned16(c.out) ||
         !pool_ok(c.k_cache, c.v_cache, c.kv_scale))
         return ACACHE_ERR_INVALID_ARG;
-    // (an empty pool: every key is a zero row, and there is no row for the tensor-core kernel to read)
-    return q8_tc_supported(c.a) && c.num_slots > 0 ? launch_q8_tc_attention(c) : launch_q8_simt_attention(c);
+    // (an empty pool: every key is a zero row, and there is no row for a tensor map to start at)
+    if (c.num_slots == 0 || !q8_tc_supported(c.a)) return launch_q8_simt_attention(c);
+    return q8_decode_supported(c.a, c.n_q) ? launch_q8_decode_attention(c) : launch_q8_tc_attention(c);
 }
 
 Q8Attn call(const AttnArgs& a, int batch, int n_q, const void* q, int seq_len, const int32_t* read_slot,

@@ -304,7 +304,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 if (!ok || e >= n_kv) break;
                 const int s = e % G::kVSt;
                 if (e >= G::kVSt)
-                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.v_empty[s], ((e / G::kVSt) - 1) & 1, abort_flag,
+                    ok = __all_sync(0xffffffffu, wait_bar<true>(&ctl.v_empty[s], ((e / G::kVSt) - 1) & 1, abort_flag,
                                                           dev_status, budget));
                 if (!ok) break;
                 convert(sV(s), dat[u], sc[u]);
@@ -387,7 +387,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             int armed = -1;
             for (int e = 0; e < n_kv; ++e) {
                 const int s = e % G::kKSt, fs = e % kFSt;
-                if (e >= G::kKSt && !__all_sync(0xffffffffu, wait_bar(&ctl.k_empty[s], ((e / G::kKSt) - 1) & 1,
+                if (e >= G::kKSt && !__all_sync(0xffffffffu, wait_bar<true>(&ctl.k_empty[s], ((e / G::kKSt) - 1) & 1,
                                                                        abort_flag, dev_status, budget)))
                     break;
                 // both warps arrive for every entry, so neither can get a phase ahead of the other
@@ -737,9 +737,10 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                     for (int x = 0; x < 32; ++x) acc[x] = 0.f;
                     for (int w = 0; w < cs; ++w) {
                         const float mw = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
-                        if (mw == -INFINITY) continue;       // no key in this part
+                        const float lw = ld_cluster_f32(mapa_shared(l_a + 4u * rr, w));
+                        if (mw == -INFINITY && lw == 0.f) continue;       // no key in this part
                         const float e = fast_exp2(mw - M);
-                        L = fmaf(e, ld_cluster_f32(mapa_shared(l_a + 4u * rr, w)), L);
+                        L = fmaf(e, lw, L);
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
                             const float4 f = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, c4 * 8 + x), w));
@@ -849,7 +850,7 @@ int launch_q8_tc_attention(const Q8Attn& c) {
     const uint64_t rows[2] = {(uint64_t)d, (uint64_t)(c.num_slots * hkv)};
     const uint64_t pool[3] = {(uint64_t)d, (uint64_t)hkv, (uint64_t)c.num_slots};
     const uint32_t one[2] = {(uint32_t)d, 1}, box[3] = {(uint32_t)d, 1, kBN};
-    if (!make_map_u8(&prm.tm_k, c.k_cache, 2, rows, one) || !make_map_u8(&prm.tm_kbox, c.k_cache, 3, pool, box))
+    if (!make_map_u8(&prm.tm_k, c.k_cache, 2, rows, one, true) || !make_map_u8(&prm.tm_kbox, c.k_cache, 3, pool, box, true))
         return ACACHE_ERR_CUDA;
     prm.q = (const bf16*)c.q;
     prm.v_cache = c.v_cache;

@@ -15,12 +15,21 @@ using bf16 = __nv_bfloat16;
 constexpr int kNoKey = INT32_MIN;           // read-slot entry of a key past the request's last
 constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles, abort path
 
+// Bounded wait for a phase.  A try that finds the phase incomplete suspends the warp for some 90 cycles;
+// what it issues between tries is taken from the working warps' slots.  kSlack: the waiter runs a
+// ring's depth ahead, so it sleeps between tries instead.
+template <bool kSlack = false>
 ACACHE_DEVFN bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_status,
                            long long budget) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
+        if (kSlack) __nanosleep(100);
         if (mbar_try_wait(bar, parity)) return true;
+        if (!kSlack) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (mbar_try_wait(bar, parity)) return true;
+        }
         if (*abort_flag) return false;
         if (clock64() - t0 > budget) {
             *abort_flag = 1;
@@ -72,7 +81,7 @@ ACACHE_DEVFN uint32_t row_chunk(uint32_t r, uint32_t c) {
 template <int D>
 ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (uint32_t)((q ^ (r & (D / 4 - 1))) << 4); }
 
-// 32 query rows -> two e4m3 terms each, by one warp.  Lane l brings the element offset of row l of the
+// n (of 32) query rows -> two e4m3 terms each, by one warp (whole groups of rows are converted).  Lane l brings the element offset of row l of the
 // 32; `hi` and `lo` are the shared-memory addresses of the first row's terms (rows of D bytes,
 // swizzled).  Returns the factor of lane l's row: its logits are S times the keys' factors times it
 // (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite, which
@@ -81,12 +90,13 @@ ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (
 // second in its row of lo: LPR lanes to a row, so the loads are whole rows.  Four groups of rows at
 // a time keep the chain load - maximum - convert - subtract - convert of several rows in flight.
 template <int D>
-ACACHE_DEVFN float query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, int lane, float scale_log2) {
+ACACHE_DEVFN float query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, int lane, float scale_log2,
+                              int n = 32) {
     constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI, GR = 4;
     const uint32_t pc = (uint32_t)(lane % LPR), row = (uint32_t)(lane / LPR);
     const uint32_t at = (pc >= LPR / 2 ? lo : hi) + (pc % (LPR / 2)) * 16u + row * D;
 #pragma unroll 4
-    for (int it = 0; it < NI; ++it) {
+    for (int it = 0; it < NI && it * RPI < n; ++it) {
         const int64_t o = __shfl_sync(0xffffffffu, off, it * RPI + row);
         cp_async16(at + (uint32_t)(it * RPI * D), q + o + pc * 8, 16);
     }
@@ -95,7 +105,7 @@ ACACHE_DEVFN float query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t
     __syncwarp();
     uint32_t e_row = 8u;
 #pragma unroll 1
-    for (int g = 0; g < NI / GR; ++g) {
+    for (int g = 0; g < NI / GR && g * GR * RPI < n; ++g) {
         uint32_t w[GR][4], top[GR];
 #pragma unroll
         for (int u = 0; u < GR; ++u) ld_shared_v4(at + (uint32_t)((g * GR + u) * RPI * D), w[u]);

@@ -249,6 +249,24 @@ def test_masked_bad_and_poisoned_keys(dtype, d, n_q, T):
     assert_attention(got[1], want, tol, "beside a poisoned request")
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("n_q", [1, 40, 300])
+def test_a_poisoned_key_among_discarded_ones_is_not_lost(dtype, d, n_q):
+    """The parts a row's keys are split into: one holds only discarded keys and the poisoned one."""
+    hq, hkv, T = 2, 1, 2000
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(1, n_q, hq, hkv, d, dtype, T, False, 21)
+    sc[7, 0, 0] = 255
+    rs[0, 64:] = -1
+    rs[0][rs[0] == 7] = 1
+    for at in (700, 1999):
+        one = rs.clone()
+        one[0, at] = 7
+        out = torch.zeros(q.shape, dtype=dtype, device="cuda")
+        ac.acache_slot_attention_q8(_desc(hq, hkv, d, dtype), 1, n_q, dev(q), T, dev(one), dev(kc), dev(vc), dev(sc), ns, out,
+                                    drop_none=True)
+        assert torch.isnan(out).all()
+
+
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 64)])
 def test_non_finite_queries_stay_in_their_rows(dtype, d):
     hq, hkv, T, n_q = 2, 1, 260, 20

@@ -9,7 +9,7 @@
 //   * S as in q8_tc.cu: hi and lo of the query rows times the codes as they lie in the pool.
 //   * O: P times V's codes converted to f16 (exact, one instruction for two).  Their power of two goes
 //     into the exponent instead: P = 2^(s + ev - m) with m the running maximum of s + ev, so P
-//     V is right whatever the rows' scales are, P never exceeds 2^15 and keys down to 2^-31 of the
+//     V is right whatever the rows' scales are, P never exceeds 2^15 and keys down to 2^-27 of the
 //     largest weighted one count (f16 subnormals); the sum adds P 2^-ev in float32.  Each thread has 32 or 64
 //     keys of a tile, so this costs less than scaling 128 x d values would.
 //   * Up to 32 (64) rows are replicated 4 (2) times over the 128 TMEM lanes, each replica taking a
@@ -20,16 +20,13 @@
 //     (maximum, sum, O) of all replicas and ranks are merged through distributed shared memory in a
 //     fixed order -- no workspace, no second launch.
 //
-// Warps (512 threads, 1 CTA per SM): 0-3 softmax; 4-7 convert V; 8 issues every MMA; 9-15 fill the ring
-// of K and V codes by TMA: a tile of consecutive slots is two boxes, any other 64 gather4 loads, 9 or 10
-// per warp (a gather4 takes its warp some 90 cycles to issue, measured).  Warp 9 also writes the
-// ring of the keys' factors.
+// Warps (416 threads, 1 CTA per SM): 0-3 softmax; 4-7 bring V's codes and convert them; 8-11 bring K's
+// codes and the keys' factors; 12 issues every MMA.  The codes come by 16-byte cp.async, a warp taking
+// 32 keys of every tile: a gather4 takes its warp some 90 cycles to issue for four rows (measured),
+// a cp.async instruction a tenth of that for as many; and pool addresses need no tensor maps.
 // TMEM (512 columns): S0 [0,128)  S1 [128,256)  O [256,384)  P0 [384,448)  P1 [448,512).
 //
 // Every mbarrier wait is bounded (see q8_tc.cu).
-#include <cuda.h>
-
-#include <algorithm>
 #include <atomic>
 
 #include "q8_tc.cuh"
@@ -40,16 +37,17 @@ namespace {
 using namespace q8;
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 512;
-constexpr int kConvWarp = 4, kConv = 4, kMmaWarp = 8, kProdWarp = 9, kProd = 7;
-constexpr int kSt = 3;                      // ring of K and V codes
+constexpr int kThreads = 416;
+constexpr int kVWarp = 4, kKWarp = 8, kMmaWarp = 12;
+constexpr int kKSt = 4, kKLag = 2;          // K ring; an entry is announced kKLag entries after its loads
+constexpr int kRSt = 3;                     // V's codes (each warp's rows are its own)
 constexpr int kVSt = 2;                     // V in f16
 constexpr int kFSt = 8;                     // factors
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS0 = 0, kColO = 256, kColP0 = 384;
-constexpr float kPHead = 7.0f;              // P of the running maximum is 2^7 ...
-constexpr float kRescaleThreshold = 8.0f;   // ... and never above 2^15
+constexpr float kPHead = 3.0f;              // P of the used maximum is 2^3 ...
+constexpr float kRescaleThreshold = 12.0f;  // ... and never above 2^15
 
 template <int D>
 struct Geo {
@@ -58,16 +56,16 @@ struct Geo {
     static constexpr uint32_t kVTile = kBN * D * 2;        // V in f16
     static constexpr uint32_t kRegion = kBN * 128;         // 64 columns of it
     static constexpr uint32_t kRing = 2 * kQPart;
-    static constexpr uint32_t kVRing = kRing + kSt * 2 * kTile;
+    static constexpr uint32_t kRRing = kRing + kKSt * kTile;
+    static constexpr uint32_t kVRing = kRRing + kRSt * kTile;
     static constexpr uint32_t kBytes = kVRing + kVSt * kVTile + 1024;
-    static_assert(kSt * 2 * kTile >= kBM * D * 4u, "partial O reuses the ring");
+    static_assert(kKSt * kTile >= kBM * D * 4u, "partial O reuses the K ring");
+    static_assert(kVSt * kVTile >= 64 * D * 4u, "and the merged rows V's");
 };
 
 struct DecParams {
-    CUtensorMap tm_k, tm_v;         // 2-D pool rows [num_slots*Hkv][d], box {d, 1} (gather4)
-    CUtensorMap tm_kbox, tm_vbox;   // 3-D pool [num_slots][Hkv][d], box {d, 1, 128}
     const bf16* q;
-    const uint8_t* kv_scale;
+    const uint8_t *k_cache, *v_cache, *kv_scale;
     const int32_t *read_slot, *q_start, *kv_start;
     bf16* out;
     int32_t* dev_status;
@@ -80,16 +78,18 @@ struct DecParams {
 
 struct Ctl {
     uint64_t q_full;
-    uint64_t full[kSt], empty[kSt];
+    uint64_t k_full[kKSt], k_empty[kKSt];
     uint64_t v_full[kVSt], v_empty[kVSt];
     uint64_t f_full[kFSt];
     uint64_t s_full[2], p_full[2];
     uint64_t pv_done, drain;
     uint32_t tmem_base;
-    int abort, unlanded;
+    int abort;
     float failed;
     uint32_t drop[kFSt][4];
-    float part_m[kBM], part_l[kBM];
+    float part_m[kBM], part_l[kBM];         // per lane
+    float row_m[64], row_l[64];             // per row, replicas merged
+    float c_row[64];
     __align__(16) float fk[kFSt][kBN];      // 2^ek
     __align__(16) float ev[kFSt][kBN];      // ev
     __align__(16) float rv[kFSt][kBN];      // 2^-ev
@@ -109,8 +109,8 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
     __shared__ Ctl ctl;
     const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
     const uint32_t sQ = base;
-    auto sK = [&](int s) { return base + G::kRing + 2u * G::kTile * (uint32_t)s; };
-    auto sR = [&](int s) { return base + G::kRing + 2u * G::kTile * (uint32_t)s + G::kTile; };
+    auto sK = [&](int s) { return base + G::kRing + G::kTile * (uint32_t)s; };
+    auto sR = [&](int s) { return base + G::kRRing + G::kTile * (uint32_t)s; };
     auto sV = [&](int s) { return base + G::kVRing + G::kVTile * (uint32_t)s; };
     const int cr = p.cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)p.cs);
     const int hk = p.cs == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)p.cs);
@@ -139,17 +139,31 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
     int32_t* dev_status = p.dev_status;
     const long long budget = p.budget;
 
+    // K and V warps: lane l looks after key 32 w + l of every tile.  The maps are not written by a store
+    // this launch may overlap: the first slots are on their way during the set-up.
+    const int w = warp & 3;
+    auto slot_of = [&](int e) -> int {
+        const int t = (kt0 + e) * kBN + 32 * w + lane;
+        int s = kNoKey;
+        if (e < n_kv && t < T_len) s = p.read_slot[kbase + t];
+        return s;
+    };
+    int s_cur = kNoKey, s_next = kNoKey;
+    if (warp >= kVWarp && warp < kMmaWarp) {
+        s_cur = slot_of(0);
+        s_next = slot_of(1);
+    }
     if (threadIdx.x == 0) {
         mbar_init(&ctl.q_full, 4);
-        for (int s = 0; s < kSt; ++s) {
-            mbar_init(&ctl.full[s], kProd);
-            mbar_init(&ctl.empty[s], 1 + kConv);     // S has read K, the converters V
+        for (int s = 0; s < kKSt; ++s) {
+            mbar_init(&ctl.k_full[s], 4);
+            mbar_init(&ctl.k_empty[s], 1);
         }
         for (int s = 0; s < kVSt; ++s) {
-            mbar_init(&ctl.v_full[s], kConv);
+            mbar_init(&ctl.v_full[s], 4);
             mbar_init(&ctl.v_empty[s], 1);
         }
-        for (int s = 0; s < kFSt; ++s) mbar_init(&ctl.f_full[s], 1);
+        for (int s = 0; s < kFSt; ++s) mbar_init(&ctl.f_full[s], 4);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&ctl.s_full[t], 1);
             mbar_init(&ctl.p_full[t], 4);
@@ -157,7 +171,6 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
         mbar_init(&ctl.pv_done, 1);
         mbar_init(&ctl.drain, 1);
         ctl.abort = 0;
-        ctl.unlanded = 0;
         ctl.failed = 0.f;
         fence_mbar_init();
     }
@@ -169,120 +182,69 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
+    // Pieces of a row (16 bytes), rows per warp instruction, instructions per tile of a K or V warp.
+    constexpr int CPR = D / 16, RPI = 32 / CPR, NI = 32 / RPI;
 
-    if (warp >= kProdWarp) {
-        // ---------------------------------------------------------------------- TMA producers
-        const int pi = warp - kProdWarp;
-        if (pi == 0 && lane == 0) {
-            tma_prefetch_desc(&p.tm_k);
-            tma_prefetch_desc(&p.tm_v);
-            tma_prefetch_desc(&p.tm_kbox);
-            tma_prefetch_desc(&p.tm_vbox);
-        }
-        // this lane's gather x: K of keys 4x .. 4x+3 (x < 32), V of keys 4(x-32) .. (x < 64), or none
-        const int x = kProd * lane + pi;
-        const int oob_row = (int)(p.num_slots * p.Hkv);
-        auto load_slots = [&](int e, int (&raw)[4]) {            // of keys 4 lane .. 4 lane + 3
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                raw[u] = kNoKey;
-                const int t = (kt0 + e) * kBN + 4 * lane + u;
-                if (e < n_kv && t < T_len) raw[u] = p.read_slot[kbase + t];
-            }
+    if (warp >= kKWarp && warp < kMmaWarp) {
+        // ---------------------------------------------------------------------- K
+        const int c = lane % CPR, rr = lane / CPR;
+        const uint8_t* src = p.k_cache + (int64_t)hk * D + c * 16;
+        const int64_t row_bytes = (int64_t)p.Hkv * D;
+        auto scale_of = [&](int s) -> uint32_t {
+            uint32_t two = 127u | 127u << 8;             // a zero row: factor 1
+            if (s >= 0 && s < p.num_slots) two = reinterpret_cast<const uint16_t*>(p.kv_scale)[(int64_t)s * p.Hkv + hk];
+            return two;
         };
-        auto resolve = [&](const int (&raw)[4], int (&own)[4], int (&rows)[4], int& slot0, uint32_t& gone) -> bool {
-            int sl[4];
-            gone = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool in = raw[u] >= 0 && raw[u] < p.num_slots;
-                sl[u] = in ? raw[u] : -1;
-                own[u] = in ? raw[u] * p.Hkv + hk : oob_row;
-                if (kDrop && raw[u] == ACACHE_SLOT_NONE) gone |= 1u << u;
-                else if (!in && raw[u] != kNoKey && pi == 0) flag(dev_status, ACACHE_DEV_BAD_SLOT);
-            }
-            bool run = sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
-            const int after = __shfl_down_sync(0xffffffffu, sl[0], 1);
-            if (lane < 31) run = run && after == sl[0] + 4;
-            slot0 = __shfl_sync(0xffffffffu, sl[0], 0);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) rows[u] = __shfl_sync(0xffffffffu, own[u], x & 31);
-            if (kDrop && pi == 0) {                  // eight lanes' keys make a word
-                gone <<= 4 * (lane & 7);
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) gone |= __shfl_xor_sync(0xffffffffu, gone, o);
-            }
-            return __all_sync(0xffffffffu, run);
-        };
-        auto load_scales = [&](const int (&own)[4], uint32_t (&sc)[4]) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                sc[u] = 127u | 127u << 8;            // a zero row: factor 1
-                if (own[u] != oob_row) sc[u] = reinterpret_cast<const uint16_t*>(p.kv_scale)[own[u]];
-            }
-        };
-        int raw[4], own[4], rows[4], slot0;
-        uint32_t sc[4], gone;
-        load_slots(0, raw);
-        bool box = resolve(raw, own, rows, slot0, gone);
-        load_slots(1, raw);
-        grid_dependency_wait();                      // store-then-attend: the pool is written now
-        if (pi == 0) load_scales(own, sc);
-        int armed = -1;
-        for (int e = 0; e < n_kv; ++e) {
-            const int s = e % kSt, fs = e % kFSt;
-            if (e >= kSt && !__all_sync(0xffffffffu, wait_bar(&ctl.empty[s], ((e / kSt) - 1) & 1, abort_flag, dev_status, budget)))
+        grid_dependency_wait();                          // store-then-attend: the pool is written now
+        uint32_t sc = scale_of(s_cur);
+        int e = 0;
+        for (; e < n_kv; ++e) {
+            const int s = e % kKSt, fs = e % kFSt;
+            if (e >= kKSt && !__all_sync(0xffffffffu, wait_bar(&ctl.k_empty[s], ((e / kKSt) - 1) & 1, abort_flag, dev_status, budget)))
                 break;
-            // every warp arrives for every entry, so none can get a phase ahead of another
-            if (lane == 0) {
-                if (pi == 0) mbar_arrive_expect_tx(&ctl.full[s], 2 * G::kTile);
-                else mbar_arrive(&ctl.full[s]);
-            }
-            armed = e;
-            __syncwarp();
-            if (box) {
-                if (pi == 0 && lane == 0) {
-                    tma_load_3d(sK(s), &p.tm_kbox, 0, hk, slot0, &ctl.full[s]);
-                    tma_load_3d(sR(s), &p.tm_vbox, 0, hk, slot0, &ctl.full[s]);
-                }
-            } else if (x < 32) {
-                tma_gather4(sK(s) + (uint32_t)x * (4u * D), &p.tm_k, 0, rows[0], rows[1], rows[2], rows[3], &ctl.full[s]);
-            } else if (x < 64) {
-                tma_gather4(sR(s) + (uint32_t)(x - 32) * (4u * D), &p.tm_v, 0, rows[0], rows[1], rows[2], rows[3],
-                            &ctl.full[s]);
-            }
-            __syncwarp();
-            if (pi == 0) {
-                // (S of an entry is issued after the softmax of the entry two before it wrote P, so the
-                // factors read last are those of entry e - kSt - 1 at the earliest: kFSt > kSt + 3)
-                float fk[4], ev[4], rv[4];
+            const bool in = s_cur >= 0 && s_cur < p.num_slots;
+            const bool none = kDrop && s_cur == ACACHE_SLOT_NONE;
+            if (!in && !none && s_cur != kNoKey) flag(dev_status, ACACHE_DEV_BAD_SLOT);
+            const int sl = in ? s_cur : -1;
+            int row[NI];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t v = sc[u] >> 8, w = max(v, (uint32_t)(kQ8MinExp + 127));
-                    fk[u] = q8_factor(sc[u] & 0xffu);
-                    ev[u] = v > kQ8MaxByte ? __uint_as_float(0x7fffffffu) : (float)((int)w - 127);
-                    rv[u] = __uint_as_float((254u - min(w, kQ8MaxByte)) << 23);
+            for (int i = 0; i < NI; ++i) row[i] = __shfl_sync(0xffffffffu, sl, i * RPI + rr);
+            const uint32_t dst = sK(s) + (uint32_t)(32 * w * D);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)                 // (a key without a row is filled with zeros)
+                cp_async16(dst + row_chunk<D>((uint32_t)(i * RPI + rr), (uint32_t)c), src + max(row[i], 0) * row_bytes,
+                           row[i] >= 0 ? 16u : 0u);
+            cp_async_commit();
+            // The factors.  S of an entry is issued after the softmax of the entry two before it wrote P,
+            // so with entry e - kKSt free the oldest factors in use are those of e - kKSt - 1.
+            static_assert(kFSt > kKSt + 1, "factor ring");
+            {
+                const uint32_t v = sc >> 8, y = max(v, (uint32_t)(kQ8MinExp + 127));
+                ctl.fk[fs][32 * w + lane] = q8_factor(sc & 0xffu);
+                ctl.ev[fs][32 * w + lane] = v > kQ8MaxByte ? __uint_as_float(0x7fffffffu) : (float)((int)y - 127);
+                ctl.rv[fs][32 * w + lane] = __uint_as_float((254u - min(y, kQ8MaxByte)) << 23);
+                if constexpr (kDrop) {
+                    const uint32_t gone = __ballot_sync(0xffffffffu, none);
+                    if (lane == 0) ctl.drop[fs][w] = gone;
                 }
-                *reinterpret_cast<float4*>(&ctl.fk[fs][4 * lane]) = make_float4(fk[0], fk[1], fk[2], fk[3]);
-                *reinterpret_cast<float4*>(&ctl.ev[fs][4 * lane]) = make_float4(ev[0], ev[1], ev[2], ev[3]);
-                *reinterpret_cast<float4*>(&ctl.rv[fs][4 * lane]) = make_float4(rv[0], rv[1], rv[2], rv[3]);
-                if (kDrop && (lane & 7) == 0) ctl.drop[fs][lane >> 3] = gone;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.f_full[fs]);
+            s_cur = s_next;
+            sc = scale_of(s_cur);
+            s_next = slot_of(e + 2);
+            if (e >= kKLag) {
+                cp_async_wait<kKLag>();
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.f_full[fs]);
-            }
-            if (e + 1 < n_kv) {
-                box = resolve(raw, own, rows, slot0, gone);
-                if (pi == 0) load_scales(own, sc);
-                load_slots(e + 2, raw);
+                if (lane == 0) mbar_arrive(&ctl.k_full[(e - kKLag) % kKSt]);
             }
         }
-        // Abort: the loads this warp issued land before the CTA exits (see tc_attn.cu)
-        if (*abort_flag && armed >= 0) {
-            bool landed = true;
-            for (int e = max(0, armed - kSt + 1); e <= armed; ++e)
-                landed = mbar_wait(&ctl.full[e % kSt], (uint32_t)(e / kSt) & 1u, kLandBudget) && landed;
-            if (!__all_sync(0xffffffffu, landed) && lane == 0) ctl.unlanded = 1;
-        }
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (e == n_kv && lane == 0)
+            for (int x = max(0, n_kv - kKLag); x < n_kv; ++x) mbar_arrive(&ctl.k_full[x % kKSt]);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------------- MMA issuer
         // S(0), S(1), then per tile j: PV(j) once P(j) is in TMEM, then S(j+2) into the buffer P(j)'s
@@ -292,9 +254,9 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
             constexpr uint32_t idS = idesc_e4m3(kBM, kBN), idO = idesc_f16(kBM, D, true);
             const uint64_t dq = sdesc_rows<D>(sQ);
             auto issue_s = [&](int j) -> bool {
-                if (!wait_bar(&ctl.full[j % kSt], (j / kSt) & 1, abort_flag, dev_status, budget)) return false;
+                if (!wait_bar(&ctl.k_full[j % kKSt], (j / kKSt) & 1, abort_flag, dev_status, budget)) return false;
                 tc_fence_after();
-                const uint64_t dk = sdesc_rows<D>(sK(j % kSt));
+                const uint64_t dk = sdesc_rows<D>(sK(j % kKSt));
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -302,7 +264,7 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
                         umma_ss_f8(tmem + kColS0 + (uint32_t)(j & 1) * 128u, dq + (uint64_t)((h * G::kQPart + k * 32) >> 4),
                                    dk + (uint64_t)(k * 32 >> 4), idS, h > 0 || k > 0);
                 umma_commit(&ctl.s_full[j & 1]);
-                umma_commit(&ctl.empty[j % kSt]);
+                umma_commit(&ctl.k_empty[j % kKSt]);
                 return true;
             };
             bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget);
@@ -325,22 +287,44 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
             mbar_wait(&ctl.drain, 0, kDrainBudget);
         }
         __syncwarp();
-    } else if (warp >= kConvWarp) {
-        // ---------------------------------------------------------------------- V converters
-        // As in q8_tc.cu's shared-memory layout: a warp converts 32 keys; the eight lanes of a phase take
-        // four 16-byte pieces of one 64-column region from each of two neighbouring rows (the raw tile
-        // has its rows one after the other, the f16 tile is swizzled), so no access meets in a bank.
-        constexpr int NI = D / 16, RPI = 32 / NI;
-        const int w = warp - kConvWarp, q = lane >> 3, k = lane & 7;
+    } else if (warp >= kVWarp) {
+        // ---------------------------------------------------------------------- V
+        // A warp's 32 rows of a tile arrive in rows of D bytes, two tiles ahead; it converts what it
+        // brought, so nobody else waits for them.
+        const int lc = lane % CPR, lr = lane / CPR;
+        const uint8_t* vsrc = p.v_cache + (int64_t)hk * D + lc * 16;
+        const int64_t row_bytes = (int64_t)p.Hkv * D;
+        auto bring = [&](int e, int slot) {
+            const int sl = (slot >= 0 && slot < p.num_slots) ? slot : -1;
+            int row[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) row[i] = __shfl_sync(0xffffffffu, sl, i * RPI + lr);
+            const uint32_t dst = sR(e % kRSt) + (uint32_t)((32 * w + lr) * D + lc * 16);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                cp_async16(dst + (uint32_t)(i * RPI * D), vsrc + max(row[i], 0) * row_bytes, row[i] >= 0 ? 16u : 0u);
+        };
+        // Conversion: 16-byte piece c of rows r0, r0 + RPI, ...  The eight lanes of a shared-memory phase take
+        // four pieces of one 64-column region from each of two neighbouring rows (the f16 tile is
+        // swizzled), so neither side meets in a bank.
+        const int q = lane >> 3, k = lane & 7;
         const int c = D == 128 ? k : (k & 3);
         const int r0 = 32 * w + (D == 128 ? (q & 2) + ((k >> 2) ^ (q & 1)) : 2 * q + (k >> 2));
+        grid_dependency_wait();
+        bring(0, s_cur);
+        cp_async_commit();
+        if (n_kv > 1) bring(1, s_next);
+        cp_async_commit();
+        s_next = slot_of(2);
         for (int e = 0; e < n_kv; ++e) {
-            const int s = e % kVSt, rs = e % kSt;
-            const bool ok = __all_sync(0xffffffffu,
-                                       wait_bar(&ctl.full[rs], (e / kSt) & 1, abort_flag, dev_status, budget) &&
-                                           (e < kVSt || wait_bar(&ctl.v_empty[s], ((e / kVSt) - 1) & 1, abort_flag,
-                                                                 dev_status, budget)));
-            if (!ok) break;
+            const int s = e % kVSt, rs = e % kRSt;
+            if (e + 2 < n_kv) bring(e + 2, s_next);
+            cp_async_commit();
+            s_next = slot_of(e + 3);
+            cp_async_wait<2>();
+            __syncwarp();
+            if (e >= kVSt && !__all_sync(0xffffffffu, wait_bar(&ctl.v_empty[s], ((e / kVSt) - 1) & 1, abort_flag, dev_status, budget)))
+                break;
             const uint32_t src = sR(rs) + (uint32_t)(r0 * D + c * 16);
             const uint32_t dst = sV(s) + (uint32_t)r0 * 128u + ((uint32_t)c >> 2) * G::kRegion;
 #pragma unroll
@@ -364,11 +348,9 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&ctl.empty[rs]);
-                mbar_arrive(&ctl.v_full[s]);
-            }
+            if (lane == 0) mbar_arrive(&ctl.v_full[s]);
         }
+        cp_async_wait<0>();
     } else {
         // ---------------------------------------------------------------------- softmax
         const int rep = warp / (4 / REP);                 // replica = key group of this warp
@@ -376,19 +358,23 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
         const int r = threadIdx.x;                        // TMEM lane
         const int row = r % GL;                           // row of the block
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        const int64_t off = [&] {
-            const int pr = row < n_rows ? row : 0, i = pr / p.g;
-            return ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
-        }();
         const bool warp_live = (warp * 32) % GL < n_rows;
-        float c_row = p.scale_log2;
-        // (lanes past the rows, and warps past them, hold what they like: it stays in their rows)
-        if (warp_live)
-            c_row = query_terms<D>(p.q, off, sQ + (uint32_t)(warp * 32 * D), sQ + G::kQPart + (uint32_t)(warp * 32 * D),
-                                   lane, p.scale_log2, min(32, n_rows - (warp * 32) % GL));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.q_full);
+        // Each warp converts a quarter of the rows for every replica.  (Lanes past the rows, and warps past
+        // them, hold what they like: it stays in their rows.)
+        {
+            constexpr int NR = GL / 4;
+            const int f0 = warp * NR;
+            const int64_t o = [&] {
+                const int pr = f0 + (lane & (NR - 1)) < n_rows ? f0 + (lane & (NR - 1)) : 0, i = pr / p.g;
+                return ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
+            }();
+            if (f0 < n_rows)
+                query_terms<D, NR, REP>(p.q, o, sQ + (uint32_t)(f0 * D), sQ + G::kQPart + (uint32_t)(f0 * D), (uint32_t)(GL * D),
+                                        lane, p.scale_log2, n_rows - f0, &ctl.c_row[f0]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.q_full);
+        }
         {   // P starts as zeros: columns outside this warp's key group are never written
             uint32_t z[32];
 #pragma unroll
@@ -398,8 +384,9 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
             tmem_st_wait();
         }
         float m_used = -INFINITY, l_sum = 0.f;
-        bool ok = true;
-        for (int j = 0; j < n_kv; ++j) {
+        bool ok = __all_sync(0xffffffffu, wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget));
+        const float c_row = ctl.c_row[row];
+        for (int j = 0; ok && j < n_kv; ++j) {
             const int sb = j & 1, fs = j % kFSt;
             ok = __all_sync(0xffffffffu, wait_bar(&ctl.f_full[fs], (j / kFSt) & 1, abort_flag, dev_status, budget) &&
                                              wait_bar(&ctl.s_full[sb], (j >> 1) & 1, abort_flag, dev_status, budget));
@@ -480,13 +467,13 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int q = 0; q < D / 8; ++q) {
-                    uint32_t o[8];
-                    tmem_ld8(lane_base + kColO + q * 8, o);
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_base + kColO + q * 32, o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tmem_st8(lane_base + kColO + q * 8, o);
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                    tmem_st32(lane_base + kColO + q * 32, o);
                 }
                 tmem_st_wait();
             }
@@ -544,61 +531,98 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (*abort_flag) settle_after_abort(ctl.unlanded != 0);
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 
     // -------------------------------------------------------------------------- merge
-    // Row r has REP x cs partials: replica w of rank q sits at lane w GL + r of CTA q.  Rank q finalises
-    // the (row, 8-column) items q, q + cs, ...
-    if (cs > 1) cluster_sync();
-    const uint32_t m_a = smem_u32(&ctl.part_m[0]), l_a = smem_u32(&ctl.part_l[0]), f_a = smem_u32(&ctl.failed);
-    bool all = true;
-    for (int q = 0; q < cs; ++q) all = all && ld_cluster_f32(mapa_shared(f_a, cs > 1 ? (uint32_t)q : cluster_ctarank())) == 0.f;
+    // First the replicas of each row (replica x at lane x GL + r), a thread taking 4 columns.
+    bool all = ctl.failed == 0.f;
+    const bool split = cs > 1;
+    const uint32_t rows_at = base + G::kVRing;               // merged rows of this part, f32
     if (all)
-        for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 8); it += cs * kThreads) {
-            const int r = it / (D / 8), c8 = it % (D / 8);
-            float M = -INFINITY;
-            for (int q = 0; q < cs; ++q) {
-                const uint32_t rank = cs > 1 ? (uint32_t)q : cluster_ctarank();
+        for (int it = (int)threadIdx.x; it < n_rows * (D / 4); it += kThreads) {
+            const int r = it / (D / 4), c4 = it % (D / 4);
+            float m[REP], M = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < REP; ++w) M = fmaxf(M, ld_cluster_f32(mapa_shared(m_a + 4u * (w * GL + r), rank)));
+            for (int x = 0; x < REP; ++x) {
+                m[x] = ctl.part_m[x * GL + r];
+                M = fmaxf(M, m[x]);
             }
-            float acc[8], L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float L = 0.f;
 #pragma unroll
-            for (int y = 0; y < 8; ++y) acc[y] = 0.f;
-            for (int q = 0; q < cs; ++q) {
-                const uint32_t rank = cs > 1 ? (uint32_t)q : cluster_ctarank();
-#pragma unroll
-                for (int w = 0; w < REP; ++w) {
-                    const int lr = w * GL + r;
-                    const float mv = ld_cluster_f32(mapa_shared(m_a + 4u * lr, rank));
-                    const float lv = ld_cluster_f32(mapa_shared(l_a + 4u * lr, rank));
-                    if (mv == -INFINITY && lv == 0.f) continue;       // no key in this partial
-                    const float e = fast_exp2(mv - M);
-                    L = fmaf(e, lv, L);
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float4 f = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(lr, c8 * 2 + y), rank));
-                        acc[4 * y] = fmaf(e, f.x, acc[4 * y]);
-                        acc[4 * y + 1] = fmaf(e, f.y, acc[4 * y + 1]);
-                        acc[4 * y + 2] = fmaf(e, f.z, acc[4 * y + 2]);
-                        acc[4 * y + 3] = fmaf(e, f.w, acc[4 * y + 3]);
-                    }
+            for (int x = 0; x < REP; ++x) {
+                const float lv = ctl.part_l[x * GL + r];
+                if (m[x] == -INFINITY && lv == 0.f) continue;        // no key in this partial
+                const float e = fast_exp2(m[x] - M);
+                uint32_t f[4];
+                ld_shared_v4(base + G::kRing + part_off<D>(x * GL + r, c4), f);
+                L = fmaf(e, lv, L);
+                acc.x = fmaf(e, __uint_as_float(f[0]), acc.x);
+                acc.y = fmaf(e, __uint_as_float(f[1]), acc.y);
+                acc.z = fmaf(e, __uint_as_float(f[2]), acc.z);
+                acc.w = fmaf(e, __uint_as_float(f[3]), acc.w);
+            }
+            if (split) {
+                if (c4 == 0) {
+                    ctl.row_m[r] = M;
+                    ctl.row_l[r] = L;
                 }
+                st_shared_v4(rows_at + (uint32_t)(it * 16), __float_as_uint(acc.x), __float_as_uint(acc.y),
+                             __float_as_uint(acc.z), __float_as_uint(acc.w));
+            } else {
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const int i = r / p.g;
+                bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D + c4 * 4;
+                __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
+            }
+        }
+    if (!split) return;
+    // Then the parts: rank x finalises the (row, 4-column) items x, x + cs, ...
+    __syncwarp();
+    cluster_sync();
+    const uint32_t m_a = smem_u32(&ctl.row_m[0]), l_a = smem_u32(&ctl.row_l[0]), f_a = smem_u32(&ctl.failed);
+    all = true;
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x)
+        if (x < cs) all = all && ld_cluster_f32(mapa_shared(f_a, x)) == 0.f;
+    if (all)
+        for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 4); it += cs * kThreads) {
+            const int r = it / (D / 4), c4 = it % (D / 4);
+            float m[kMaxCluster], l[kMaxCluster], M = -INFINITY;
+            float4 o[kMaxCluster];
+#pragma unroll
+            for (int x = 0; x < kMaxCluster; ++x) {
+                m[x] = -INFINITY;
+                l[x] = 0.f;
+                if (x < cs) {
+                    m[x] = ld_cluster_f32(mapa_shared(m_a + 4u * r, x));
+                    l[x] = ld_cluster_f32(mapa_shared(l_a + 4u * r, x));
+                    o[x] = ld_cluster_v4(mapa_shared(rows_at + (uint32_t)(it * 16), x));
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kMaxCluster; ++x) M = fmaxf(M, m[x]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float L = 0.f;
+#pragma unroll
+            for (int x = 0; x < kMaxCluster; ++x) {
+                if (m[x] == -INFINITY && l[x] == 0.f) continue;      // no key in this part
+                const float e = fast_exp2(m[x] - M);
+                L = fmaf(e, l[x], L);
+                acc.x = fmaf(e, o[x].x, acc.x);
+                acc.y = fmaf(e, o[x].y, acc.y);
+                acc.z = fmaf(e, o[x].z, acc.z);
+                acc.w = fmaf(e, o[x].w, acc.w);
             }
             const float inv = L == 0.f ? 0.f : 1.f / L;
             const int i = r / p.g;
-            bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D + c8 * 8;
-            uint32_t k[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                __nv_bfloat162 two = __floats2bfloat162_rn(acc[2 * y] * inv, acc[2 * y + 1] * inv);
-                k[y] = *reinterpret_cast<uint32_t*>(&two);
-            }
-            *reinterpret_cast<uint4*>(o) = make_uint4(k[0], k[1], k[2], k[3]);
+            bf16* o2 = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D + c4 * 4;
+            __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(o2) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
         }
     __syncwarp();
-    if (cs > 1) cluster_sync();    // no CTA may leave while another still reads its shared memory
+    cluster_sync();                // no CTA may leave while another still reads its shared memory
 }
 
 std::atomic<int> g_prepared[8][64];   // see q8_tc.cu
@@ -662,15 +686,10 @@ bool q8_decode_supported(const AttnArgs& a, int n_q) {
 
 int launch_q8_decode_attention(const Q8Attn& c) {
     const int d = c.a.d, hkv = c.a.hkv, g = c.a.hq / hkv;
-    if (c.num_slots * hkv >= 0x7fffffffLL || c.B > 65535 || (int64_t)hkv * kMaxCluster > 0x7fffffff)
-        return ACACHE_ERR_INVALID_ARG;
+    if (c.B > 65535 || (int64_t)hkv * kMaxCluster > 0x7fffffff) return ACACHE_ERR_INVALID_ARG;
     DecParams prm{};
-    const uint64_t rows[2] = {(uint64_t)d, (uint64_t)(c.num_slots * hkv)};
-    const uint64_t pool[3] = {(uint64_t)d, (uint64_t)hkv, (uint64_t)c.num_slots};
-    const uint32_t one[2] = {(uint32_t)d, 1}, box[3] = {(uint32_t)d, 1, kBN};
-    if (!make_map_u8(&prm.tm_k, c.k_cache, 2, rows, one, true) || !make_map_u8(&prm.tm_kbox, c.k_cache, 3, pool, box, true) ||
-        !make_map_u8(&prm.tm_v, c.v_cache, 2, rows, one, false) || !make_map_u8(&prm.tm_vbox, c.v_cache, 3, pool, box, false))
-        return ACACHE_ERR_CUDA;
+    prm.k_cache = c.k_cache;
+    prm.v_cache = c.v_cache;
     prm.q = (const bf16*)c.q;
     prm.kv_scale = c.kv_scale;
     prm.read_slot = c.read_slot;

@@ -500,7 +500,10 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             // what they hold only reaches output rows that are never read)
             if (warp_live) {
                 const uint32_t at = sQ(t) + (uint32_t)((warp & 3) * 32 * D);
-                c_row = query_terms<D>(p.q, off, at, at + G::kQPart, lane, p.scale_log2);
+                float* cr_at = &ctl.part_l[t * kBM + (warp & 3) * 32];      // (free until the end)
+                query_terms<D, 32, 1>(p.q, off, at, at + G::kQPart, 0u, lane, p.scale_log2, 32, cr_at);
+                __syncwarp();
+                c_row = cr_at[lane];
             }
             // a split block's chain B converts into the free query buffer: it needs the rows' powers of two
             if (!(split && t == 1)) {

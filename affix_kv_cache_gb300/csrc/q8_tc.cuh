@@ -81,18 +81,19 @@ ACACHE_DEVFN uint32_t row_chunk(uint32_t r, uint32_t c) {
 template <int D>
 ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (uint32_t)((q ^ (r & (D / 4 - 1))) << 4); }
 
-// n (of 32) query rows -> two e4m3 terms each, by one warp (whole groups of rows are converted).  Lane l brings the element offset of row l of the
-// 32; `hi` and `lo` are the shared-memory addresses of the first row's terms (rows of D bytes,
-// swizzled).  Returns the factor of lane l's row: its logits are S times the keys' factors times it
-// (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite, which
-// is carried as zeros).
+// NR query rows (8, 16 or 32; the first n of them, rounded up to whole groups) -> two e4m3 terms each, by
+// one warp.  Lane i brings the element offset of row i; `hi` and `lo` are the shared-memory addresses
+// of row 0's terms (rows of D bytes, swizzled, row 0 a multiple of 8), written `copies` times at a distance of `stride`
+// bytes.  c_row[i] receives the factor of row i: its logits are S times the keys' factors times it
+// (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite, which is
+// carried as zeros).
 // The rows land by cp.async where their terms will be, the first half of a row in its row of hi, the
-// second in its row of lo: LPR lanes to a row, so the loads are whole rows.  Four groups of rows at
-// a time keep the chain load - maximum - convert - subtract - convert of several rows in flight.
-template <int D>
-ACACHE_DEVFN float query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, int lane, float scale_log2,
-                              int n = 32) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI, GR = 4;
+// second in its row of lo: LPR lanes to a row, so the loads are whole rows.  GR groups of rows at a
+// time keep the chain load - maximum - convert - subtract - convert of several rows in flight.
+template <int D, int NR, int copies>
+ACACHE_DEVFN void query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, uint32_t stride, int lane,
+                              float scale_log2, int n, float* c_row) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = NR / RPI, GR = NI < 4 ? NI : 4;
     const uint32_t pc = (uint32_t)(lane % LPR), row = (uint32_t)(lane / LPR);
     const uint32_t at = (pc >= LPR / 2 ? lo : hi) + (pc % (LPR / 2)) * 16u + row * D;
 #pragma unroll 4
@@ -103,7 +104,6 @@ ACACHE_DEVFN float query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t
     cp_async_commit();
     cp_async_wait<0>();
     __syncwarp();
-    uint32_t e_row = 8u;
 #pragma unroll 1
     for (int g = 0; g < NI / GR && g * GR * RPI < n; ++g) {
         uint32_t w[GR][4], top[GR];
@@ -121,11 +121,11 @@ ACACHE_DEVFN float query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t
             for (int u = 0; u < GR; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
 #pragma unroll
         for (int u = 0; u < GR; ++u) {
+            const uint32_t r = (uint32_t)((g * GR + u) * RPI) + row;
             const uint32_t E = max(top[u] >> 7, 8u);              // biased exponent of the row's largest
-            const uint32_t mine = __shfl_sync(0xffffffffu, E, (lane % RPI) * LPR);
-            if (lane / RPI == g * GR + u) e_row = mine;
             const bool finite = E != 255u;
             const float up = finite ? __uint_as_float((261u - E) << 23) : 0.f;      // 2^(134 - E): largest in [128, 256)
+            if (pc == 0) c_row[r] = finite ? scale_log2 * __uint_as_float((E - 7u) << 23) : __uint_as_float(0x7fffffffu);
             uint32_t h[4], l[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -136,13 +136,14 @@ ACACHE_DEVFN float query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t
                 l[y] = q8_encode2(a - hf.x, d - hf.y);
             }
             // (the shuffles ordered the rows' reads before these writes)
-            const uint32_t r = (uint32_t)((g * GR + u) * RPI) + row;
             const uint32_t o = row_chunk<D>(r, pc >> 1) + (pc & 1u) * 8u;
-            st_shared_v2(hi + o, h[0] | h[1] << 16, h[2] | h[3] << 16);
-            st_shared_v2(lo + o, l[0] | l[1] << 16, l[2] | l[3] << 16);
+#pragma unroll
+            for (int x = 0; x < copies; ++x) {
+                st_shared_v2(hi + o + x * stride, h[0] | h[1] << 16, h[2] | h[3] << 16);
+                st_shared_v2(lo + o + x * stride, l[0] | l[1] << 16, l[2] | l[3] << 16);
+            }
         }
     }
-    return e_row == 255u ? __uint_as_float(0x7fffffffu) : scale_log2 * __uint_as_float((e_row - 7u) << 23);
 }
 
 }  // namespace q8

@@ -1,32 +1,35 @@
 // q8_decode.cu -- read-slot attention over an 8-bit pool for few query rows per (request, KV head): the
-// block-decode step and single tokens.  bf16 queries and outputs, head dim 64 or 128, tcgen05 + TMEM.
+// block-decode step and single tokens.  bf16 queries and outputs, head dim 64 or 128.
 //
 // Page: "Affix Cache for Diffusion Large Language Models", Sec. 4.3, App. C.1 and Sec. 5 (block length
 // 32); the 8-bit pool is this library's.
 //
 // Memory-bound: each (request, KV head) streams its keys' and values' codes once, 256 bytes a key
-// (d = 128), against at most 64 packed rows (queries x heads of the group).
-//   * S as in q8_tc.cu: hi and lo of the query rows times the codes as they lie in the pool.
-//   * O: P times V's codes converted to f16 (exact, one instruction for two).  Their power of two goes
-//     into the exponent instead: P = 2^(s + ev - m) with m the running maximum of s + ev, so P
-//     V is right whatever the rows' scales are, P never exceeds 2^15 and keys down to 2^-27 of the
-//     largest weighted one count (f16 subnormals); the sum adds P 2^-ev in float32.  Each thread has 32 or 64
-//     keys of a tile, so this costs less than scaling 128 x d values would.
-//   * Up to 32 (64) rows are replicated 4 (2) times over the 128 TMEM lanes, each replica taking a
-//     quarter (half) of every tile's keys, so that the four softmax warps share a tile's
-//     exponentials; P buffers whose other columns stay zero let one MMA add every replica's keys
-//     into its own O rows.  S and P are double-buffered.
-//   * The key range is split over a cluster of up to 8 CTAs when that fills the SMs better; partial
-//     (maximum, sum, O) of all replicas and ranks are merged through distributed shared memory in a
-//     fixed order -- no workspace, no second launch.
+// (d = 128), against at most 64 packed rows (queries x heads of the group).  What limits it is how many
+// bytes are in flight and what a CTA costs besides its keys.  So a warp owns 16 rows and works alone: it
+// brings 16 keys at a time into its own three-stage ring by cp.async, two chunks ahead of the one it
+// works on, and no barrier stands between a load and its use; three CTAs of four warps to an SM.
+//   * S = q' kc, m16n8k16 f16 products.  A bf16 query row divided by a power of two so that its largest
+//     element lies in [128, 256) is f16 exactly down to 2^-22 of the largest (and off by at most 2^-32 of
+//     it below); codes are f16 exactly, one instruction for two.  The contraction order over d is
+//     free, so a thread's 16-byte piece of a key row is its operand as it lies.  (m16n8k32 e4m3
+//     products are carried out as f16 ones here, and convert both operands every time.  Loading the
+//     operands straight into registers, a chunk ahead, was slower than the ring: the loads of one chunk
+//     waited for those of the last.)
+//   * O: P times V's codes converted to f16 (exact, one instruction for two), m16n8k16.  The output column
+//     order is free too: thread group g takes the 16 bytes of columns 16 g .. 16 g + 15 of four keys, and
+//     byte j of two neighbouring keys is the operand of column tile j.
+//   * V's power of two goes into the exponent: P = 2^(s + ev - m) with m the running maximum of
+//     s + ev, so P V is right whatever the rows' scales are, P never exceeds 2^15 and keys down to 2^-27
+//     of the largest weighted one count (f16 subnormals); the sum adds P 2^-ev in float32.
+// The warps of a CTA, the CTAs of a cluster (up to 8, where that fills the SMs better) share the keys; partial
+// (maximum, sum, O) are merged in a fixed order through (distributed) shared memory.
 //
-// Warps (416 threads, 1 CTA per SM): 0-3 softmax; 4-7 bring V's codes and convert them; 8-11 bring K's
-// codes and the keys' factors; 12 issues every MMA.  The codes come by 16-byte cp.async, a warp taking
-// 32 keys of every tile: a gather4 takes its warp some 90 cycles to issue for four rows (measured),
-// a cp.async instruction a tenth of that for as many; and pool addresses need no tensor maps.
-// TMEM (512 columns): S0 [0,128)  S1 [128,256)  O [256,384)  P0 [384,448)  P1 [448,512).
-//
-// Every mbarrier wait is bounded (see q8_tc.cu).
+// The register-operand products run at a quarter of tcgen05's rate, which 16 or 32 rows do not need:
+// 128 keys against 16 rows are 525 cycles of an SM's matrix pipes, and reading them at the memory's rate
+// takes 1400.  The tcgen05 form of this kernel (rows replicated over the 128 TMEM lanes, f16 V through
+// shared memory) took 2300 cycles a tile, 1600 of them its M = 128 products of mostly unused rows.
+#include <algorithm>
 #include <atomic>
 
 #include "q8_tc.cuh"
@@ -36,32 +39,13 @@ namespace {
 
 using namespace q8;
 
-constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 416;
-constexpr int kVWarp = 4, kKWarp = 8, kMmaWarp = 12;
-constexpr int kKSt = 4, kKLag = 2;          // K ring; an entry is announced kKLag entries after its loads
-constexpr int kRSt = 3;                     // V's codes (each warp's rows are its own)
-constexpr int kVSt = 2;                     // V in f16
-constexpr int kFSt = 8;                     // factors
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kChunk = 16;                  // keys a warp takes at a time
+constexpr int kSt = 3;                      // chunks in a warp's ring
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS0 = 0, kColO = 256, kColP0 = 384;
+constexpr int kCtasPerSm = 3;
 constexpr float kPHead = 3.0f;              // P of the used maximum is 2^3 ...
 constexpr float kRescaleThreshold = 12.0f;  // ... and never above 2^15
-
-template <int D>
-struct Geo {
-    static constexpr uint32_t kQPart = kBM * D;
-    static constexpr uint32_t kTile = kBN * D;             // codes of K or of V
-    static constexpr uint32_t kVTile = kBN * D * 2;        // V in f16
-    static constexpr uint32_t kRegion = kBN * 128;         // 64 columns of it
-    static constexpr uint32_t kRing = 2 * kQPart;
-    static constexpr uint32_t kRRing = kRing + kKSt * kTile;
-    static constexpr uint32_t kVRing = kRRing + kRSt * kTile;
-    static constexpr uint32_t kBytes = kVRing + kVSt * kVTile + 1024;
-    static_assert(kKSt * kTile >= kBM * D * 4u, "partial O reuses the K ring");
-    static_assert(kVSt * kVTile >= 64 * D * 4u, "and the merged rows V's");
-};
 
 struct DecParams {
     const bf16* q;
@@ -71,47 +55,90 @@ struct DecParams {
     int32_t* dev_status;
     int64_t num_slots;
     int n_q, T_len, Hq, Hkv, g;
-    int cs, part;                   // CTAs per cluster; key tiles per part
+    int cs, part;                   // CTAs per cluster; chunks per part
+    int drop;
     float scale_log2;
-    long long budget;
 };
 
-struct Ctl {
-    uint64_t q_full;
-    uint64_t k_full[kKSt], k_empty[kKSt];
-    uint64_t v_full[kVSt], v_empty[kVSt];
-    uint64_t f_full[kFSt];
-    uint64_t s_full[2], p_full[2];
-    uint64_t pv_done, drain;
-    uint32_t tmem_base;
-    int abort;
-    float failed;
-    uint32_t drop[kFSt][4];
-    float part_m[kBM], part_l[kBM];         // per lane
-    float row_m[64], row_l[64];             // per row, replicas merged
-    float c_row[64];
-    __align__(16) float fk[kFSt][kBN];      // 2^ek
-    __align__(16) float ev[kFSt][kBN];      // ev
-    __align__(16) float rv[kFSt][kBN];      // 2^-ev
+template <int D, int RG>
+struct Smem {
+    alignas(128) uint8_t q[RG * 16 * D * 2];        // query rows in f16
+    union {
+        alignas(128) uint8_t ring[kWarps][kSt][2][kChunk * D];      // codes of K and V, a warp's own
+        alignas(16) float o[kWarps][16 * D];                        // partials, warp rg KG + kg
+    };
+    float m[kWarps][16], l[kWarps][16];
+    float row_m[RG * 16], row_l[RG * 16];           // merged over the CTA's warps
+    float c_row[RG * 16];
 };
 
-constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
-    return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+ACACHE_DEVFN void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// NR query rows -> f16, by one warp: lane i brings the element offset of row i; row i goes to `at` + i 2 D
+// bytes and its factor (scale_log2 times the power of two it was divided by; NaN for a row that is not
+// finite, which is carried as zeros) to c_row[i].
+template <int D, int NR>
+ACACHE_DEVFN void query_rows(const bf16* q, int64_t off, uint32_t at, int lane, float scale_log2, float* c_row) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = NR / RPI;
+    const int row = lane / LPR, pc = lane % LPR;
+    uint4 w[NI];
+    int64_t o[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) o[i] = __shfl_sync(0xffffffffu, off, i * RPI + row);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(q + o[i]) + pc);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t top = __vmaxu2(__vmaxu2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu), __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu));
+        top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int s = LPR / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const uint32_t E = max(top >> 7, 8u);                    // biased exponent of the row's largest
+        const bool finite = E != 255u;
+        const float up = __uint_as_float((261u - E) << 23);      // 2^(134 - E): largest in [128, 256)
+        if (pc == 0) c_row[i * RPI + row] = finite ? scale_log2 * __uint_as_float((E - 7u) << 23) : __uint_as_float(0x7fffffffu);
+        uint32_t h[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            __half2 two = __floats2half2_rn(__uint_as_float(x[y] << 16) * up, __uint_as_float(x[y] & 0xffff0000u) * up);
+            h[y] = finite ? *reinterpret_cast<uint32_t*>(&two) : 0u;
+        }
+        st_shared_v4(at + (uint32_t)((i * RPI + row) * 2 * D + pc * 16), h[0], h[1], h[2], h[3]);
+    }
+}
+ACACHE_DEVFN void ld_words(uint32_t addr, uint32_t (&r)[4]) { ld_shared_v4(addr, r); }
+ACACHE_DEVFN void ld_words(uint32_t addr, uint32_t (&r)[2]) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+// 16 bytes global -> shared through L1 (the warps of other row groups read the same keys)
+ACACHE_DEVFN void cp_async16_l1(uint32_t dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// Position of 16-byte piece c of row r in a chunk: a K operand is read by four lanes a row from two
+// neighbouring rows at a time, a V operand by two lanes a row from every other row.
+template <int D> ACACHE_DEVFN uint32_t k_piece(uint32_t r, uint32_t c) { return r * D + ((D == 128 ? c ^ ((r & 1u) << 2) : c) << 4); }
+template <int D> ACACHE_DEVFN uint32_t v_piece(uint32_t r, uint32_t c) {
+    return r * D + ((D == 128 ? c ^ (((r >> 1) & 3u) << 1) : c ^ ((r >> 1) & 3u)) << 4);
+}
+ACACHE_DEVFN uint32_t to_f16x2(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
+    return h;
 }
 
-template <int D, int REP, bool kDrop>
-__global__ void __launch_bounds__(kThreads, 1)
-q8_decode_kernel(const __grid_constant__ DecParams p) {
-    using G = Geo<D>;
-    constexpr int GL = kBM / REP;                    // lanes per replica
-    constexpr int NC = 4 / REP;                      // 32-key chunks of a thread
-    extern __shared__ uint8_t dsm[];
-    __shared__ Ctl ctl;
-    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
-    const uint32_t sQ = base;
-    auto sK = [&](int s) { return base + G::kRing + G::kTile * (uint32_t)s; };
-    auto sR = [&](int s) { return base + G::kRRing + G::kTile * (uint32_t)s; };
-    auto sV = [&](int s) { return base + G::kVRing + G::kVTile * (uint32_t)s; };
+// RG: 16-row groups of the block, one per warp; the KG = 4 / RG warps of a group share the keys.
+template <int D, int RG>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+q8_decode_kernel(const DecParams p) {
+    constexpr int KG = kWarps / RG;
+    constexpr int H = D / 64;                        // 16-byte pieces of a key row per thread
+    constexpr int NT = D / 8;                        // column tiles of O = bytes of a value row per thread
+    extern __shared__ __align__(128) uint8_t raw_smem[];
+    Smem<D, RG>& sm = *reinterpret_cast<Smem<D, RG>*>(raw_smem);
     const int cr = p.cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)p.cs);
     const int hk = p.cs == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)p.cs);
     const int b = (int)blockIdx.y;
@@ -127,517 +154,323 @@ q8_decode_kernel(const __grid_constant__ DecParams p) {
             return;
         }
     }
-    const int n_rows = n_q * p.g;                    // <= GL
+    const int n_rows = n_q * p.g;                    // <= 16 RG
     if (n_rows == 0) return;
-    const int n_all = (T_len + kBN - 1) / kBN;
-    const int cs = (n_all + p.part - 1) / p.part;    // parts of this request's keys (<= p.cs)
+    const int n_ch = (T_len + kChunk - 1) / kChunk;
+    const int cs = (n_ch + p.part - 1) / p.part;     // parts of this request's keys (<= p.cs)
     if (cr >= cs) return;
-    const int kt0 = (int)((int64_t)cr * n_all / cs);
-    const int n_kv = (int)((int64_t)(cr + 1) * n_all / cs) - kt0;      // >= 1
+    const int ch0 = (int)((int64_t)cr * n_ch / cs), ch1 = (int)((int64_t)(cr + 1) * n_ch / cs);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int* abort_flag = &ctl.abort;
-    int32_t* dev_status = p.dev_status;
-    const long long budget = p.budget;
+    const int rg = warp / KG, kg = warp % KG;
+    const int g = lane >> 2, t = lane & 3;           // fragment coordinates
 
-    // K and V warps: lane l looks after key 32 w + l of every tile.  The maps are not written by a store
-    // this launch may overlap: the first slots are on their way during the set-up.
-    const int w = warp & 3;
-    auto slot_of = [&](int e) -> int {
-        const int t = (kt0 + e) * kBN + 32 * w + lane;
+    // lanes 0-15 look after the keys of a chunk (16-31 repeat them)
+    auto slot_of = [&](int ch) -> int {
+        const int key = ch * kChunk + (lane & 15);
         int s = kNoKey;
-        if (e < n_kv && t < T_len) s = p.read_slot[kbase + t];
+        if (ch < ch1 && key < T_len) s = p.read_slot[kbase + key];
         return s;
     };
-    int s_cur = kNoKey, s_next = kNoKey;
-    if (warp >= kVWarp && warp < kMmaWarp) {
-        s_cur = slot_of(0);
-        s_next = slot_of(1);
+    // slots of the chunk at hand and the two after it (the maps are not written by a store)
+    int s0 = slot_of(ch0 + kg), s1 = slot_of(ch0 + kg + KG), s2 = slot_of(ch0 + kg + 2 * KG);
+    {   // query rows: each warp converts its share of its group's 16 rows
+        constexpr int NR = 16 / KG < 8 ? 8 : 16 / KG;                   // at least 8 rows to a warp
+        const int f0 = rg * 16 + kg * NR;
+        if (kg * NR < 16) {
+            const int pr = f0 + (lane & (NR - 1)) < n_rows ? f0 + (lane & (NR - 1)) : 0, i = pr / p.g;
+            const int64_t off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
+            query_rows<D, NR>(p.q, off, smem_u32(&sm.q[f0 * D * 2]), lane, p.scale_log2, &sm.c_row[f0]);
+        }
     }
-    if (threadIdx.x == 0) {
-        mbar_init(&ctl.q_full, 4);
-        for (int s = 0; s < kKSt; ++s) {
-            mbar_init(&ctl.k_full[s], 4);
-            mbar_init(&ctl.k_empty[s], 1);
+    const int64_t row_bytes = (int64_t)p.Hkv * D;
+    constexpr int CPR = D / 16, RPI = 32 / CPR, NI = kChunk / RPI;      // pieces a row, rows an instruction
+    const uint32_t rr = (uint32_t)(lane / CPR), pc = (uint32_t)(lane % CPR);
+    const uint8_t* ksrc = p.k_cache + (int64_t)hk * D + pc * 16;
+    const uint8_t* vsrc = p.v_cache + (int64_t)hk * D + pc * 16;
+    const uint32_t ring = smem_u32(&sm.ring[warp][0][0][0]);
+    // 2^ek as bf16 with ev as bf16 above it, of this lane's key; a key that takes no part has ev = -inf
+    auto factors = [&](int slot, uint32_t sc) -> uint32_t {
+        if (slot >= 0 && slot < p.num_slots) {
+            const uint32_t k = sc & 0xffu, v = sc >> 8;
+            const uint32_t ev = v > kQ8MaxByte ? 0x7fff0000u
+                                               : __float_as_uint((float)((int)max(v, (uint32_t)(kQ8MinExp + 127)) - 127));
+            return (k > kQ8MaxByte ? 0x7fffu : k << 7) | (ev & 0xffff0000u);
         }
-        for (int s = 0; s < kVSt; ++s) {
-            mbar_init(&ctl.v_full[s], 4);
-            mbar_init(&ctl.v_empty[s], 1);
-        }
-        for (int s = 0; s < kFSt; ++s) mbar_init(&ctl.f_full[s], 4);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&ctl.s_full[t], 1);
-            mbar_init(&ctl.p_full[t], 4);
-        }
-        mbar_init(&ctl.pv_done, 1);
-        mbar_init(&ctl.drain, 1);
-        ctl.abort = 0;
-        ctl.failed = 0.f;
-        fence_mbar_init();
-    }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&ctl.tmem_base, kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = ctl.tmem_base;
-    // Pieces of a row (16 bytes), rows per warp instruction, instructions per tile of a K or V warp.
-    constexpr int CPR = D / 16, RPI = 32 / CPR, NI = 32 / RPI;
-
-    if (warp >= kKWarp && warp < kMmaWarp) {
-        // ---------------------------------------------------------------------- K
-        const int c = lane % CPR, rr = lane / CPR;
-        const uint8_t* src = p.k_cache + (int64_t)hk * D + c * 16;
-        const int64_t row_bytes = (int64_t)p.Hkv * D;
-        auto scale_of = [&](int s) -> uint32_t {
-            uint32_t two = 127u | 127u << 8;             // a zero row: factor 1
-            if (s >= 0 && s < p.num_slots) two = reinterpret_cast<const uint16_t*>(p.kv_scale)[(int64_t)s * p.Hkv + hk];
-            return two;
-        };
-        grid_dependency_wait();                          // store-then-attend: the pool is written now
-        uint32_t sc = scale_of(s_cur);
-        int e = 0;
-        for (; e < n_kv; ++e) {
-            const int s = e % kKSt, fs = e % kFSt;
-            if (e >= kKSt && !__all_sync(0xffffffffu, wait_bar(&ctl.k_empty[s], ((e / kKSt) - 1) & 1, abort_flag, dev_status, budget)))
-                break;
-            const bool in = s_cur >= 0 && s_cur < p.num_slots;
-            const bool none = kDrop && s_cur == ACACHE_SLOT_NONE;
-            if (!in && !none && s_cur != kNoKey) flag(dev_status, ACACHE_DEV_BAD_SLOT);
-            const int sl = in ? s_cur : -1;
-            int row[NI];
+        if (slot == kNoKey || (p.drop && slot == ACACHE_SLOT_NONE)) return 0xff800000u;
+        return 0x3f80u;                              // outside the pool: a zero row that counts
+    };
+    auto load_scale = [&](int slot) -> uint32_t {
+        uint32_t sc = 0;
+        if (slot >= 0 && slot < p.num_slots) sc = reinterpret_cast<const uint16_t*>(p.kv_scale)[(int64_t)slot * p.Hkv + hk];
+        return sc;
+    };
+    auto bring = [&](int slot, uint32_t stage) {     // all shuffles before all loads
+        const int sl = (slot >= 0 && slot < p.num_slots) ? slot : -1;
+        int r[NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) row[i] = __shfl_sync(0xffffffffu, sl, i * RPI + rr);
-            const uint32_t dst = sK(s) + (uint32_t)(32 * w * D);
+        for (int i = 0; i < NI; ++i) r[i] = __shfl_sync(0xffffffffu, sl, i * RPI + rr);
 #pragma unroll
-            for (int i = 0; i < NI; ++i)                 // (a key without a row is filled with zeros)
-                cp_async16(dst + row_chunk<D>((uint32_t)(i * RPI + rr), (uint32_t)c), src + max(row[i], 0) * row_bytes,
-                           row[i] >= 0 ? 16u : 0u);
-            cp_async_commit();
-            // The factors.  S of an entry is issued after the softmax of the entry two before it wrote P,
-            // so with entry e - kKSt free the oldest factors in use are those of e - kKSt - 1.
-            static_assert(kFSt > kKSt + 1, "factor ring");
-            {
-                const uint32_t v = sc >> 8, y = max(v, (uint32_t)(kQ8MinExp + 127));
-                ctl.fk[fs][32 * w + lane] = q8_factor(sc & 0xffu);
-                ctl.ev[fs][32 * w + lane] = v > kQ8MaxByte ? __uint_as_float(0x7fffffffu) : (float)((int)y - 127);
-                ctl.rv[fs][32 * w + lane] = __uint_as_float((254u - min(y, kQ8MaxByte)) << 23);
-                if constexpr (kDrop) {
-                    const uint32_t gone = __ballot_sync(0xffffffffu, none);
-                    if (lane == 0) ctl.drop[fs][w] = gone;
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.f_full[fs]);
-            s_cur = s_next;
-            sc = scale_of(s_cur);
-            s_next = slot_of(e + 2);
-            if (e >= kKLag) {
-                cp_async_wait<kKLag>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.k_full[(e - kKLag) % kKSt]);
-            }
-        }
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (e == n_kv && lane == 0)
-            for (int x = max(0, n_kv - kKLag); x < n_kv; ++x) mbar_arrive(&ctl.k_full[x % kKSt]);
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------------- MMA issuer
-        // S(0), S(1), then per tile j: PV(j) once P(j) is in TMEM, then S(j+2) into the buffer P(j)'s
-        // scores came from.  MMAs of one thread run in issue order: S(j+2) complete implies PV(j)
-        // complete, so the softmax of tile j+2 may overwrite P buffer j % 2.
-        if (lane == 0) {
-            constexpr uint32_t idS = idesc_e4m3(kBM, kBN), idO = idesc_f16(kBM, D, true);
-            const uint64_t dq = sdesc_rows<D>(sQ);
-            auto issue_s = [&](int j) -> bool {
-                if (!wait_bar(&ctl.k_full[j % kKSt], (j / kKSt) & 1, abort_flag, dev_status, budget)) return false;
-                tc_fence_after();
-                const uint64_t dk = sdesc_rows<D>(sK(j % kKSt));
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        umma_ss_f8(tmem + kColS0 + (uint32_t)(j & 1) * 128u, dq + (uint64_t)((h * G::kQPart + k * 32) >> 4),
-                                   dk + (uint64_t)(k * 32 >> 4), idS, h > 0 || k > 0);
-                umma_commit(&ctl.s_full[j & 1]);
-                umma_commit(&ctl.k_empty[j % kKSt]);
-                return true;
-            };
-            bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget);
-            for (int j = 0; ok && j < 2 && j < n_kv; ++j) ok = issue_s(j);
-            for (int j = 0; ok && j < n_kv; ++j) {
-                ok = wait_bar(&ctl.v_full[j % kVSt], (j / kVSt) & 1, abort_flag, dev_status, budget) &&
-                     wait_bar(&ctl.p_full[j & 1], (j >> 1) & 1, abort_flag, dev_status, budget);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t dv = sdesc_sw128(sV(j % kVSt), G::kRegion, 1024);
-                const uint32_t a_p = tmem + kColP0 + (uint32_t)(j & 1) * 64u;
-#pragma unroll
-                for (int k = 0; k < kBN / 16; ++k)
-                    umma_ts(tmem + kColO, a_p + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (j > 0 || k > 0));
-                umma_commit(&ctl.v_empty[j % kVSt]);
-                umma_commit(&ctl.pv_done);
-                if (j + 2 < n_kv) ok = issue_s(j + 2);
-            }
-            umma_commit(&ctl.drain);
-            mbar_wait(&ctl.drain, 0, kDrainBudget);
-        }
-        __syncwarp();
-    } else if (warp >= kVWarp) {
-        // ---------------------------------------------------------------------- V
-        // A warp's 32 rows of a tile arrive in rows of D bytes, two tiles ahead; it converts what it
-        // brought, so nobody else waits for them.
-        const int lc = lane % CPR, lr = lane / CPR;
-        const uint8_t* vsrc = p.v_cache + (int64_t)hk * D + lc * 16;
-        const int64_t row_bytes = (int64_t)p.Hkv * D;
-        auto bring = [&](int e, int slot) {
-            const int sl = (slot >= 0 && slot < p.num_slots) ? slot : -1;
-            int row[NI];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) row[i] = __shfl_sync(0xffffffffu, sl, i * RPI + lr);
-            const uint32_t dst = sR(e % kRSt) + (uint32_t)((32 * w + lr) * D + lc * 16);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                cp_async16(dst + (uint32_t)(i * RPI * D), vsrc + max(row[i], 0) * row_bytes, row[i] >= 0 ? 16u : 0u);
-        };
-        // Conversion: 16-byte piece c of rows r0, r0 + RPI, ...  The eight lanes of a shared-memory phase take
-        // four pieces of one 64-column region from each of two neighbouring rows (the f16 tile is
-        // swizzled), so neither side meets in a bank.
-        const int q = lane >> 3, k = lane & 7;
-        const int c = D == 128 ? k : (k & 3);
-        const int r0 = 32 * w + (D == 128 ? (q & 2) + ((k >> 2) ^ (q & 1)) : 2 * q + (k >> 2));
-        grid_dependency_wait();
-        bring(0, s_cur);
-        cp_async_commit();
-        if (n_kv > 1) bring(1, s_next);
-        cp_async_commit();
-        s_next = slot_of(2);
-        for (int e = 0; e < n_kv; ++e) {
-            const int s = e % kVSt, rs = e % kRSt;
-            if (e + 2 < n_kv) bring(e + 2, s_next);
-            cp_async_commit();
-            s_next = slot_of(e + 3);
-            cp_async_wait<2>();
-            __syncwarp();
-            if (e >= kVSt && !__all_sync(0xffffffffu, wait_bar(&ctl.v_empty[s], ((e / kVSt) - 1) & 1, abort_flag, dev_status, budget)))
-                break;
-            const uint32_t src = sR(rs) + (uint32_t)(r0 * D + c * 16);
-            const uint32_t dst = sV(s) + (uint32_t)r0 * 128u + ((uint32_t)c >> 2) * G::kRegion;
-#pragma unroll
-            for (int i0 = 0; i0 < NI; i0 += 4) {
-                uint32_t d[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ld_shared_v4(src + (uint32_t)((i0 + i) * RPI * D), d[i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[8];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[2 * y]) : "h"((unsigned short)(d[i][y] & 0xffffu)));
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[2 * y + 1]) : "h"((unsigned short)(d[i][y] >> 16)));
-                    }
-                    const uint32_t r8 = (uint32_t)(r0 + (i0 + i) * RPI) & 7u;
-                    const uint32_t a0 = dst + (uint32_t)((i0 + i) * RPI) * 128u + (((2u * c & 7u) ^ r8) << 4);
-                    st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-                    st_shared_v4(a0 ^ 16u, o[4], o[5], o[6], o[7]);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.v_full[s]);
-        }
-        cp_async_wait<0>();
-    } else {
-        // ---------------------------------------------------------------------- softmax
-        const int rep = warp / (4 / REP);                 // replica = key group of this warp
-        const int kb = rep * (kBN / REP);                 // first key of the group in a tile
-        const int r = threadIdx.x;                        // TMEM lane
-        const int row = r % GL;                           // row of the block
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        const bool warp_live = (warp * 32) % GL < n_rows;
-        // Each warp converts a quarter of the rows for every replica.  (Lanes past the rows, and warps past
-        // them, hold what they like: it stays in their rows.)
-        {
-            constexpr int NR = GL / 4;
-            const int f0 = warp * NR;
-            const int64_t o = [&] {
-                const int pr = f0 + (lane & (NR - 1)) < n_rows ? f0 + (lane & (NR - 1)) : 0, i = pr / p.g;
-                return ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
-            }();
-            if (f0 < n_rows)
-                query_terms<D, NR, REP>(p.q, o, sQ + (uint32_t)(f0 * D), sQ + G::kQPart + (uint32_t)(f0 * D), (uint32_t)(GL * D),
-                                        lane, p.scale_log2, n_rows - f0, &ctl.c_row[f0]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.q_full);
-        }
-        {   // P starts as zeros: columns outside this warp's key group are never written
-            uint32_t z[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = 0u;
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) tmem_st32(lane_base + kColP0 + cc * 32, z);
-            tmem_st_wait();
-        }
-        float m_used = -INFINITY, l_sum = 0.f;
-        bool ok = __all_sync(0xffffffffu, wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget));
-        const float c_row = ctl.c_row[row];
-        for (int j = 0; ok && j < n_kv; ++j) {
-            const int sb = j & 1, fs = j % kFSt;
-            ok = __all_sync(0xffffffffu, wait_bar(&ctl.f_full[fs], (j / kFSt) & 1, abort_flag, dev_status, budget) &&
-                                             wait_bar(&ctl.s_full[sb], (j >> 1) & 1, abort_flag, dev_status, budget));
-            if (!ok) break;
-            tc_fence_after();
-            if (!warp_live) {
-                if (lane == 0) mbar_arrive(&ctl.p_full[sb]);
-                continue;
-            }
-            uint32_t v[NC][32];
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc) tmem_ld32(lane_base + kColS0 + sb * 128 + kb + cc * 32, v[cc]);
-            tmem_ld_wait();
-            // t = s + ev in log2 units
-            const uint64_t c2 = f2pack(c_row, c_row);
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(&ctl.fk[fs][kb + cc * 32 + i]);
-                    const float4 e = *reinterpret_cast<const float4*>(&ctl.ev[fs][kb + cc * 32 + i]);
-                    float t0, t1;
-                    f2unpack(f2fma(f2mul(f2pack(__uint_as_float(v[cc][i]), __uint_as_float(v[cc][i + 1])), f2pack(f.x, f.y)),
-                                   c2, f2pack(e.x, e.y)), t0, t1);
-                    v[cc][i] = __float_as_uint(t0);
-                    v[cc][i + 1] = __float_as_uint(t1);
-                    f2unpack(f2fma(f2mul(f2pack(__uint_as_float(v[cc][i + 2]), __uint_as_float(v[cc][i + 3])), f2pack(f.z, f.w)),
-                                   c2, f2pack(e.z, e.w)), t0, t1);
-                    v[cc][i + 2] = __float_as_uint(t0);
-                    v[cc][i + 3] = __float_as_uint(t1);
-                }
-            const int valid = T_len - (kt0 + j) * kBN - kb;       // keys of the group in range
-            if (valid < kBN / REP) {
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (cc * 32 + i >= valid) v[cc][i] = __float_as_uint(-INFINITY);
-            }
-            if constexpr (kDrop) {
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    const uint32_t gone = ctl.drop[fs][kb / 32 + cc];
-                    if (gone) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if ((gone >> i) & 1u) v[cc][i] = __float_as_uint(-INFINITY);
-                    }
-                }
-            }
-            float mt = 0.f;
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                float mx[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t* y = &v[cc][q * 16];
-                    mx[q] = max3f(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
-#pragma unroll
-                    for (int i = 3; i < 15; i += 2) mx[q] = max3f(mx[q], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-                    mx[q] = fmaxf(mx[q], __uint_as_float(y[15]));
-                }
-                // (no -inf to start from: a row of NaN stays NaN)
-                mt = cc == 0 ? fmaxf(mx[0], mx[1]) : max3f(mt, mx[0], mx[1]);
-            }
-            float alpha = 1.f;
-            bool resc = false;
-            if (j == 0) {
-                m_used = mt;
-            } else if (row < n_rows && mt > m_used + kRescaleThreshold) {
-                alpha = fast_exp2(m_used - mt);   // 0 while no key of the group was there
-                m_used = mt;
-                resc = true;
-            }
-            if (__any_sync(0xffffffffu, resc)) {
-                // O holds tiles 0..j-1 once PV(j-1) is complete
-                ok = __all_sync(0xffffffffu, wait_bar(&ctl.pv_done, (j - 1) & 1, abort_flag, dev_status, budget));
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(lane_base + kColO + q * 32, o);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tmem_st32(lane_base + kColO + q * 32, o);
-                }
-                tmem_st_wait();
-            }
-            // a group without a key so far exponentiates against 0 (every value is -inf)
-            const float ms = m_used == -INFINITY ? 0.f : m_used - kPHead;
-            const uint64_t nm2 = f2pack(-ms, -ms);
-            uint64_t ls2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 rv = *reinterpret_cast<const float4*>(&ctl.rv[fs][kb + cc * 32 + i]);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float x0, x1;
-                        f2unpack(f2add(f2pack(__uint_as_float(v[cc][i + 2 * h]), __uint_as_float(v[cc][i + 2 * h + 1])), nm2), x0, x1);
-                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                        ls2[h] = f2fma(f2pack(p0, p1), h ? f2pack(rv.z, rv.w) : f2pack(rv.x, rv.y), ls2[h]);
-                        // f16 keeps 11 bits, so P is rounded finer than bf16 would
-                        __half2 two = __floats2half2_rn(p0, p1);
-                        pk[i / 2 + h] = *reinterpret_cast<uint32_t*>(&two);
-                    }
-                }
-                tmem_st16(lane_base + kColP0 + sb * 64 + kb / 2 + cc * 16, pk);
-            }
-            float l0, l1, l2, l3;
-            f2unpack(ls2[0], l0, l1);
-            f2unpack(ls2[1], l2, l3);
-            l_sum = l_sum * alpha + ((l0 + l1) + (l2 + l3));
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.p_full[sb]);
-        }
-        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain, 0, abort_flag, dev_status, budget));
-        if (!ok) {
-            ctl.failed = 1.f;
-        } else if (warp_live) {
-            // this lane's partial, over the free ring
-            tc_fence_after();
-#pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t o[32];
-                tmem_ld32(lane_base + kColO + cc * 32, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int y = 0; y < 8; ++y)
-                    st_shared_v4(base + G::kRing + part_off<D>(r, cc * 8 + y), o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-            }
-        }
-        ctl.part_m[r] = m_used;
-        ctl.part_l[r] = l_sum;
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-
-    // -------------------------------------------------------------------------- merge
-    // First the replicas of each row (replica x at lane x GL + r), a thread taking 4 columns.
-    bool all = ctl.failed == 0.f;
-    const bool split = cs > 1;
-    const uint32_t rows_at = base + G::kVRing;               // merged rows of this part, f32
-    if (all)
-        for (int it = (int)threadIdx.x; it < n_rows * (D / 4); it += kThreads) {
-            const int r = it / (D / 4), c4 = it % (D / 4);
-            float m[REP], M = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < REP; ++x) {
-                m[x] = ctl.part_m[x * GL + r];
-                M = fmaxf(M, m[x]);
-            }
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float L = 0.f;
-#pragma unroll
-            for (int x = 0; x < REP; ++x) {
-                const float lv = ctl.part_l[x * GL + r];
-                if (m[x] == -INFINITY && lv == 0.f) continue;        // no key in this partial
-                const float e = fast_exp2(m[x] - M);
-                uint32_t f[4];
-                ld_shared_v4(base + G::kRing + part_off<D>(x * GL + r, c4), f);
-                L = fmaf(e, lv, L);
-                acc.x = fmaf(e, __uint_as_float(f[0]), acc.x);
-                acc.y = fmaf(e, __uint_as_float(f[1]), acc.y);
-                acc.z = fmaf(e, __uint_as_float(f[2]), acc.z);
-                acc.w = fmaf(e, __uint_as_float(f[3]), acc.w);
-            }
-            if (split) {
-                if (c4 == 0) {
-                    ctl.row_m[r] = M;
-                    ctl.row_l[r] = L;
-                }
-                st_shared_v4(rows_at + (uint32_t)(it * 16), __float_as_uint(acc.x), __float_as_uint(acc.y),
-                             __float_as_uint(acc.z), __float_as_uint(acc.w));
+        for (int i = 0; i < NI; ++i) {               // (a key without a row is zeros)
+            const int64_t at = max(r[i], 0) * row_bytes;
+            const uint32_t bytes = r[i] >= 0 ? 16u : 0u, row = (uint32_t)(i * RPI) + rr;
+            if (RG == 1) {
+                cp_async16(stage + k_piece<D>(row, pc), ksrc + at, bytes);
+                cp_async16(stage + kChunk * D + v_piece<D>(row, pc), vsrc + at, bytes);
             } else {
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                const int i = r / p.g;
-                bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D + c4 * 4;
-                __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-                *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
+                cp_async16_l1(stage + k_piece<D>(row, pc), ksrc + at, bytes);
+                cp_async16_l1(stage + kChunk * D + v_piece<D>(row, pc), vsrc + at, bytes);
             }
         }
+    };
+    grid_dependency_wait();                          // store-then-attend: the pool is written now
+    bring(s0, ring);
+    cp_async_commit();
+    bring(s1, ring + 2 * kChunk * D);
+    cp_async_commit();
+    uint32_t sc0 = load_scale(s0), sc1 = load_scale(s1), sc2 = 0;
+    __syncthreads();                                 // the query terms are there
+    uint32_t qf[2][H][2][4];                         // [row g, g + 8][piece][half of its 16 elements]
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                ld_shared_v4(smem_u32(&sm.q[0]) + (uint32_t)((rg * 16 + 8 * y + g) * 2 * D + (t + 4 * h) * 32 + x * 16), qf[y][h][x]);
+    const float c0 = sm.c_row[rg * 16 + g], c1 = sm.c_row[rg * 16 + 8 + g];
+    float o[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    uint32_t at = 0, at2 = 2;                        // stages of the chunk at hand and of the one to bring
+    for (int ch = ch0 + kg; ch < ch1; ch += KG) {
+        bring(s2, ring + at2 * (2 * kChunk * D));
+        cp_async_commit();
+        sc2 = load_scale(s2);
+        const uint32_t fe_own = factors(s0, sc0);
+        if (s0 != kNoKey && (s0 < 0 || s0 >= p.num_slots) && !(p.drop && s0 == ACACHE_SLOT_NONE))
+            flag(p.dev_status, ACACHE_DEV_BAD_SLOT);
+        s0 = s1;
+        s1 = s2;
+        sc0 = sc1;
+        sc1 = sc2;
+        s2 = slot_of(ch + 3 * KG);
+        uint32_t fe[4];                              // of keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int x = 0; x < 4; ++x) fe[x] = __shfl_sync(0xffffffffu, fe_own, 2 * t + (x & 1) + 8 * (x >> 1));
+        cp_async_wait<2>();
+        __syncwarp();
+        const uint32_t kat = ring + at * (2 * kChunk * D), vat = kat + kChunk * D;
+        at2 = at;
+        at = at == kSt - 1 ? 0 : at + 1;
+        float s[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                uint32_t kf[4];
+                ld_shared_v4(kat + k_piece<D>((uint32_t)(8 * n + g), (uint32_t)(t + 4 * h)), kf);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)          // four elements of the piece to a product
+                    mma_f16(s[n], qf[0][h][y >> 1][2 * (y & 1)], qf[1][h][y >> 1][2 * (y & 1)], qf[0][h][y >> 1][2 * (y & 1) + 1],
+                            qf[1][h][y >> 1][2 * (y & 1) + 1], to_f16x2(kf[y] & 0xffffu), to_f16x2(kf[y] >> 16));
+            }
+        }
+        uint32_t vf[4][NT / 4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const uint32_t key = (uint32_t)(2 * t + (x & 1) + 8 * (x >> 1));
+            ld_words(vat + (D == 128 ? v_piece<D>(key, (uint32_t)g) : v_piece<D>(key, (uint32_t)g >> 1) + 8u * (g & 1)), vf[x]);
+        }
+        // t = s + ev in log2 units; s[n][0], s[n][1]: row g, keys 8n + 2t, + 1; s[n][2], s[n][3]: row g + 8
+        float ev[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float fk = __uint_as_float(fe[x] << 16);
+            ev[x] = __uint_as_float(fe[x] & 0xffff0000u);
+            s[x >> 1][x & 1] = fmaf(s[x >> 1][x & 1] * fk, c0, ev[x]);
+            s[x >> 1][2 + (x & 1)] = fmaf(s[x >> 1][2 + (x & 1)] * fk, c1, ev[x]);
+        }
+        float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float t1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        // (a maximum that is NaN -- every key of the row so far -- is left alone)
+        if (__any_sync(0xffffffffu, t0 > m0 + kRescaleThreshold || t1 > m1 + kRescaleThreshold)) {
+#pragma unroll
+            for (int x = 1; x < 4; x <<= 1) {        // over the row's four threads
+                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+            }
+            const float n0 = t0 > m0 + kRescaleThreshold ? t0 : m0, n1 = t1 > m1 + kRescaleThreshold ? t1 : m1;
+            const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+            // (without a key so far O and the sum are 0, or NaN where a poisoned key was met: keep that)
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                o[j][0] *= a0;
+                o[j][1] *= a0;
+                o[j][2] *= a1;
+                o[j][3] *= a1;
+            }
+            m0 = n0;
+            m1 = n1;
+        }
+        const float ms0 = m0 == -INFINITY ? 0.f : m0 - kPHead, ms1 = m1 == -INFINITY ? 0.f : m1 - kPHead;
+        uint32_t pa[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float pr[4], rv[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                rv[x] = ev[2 * n + x] == -INFINITY ? 0.f : fast_exp2(-ev[2 * n + x]);
+                pr[x] = fast_exp2(s[n][x] - ms0);
+                pr[2 + x] = fast_exp2(s[n][2 + x] - ms1);
+                l0 = fmaf(pr[x], rv[x], l0);
+                l1 = fmaf(pr[2 + x], rv[x], l1);
+            }
+            // f16 keeps 11 bits, so P is rounded finer than bf16 would
+            const __half2 u = __floats2half2_rn(pr[0], pr[1]), w = __floats2half2_rn(pr[2], pr[3]);
+            pa[2 * n] = *reinterpret_cast<const uint32_t*>(&u);
+            pa[2 * n + 1] = *reinterpret_cast<const uint32_t*>(&w);
+        }
+#pragma unroll
+        for (int y = 0; y < NT / 4; ++y) {
+            // bytes 4y .. 4y + 3 of the four keys, two keys to an operand
+            const uint32_t u0 = __byte_perm(vf[0][y], vf[1][y], 0x5140), u1 = __byte_perm(vf[0][y], vf[1][y], 0x7362);
+            const uint32_t w0 = __byte_perm(vf[2][y], vf[3][y], 0x5140), w1 = __byte_perm(vf[2][y], vf[3][y], 0x7362);
+            mma_f16(o[4 * y], pa[0], pa[1], pa[2], pa[3], to_f16x2(u0 & 0xffffu), to_f16x2(w0 & 0xffffu));
+            mma_f16(o[4 * y + 1], pa[0], pa[1], pa[2], pa[3], to_f16x2(u0 >> 16), to_f16x2(w0 >> 16));
+            mma_f16(o[4 * y + 2], pa[0], pa[1], pa[2], pa[3], to_f16x2(u1 & 0xffffu), to_f16x2(w1 & 0xffffu));
+            mma_f16(o[4 * y + 3], pa[0], pa[1], pa[2], pa[3], to_f16x2(u1 >> 16), to_f16x2(w1 >> 16));
+        }
+        __syncwarp();                                // the next chunk but two lands in this stage
+    }
+    cp_async_wait<0>();
+    __syncthreads();                                 // the partials go over the rings
+    // -------------------------------------------------------------------------- merge
+    // o[j][0] is column 2 NT t + j of row g, o[j][1] the one NT further; o[j][2], o[j][3] of row g + 8
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    if (t == 0) {
+        sm.m[warp][g] = m0;
+        sm.m[warp][g + 8] = m1;
+        sm.l[warp][g] = l0;
+        sm.l[warp][g + 8] = l1;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j += 4)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            // float4 slot of a row, moved by row and thread so that the lanes spread over the banks
+            const int r = g + 8 * (x >> 1), q4 = (2 * NT * t + NT * (x & 1) + j) / 4;
+            *reinterpret_cast<float4*>(&sm.o[warp][r * D + 4 * (((q4 ^ (q4 / (NT / 2))) + 2 * (r & 7)) & (D / 4 - 1))]) =
+                make_float4(o[j][x], o[j + 1][x], o[j + 2][x], o[j + 3][x]);
+        }
+    __syncthreads();
+    // First the warps of each row group, a thread taking 4 columns of a row.
+    const bool split = cs > 1;
+    auto slot4 = [&](int r, int q4) { return (r & 15) * D + 4 * (((q4 ^ (q4 / (NT / 2))) + 2 * (r & 7)) & (D / 4 - 1)); };
+    for (int it = (int)threadIdx.x; it < n_rows * (D / 4); it += kThreads) {
+        const int r = it / (D / 4), q4 = it % (D / 4), w0 = (r >> 4) * KG;
+        float m[KG], M = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < KG; ++x) {
+            m[x] = sm.m[w0 + x][r & 15];
+            M = fmaxf(M, m[x]);
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+#pragma unroll
+        for (int x = 0; x < KG; ++x) {
+            const float lv = sm.l[w0 + x][r & 15];
+            if (m[x] == -INFINITY && lv == 0.f) continue;        // no key in this partial
+            const float e = fast_exp2(m[x] - M);
+            const float4 f = *reinterpret_cast<const float4*>(&sm.o[w0 + x][slot4(r, q4)]);
+            L = fmaf(e, lv, L);
+            acc.x = fmaf(e, f.x, acc.x);
+            acc.y = fmaf(e, f.y, acc.y);
+            acc.z = fmaf(e, f.z, acc.z);
+            acc.w = fmaf(e, f.w, acc.w);
+        }
+        if (split) {
+            if (q4 == 0) {
+                sm.row_m[r] = M;
+                sm.row_l[r] = L;
+            }
+            *reinterpret_cast<float4*>(&sm.o[w0][slot4(r, q4)]) = acc;      // (only this thread reads or writes it)
+        } else {
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const int i = r / p.g;
+            bf16* dst = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D + q4 * 4;
+            __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
+        }
+    }
     if (!split) return;
     // Then the parts: rank x finalises the (row, 4-column) items x, x + cs, ...
     __syncwarp();
     cluster_sync();
-    const uint32_t m_a = smem_u32(&ctl.row_m[0]), l_a = smem_u32(&ctl.row_l[0]), f_a = smem_u32(&ctl.failed);
-    all = true;
+    const uint32_t m_a = smem_u32(&sm.row_m[0]), l_a = smem_u32(&sm.row_l[0]);
+    for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 4); it += cs * kThreads) {
+        const int r = it / (D / 4), q4 = it % (D / 4);
+        const uint32_t at = smem_u32(&sm.o[(r >> 4) * KG][slot4(r, q4)]);
+        float m[kMaxCluster], l[kMaxCluster], M = -INFINITY;
+        float4 f[kMaxCluster];
 #pragma unroll
-    for (int x = 0; x < kMaxCluster; ++x)
-        if (x < cs) all = all && ld_cluster_f32(mapa_shared(f_a, x)) == 0.f;
-    if (all)
-        for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 4); it += cs * kThreads) {
-            const int r = it / (D / 4), c4 = it % (D / 4);
-            float m[kMaxCluster], l[kMaxCluster], M = -INFINITY;
-            float4 o[kMaxCluster];
-#pragma unroll
-            for (int x = 0; x < kMaxCluster; ++x) {
-                m[x] = -INFINITY;
-                l[x] = 0.f;
-                if (x < cs) {
-                    m[x] = ld_cluster_f32(mapa_shared(m_a + 4u * r, x));
-                    l[x] = ld_cluster_f32(mapa_shared(l_a + 4u * r, x));
-                    o[x] = ld_cluster_v4(mapa_shared(rows_at + (uint32_t)(it * 16), x));
-                }
+        for (int x = 0; x < kMaxCluster; ++x) {
+            m[x] = -INFINITY;
+            l[x] = 0.f;
+            if (x < cs) {
+                m[x] = ld_cluster_f32(mapa_shared(m_a + 4u * r, x));
+                l[x] = ld_cluster_f32(mapa_shared(l_a + 4u * r, x));
+                f[x] = ld_cluster_v4(mapa_shared(at, x));
             }
-#pragma unroll
-            for (int x = 0; x < kMaxCluster; ++x) M = fmaxf(M, m[x]);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float L = 0.f;
-#pragma unroll
-            for (int x = 0; x < kMaxCluster; ++x) {
-                if (m[x] == -INFINITY && l[x] == 0.f) continue;      // no key in this part
-                const float e = fast_exp2(m[x] - M);
-                L = fmaf(e, l[x], L);
-                acc.x = fmaf(e, o[x].x, acc.x);
-                acc.y = fmaf(e, o[x].y, acc.y);
-                acc.z = fmaf(e, o[x].z, acc.z);
-                acc.w = fmaf(e, o[x].w, acc.w);
-            }
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            const int i = r / p.g;
-            bf16* o2 = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D + c4 * 4;
-            __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(o2) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
         }
+#pragma unroll
+        for (int x = 0; x < kMaxCluster; ++x) M = fmaxf(M, m[x]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+#pragma unroll
+        for (int x = 0; x < kMaxCluster; ++x) {
+            if (m[x] == -INFINITY && l[x] == 0.f) continue;      // no key in this part
+            const float e = fast_exp2(m[x] - M);
+            L = fmaf(e, l[x], L);
+            acc.x = fmaf(e, f[x].x, acc.x);
+            acc.y = fmaf(e, f[x].y, acc.y);
+            acc.z = fmaf(e, f[x].z, acc.z);
+            acc.w = fmaf(e, f[x].w, acc.w);
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int i = r / p.g;
+        bf16* dst = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D + q4 * 4;
+        __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
+    }
     __syncwarp();
     cluster_sync();                // no CTA may leave while another still reads its shared memory
 }
 
-std::atomic<int> g_prepared[8][64];   // see q8_tc.cu
+std::atomic<int> g_prepared[6][64];   // the kernel's shared memory is allowed for, per device and variant
 
-template <int D, int REP, bool kDrop>
+template <int D, int RG>
 int launch(const DecParams& prm, dim3 grid, cudaStream_t stream, bool pdl) {
-    auto kern = q8_decode_kernel<D, REP, kDrop>;
+    auto kern = q8_decode_kernel<D, RG>;
+    constexpr int smem = (int)sizeof(Smem<D, RG>);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
-    std::atomic<int>& st = g_prepared[(D == 128 ? 4 : 0) + (REP == 4 ? 2 : 0) + (kDrop ? 1 : 0)][dev];
+    std::atomic<int>& st = g_prepared[(D == 128 ? 3 : 0) + RG / 2][dev];
     if (!st.load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kBytes) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
             (void)cudaGetLastError();
             return ACACHE_ERR_CUDA;
         }
@@ -646,7 +479,7 @@ int launch(const DecParams& prm, dim3 grid, cudaStream_t stream, bool pdl) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Geo<D>::kBytes;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     unsigned na = 0;
@@ -672,10 +505,10 @@ int launch(const DecParams& prm, dim3 grid, cudaStream_t stream, bool pdl) {
 }
 
 template <int D>
-int dispatch(const DecParams& prm, int rep, bool drop, dim3 grid, cudaStream_t stream, bool pdl) {
-    if (rep == 4)
-        return drop ? launch<D, 4, true>(prm, grid, stream, pdl) : launch<D, 4, false>(prm, grid, stream, pdl);
-    return drop ? launch<D, 2, true>(prm, grid, stream, pdl) : launch<D, 2, false>(prm, grid, stream, pdl);
+int dispatch(const DecParams& prm, int rows, dim3 grid, cudaStream_t stream, bool pdl) {
+    if (rows <= 16) return launch<D, 1>(prm, grid, stream, pdl);
+    if (rows <= 32) return launch<D, 2>(prm, grid, stream, pdl);
+    return launch<D, 4>(prm, grid, stream, pdl);
 }
 
 }  // namespace
@@ -688,9 +521,9 @@ int launch_q8_decode_attention(const Q8Attn& c) {
     const int d = c.a.d, hkv = c.a.hkv, g = c.a.hq / hkv;
     if (c.B > 65535 || (int64_t)hkv * kMaxCluster > 0x7fffffff) return ACACHE_ERR_INVALID_ARG;
     DecParams prm{};
+    prm.q = (const bf16*)c.q;
     prm.k_cache = c.k_cache;
     prm.v_cache = c.v_cache;
-    prm.q = (const bf16*)c.q;
     prm.kv_scale = c.kv_scale;
     prm.read_slot = c.read_slot;
     prm.q_start = c.q_start;
@@ -703,25 +536,30 @@ int launch_q8_decode_attention(const Q8Attn& c) {
     prm.Hq = c.a.hq;
     prm.Hkv = hkv;
     prm.g = g;
+    prm.drop = c.drop_none;
     prm.scale_log2 = c.a.scale * kLog2e;
-    prm.budget = wait_budget();
-    // Parts of the key range: waves x (tiles per part + the fixed cost of a CTA and of a merge)
-    const int n_all = (c.T_len + kBN - 1) / kBN;
-    const int64_t units = (int64_t)c.B * hkv, nsm = sm_count();
+    // Parts of the key range, in chunks of a warp: kFix is what a CTA costs besides its keys, kMerge a merge
+    // over the cluster.  A fixed batch runs in waves of equal CTAs.  Of a ragged batch the host knows the
+    // longest request only: parts until that one no longer outlasts the others, taken as a third as long.
+    constexpr int kFix = 6, kMerge = 2;
+    const int rows = c.n_q * g, kgs = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;
+    const int n_ch = (c.T_len + kChunk - 1) / kChunk;
+    const int64_t units = (int64_t)c.B * hkv, slots = (int64_t)sm_count() * kCtasPerSm;
     prm.cs = 1;
     int64_t best = 0;
-    for (int cs = 1; cs <= kMaxCluster && cs <= n_all; cs *= 2) {
-        const int64_t est = ((units * cs + nsm - 1) / nsm) * ((n_all + cs - 1) / cs + 6 + (cs > 1 ? 2 : 0));
+    for (int cs = 1; cs <= kMaxCluster && cs <= n_ch; cs *= 2) {
+        const int64_t per = (n_ch + cs * kgs - 1) / (cs * kgs) + kFix + (cs > 1 ? kMerge : 0);
+        int64_t est = ((units * cs + slots - 1) / slots) * per;
+        if (c.q_start) est = std::max(per, (units * (n_ch / (3 * kgs) + kFix + (cs > 1 ? kMerge : 0)) + slots - 1) / slots);
         if (cs == 1 || est < best) {
             best = est;
             prm.cs = cs;
         }
     }
-    prm.part = (n_all + prm.cs - 1) / prm.cs;
+    prm.part = (n_ch + prm.cs - 1) / prm.cs;
     const dim3 grid((unsigned)(hkv * prm.cs), (unsigned)c.B, 1);
-    const int rep = (int64_t)c.n_q * g <= 32 ? 4 : 2;
-    return d == 128 ? dispatch<128>(prm, rep, c.drop_none, grid, c.stream, c.after_store)
-                    : dispatch<64>(prm, rep, c.drop_none, grid, c.stream, c.after_store);
+    return d == 128 ? dispatch<128>(prm, rows, grid, c.stream, c.after_store)
+                    : dispatch<64>(prm, rows, grid, c.stream, c.after_store);
 }
 
 }  // namespace acache

@@ -501,7 +501,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             if (warp_live) {
                 const uint32_t at = sQ(t) + (uint32_t)((warp & 3) * 32 * D);
                 float* cr_at = &ctl.part_l[t * kBM + (warp & 3) * 32];      // (free until the end)
-                query_terms<D, 32, 1>(p.q, off, at, at + G::kQPart, 0u, lane, p.scale_log2, 32, cr_at);
+                query_terms<D, 32>(p.q, off, at, at + G::kQPart, lane, p.scale_log2, 32, cr_at);
                 __syncwarp();
                 c_row = cr_at[lane];
             }

@@ -50,6 +50,11 @@ ACACHE_DEVFN void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
 ACACHE_DEVFN void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
+ACACHE_DEVFN uint64_t f2sub(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 // D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit float inputs, fp32 accumulate
 ACACHE_DEVFN void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -57,6 +62,15 @@ ACACHE_DEVFN void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, 
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in TMEM (four elements to a 32-bit column)
+ACACHE_DEVFN void umma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // e4m3 A and B (format 0), fp32 D, K-major operands
@@ -83,16 +97,15 @@ ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (
 
 // NR query rows (8, 16 or 32; the first n of them, rounded up to whole groups) -> two e4m3 terms each, by
 // one warp.  Lane i brings the element offset of row i; `hi` and `lo` are the shared-memory addresses
-// of row 0's terms (rows of D bytes, swizzled, row 0 a multiple of 8), written `copies` times at a distance of `stride`
-// bytes.  c_row[i] receives the factor of row i: its logits are S times the keys' factors times it
+// of row 0's terms (rows of D bytes, swizzled, row 0 a multiple of 8).  c_row[i] receives the factor of row i: its logits are S times the keys' factors times it
 // (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite, which is
 // carried as zeros).
 // The rows land by cp.async where their terms will be, the first half of a row in its row of hi, the
 // second in its row of lo: LPR lanes to a row, so the loads are whole rows.  GR groups of rows at a
 // time keep the chain load - maximum - convert - subtract - convert of several rows in flight.
-template <int D, int NR, int copies>
-ACACHE_DEVFN void query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, uint32_t stride, int lane,
-                              float scale_log2, int n, float* c_row) {
+template <int D, int NR>
+ACACHE_DEVFN void query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, int lane, float scale_log2, int n,
+                              float* c_row) {
     constexpr int LPR = D / 8, RPI = 32 / LPR, NI = NR / RPI, GR = NI < 4 ? NI : 4;
     const uint32_t pc = (uint32_t)(lane % LPR), row = (uint32_t)(lane / LPR);
     const uint32_t at = (pc >= LPR / 2 ? lo : hi) + (pc % (LPR / 2)) * 16u + row * D;
@@ -137,11 +150,8 @@ ACACHE_DEVFN void query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t 
             }
             // (the shuffles ordered the rows' reads before these writes)
             const uint32_t o = row_chunk<D>(r, pc >> 1) + (pc & 1u) * 8u;
-#pragma unroll
-            for (int x = 0; x < copies; ++x) {
-                st_shared_v2(hi + o + x * stride, h[0] | h[1] << 16, h[2] | h[3] << 16);
-                st_shared_v2(lo + o + x * stride, l[0] | l[1] << 16, l[2] | l[3] << 16);
-            }
+            st_shared_v2(hi + o, h[0] | h[1] << 16, h[2] | h[3] << 16);
+            st_shared_v2(lo + o, l[0] | l[1] << 16, l[2] | l[3] << 16);
         }
     }
 }

@@ -6,9 +6,10 @@
 //
 // Memory-bound: each (request, KV head) streams its keys' and values' codes once, 256 bytes a key
 // (d = 128), against at most 64 packed rows (queries x heads of the group).  What limits it is how many
-// bytes are in flight and what a CTA costs besides its keys.  So a warp owns 16 rows and works alone: it
-// brings 16 keys at a time into its own three-stage ring by cp.async, two chunks ahead of the one it
-// works on, and no barrier stands between a load and its use; three CTAs of four warps to an SM.
+// bytes are in flight and what a CTA costs besides its keys.  So a warp owns 8, 16 or 32 rows and works
+// alone: it brings 16 keys at a time into its own three-stage ring by cp.async, two chunks ahead of the
+// one it works on, and no barrier stands between a load and its use; two to four CTAs of four warps
+// to an SM.
 //   * S = q' kc, m16n8k16 f16 products.  A bf16 query row divided by a power of two so that its largest
 //     element lies in [128, 256) is f16 exactly down to 2^-22 of the largest (and off by at most 2^-32 of
 //     it below); codes are f16 exactly, one instruction for two.  The contraction order over d is
@@ -16,19 +17,20 @@
 //     products are carried out as f16 ones here, and convert both operands every time.  Loading the
 //     operands straight into registers, a chunk ahead, was slower than the ring: the loads of one chunk
 //     waited for those of the last.)
-//   * O: P times V's codes converted to f16 (exact, one instruction for two), m16n8k16.  The output column
-//     order is free too: thread group g takes the 16 bytes of columns 16 g .. 16 g + 15 of four keys, and
-//     byte j of two neighbouring keys is the operand of column tile j.
+//   * O^T: V's codes converted to f16 (exact) times P.  The order of its rows (the columns of O) is free
+//     too: thread group g takes the 16 bytes of columns 16 g .. 16 g + 15 of four keys, and byte j of
+//     two neighbouring keys is an operand.  S of rows x keys is the P operand as it comes, and 8 rows
+//     cost 8 rows' products and registers.
 //   * V's power of two goes into the exponent: P = 2^(s + ev - m) with m the running maximum of
 //     s + ev, so P V is right whatever the rows' scales are, P never exceeds 2^15 and keys down to 2^-27
 //     of the largest weighted one count (f16 subnormals); the sum adds P 2^-ev in float32.
 // The warps of a CTA, the CTAs of a cluster (up to 8, where that fills the SMs better) share the keys; partial
 // (maximum, sum, O) are merged in a fixed order through (distributed) shared memory.
 //
-// The register-operand products run at a quarter of tcgen05's rate, which 16 or 32 rows do not need:
-// 128 keys against 16 rows are 525 cycles of an SM's matrix pipes, and reading them at the memory's rate
-// takes 1400.  The tcgen05 form of this kernel (rows replicated over the 128 TMEM lanes, f16 V through
-// shared memory) took 2300 cycles a tile, 1600 of them its M = 128 products of mostly unused rows.
+// The register-operand products run at a quarter of tcgen05's rate, which few rows do not need: 128 keys
+// against 16 rows are 525 cycles of an SM's matrix pipes, and reading them at the memory's rate takes
+// 1400.  The tcgen05 form of this kernel (rows replicated over the 128 TMEM lanes, f16 V through shared
+// memory) took 2300 cycles a tile of 128 keys, 1600 of them its M = 128 products of mostly unused rows.
 #include <algorithm>
 #include <atomic>
 
@@ -43,9 +45,12 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys a warp takes at a time
 constexpr int kSt = 3;                      // chunks in a warp's ring
 constexpr int kMaxCluster = 8;
-constexpr int kCtasPerSm = 3;
+// CTAs to an SM for NB groups of 8 rows to a warp (registers: 32 NB of O and what one chunk needs)
+__host__ __device__ constexpr int ctas_per_sm(int NB) { return NB == 1 ? 4 : NB == 2 ? 3 : 2; }
 constexpr float kPHead = 3.0f;              // P of the used maximum is 2^3 ...
 constexpr float kRescaleThreshold = 12.0f;  // ... and never above 2^15
+constexpr float kNoMax = -1e38f;            // maximum before any key; a key that takes no part lies below it
+constexpr uint32_t kNoEv = 0xff610000u;     // bf16 -2.99e38: its ev
 
 struct DecParams {
     const bf16* q;
@@ -60,16 +65,17 @@ struct DecParams {
     float scale_log2;
 };
 
-template <int D, int RG>
+// NR: rows of a warp
+template <int D, int NR, int RG>
 struct Smem {
-    alignas(128) uint8_t q[RG * 16 * D * 2];        // query rows in f16
+    alignas(128) uint8_t q[RG * NR * D * 2];        // query rows in f16
     union {
         alignas(128) uint8_t ring[kWarps][kSt][2][kChunk * D];      // codes of K and V, a warp's own
-        alignas(16) float o[kWarps][16 * D];                        // partials, warp rg KG + kg
+        alignas(16) float o[kWarps][NR * D];                        // partials, warp rg KG + kg
     };
-    float m[kWarps][16], l[kWarps][16];
-    float row_m[RG * 16], row_l[RG * 16];           // merged over the CTA's warps
-    float c_row[RG * 16];
+    float m[kWarps][NR], l[kWarps][NR];
+    float row_m[RG * NR], row_l[RG * NR];           // merged over the CTA's warps
+    float c_row[RG * NR];
 };
 
 ACACHE_DEVFN void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -124,21 +130,26 @@ template <int D> ACACHE_DEVFN uint32_t k_piece(uint32_t r, uint32_t c) { return 
 template <int D> ACACHE_DEVFN uint32_t v_piece(uint32_t r, uint32_t c) {
     return r * D + ((D == 128 ? c ^ (((r >> 1) & 3u) << 1) : c ^ ((r >> 1) & 3u)) << 4);
 }
-ACACHE_DEVFN uint32_t to_f16x2(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
-    return h;
+// four codes -> f16 pairs
+ACACHE_DEVFN void to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 
-// RG: 16-row groups of the block, one per warp; the KG = 4 / RG warps of a group share the keys.
-template <int D, int RG>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+// NB: groups of 8 rows to a warp; RG: row groups of the block, the KG = 4 / RG warps of a group share the
+// keys.
+template <int D, int NB, int RG>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NB))
 q8_decode_kernel(const DecParams p) {
+    constexpr int NR = 8 * NB;
+    constexpr int MT = (NB + 1) / 2;                 // 16-row operands of S
     constexpr int KG = kWarps / RG;
     constexpr int H = D / 64;                        // 16-byte pieces of a key row per thread
-    constexpr int NT = D / 8;                        // column tiles of O = bytes of a value row per thread
+    constexpr int NV = D / 8;                        // bytes of a value row per thread
     extern __shared__ __align__(128) uint8_t raw_smem[];
-    Smem<D, RG>& sm = *reinterpret_cast<Smem<D, RG>*>(raw_smem);
+    Smem<D, NR, RG>& sm = *reinterpret_cast<Smem<D, NR, RG>*>(raw_smem);
     const int cr = p.cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)p.cs);
     const int hk = p.cs == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)p.cs);
     const int b = (int)blockIdx.y;
@@ -154,7 +165,7 @@ q8_decode_kernel(const DecParams p) {
             return;
         }
     }
-    const int n_rows = n_q * p.g;                    // <= 16 RG
+    const int n_rows = n_q * p.g;                    // <= NR RG
     if (n_rows == 0) return;
     const int n_ch = (T_len + kChunk - 1) / kChunk;
     const int cs = (n_ch + p.part - 1) / p.part;     // parts of this request's keys (<= p.cs)
@@ -173,22 +184,22 @@ q8_decode_kernel(const DecParams p) {
     };
     // slots of the chunk at hand and the two after it (the maps are not written by a store)
     int s0 = slot_of(ch0 + kg), s1 = slot_of(ch0 + kg + KG), s2 = slot_of(ch0 + kg + 2 * KG);
-    {   // query rows: each warp converts its share of its group's 16 rows
-        constexpr int NR = 16 / KG < 8 ? 8 : 16 / KG;                   // at least 8 rows to a warp
-        const int f0 = rg * 16 + kg * NR;
-        if (kg * NR < 16) {
-            const int pr = f0 + (lane & (NR - 1)) < n_rows ? f0 + (lane & (NR - 1)) : 0, i = pr / p.g;
+    {   // query rows: each warp converts its share of its group's, 8 at least
+        constexpr int NC = NR / KG < 8 ? 8 : NR / KG;
+        const int f0 = rg * NR + kg * NC;
+        if (kg * NC < NR) {
+            const int pr = f0 + (lane & (NC - 1)) < n_rows ? f0 + (lane & (NC - 1)) : 0, i = pr / p.g;
             const int64_t off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
-            query_rows<D, NR>(p.q, off, smem_u32(&sm.q[f0 * D * 2]), lane, p.scale_log2, &sm.c_row[f0]);
+            query_rows<D, NC>(p.q, off, smem_u32(&sm.q[f0 * D * 2]), lane, p.scale_log2, &sm.c_row[f0]);
         }
     }
-    const int64_t row_bytes = (int64_t)p.Hkv * D;
+    const uint32_t row_bytes = (uint32_t)p.Hkv * D;
     constexpr int CPR = D / 16, RPI = 32 / CPR, NI = kChunk / RPI;      // pieces a row, rows an instruction
     const uint32_t rr = (uint32_t)(lane / CPR), pc = (uint32_t)(lane % CPR);
     const uint8_t* ksrc = p.k_cache + (int64_t)hk * D + pc * 16;
     const uint8_t* vsrc = p.v_cache + (int64_t)hk * D + pc * 16;
     const uint32_t ring = smem_u32(&sm.ring[warp][0][0][0]);
-    // 2^ek as bf16 with ev as bf16 above it, of this lane's key; a key that takes no part has ev = -inf
+    // 2^ek as bf16 with ev as bf16 above it, of this lane's key
     auto factors = [&](int slot, uint32_t sc) -> uint32_t {
         if (slot >= 0 && slot < p.num_slots) {
             const uint32_t k = sc & 0xffu, v = sc >> 8;
@@ -196,7 +207,7 @@ q8_decode_kernel(const DecParams p) {
                                                : __float_as_uint((float)((int)max(v, (uint32_t)(kQ8MinExp + 127)) - 127));
             return (k > kQ8MaxByte ? 0x7fffu : k << 7) | (ev & 0xffff0000u);
         }
-        if (slot == kNoKey || (p.drop && slot == ACACHE_SLOT_NONE)) return 0xff800000u;
+        if (slot == kNoKey || (p.drop && slot == ACACHE_SLOT_NONE)) return kNoEv;
         return 0x3f80u;                              // outside the pool: a zero row that counts
     };
     auto load_scale = [&](int slot) -> uint32_t {
@@ -211,7 +222,7 @@ q8_decode_kernel(const DecParams p) {
         for (int i = 0; i < NI; ++i) r[i] = __shfl_sync(0xffffffffu, sl, i * RPI + rr);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {               // (a key without a row is zeros)
-            const int64_t at = max(r[i], 0) * row_bytes;
+            const uint64_t at = (uint64_t)(uint32_t)max(r[i], 0) * row_bytes;
             const uint32_t bytes = r[i] >= 0 ? 16u : 0u, row = (uint32_t)(i * RPI) + rr;
             if (RG == 1) {
                 cp_async16(stage + k_piece<D>(row, pc), ksrc + at, bytes);
@@ -229,21 +240,35 @@ q8_decode_kernel(const DecParams p) {
     cp_async_commit();
     uint32_t sc0 = load_scale(s0), sc1 = load_scale(s1), sc2 = 0;
     __syncthreads();                                 // the query terms are there
-    uint32_t qf[2][H][2][4];                         // [row g, g + 8][piece][half of its 16 elements]
+    // the query operand: rows g, g + 8, ... of the warp, the thread's pieces (NB = 4 reads it as it goes)
+    auto load_q = [&](int b, int h, int x, uint32_t (&r)[4]) {
+        ld_shared_v4(smem_u32(&sm.q[0]) + (uint32_t)((rg * NR + 8 * b + g) * 2 * D + (t + 4 * h) * 32 + x * 16), r);
+    };
+    constexpr bool kQRegs = NB <= 2;
+    uint32_t qf[kQRegs ? NB : 1][H][2][4];           // [group of 8 rows][piece][half of its 16 elements]
+    if constexpr (kQRegs) {
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int h = 0; h < H; ++h)
+            for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-                ld_shared_v4(smem_u32(&sm.q[0]) + (uint32_t)((rg * 16 + 8 * y + g) * 2 * D + (t + 4 * h) * 32 + x * 16), qf[y][h][x]);
-    const float c0 = sm.c_row[rg * 16 + g], c1 = sm.c_row[rg * 16 + 8 + g];
-    float o[NT][4];
+                for (int x = 0; x < 2; ++x) load_q(b, h, x, qf[b][h][x]);
+    }
+    float c[NB], m[NB], l[NB];                       // of rows g, g + 8, ...
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int b = 0; b < NB; ++b) {
+        c[b] = sm.c_row[rg * NR + 8 * b + g];
+        m[b] = kNoMax;
+        l[b] = 0.f;
+    }
+    // O^T: o[j][b][0..3] = columns NV g + 2 j (rows 2t, 2t + 1 of group b) and NV g + 2 j + 1 (the same rows)
+    float o[NV / 2][NB][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int j = 0; j < NV / 2; ++j)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[j][b][x] = 0.f;
     uint32_t at = 0, at2 = 2;                        // stages of the chunk at hand and of the one to bring
     for (int ch = ch0 + kg; ch < ch1; ch += KG) {
         bring(s2, ring + at2 * (2 * kChunk * D));
@@ -265,132 +290,159 @@ q8_decode_kernel(const DecParams p) {
         const uint32_t kat = ring + at * (2 * kChunk * D), vat = kat + kChunk * D;
         at2 = at;
         at = at == kSt - 1 ? 0 : at + 1;
-        float s[2][4];
+        constexpr int CH = MT == 1 ? 2 : 1;          // chains of products per result: four in all
+        float s[MT][2][CH][4];
+        uint32_t kf[2][H][4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
+            for (int i = 0; i < MT * CH * 4; ++i) s[i / (CH * 4)][n][i / 4 % CH][i % 4] = 0.f;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                uint32_t kf[4];
-                ld_shared_v4(kat + k_piece<D>((uint32_t)(8 * n + g), (uint32_t)(t + 4 * h)), kf);
-#pragma unroll
-                for (int y = 0; y < 4; ++y)          // four elements of the piece to a product
-                    mma_f16(s[n], qf[0][h][y >> 1][2 * (y & 1)], qf[1][h][y >> 1][2 * (y & 1)], qf[0][h][y >> 1][2 * (y & 1) + 1],
-                            qf[1][h][y >> 1][2 * (y & 1) + 1], to_f16x2(kf[y] & 0xffffu), to_f16x2(kf[y] >> 16));
-            }
+            for (int h = 0; h < H; ++h)
+                ld_shared_v4(kat + k_piece<D>((uint32_t)(8 * n + g), (uint32_t)(t + 4 * h)), kf[n][h]);
         }
-        uint32_t vf[4][NT / 4];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t a[2 * MT][4];
+#pragma unroll
+                for (int b = 0; b < 2 * MT; ++b) {
+                    if constexpr (!kQRegs) {
+                        load_q(b, h, x, a[b]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) a[b][i] = b < NB ? qf[b < NB ? b : 0][h][x][i] : 0u;
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)          // four elements of the piece to a product
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        uint32_t b0, b1;
+                        to_f16(kf[n][h][2 * x + y], b0, b1);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+                            mma_f16(s[i][n][y % CH], a[2 * i][2 * y], a[2 * i + 1][2 * y], a[2 * i][2 * y + 1],
+                                    a[2 * i + 1][2 * y + 1], b0, b1);
+                    }
+            }
+        uint32_t vf[4][NV / 4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const uint32_t key = (uint32_t)(2 * t + (x & 1) + 8 * (x >> 1));
             ld_words(vat + (D == 128 ? v_piece<D>(key, (uint32_t)g) : v_piece<D>(key, (uint32_t)g >> 1) + 8u * (g & 1)), vf[x]);
         }
-        // t = s + ev in log2 units; s[n][0], s[n][1]: row g, keys 8n + 2t, + 1; s[n][2], s[n][3]: row g + 8
-        float ev[4];
+        // u = s + ev in log2 units, of row g of group b and keys 2t, 2t + 1, 2t + 8, 2t + 9
+        float ev[4], rv[4], u[NB][4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const float fk = __uint_as_float(fe[x] << 16);
             ev[x] = __uint_as_float(fe[x] & 0xffff0000u);
-            s[x >> 1][x & 1] = fmaf(s[x >> 1][x & 1] * fk, c0, ev[x]);
-            s[x >> 1][2 + (x & 1)] = fmaf(s[x >> 1][2 + (x & 1)] * fk, c1, ev[x]);
-        }
-        float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float t1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        // (a maximum that is NaN -- every key of the row so far -- is left alone)
-        if (__any_sync(0xffffffffu, t0 > m0 + kRescaleThreshold || t1 > m1 + kRescaleThreshold)) {
+            rv[x] = fast_exp2(fminf(-ev[x], 126.f));             // (finite where the key takes no part)
 #pragma unroll
-            for (int x = 1; x < 4; x <<= 1) {        // over the row's four threads
-                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+            for (int b = 0; b < NB; ++b) {
+                float d = s[b >> 1][x >> 1][0][2 * (b & 1) + (x & 1)];
+                if constexpr (CH == 2) d += s[b >> 1][x >> 1][CH - 1][2 * (b & 1) + (x & 1)];
+                u[b][x] = fmaf(d * fk, c[b], ev[x]);
             }
-            const float n0 = t0 > m0 + kRescaleThreshold ? t0 : m0, n1 = t1 > m1 + kRescaleThreshold ? t1 : m1;
-            const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
-            // (without a key so far O and the sum are 0, or NaN where a poisoned key was met: keep that)
-            l0 *= a0;
-            l1 *= a1;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                o[j][0] *= a0;
-                o[j][1] *= a0;
-                o[j][2] *= a1;
-                o[j][3] *= a1;
-            }
-            m0 = n0;
-            m1 = n1;
         }
-        const float ms0 = m0 == -INFINITY ? 0.f : m0 - kPHead, ms1 = m1 == -INFINITY ? 0.f : m1 - kPHead;
-        uint32_t pa[4];
+        bool grow = false;                           // (a maximum that is NaN -- every key of the row so far -- is left alone)
+        float top[NB];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float pr[4], rv[2];
+        for (int b = 0; b < NB; ++b) {
+            top[b] = fmaxf(fmaxf(u[b][0], u[b][1]), fmaxf(u[b][2], u[b][3]));
+            grow = grow || top[b] > m[b] + kRescaleThreshold;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                rv[x] = ev[2 * n + x] == -INFINITY ? 0.f : fast_exp2(-ev[2 * n + x]);
-                pr[x] = fast_exp2(s[n][x] - ms0);
-                pr[2 + x] = fast_exp2(s[n][2 + x] - ms1);
-                l0 = fmaf(pr[x], rv[x], l0);
-                l1 = fmaf(pr[2 + x], rv[x], l1);
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int x = 1; x < 4; x <<= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], x));   // over the row's threads
+                const float mn = top[b] > m[b] + kRescaleThreshold ? top[b] : m[b];
+                const float al = fast_exp2(m[b] - mn);
+                l[b] *= al;
+                m[b] = mn;
+                const float a0 = __shfl_sync(0xffffffffu, al, 8 * t), a1 = __shfl_sync(0xffffffffu, al, 8 * t + 4);   // of rows 2t, 2t + 1
+#pragma unroll
+                for (int j = 0; j < NV / 2; ++j) {
+                    o[j][b][0] *= a0;
+                    o[j][b][1] *= a1;
+                    o[j][b][2] *= a0;
+                    o[j][b][3] *= a1;
+                }
+            }
+        }
+        uint32_t pb[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float ms = m[b] - kPHead;
+            float pr[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                pr[x] = fast_exp2(u[b][x] - ms);
+                l[b] = fmaf(pr[x], rv[x], l[b]);
             }
             // f16 keeps 11 bits, so P is rounded finer than bf16 would
-            const __half2 u = __floats2half2_rn(pr[0], pr[1]), w = __floats2half2_rn(pr[2], pr[3]);
-            pa[2 * n] = *reinterpret_cast<const uint32_t*>(&u);
-            pa[2 * n + 1] = *reinterpret_cast<const uint32_t*>(&w);
+            const __half2 w0 = __floats2half2_rn(pr[0], pr[1]), w1 = __floats2half2_rn(pr[2], pr[3]);
+            pb[b][0] = *reinterpret_cast<const uint32_t*>(&w0);
+            pb[b][1] = *reinterpret_cast<const uint32_t*>(&w1);
         }
 #pragma unroll
-        for (int y = 0; y < NT / 4; ++y) {
+        for (int y = 0; y < NV / 4; ++y) {
             // bytes 4y .. 4y + 3 of the four keys, two keys to an operand
-            const uint32_t u0 = __byte_perm(vf[0][y], vf[1][y], 0x5140), u1 = __byte_perm(vf[0][y], vf[1][y], 0x7362);
-            const uint32_t w0 = __byte_perm(vf[2][y], vf[3][y], 0x5140), w1 = __byte_perm(vf[2][y], vf[3][y], 0x7362);
-            mma_f16(o[4 * y], pa[0], pa[1], pa[2], pa[3], to_f16x2(u0 & 0xffffu), to_f16x2(w0 & 0xffffu));
-            mma_f16(o[4 * y + 1], pa[0], pa[1], pa[2], pa[3], to_f16x2(u0 >> 16), to_f16x2(w0 >> 16));
-            mma_f16(o[4 * y + 2], pa[0], pa[1], pa[2], pa[3], to_f16x2(u1 & 0xffffu), to_f16x2(w1 & 0xffffu));
-            mma_f16(o[4 * y + 3], pa[0], pa[1], pa[2], pa[3], to_f16x2(u1 >> 16), to_f16x2(w1 >> 16));
+            uint32_t a[4][2];
+            to_f16(__byte_perm(vf[0][y], vf[1][y], 0x5140), a[0][0], a[1][0]);
+            to_f16(__byte_perm(vf[0][y], vf[1][y], 0x7362), a[2][0], a[3][0]);
+            to_f16(__byte_perm(vf[2][y], vf[3][y], 0x5140), a[0][1], a[1][1]);
+            to_f16(__byte_perm(vf[2][y], vf[3][y], 0x7362), a[2][1], a[3][1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    mma_f16(o[2 * y + x][b], a[2 * x][0], a[2 * x + 1][0], a[2 * x][1], a[2 * x + 1][1], pb[b][0], pb[b][1]);
         }
         __syncwarp();                                // the next chunk but two lands in this stage
     }
     cp_async_wait<0>();
     __syncthreads();                                 // the partials go over the rings
     // -------------------------------------------------------------------------- merge
-    // o[j][0] is column 2 NT t + j of row g, o[j][1] the one NT further; o[j][2], o[j][3] of row g + 8
 #pragma unroll
-    for (int x = 1; x < 4; x <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-    }
-    if (t == 0) {
-        sm.m[warp][g] = m0;
-        sm.m[warp][g + 8] = m1;
-        sm.l[warp][g] = l0;
-        sm.l[warp][g + 8] = l1;
-    }
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-    for (int j = 0; j < NT; j += 4)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            // float4 slot of a row, moved by row and thread so that the lanes spread over the banks
-            const int r = g + 8 * (x >> 1), q4 = (2 * NT * t + NT * (x & 1) + j) / 4;
-            *reinterpret_cast<float4*>(&sm.o[warp][r * D + 4 * (((q4 ^ (q4 / (NT / 2))) + 2 * (r & 7)) & (D / 4 - 1))]) =
-                make_float4(o[j][x], o[j + 1][x], o[j + 2][x], o[j + 3][x]);
+        for (int x = 1; x < 4; x <<= 1) l[b] += __shfl_xor_sync(0xffffffffu, l[b], x);
+        if (t == 0) {
+            sm.m[warp][8 * b + g] = m[b];
+            sm.l[warp][8 * b + g] = l[b];
         }
+    }
+    // float4 slot of a row, moved by row and by thread group so that the lanes spread over the banks
+    auto slot4 = [&](int r, int q4) { return (r & (NR - 1)) * D + 4 * (((q4 ^ (q4 / (NV / 4) & (NV / 4 - 1))) + (r & 7) * 2) & (D / 4 - 1)); };
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)                  // row 2t + x of group b, columns NV g ...
+#pragma unroll
+            for (int j = 0; j < NV / 4; ++j)
+                *reinterpret_cast<float4*>(&sm.o[warp][slot4(8 * b + 2 * t + x, g * (NV / 4) + j)]) =
+                    make_float4(o[2 * j][b][x], o[2 * j][b][2 + x], o[2 * j + 1][b][x], o[2 * j + 1][b][2 + x]);
     __syncthreads();
     // First the warps of each row group, a thread taking 4 columns of a row.
     const bool split = cs > 1;
-    auto slot4 = [&](int r, int q4) { return (r & 15) * D + 4 * (((q4 ^ (q4 / (NT / 2))) + 2 * (r & 7)) & (D / 4 - 1)); };
     for (int it = (int)threadIdx.x; it < n_rows * (D / 4); it += kThreads) {
-        const int r = it / (D / 4), q4 = it % (D / 4), w0 = (r >> 4) * KG;
-        float m[KG], M = -INFINITY;
+        const int r = it / (D / 4), q4 = it % (D / 4), w0 = r / NR * KG;
+        float m[KG], M = kNoMax;
 #pragma unroll
         for (int x = 0; x < KG; ++x) {
-            m[x] = sm.m[w0 + x][r & 15];
+            m[x] = sm.m[w0 + x][r & (NR - 1)];
             M = fmaxf(M, m[x]);
         }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float L = 0.f;
 #pragma unroll
         for (int x = 0; x < KG; ++x) {
-            const float lv = sm.l[w0 + x][r & 15];
-            if (m[x] == -INFINITY && lv == 0.f) continue;        // no key in this partial
+            const float lv = sm.l[w0 + x][r & (NR - 1)];
+            if (lv == 0.f) continue;                             // no key in this partial
             const float e = fast_exp2(m[x] - M);
             const float4 f = *reinterpret_cast<const float4*>(&sm.o[w0 + x][slot4(r, q4)]);
             L = fmaf(e, lv, L);
@@ -420,12 +472,12 @@ q8_decode_kernel(const DecParams p) {
     const uint32_t m_a = smem_u32(&sm.row_m[0]), l_a = smem_u32(&sm.row_l[0]);
     for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 4); it += cs * kThreads) {
         const int r = it / (D / 4), q4 = it % (D / 4);
-        const uint32_t at = smem_u32(&sm.o[(r >> 4) * KG][slot4(r, q4)]);
-        float m[kMaxCluster], l[kMaxCluster], M = -INFINITY;
+        const uint32_t at = smem_u32(&sm.o[r / NR * KG][slot4(r, q4)]);
+        float m[kMaxCluster], l[kMaxCluster], M = kNoMax;
         float4 f[kMaxCluster];
 #pragma unroll
         for (int x = 0; x < kMaxCluster; ++x) {
-            m[x] = -INFINITY;
+            m[x] = kNoMax;
             l[x] = 0.f;
             if (x < cs) {
                 m[x] = ld_cluster_f32(mapa_shared(m_a + 4u * r, x));
@@ -439,7 +491,7 @@ q8_decode_kernel(const DecParams p) {
         float L = 0.f;
 #pragma unroll
         for (int x = 0; x < kMaxCluster; ++x) {
-            if (m[x] == -INFINITY && l[x] == 0.f) continue;      // no key in this part
+            if (l[x] == 0.f) continue;                           // no key in this part
             const float e = fast_exp2(m[x] - M);
             L = fmaf(e, l[x], L);
             acc.x = fmaf(e, f[x].x, acc.x);
@@ -457,18 +509,18 @@ q8_decode_kernel(const DecParams p) {
     cluster_sync();                // no CTA may leave while another still reads its shared memory
 }
 
-std::atomic<int> g_prepared[6][64];   // the kernel's shared memory is allowed for, per device and variant
+std::atomic<int> g_prepared[8][64];   // the kernel's shared memory is allowed for, per device and variant
 
-template <int D, int RG>
+template <int D, int NB, int RG>
 int launch(const DecParams& prm, dim3 grid, cudaStream_t stream, bool pdl) {
-    auto kern = q8_decode_kernel<D, RG>;
-    constexpr int smem = (int)sizeof(Smem<D, RG>);
+    auto kern = q8_decode_kernel<D, NB, RG>;
+    constexpr int smem = (int)sizeof(Smem<D, 8 * NB, RG>);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
-    std::atomic<int>& st = g_prepared[(D == 128 ? 3 : 0) + RG / 2][dev];
+    std::atomic<int>& st = g_prepared[(D == 128 ? 4 : 0) + NB / 2 + RG - 1][dev];
     if (!st.load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
             (void)cudaGetLastError();
@@ -506,9 +558,10 @@ int launch(const DecParams& prm, dim3 grid, cudaStream_t stream, bool pdl) {
 
 template <int D>
 int dispatch(const DecParams& prm, int rows, dim3 grid, cudaStream_t stream, bool pdl) {
-    if (rows <= 16) return launch<D, 1>(prm, grid, stream, pdl);
-    if (rows <= 32) return launch<D, 2>(prm, grid, stream, pdl);
-    return launch<D, 4>(prm, grid, stream, pdl);
+    if (rows <= 8) return launch<D, 1, 1>(prm, grid, stream, pdl);
+    if (rows <= 16) return launch<D, 2, 1>(prm, grid, stream, pdl);
+    if (rows <= 32) return launch<D, 4, 1>(prm, grid, stream, pdl);
+    return launch<D, 4, 2>(prm, grid, stream, pdl);
 }
 
 }  // namespace
@@ -540,17 +593,18 @@ int launch_q8_decode_attention(const Q8Attn& c) {
     prm.scale_log2 = c.a.scale * kLog2e;
     // Parts of the key range, in chunks of a warp: kFix is what a CTA costs besides its keys, kMerge a merge
     // over the cluster.  A fixed batch runs in waves of equal CTAs.  Of a ragged batch the host knows the
-    // longest request only: parts until that one no longer outlasts the others, taken as a third as long.
+    // longest request only: parts until that one no longer outlasts the others, taken as an eighth as
+    // long.
     constexpr int kFix = 6, kMerge = 2;
-    const int rows = c.n_q * g, kgs = rows <= 16 ? 4 : rows <= 32 ? 2 : 1;
+    const int rows = c.n_q * g, kgs = rows <= 32 ? 4 : 2;
     const int n_ch = (c.T_len + kChunk - 1) / kChunk;
-    const int64_t units = (int64_t)c.B * hkv, slots = (int64_t)sm_count() * kCtasPerSm;
+    const int64_t units = (int64_t)c.B * hkv, slots = (int64_t)sm_count() * ctas_per_sm(rows <= 8 ? 1 : rows <= 16 ? 2 : 4);
     prm.cs = 1;
     int64_t best = 0;
     for (int cs = 1; cs <= kMaxCluster && cs <= n_ch; cs *= 2) {
         const int64_t per = (n_ch + cs * kgs - 1) / (cs * kgs) + kFix + (cs > 1 ? kMerge : 0);
         int64_t est = ((units * cs + slots - 1) / slots) * per;
-        if (c.q_start) est = std::max(per, (units * (n_ch / (3 * kgs) + kFix + (cs > 1 ? kMerge : 0)) + slots - 1) / slots);
+        if (c.q_start) est = std::max(per, (units * (n_ch / (8 * kgs) + kFix + (cs > 1 ? kMerge : 0)) + slots - 1) / slots);
         if (cs == 1 || est < best) {
             best = est;
             prm.cs = cs;

@@ -10,17 +10,16 @@
 // alone: it brings 16 keys at a time into its own three-stage ring by cp.async, two chunks ahead of the
 // one it works on, and no barrier stands between a load and its use; two to four CTAs of four warps
 // to an SM.
-//   * S = q' kc, m16n8k16 f16 products.  A bf16 query row divided by a power of two so that its largest
-//     element lies in [128, 256) is f16 exactly down to 2^-22 of the largest (and off by at most 2^-32 of
-//     it below); codes are f16 exactly, one instruction for two.  The contraction order over d is
-//     free, so a thread's 16-byte piece of a key row is its operand as it lies.  (m16n8k32 e4m3
-//     products are carried out as f16 ones here, and convert both operands every time.  Loading the
-//     operands straight into registers, a chunk ahead, was slower than the ring: the loads of one chunk
-//     waited for those of the last.)
-//   * O^T: V's codes converted to f16 (exact) times P.  The order of its rows (the columns of O) is free
-//     too: thread group g takes the 16 bytes of columns 16 g .. 16 g + 15 of four keys, and byte j of
-//     two neighbouring keys is an operand.  S of rows x keys is the P operand as it comes, and 8 rows
-//     cost 8 rows' products and registers.
+//   * S^T = kc q', m16n8k16 f16 products of 16 keys x 8 rows.  A bf16 query row divided by a power of two so
+//     that its largest element lies in [128, 256) is f16 exactly down to 2^-22 of the largest (and off by
+//     at most 2^-32 of it below); codes are f16 exactly, one instruction for two.  The contraction
+//     order over d is free, so a thread's 16-byte piece of a key row is its operand as it lies.
+//     (m16n8k32 e4m3 products are carried out as f16 ones here, and convert both operands every time.
+//     Loading the operands straight into registers, a chunk ahead, was slower than the ring: the loads
+//     of one chunk waited for those of the last.  S of rows x keys wastes half of an operand on 8 rows.)
+//   * O^T = V^T P^T, V's codes converted to f16 likewise.  The order of its rows (the columns of O) is
+//     free too: thread group g takes the 16 bytes of columns 16 g .. 16 g + 15 of four keys, and byte j
+//     of two neighbouring keys is an operand.  P^T becomes one by an 8 x 8 transposition.
 //   * V's power of two goes into the exponent: P = 2^(s + ev - m) with m the running maximum of
 //     s + ev, so P V is right whatever the rows' scales are, P never exceeds 2^15 and keys down to 2^-27
 //     of the largest weighted one count (f16 subnormals); the sum adds P 2^-ev in float32.
@@ -113,7 +112,8 @@ ACACHE_DEVFN void query_rows(const bf16* q, int64_t off, uint32_t at, int lane, 
             __half2 two = __floats2half2_rn(__uint_as_float(x[y] << 16) * up, __uint_as_float(x[y] & 0xffff0000u) * up);
             h[y] = finite ? *reinterpret_cast<uint32_t*>(&two) : 0u;
         }
-        st_shared_v4(at + (uint32_t)((i * RPI + row) * 2 * D + pc * 16), h[0], h[1], h[2], h[3]);
+        // (odd rows have their 16-byte pieces exchanged in pairs: see the operand's reads)
+        st_shared_v4(at + (uint32_t)((i * RPI + row) * 2 * D + (pc ^ (row & 1)) * 16), h[0], h[1], h[2], h[3]);
     }
 }
 ACACHE_DEVFN void ld_words(uint32_t addr, uint32_t (&r)[4]) { ld_shared_v4(addr, r); }
@@ -144,7 +144,6 @@ template <int D, int NB, int RG>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB))
 q8_decode_kernel(const DecParams p) {
     constexpr int NR = 8 * NB;
-    constexpr int MT = (NB + 1) / 2;                 // 16-row operands of S
     constexpr int KG = kWarps / RG;
     constexpr int H = D / 64;                        // 16-byte pieces of a key row per thread
     constexpr int NV = D / 8;                        // bytes of a value row per thread
@@ -240,12 +239,12 @@ q8_decode_kernel(const DecParams p) {
     cp_async_commit();
     uint32_t sc0 = load_scale(s0), sc1 = load_scale(s1), sc2 = 0;
     __syncthreads();                                 // the query terms are there
-    // the query operand: rows g, g + 8, ... of the warp, the thread's pieces (NB = 4 reads it as it goes)
+    // the query operand: row g of group b, half x of the thread's piece h (NB = 4 reads it as it goes)
     auto load_q = [&](int b, int h, int x, uint32_t (&r)[4]) {
-        ld_shared_v4(smem_u32(&sm.q[0]) + (uint32_t)((rg * NR + 8 * b + g) * 2 * D + (t + 4 * h) * 32 + x * 16), r);
+        ld_shared_v4(smem_u32(&sm.q[0]) + (uint32_t)((rg * NR + 8 * b + g) * 2 * D + (t + 4 * h) * 32 + ((x ^ (g & 1)) * 16)), r);
     };
     constexpr bool kQRegs = NB <= 2;
-    uint32_t qf[kQRegs ? NB : 1][H][2][4];           // [group of 8 rows][piece][half of its 16 elements]
+    uint32_t qf[kQRegs ? NB : 1][H][2][4];
     if constexpr (kQRegs) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -254,13 +253,15 @@ q8_decode_kernel(const DecParams p) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) load_q(b, h, x, qf[b][h][x]);
     }
-    float c[NB], m[NB], l[NB];                       // of rows g, g + 8, ...
+    float c[NB][2], m[NB][2], l[NB][2];              // of rows 2t, 2t + 1 of each group
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        c[b] = sm.c_row[rg * NR + 8 * b + g];
-        m[b] = kNoMax;
-        l[b] = 0.f;
-    }
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            c[b][x] = sm.c_row[rg * NR + 8 * b + 2 * t + x];
+            m[b][x] = kNoMax;
+            l[b][x] = 0.f;
+        }
     // O^T: o[j][b][0..3] = columns NV g + 2 j (rows 2t, 2t + 1 of group b) and NV g + 2 j + 1 (the same rows)
     float o[NV / 2][NB][4];
 #pragma unroll
@@ -282,112 +283,108 @@ q8_decode_kernel(const DecParams p) {
         sc0 = sc1;
         sc1 = sc2;
         s2 = slot_of(ch + 3 * KG);
-        uint32_t fe[4];                              // of keys 2t, 2t + 1, 2t + 8, 2t + 9
+        uint32_t fe[2];                              // of keys g and g + 8
 #pragma unroll
-        for (int x = 0; x < 4; ++x) fe[x] = __shfl_sync(0xffffffffu, fe_own, 2 * t + (x & 1) + 8 * (x >> 1));
+        for (int x = 0; x < 2; ++x) fe[x] = __shfl_sync(0xffffffffu, fe_own, g + 8 * x);
         cp_async_wait<2>();
         __syncwarp();
         const uint32_t kat = ring + at * (2 * kChunk * D), vat = kat + kChunk * D;
         at2 = at;
         at = at == kSt - 1 ? 0 : at + 1;
-        constexpr int CH = MT == 1 ? 2 : 1;          // chains of products per result: four in all
-        float s[MT][2][CH][4];
-        uint32_t kf[2][H][4];
+        constexpr int CH = NB == 1 ? 4 : NB == 2 ? 2 : 1;      // chains of products per result: four in all
+        float s[NB][CH][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int i = 0; i < NB * CH * 4; ++i) s[i / (CH * 4)][i / 4 % CH][i % 4] = 0.f;
 #pragma unroll
-            for (int i = 0; i < MT * CH * 4; ++i) s[i / (CH * 4)][n][i / 4 % CH][i % 4] = 0.f;
+        for (int h = 0; h < H; ++h) {
+            uint32_t kf[2][4];
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-                ld_shared_v4(kat + k_piece<D>((uint32_t)(8 * n + g), (uint32_t)(t + 4 * h)), kf[n][h]);
-        }
-#pragma unroll
-        for (int h = 0; h < H; ++h)
+            for (int n = 0; n < 2; ++n) ld_shared_v4(kat + k_piece<D>((uint32_t)(8 * n + g), (uint32_t)(t + 4 * h)), kf[n]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                uint32_t a[2 * MT][4];
+                uint32_t a[2][4], qr[NB][4];
 #pragma unroll
-                for (int b = 0; b < 2 * MT; ++b) {
-                    if constexpr (!kQRegs) {
-                        load_q(b, h, x, a[b]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) a[b][i] = b < NB ? qf[b < NB ? b : 0][h][x][i] : 0u;
-                    }
+                for (int y = 0; y < 2; ++y) {        // four elements of the piece to a product
+                    to_f16(kf[0][2 * x + y], a[y][0], a[y][2]);
+                    to_f16(kf[1][2 * x + y], a[y][1], a[y][3]);
                 }
 #pragma unroll
-                for (int y = 0; y < 2; ++y)          // four elements of the piece to a product
+                for (int b = 0; b < NB; ++b) {
+                    if constexpr (!kQRegs) {
+                        load_q(b, h, x, qr[b]);
+                    } else {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        uint32_t b0, b1;
-                        to_f16(kf[n][h][2 * x + y], b0, b1);
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            mma_f16(s[i][n][y % CH], a[2 * i][2 * y], a[2 * i + 1][2 * y], a[2 * i][2 * y + 1],
-                                    a[2 * i + 1][2 * y + 1], b0, b1);
+                        for (int i = 0; i < 4; ++i) qr[b][i] = qf[b][h][x][i];
                     }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        mma_f16(s[b][(2 * x + y) % CH], a[y][0], a[y][1], a[y][2], a[y][3], qr[b][2 * y], qr[b][2 * y + 1]);
+                }
             }
+        }
         uint32_t vf[4][NV / 4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const uint32_t key = (uint32_t)(2 * t + (x & 1) + 8 * (x >> 1));
             ld_words(vat + (D == 128 ? v_piece<D>(key, (uint32_t)g) : v_piece<D>(key, (uint32_t)g >> 1) + 8u * (g & 1)), vf[x]);
         }
-        // u = s + ev in log2 units, of row g of group b and keys 2t, 2t + 1, 2t + 8, 2t + 9
-        float ev[4], rv[4], u[NB][4];
+        // u = s + ev in log2 units, u[b][2 k + x]: key g + 8 k, row 2t + x of group b
+        float ev[2], rv[2], u[NB][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float fk = __uint_as_float(fe[x] << 16);
-            ev[x] = __uint_as_float(fe[x] & 0xffff0000u);
-            rv[x] = fast_exp2(fminf(-ev[x], 126.f));             // (finite where the key takes no part)
+        for (int k = 0; k < 2; ++k) {
+            const float fk = __uint_as_float(fe[k] << 16);
+            ev[k] = __uint_as_float(fe[k] & 0xffff0000u);
+            rv[k] = fast_exp2(fminf(-ev[k], 126.f));             // (finite where the key takes no part)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float d = s[b >> 1][x >> 1][0][2 * (b & 1) + (x & 1)];
-                if constexpr (CH == 2) d += s[b >> 1][x >> 1][CH - 1][2 * (b & 1) + (x & 1)];
-                u[b][x] = fmaf(d * fk, c[b], ev[x]);
-            }
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float d = s[b][0][2 * k + x];
+#pragma unroll
+                    for (int i = 1; i < CH; ++i) d += s[b][i][2 * k + x];
+                    u[b][2 * k + x] = fmaf(d * fk, c[b][x], ev[k]);
+                }
         }
         bool grow = false;                           // (a maximum that is NaN -- every key of the row so far -- is left alone)
-        float top[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            top[b] = fmaxf(fmaxf(u[b][0], u[b][1]), fmaxf(u[b][2], u[b][3]));
-            grow = grow || top[b] > m[b] + kRescaleThreshold;
-        }
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) grow = grow || fmaxf(u[b][x], u[b][2 + x]) > m[b][x] + kRescaleThreshold;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
+                float al[2];
 #pragma unroll
-                for (int x = 1; x < 4; x <<= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], x));   // over the row's threads
-                const float mn = top[b] > m[b] + kRescaleThreshold ? top[b] : m[b];
-                const float al = fast_exp2(m[b] - mn);
-                l[b] *= al;
-                m[b] = mn;
-                const float a0 = __shfl_sync(0xffffffffu, al, 8 * t), a1 = __shfl_sync(0xffffffffu, al, 8 * t + 4);   // of rows 2t, 2t + 1
+                for (int x = 0; x < 2; ++x) {
+                    float top = fmaxf(u[b][x], u[b][2 + x]);
 #pragma unroll
-                for (int j = 0; j < NV / 2; ++j) {
-                    o[j][b][0] *= a0;
-                    o[j][b][1] *= a1;
-                    o[j][b][2] *= a0;
-                    o[j][b][3] *= a1;
+                    for (int i = 4; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));   // over the chunk's keys
+                    const float mn = top > m[b][x] + kRescaleThreshold ? top : m[b][x];
+                    al[x] = fast_exp2(m[b][x] - mn);
+                    l[b][x] *= al[x];
+                    m[b][x] = mn;
                 }
+#pragma unroll
+                for (int j = 0; j < NV / 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[j][b][i] *= al[i & 1];
             }
         }
         uint32_t pb[NB][2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const float ms = m[b] - kPHead;
-            float pr[4];
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                pr[x] = fast_exp2(u[b][x] - ms);
-                l[b] = fmaf(pr[x], rv[x], l[b]);
+            for (int k = 0; k < 2; ++k) {
+                float pr[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    pr[x] = fast_exp2(u[b][2 * k + x] - (m[b][x] - kPHead));
+                    l[b][x] = fmaf(pr[x], rv[k], l[b][x]);
+                }
+                // f16 keeps 11 bits, so P is rounded finer than bf16 would
+                const __half2 w = __floats2half2_rn(pr[0], pr[1]);
+                asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb[b][k]) : "r"(*reinterpret_cast<const uint32_t*>(&w)));
             }
-            // f16 keeps 11 bits, so P is rounded finer than bf16 would
-            const __half2 w0 = __floats2half2_rn(pr[0], pr[1]), w1 = __floats2half2_rn(pr[2], pr[3]);
-            pb[b][0] = *reinterpret_cast<const uint32_t*>(&w0);
-            pb[b][1] = *reinterpret_cast<const uint32_t*>(&w1);
-        }
 #pragma unroll
         for (int y = 0; y < NV / 4; ++y) {
             // bytes 4y .. 4y + 3 of the four keys, two keys to an operand
@@ -408,14 +405,16 @@ q8_decode_kernel(const DecParams p) {
     __syncthreads();                                 // the partials go over the rings
     // -------------------------------------------------------------------------- merge
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int x = 1; x < 4; x <<= 1) l[b] += __shfl_xor_sync(0xffffffffu, l[b], x);
-        if (t == 0) {
-            sm.m[warp][8 * b + g] = m[b];
-            sm.l[warp][8 * b + g] = l[b];
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) l[b][x] += __shfl_xor_sync(0xffffffffu, l[b][x], i);
+            if (g == 0) {
+                sm.m[warp][8 * b + 2 * t + x] = m[b][x];
+                sm.l[warp][8 * b + 2 * t + x] = l[b][x];
+            }
         }
-    }
     // float4 slot of a row, moved by row and by thread group so that the lanes spread over the banks
     auto slot4 = [&](int r, int q4) { return (r & (NR - 1)) * D + 4 * (((q4 ^ (q4 / (NV / 4) & (NV / 4 - 1))) + (r & 7) * 2) & (D / 4 - 1)); };
 #pragma unroll

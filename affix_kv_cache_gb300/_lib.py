@@ -132,17 +132,29 @@ def version() -> int:
 def _p(t):
     if t is None:
         return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr() or None
+    except AttributeError:       # a plain address
         return t or None
-    return t.data_ptr() or None
 
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        # the current stream's handle, as torch.cuda.current_stream().cuda_stream gives it in 15 times the
+        # time; before torch has touched CUDA that is the default stream
+        if not torch.cuda.is_initialized():
+            return None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
+
+
+def _stream_of(t, stream):
+    """_stream, for a call on tensor `t`: the tensors of a call live on the current device."""
+    if torch.cuda.is_initialized() and isinstance(t, torch.Tensor) and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"tensor on {t.device}, current device is cuda:{torch._C._cuda_getDevice()}")
+    return _stream(stream)
 
 
 def _check(fn, status):
@@ -332,7 +344,7 @@ def acache_write_slots_q8(desc, batch, rows, write_slot, k_new, v_new, k_cache, 
     """The store step into an 8-bit pool: quantises as it writes."""
     st = lib().acache_write_slots_q8(ctypes.byref(desc), batch, rows, _p(write_slot), _p(k_new), _p(v_new),
                                      _p(k_cache), _p(v_cache), _p(kv_scale), num_slots, private_begin,
-                                     _p(dev_status), _stream(stream))
+                                     _p(dev_status), _stream_of(k_cache, stream))
     return _check("acache_write_slots_q8", st) if check else st
 
 
@@ -341,7 +353,7 @@ def acache_gather_slots_q8(desc, batch, seq_len, read_slot, k_cache, v_cache, kv
     """The logical K/V view of an 8-bit pool, in the descriptor's dtype."""
     st = lib().acache_gather_slots_q8(ctypes.byref(desc), batch, seq_len, _p(read_slot), _p(k_cache), _p(v_cache),
                                       _p(kv_scale), num_slots, _p(k_out), _p(v_out), _p(dev_status),
-                                      _stream(stream))
+                                      _stream_of(k_cache, stream))
     return _check("acache_gather_slots_q8", st) if check else st
 
 
@@ -350,7 +362,7 @@ def acache_slot_attention_q8(desc, batch, n_q, q, seq_len, read_slot, k_cache, v
     """Read-slot attention over an 8-bit pool; with drop_none, SLOT_NONE entries are discarded keys."""
     st = lib().acache_slot_attention_q8(ctypes.byref(desc), batch, n_q, _p(q), seq_len, _p(read_slot), _p(k_cache),
                                         _p(v_cache), _p(kv_scale), num_slots, _p(out), int(bool(drop_none)),
-                                        _p(dev_status), _stream(stream))
+                                        _p(dev_status), _stream_of(k_cache, stream))
     return _check("acache_slot_attention_q8", st) if check else st
 
 
@@ -362,7 +374,7 @@ def acache_slot_attention_varlen_q8(desc, batch, q_start, max_q_rows, total_q_ro
     st = lib().acache_slot_attention_varlen_q8(ctypes.byref(desc), batch, _p(q_start), max_q_rows, total_q_rows,
                                                _p(q), _p(kv_start), max_seq_len, _p(read_slot), _p(k_cache),
                                                _p(v_cache), _p(kv_scale), num_slots, _p(out), int(bool(drop_none)),
-                                               _p(dev_status), _stream(stream))
+                                               _p(dev_status), _stream_of(k_cache, stream))
     return _check("acache_slot_attention_varlen_q8", st) if check else st
 
 
@@ -373,7 +385,7 @@ def acache_store_attend_q8(desc, batch, rows, write_slot, k_new, v_new, k_cache,
     st = lib().acache_store_attend_q8(ctypes.byref(desc), batch, rows, _p(write_slot), _p(k_new), _p(v_new),
                                       _p(k_cache), _p(v_cache), _p(kv_scale), num_slots, private_begin, n_q, _p(q),
                                       seq_len, _p(read_slot), _p(out), int(bool(drop_none)), _p(dev_status),
-                                      _stream(stream))
+                                      _stream_of(k_cache, stream))
     return _check("acache_store_attend_q8", st) if check else st
 
 

@@ -508,3 +508,11 @@ def test_the_whole_path_over_an_8_bit_pool():
         for b in range(w.batch):
             want, tol = attention(q[b], rs[b].cpu().numpy(), values(k, s[..., 0]), values(v, s[..., 1]), w.scale)
             assert_attention(o[b].double().cpu().numpy(), want, tol, f"request {b}")
+
+
+def test_a_tensor_off_the_current_device_is_refused():
+    args = _step(1, 5, 6, 4, 2, 128, BF16, 130, 1)
+    kc, vc, sc, ns, priv0, ws, rs, kn, vn, q = args
+    out = torch.empty(q.shape, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="current device"):
+        ac.acache_slot_attention_q8(_desc(4, 2, 128, BF16), 1, 6, dev(q), 130, dev(rs), kc, vc, sc, ns, out)

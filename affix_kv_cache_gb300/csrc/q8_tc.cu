@@ -197,6 +197,21 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
     int32_t* dev_status = p.dev_status;
     const long long budget = p.budget;
 
+    // Softmax warps: chain t, row r of its tile (= TMEM lane), the row of the block it works on, and that
+    // row's element offset in q and out.  The query rows are on their way during the set-up.  (Rows past
+    // the block read the block's first row; warps past it leave theirs unwritten: what they hold
+    // only reaches output rows that are never read.)
+    const int t = wg, r = threadIdx.x & 127;
+    const int row_of = split ? r : t * kBM + r;
+    const bool live = t < n_ch && row_of < n_rows;
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const uint32_t q_at = sQ(t & 1) + (uint32_t)((warp & 3) * 32 * D);
+    int64_t off = 0;
+    if (wg < 2) {
+        const int64_t pr = row0 + (row_of < n_rows ? row_of : 0), i = pr / p.g;
+        off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
+        if (warp_live) query_load<D>(p.q, off, q_at, q_at + G::kQPart, lane);
+    }
     if (threadIdx.x == 0) {
         const int readers = split ? 1 : n_qt;
         mbar_init(&ctl.q_full, 4u * n_qt);
@@ -427,7 +442,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             __syncwarp();
         } else {
             // ------------------------------------------------------------------ MMA issuers
-            const int t = warp - kMmaWarp;
+            const int t = warp - kMmaWarp;             // chain
             if (t < n_ch && lane == 0) {
                 constexpr uint32_t idS = idesc_e4m3(kBM, kStep);
                 const uint32_t idO = idesc_bf16(kBM, D, false, true);
@@ -482,30 +497,16 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         }
     } else {
         setmaxnreg_inc<kRegSoftmax>();
-        const int t = wg;                                  // chain
-        const int r = threadIdx.x - t * 128;               // row of the tile = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const int row_of = split ? r : t * kBM + r;        // row of the block this thread works on
-        const bool live = row_of < n_rows && t < n_ch;
-        // element offset of this thread's row in q and out
-        const int64_t off = [&] {
-            const int64_t pr = row0 + (row_of < n_rows ? row_of : 0), i = pr / p.g;
-            return ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
-        }();
-        const bool warp_live = __any_sync(0xffffffffu, live);
         float c_row = p.scale_log2;
         if (t < n_ch) {
-            // ---------------------------------------------------------------- query rows -> hi + lo
-            // (rows past the block read the block's first row; warps past it leave theirs unwritten:
-            // what they hold only reaches output rows that are never read)
             if (warp_live) {
-                const uint32_t at = sQ(t) + (uint32_t)((warp & 3) * 32 * D);
                 float* cr_at = &ctl.part_l[t * kBM + (warp & 3) * 32];      // (free until the end)
-                query_terms<D, 32>(p.q, off, at, at + G::kQPart, lane, p.scale_log2, 32, cr_at);
+                query_terms<D>(q_at, q_at + G::kQPart, lane, p.scale_log2, cr_at);
                 __syncwarp();
                 c_row = cr_at[lane];
             }
-            // a split block's chain B converts into the free query buffer: it needs the rows' powers of two
+            // a split block's chain B converted into the free query buffer: it needs the rows' factors
             if (!(split && t == 1)) {
                 fence_proxy_async_smem();
                 __syncwarp();

@@ -95,30 +95,37 @@ ACACHE_DEVFN uint32_t row_chunk(uint32_t r, uint32_t c) {
 template <int D>
 ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (uint32_t)((q ^ (r & (D / 4 - 1))) << 4); }
 
-// NR query rows (8, 16 or 32; the first n of them, rounded up to whole groups) -> two e4m3 terms each, by
-// one warp.  Lane i brings the element offset of row i; `hi` and `lo` are the shared-memory addresses
-// of row 0's terms (rows of D bytes, swizzled, row 0 a multiple of 8).  c_row[i] receives the factor of row i: its logits are S times the keys' factors times it
-// (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite, which is
-// carried as zeros).
-// The rows land by cp.async where their terms will be, the first half of a row in its row of hi, the
-// second in its row of lo: LPR lanes to a row, so the loads are whole rows.  GR groups of rows at a
-// time keep the chain load - maximum - convert - subtract - convert of several rows in flight.
-template <int D, int NR>
-ACACHE_DEVFN void query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, int lane, float scale_log2, int n,
-                              float* c_row) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = NR / RPI, GR = NI < 4 ? NI : 4;
+// 32 query rows -> two e4m3 terms each, by one warp, in two steps.  Lane i brings the element offset of row i;
+// `hi` and `lo` are the shared-memory addresses of row 0's terms (rows of D bytes, swizzled, row 0 a
+// multiple of 8).
+// First the rows land by cp.async where their terms will be, the first half of a row in its row of hi, the
+// second in its row of lo: LPR lanes to a row, so the loads are whole rows.
+template <int D>
+ACACHE_DEVFN void query_load(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, int lane) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;
     const uint32_t pc = (uint32_t)(lane % LPR), row = (uint32_t)(lane / LPR);
     const uint32_t at = (pc >= LPR / 2 ? lo : hi) + (pc % (LPR / 2)) * 16u + row * D;
 #pragma unroll 4
-    for (int it = 0; it < NI && it * RPI < n; ++it) {
+    for (int it = 0; it < NI; ++it) {
         const int64_t o = __shfl_sync(0xffffffffu, off, it * RPI + row);
         cp_async16(at + (uint32_t)(it * RPI * D), q + o + pc * 8, 16);
     }
     cp_async_commit();
+}
+// Then the terms, in place.  c_row[i] receives the factor of row i: its logits are S times the keys' factors
+// times it (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite,
+// which is carried as zeros).  GR groups of rows at a time keep the chain load - maximum - convert -
+// subtract - convert of several rows in flight.  The scaled elements are carried in f16: exact down to
+// 2^-22 of the row's largest, below that off by less than the low term's own last place.
+template <int D>
+ACACHE_DEVFN void query_terms(uint32_t hi, uint32_t lo, int lane, float scale_log2, float* c_row) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI, GR = 4;
+    const uint32_t pc = (uint32_t)(lane % LPR), row = (uint32_t)(lane / LPR);
+    const uint32_t at = (pc >= LPR / 2 ? lo : hi) + (pc % (LPR / 2)) * 16u + row * D;
     cp_async_wait<0>();
     __syncwarp();
 #pragma unroll 1
-    for (int g = 0; g < NI / GR && g * GR * RPI < n; ++g) {
+    for (int g = 0; g < NI / GR; ++g) {
         uint32_t w[GR][4], top[GR];
 #pragma unroll
         for (int u = 0; u < GR; ++u) ld_shared_v4(at + (uint32_t)((g * GR + u) * RPI * D), w[u]);
@@ -137,21 +144,27 @@ ACACHE_DEVFN void query_terms(const bf16* q, int64_t off, uint32_t hi, uint32_t 
             const uint32_t r = (uint32_t)((g * GR + u) * RPI) + row;
             const uint32_t E = max(top[u] >> 7, 8u);              // biased exponent of the row's largest
             const bool finite = E != 255u;
-            const float up = finite ? __uint_as_float((261u - E) << 23) : 0.f;      // 2^(134 - E): largest in [128, 256)
+            const uint32_t keep = finite ? 0xffffffffu : 0u;
+            const uint32_t up2 = (261u - E) << 7 | (261u - E) << 23;              // 2^(134 - E) in bf16: largest in [128, 256)
             if (pc == 0) c_row[r] = finite ? scale_log2 * __uint_as_float((E - 7u) << 23) : __uint_as_float(0x7fffffffu);
-            uint32_t h[4], l[4];
+            uint32_t h[2], l[2];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const float a = finite ? __uint_as_float(w[u][y] << 16) * up : 0.f;
-                const float d = finite ? __uint_as_float(w[u][y] & 0xffff0000u) * up : 0.f;
-                h[y] = q8_encode2(a, d);
-                const float2 hf = q8_decode2(h[y]);
-                l[y] = q8_encode2(a - hf.x, d - hf.y);
+                uint32_t x, f, back;
+                unsigned short t;
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[u][y] & keep), "r"(up2));
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(f));
+                h[y >> 1] = (y & 1) ? h[y >> 1] | (uint32_t)t << 16 : t;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(t));
+                asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(f) : "r"(f), "r"(back));
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(f));
+                l[y >> 1] = (y & 1) ? l[y >> 1] | (uint32_t)t << 16 : t;
             }
             // (the shuffles ordered the rows' reads before these writes)
             const uint32_t o = row_chunk<D>(r, pc >> 1) + (pc & 1u) * 8u;
-            st_shared_v2(hi + o, h[0] | h[1] << 16, h[2] | h[3] << 16);
-            st_shared_v2(lo + o, l[0] | l[1] << 16, l[2] | l[3] << 16);
+            st_shared_v2(hi + o, h[0], h[1]);
+            st_shared_v2(lo + o, l[0], l[1]);
         }
     }
 }

@@ -193,6 +193,12 @@ ACACHE_DEVFN void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uin
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// True in one lane of the (converged) warp.
+ACACHE_DEVFN bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
 // Arrive once on `bar` when every MMA issued so far by this thread has completed.
 ACACHE_DEVFN void umma_commit(uint64_t* bar) {
     asm volatile(

@@ -208,11 +208,11 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
     const uint32_t q_at = sQ(t & 1) + (uint32_t)((warp & 3) * 32 * D);
     int64_t off = 0;
     if (wg < 2) {
-        const int64_t pr = row0 + (row_of < n_rows ? row_of : 0), i = pr / p.g;
-        off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
+        const uint32_t pr = (uint32_t)row0 + (row_of < n_rows ? row_of : 0), i = pr / (uint32_t)p.g;   // (below 2^24)
+        off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D;
         if (warp_live) query_load<D>(p.q, off, q_at, q_at + G::kQPart, lane);
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32 * (kMmaWarp + 1)) {
         const int readers = split ? 1 : n_qt;
         mbar_init(&ctl.q_full, 4u * n_qt);
         for (int s = 0; s < G::kKSt; ++s) {
@@ -226,7 +226,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         for (int t = 0; t < kQT; ++t) {
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&ctl.s_full[t][h], 1);
-                mbar_init(&ctl.p_full[t][h], 128);
+                mbar_init(&ctl.p_full[t][h], 4);
             }
             mbar_init(&ctl.pv_done[t], 1);
             mbar_init(&ctl.drain[t], 1);
@@ -442,51 +442,60 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             __syncwarp();
         } else {
             // ------------------------------------------------------------------ MMA issuers
-            const int t = warp - kMmaWarp;             // chain
-            if (t < n_ch && lane == 0) {
+            // The whole warp walks the steps, so addresses and descriptors stay in uniform registers, and
+            // one lane issues: with the walk inside a one-lane branch each MMA took some 80 cycles to issue.
+            const int t = __shfl_sync(0xffffffffu, warp, 0) - kMmaWarp;         // chain
+            if (t < n_ch) {
+                const bool leader = elect_one();
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
                 constexpr uint32_t idS = idesc_e4m3(kBM, kStep);
                 const uint32_t idO = idesc_bf16(kBM, D, false, true);
-                const uint32_t d_s = tmem + col_s(t), d_o = tmem + col_o(t);
+                const uint32_t d_s = tm + col_s(t), d_o = tm + col_o(t);
                 const uint64_t dq = sdesc_rows<D>(sQ(split ? 0 : t));
                 const int n_st = sch.n_steps(t, last_keys);
+                auto wait = [&](uint64_t* bar, int phase) {
+                    return __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)phase & 1u, abort_flag, dev_status, budget));
+                };
                 // step u: half u & 1 of the chain's tile u / 2, into S buffer u & 1
                 auto issue_s = [&](int u) -> bool {
                     const int e = sch.entry(t, u >> 1), h = u & 1;
-                    if (h == 0 && !wait_bar(&ctl.k_full[e % G::kKSt], (e / G::kKSt) & 1, abort_flag, dev_status, budget))
-                        return false;
+                    if (h == 0 && !wait(&ctl.k_full[e % G::kKSt], e / G::kKSt)) return false;
                     tc_fence_after();
                     const uint64_t dk = sdesc_rows<D>(sK(e % G::kKSt) + (uint32_t)(h * kStep * D));
+                    if (leader) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)                    // hi, lo
+                        for (int x = 0; x < 2; ++x)                // hi, lo
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k)
-                            umma_ss_f8(d_s + h * kStep, dq + (uint64_t)((x * G::kQPart + k * 32) >> 4),
-                                       dk + (uint64_t)(k * 32 >> 4), idS, x > 0 || k > 0);
-                    umma_commit(&ctl.s_full[t][h]);
-                    if (h == 1 || u + 1 == n_st) umma_commit(&ctl.k_empty[e % G::kKSt]);
+                            for (int k = 0; k < D / 32; ++k)
+                                umma_ss_f8(d_s + h * kStep, dq + (uint64_t)((x * G::kQPart + k * 32) >> 4),
+                                           dk + (uint64_t)(k * 32 >> 4), idS, x > 0 || k > 0);
+                        umma_commit(&ctl.s_full[t][h]);
+                        if (h == 1 || u + 1 == n_st) umma_commit(&ctl.k_empty[e % G::kKSt]);
+                    }
                     return true;
                 };
-                bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget);
+                bool ok = wait(&ctl.q_full, 0);
                 for (int u = 0; ok && u < 2 && u < n_st; ++u) ok = issue_s(u);
                 // PV of step u once its P is in TMEM, then S of step u + 2 into the buffer P came from
                 // (MMAs of one thread run in issue order); S of step u + 1 is there already, so the
                 // softmax never waits for it.
                 for (int u = 0; ok && u < n_st; ++u) {
                     const int e = sch.entry(t, u >> 1), h = u & 1;
-                    ok = (h == 1 || wait_bar(&ctl.v_full[e % G::kVSt], (e / G::kVSt) & 1, abort_flag, dev_status, budget)) &&
-                         wait_bar(&ctl.p_full[t][h], (u >> 1) & 1, abort_flag, dev_status, budget);
+                    ok = (h == 1 || wait(&ctl.v_full[e % G::kVSt], e / G::kVSt)) && wait(&ctl.p_full[t][h], u >> 1);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t dv = sdesc_sw128(sV(e % G::kVSt) + (uint32_t)(h * kStep * 128), G::kRegion, 1024);
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < kStep / 16; ++k)
-                        umma_ts(d_o, d_s + h * kStep + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (u > 0 || k > 0));
-                    umma_commit(&ctl.pv_done[t]);
-                    if (h == 1 || u + 1 == n_st) umma_commit(&ctl.v_empty[e % G::kVSt]);
+                        for (int k = 0; k < kStep / 16; ++k)
+                            umma_ts(d_o, d_s + h * kStep + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (u > 0 || k > 0));
+                        umma_commit(&ctl.pv_done[t]);
+                    }
                     if (u + 2 < n_st) ok = issue_s(u + 2);
+                    if (leader && (h == 1 || u + 1 == n_st)) umma_commit(&ctl.v_empty[e % G::kVSt]);
                 }
                 // no MMA may still run when TMEM is released
-                umma_commit(&ctl.drain[t]);
+                if (leader) umma_commit(&ctl.drain[t]);
                 mbar_wait(&ctl.drain[t], 0, kDrainBudget);
             }
             __syncwarp();
@@ -500,12 +509,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         float c_row = p.scale_log2;
         if (t < n_ch) {
-            if (warp_live) {
-                float* cr_at = &ctl.part_l[t * kBM + (warp & 3) * 32];      // (free until the end)
-                query_terms<D>(q_at, q_at + G::kQPart, lane, p.scale_log2, cr_at);
-                __syncwarp();
-                c_row = cr_at[lane];
-            }
+            if (warp_live) c_row = query_terms<D>(q_at, q_at + G::kQPart, lane, p.scale_log2);
             // a split block's chain B converted into the free query buffer: it needs the rows' factors
             if (!(split && t == 1)) {
                 fence_proxy_async_smem();
@@ -534,7 +538,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 tc_fence_after();
                 if (!warp_live) {
                     // rows past the block: whatever P holds only reaches rows that are never read
-                    mbar_arrive(&ctl.p_full[t][h]);
+                    if (lane == 0) mbar_arrive(&ctl.p_full[t][h]);
                     continue;
                 }
                 const uint32_t s_at = lane_base + col_s(t) + (uint32_t)(h * kStep);
@@ -627,7 +631,8 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 l_sum = l_sum * alpha + ((l0 + l1) + (l2 + l3));
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&ctl.p_full[t][h]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_full[t][h]);
             }
             if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget));
         }
@@ -654,12 +659,11 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             }
         }
         auto load_o = [&](int cc, uint32_t (&o)[32]) {
+            uint32_t ob[32];
             tmem_ld32(lane_base + col_o(t) + cc * 32, o);
+            if (split) tmem_ld32(lane_base + col_o(1) + cc * 32, ob);
             tmem_ld_wait();
             if (split) {
-                uint32_t ob[32];
-                tmem_ld32(lane_base + col_o(1) + cc * 32, ob);
-                tmem_ld_wait();
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
                     o[x] = __float_as_uint(fmaf(__uint_as_float(o[x]), w_a, __uint_as_float(ob[x]) * w_b));
@@ -755,8 +759,8 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                         }
                     }
                     const float inv = L == 0.f ? 0.f : kUnshift / L;
-                    const int64_t i = (row0 + rr) / p.g;
-                    bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (row0 + rr - i * p.g)) * D + c4 * 32;
+                    const uint32_t pr = (uint32_t)(row0 + rr), i = pr / (uint32_t)p.g;
+                    bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D + c4 * 32;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         uint32_t k[4];

@@ -47,14 +47,6 @@ ACACHE_DEVFN uint64_t f2mul(uint64_t a, uint64_t b) {
 ACACHE_DEVFN void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-ACACHE_DEVFN void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
-ACACHE_DEVFN uint64_t f2sub(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 // D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit float inputs, fp32 accumulate
 ACACHE_DEVFN void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -62,15 +54,6 @@ ACACHE_DEVFN void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, 
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// The same with A in TMEM (four elements to a 32-bit column)
-ACACHE_DEVFN void umma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // e4m3 A and B (format 0), fp32 D, K-major operands
@@ -95,78 +78,77 @@ ACACHE_DEVFN uint32_t row_chunk(uint32_t r, uint32_t c) {
 template <int D>
 ACACHE_DEVFN uint32_t part_off(int r, int q) { return (uint32_t)r * (D * 4u) + (uint32_t)((q ^ (r & (D / 4 - 1))) << 4); }
 
-// 32 query rows -> two e4m3 terms each, by one warp, in two steps.  Lane i brings the element offset of row i;
-// `hi` and `lo` are the shared-memory addresses of row 0's terms (rows of D bytes, swizzled, row 0 a
-// multiple of 8).
+// 32 query rows -> two e4m3 terms each, by one warp, in two steps.  `hi` and `lo` are the shared-memory
+// addresses of row 0's terms (rows of D bytes, swizzled, row 0 a multiple of 8).
 // First the rows land by cp.async where their terms will be, the first half of a row in its row of hi, the
-// second in its row of lo: LPR lanes to a row, so the loads are whole rows.
+// second in its row of lo.  Lane i brings the element offset of row i; D / 8 lanes to a row, so the loads
+// are whole rows.
 template <int D>
 ACACHE_DEVFN void query_load(const bf16* q, int64_t off, uint32_t hi, uint32_t lo, int lane) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;
+    constexpr int LPR = D / 8, RPI = 32 / LPR;
     const uint32_t pc = (uint32_t)(lane % LPR), row = (uint32_t)(lane / LPR);
-    const uint32_t at = (pc >= LPR / 2 ? lo : hi) + (pc % (LPR / 2)) * 16u + row * D;
+    const uint32_t to = pc >= LPR / 2 ? lo : hi;
 #pragma unroll 4
-    for (int it = 0; it < NI; ++it) {
-        const int64_t o = __shfl_sync(0xffffffffu, off, it * RPI + row);
-        cp_async16(at + (uint32_t)(it * RPI * D), q + o + pc * 8, 16);
+    for (int it = 0; it < 32 / RPI; ++it) {
+        const uint32_t r = (uint32_t)(it * RPI) + row;
+        const int64_t o = __shfl_sync(0xffffffffu, off, (int)r);
+        cp_async16(to + row_chunk<D>(r, pc % (LPR / 2)), q + o + pc * 8, 16);
     }
     cp_async_commit();
 }
-// Then the terms, in place.  c_row[i] receives the factor of row i: its logits are S times the keys' factors
-// times it (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite,
-// which is carried as zeros).  GR groups of rows at a time keep the chain load - maximum - convert -
-// subtract - convert of several rows in flight.  The scaled elements are carried in f16: exact down to
-// 2^-22 of the row's largest, below that off by less than the low term's own last place.
+// Two pairs of bf16, each below 2^-111, to the four e4m3 codes of 2^120 times them, cut to e4m3's last place:
+// a bf16 of that range has e4m3's exponent (or its subnormal form) 4 bits higher.
+ACACHE_DEVFN uint32_t cut_codes(uint32_t a, uint32_t b) {
+    uint32_t m, s;
+    asm("prmt.b32 %0, %1, %2, 0x6420;" : "=r"(m) : "r"(a >> 4), "r"(b >> 4));
+    asm("prmt.b32 %0, %1, %2, 0x7531;" : "=r"(s) : "r"(a), "r"(b));
+    return (m & 0x7f7f7f7fu) | (s & 0x80808080u);
+}
+// Then the terms, in place, row `lane` by its lane: whole rows pass through its registers, so the row's
+// largest needs no exchange.  Returns the row's factor: its logits are S times the keys' factors times it
+// (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite, which is
+// carried as zeros).  The factor stays a normal number: a logit that the raise would change is below
+// 2^-60, and 0 times a masked key's -infinity would be NaN.
+// hi is q' cut to 4 significant bits and lo the rest, rounded to e4m3's subnormal step where it is longer.
 template <int D>
-ACACHE_DEVFN void query_terms(uint32_t hi, uint32_t lo, int lane, float scale_log2, float* c_row) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI, GR = 4;
-    const uint32_t pc = (uint32_t)(lane % LPR), row = (uint32_t)(lane / LPR);
-    const uint32_t at = (pc >= LPR / 2 ? lo : hi) + (pc % (LPR / 2)) * 16u + row * D;
+ACACHE_DEVFN float query_terms(uint32_t hi, uint32_t lo, int lane, float scale_log2) {
+    constexpr int NC = D / 8;                                 // 16-byte pieces of a bf16 row
     cp_async_wait<0>();
-    __syncwarp();
-#pragma unroll 1
-    for (int g = 0; g < NI / GR; ++g) {
-        uint32_t w[GR][4], top[GR];
+    __syncwarp();                                             // (a row's pieces came by several lanes' copies)
+    uint32_t w[NC][4], top = 0;
 #pragma unroll
-        for (int u = 0; u < GR; ++u) ld_shared_v4(at + (uint32_t)((g * GR + u) * RPI * D), w[u]);
+    for (int c = 0; c < NC; ++c) {
+        ld_shared_v4((c < NC / 2 ? hi : lo) + row_chunk<D>(lane, c % (NC / 2)), w[c]);
 #pragma unroll
-        for (int u = 0; u < GR; ++u) {
-            top[u] = __vmaxu2(__vmaxu2(w[u][0] & 0x7fff7fffu, w[u][1] & 0x7fff7fffu),
-                              __vmaxu2(w[u][2] & 0x7fff7fffu, w[u][3] & 0x7fff7fffu));
-            top[u] = max(top[u] & 0xffffu, top[u] >> 16);
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int u = 0; u < GR; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
-#pragma unroll
-        for (int u = 0; u < GR; ++u) {
-            const uint32_t r = (uint32_t)((g * GR + u) * RPI) + row;
-            const uint32_t E = max(top[u] >> 7, 8u);              // biased exponent of the row's largest
-            const bool finite = E != 255u;
-            const uint32_t keep = finite ? 0xffffffffu : 0u;
-            const uint32_t up2 = (261u - E) << 7 | (261u - E) << 23;              // 2^(134 - E) in bf16: largest in [128, 256)
-            if (pc == 0) c_row[r] = finite ? scale_log2 * __uint_as_float((E - 7u) << 23) : __uint_as_float(0x7fffffffu);
-            uint32_t h[2], l[2];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                uint32_t x, f, back;
-                unsigned short t;
-                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[u][y] & keep), "r"(up2));
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
-                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(f));
-                h[y >> 1] = (y & 1) ? h[y >> 1] | (uint32_t)t << 16 : t;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(t));
-                asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(f) : "r"(f), "r"(back));
-                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(f));
-                l[y >> 1] = (y & 1) ? l[y >> 1] | (uint32_t)t << 16 : t;
-            }
-            // (the shuffles ordered the rows' reads before these writes)
-            const uint32_t o = row_chunk<D>(r, pc >> 1) + (pc & 1u) * 8u;
-            st_shared_v2(hi + o, h[0], h[1]);
-            st_shared_v2(lo + o, l[0], l[1]);
-        }
+        for (int y = 0; y < 4; ++y) top = __vmaxu2(top, w[c][y] & 0x7fff7fffu);
     }
+    top = max(top & 0xffffu, top >> 16);
+    const uint32_t E = max(top >> 7, 8u);                     // biased exponent of the row's largest
+    const bool finite = E != 255u;
+    const uint32_t keep = finite ? 0xffffffffu : 0u;
+    const uint32_t up2 = (261u - E) << 7 | (261u - E) << 23;  // 2^(134 - E), twice: the largest goes to [128, 256)
+    constexpr uint32_t kDown2 = 0x03800380u;                  // 2^-120, twice
+#pragma unroll
+    for (int c = 0; c < NC; c += 2) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int y = 0; y < 8; y += 2) {
+            uint32_t x[2], r[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t v = w[c + (y >> 2)][(y & 3) + j] & keep;
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x[j]) : "r"(v), "r"(up2));
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x[j]) : "r"(x[j]), "r"(kDown2));
+                asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r[j]) : "r"(x[j]), "r"(x[j] & 0xfff0fff0u));
+            }
+            h[y >> 1] = cut_codes(x[0], x[1]);
+            l[y >> 1] = cut_codes(r[0] + 0x00080008u, r[1] + 0x00080008u);
+        }
+        const uint32_t o = row_chunk<D>(lane, c >> 1);
+        st_shared_v4(hi + o, h[0], h[1], h[2], h[3]);
+        st_shared_v4(lo + o, l[0], l[1], l[2], l[3]);
+    }
+    return finite ? fmaxf(scale_log2 * __uint_as_float((E - 7u) << 23), 0x1p-126f) : __uint_as_float(0x7fffffffu);
 }
 
 }  // namespace q8

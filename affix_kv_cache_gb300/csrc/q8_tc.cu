@@ -108,7 +108,6 @@ struct Ctl {
     uint64_t s_full[kQT][2], p_full[kQT][2];   // by step parity
     uint64_t pv_done[kQT];             // phase u: PV of step u is complete
     uint64_t drain[kQT];
-    uint64_t f_full[kFSt];             // the keys' factors of a ring entry are in `factor`
     uint32_t tmem_base;
     int abort, unlanded;
     uint32_t drop[kFSt][4];            // discarded keys, 32 per word
@@ -216,7 +215,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         const int readers = split ? 1 : n_qt;
         mbar_init(&ctl.q_full, 4u * n_qt);
         for (int s = 0; s < G::kKSt; ++s) {
-            mbar_init(&ctl.k_full[s], kProd);
+            mbar_init(&ctl.k_full[s], 1 + kProd);       // the bytes, and each producer's factors
             mbar_init(&ctl.k_empty[s], readers);
         }
         for (int s = 0; s < G::kVSt; ++s) {
@@ -231,7 +230,6 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             mbar_init(&ctl.pv_done[t], 1);
             mbar_init(&ctl.drain[t], 1);
         }
-        for (int s = 0; s < kFSt; ++s) mbar_init(&ctl.f_full[s], kProd);
         ctl.abort = 0;
         ctl.unlanded = 0;
         ctl.failed = 0.f;
@@ -405,9 +403,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 if (e >= G::kKSt && !__all_sync(0xffffffffu, wait_bar<true>(&ctl.k_empty[s], ((e / G::kKSt) - 1) & 1,
                                                                        abort_flag, dev_status, budget)))
                     break;
-                // both warps arrive for every entry, so neither can get a phase ahead of the other
                 if (leader) mbar_arrive_expect_tx(&ctl.k_full[s], G::kKTile);
-                else if (lane == 0) mbar_arrive(&ctl.k_full[s]);
                 armed = e;
                 __syncwarp();
                 if (box) {
@@ -424,8 +420,12 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                     *reinterpret_cast<float4*>(&ctl.factor[fs][4 * x]) =
                         make_float4(q8_factor(sc[0]), q8_factor(sc[1]), q8_factor(sc[2]), q8_factor(sc[3]));
                 if (kDrop && pi == 0 && (lane & 7) == 0) ctl.drop[fs][lane >> 3] = gone;
+                // Both warps arrive for every entry, so neither can get a phase ahead of the other.  The
+                // softmax reads the factors on the strength of S: its MMAs are issued after this arrival
+                // was seen, so their completion comes after these writes.  (With a barrier of the
+                // factors' own, the wait for it cost 7 % of a long call.)
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.f_full[fs]);
+                if (lane == 0) mbar_arrive(&ctl.k_full[s]);
                 if (e + 1 < n_kv) {
                     box = resolve(raw, rows, slot0, gone);
                     load_scales(rows, sc);
@@ -524,15 +524,6 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             const int n_st = sch.n_steps(t, last_keys);
             for (int u = 0; u < n_st; ++u) {
                 const int e = sch.entry(t, u >> 1), h = u & 1, fs = e % kFSt;
-                if (h == 0) {
-                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.f_full[fs], (e / kFSt) & 1, abort_flag, dev_status, budget));
-                    if (!ok) break;
-                }
-                // the keys' factors, on their way while S is waited for
-                uint32_t f[kStep / 4][4];
-#pragma unroll
-                for (int x = 0; x < kStep / 4; ++x)
-                    ld_shared_v4(smem_u32(&ctl.factor[fs][0]) + (uint32_t)(h * kStep + 4 * x) * 4u, f[x]);
                 ok = __all_sync(0xffffffffu, wait_bar(&ctl.s_full[t][h], (u >> 1) & 1, abort_flag, dev_status, budget));
                 if (!ok) break;
                 tc_fence_after();
@@ -545,6 +536,11 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 uint32_t v[2][32];
                 tmem_ld32(s_at, v[0]);
                 tmem_ld32(s_at + 32, v[1]);
+                // the keys' factors
+                uint32_t f[kStep / 4][4];
+#pragma unroll
+                for (int x = 0; x < kStep / 4; ++x)
+                    ld_shared_v4(smem_u32(&ctl.factor[fs][0]) + (uint32_t)(h * kStep + 4 * x) * 4u, f[x]);
                 tmem_ld_wait();
                 // logits in units of c_row: S times the keys' factors
 #pragma unroll

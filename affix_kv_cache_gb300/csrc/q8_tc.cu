@@ -59,8 +59,15 @@ constexpr int kProdWarp = 10, kProd = 2;    // K producer warps
 constexpr int kConvWarp = 12, kConv = 4;    // V converter warps
 constexpr int kThreads = 512;
 // Registers: 512 x 128 at launch = 65536; 2 x 128 x 168 + 128 x 56 + 128 x 120 = 65536.
-constexpr int kRegSoftmax = 168, kRegIssue = 56, kRegConv = 120;
-static_assert(2 * 128 * kRegSoftmax + 128 * kRegIssue + 128 * kRegConv <= kThreads * 128, "register split");
+// Registers per thread of the warpgroups.  The producers of a call with discarded keys carry their masks:
+// with 56 they spill, and a long ragged batch takes 76 us instead of 72.
+constexpr int kRegSoftmax = 168;
+template <bool kDrop>
+constexpr int kRegIssue = kDrop ? 64 : 56;
+template <bool kDrop>
+constexpr int kRegConv = kDrop ? 112 : 120;
+constexpr int kRegSum = 2 * kRegSoftmax + kRegIssue<true> + kRegConv<true>;
+static_assert(kRegSum == 2 * kRegSoftmax + kRegIssue<false> + kRegConv<false> && 128 * kRegSum <= kThreads * 128, "register split");
 constexpr uint32_t kTmemCols = 512;         // two S buffers of 64 columns per chain, O_A, O_B
 __host__ __device__ constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + (uint32_t)t * 128u; }
@@ -245,7 +252,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
     const uint32_t tmem = ctl.tmem_base;
 
     if (wg == 3) {
-        setmaxnreg_dec<kRegConv>();
+        setmaxnreg_dec<kRegConv<kDrop>>();
         // ------------------------------------------------------------------ V converters
         constexpr int CPR = D / 16;                  // 16-byte pieces per pool row
         constexpr int RPI = 32 / CPR;                // rows per warp load
@@ -334,7 +341,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             cluster_sync();
         }
     } else if (wg == 2) {
-        setmaxnreg_dec<kRegIssue>();
+        setmaxnreg_dec<kRegIssue<kDrop>>();
         if (warp >= kProdWarp) {
             // -------------------------------------------------------------- K producers
             const int pi = warp - kProdWarp;
@@ -568,63 +575,71 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                         }
                     }
                 }
-                float mx[4];
+                auto row_max = [&]() {
+                    float mx[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t* y = &v[q >> 1][(q & 1) * 16];
-                    mx[q] = max3f(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t* y = &v[q >> 1][(q & 1) * 16];
+                        mx[q] = max3f(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
 #pragma unroll
-                    for (int x = 3; x < 15; x += 2) mx[q] = max3f(mx[q], __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
-                    mx[q] = fmaxf(mx[q], __uint_as_float(y[15]));
-                }
-                const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c_row;
-                float alpha = 1.f;
-                bool resc = false;
-                if (u == 0) {
-                    m_used = mt;
-                } else if (mt > m_used + kRescaleThreshold) {
-                    alpha = fast_exp2(m_used - mt);
-                    m_used = mt;
-                    resc = true;
-                }
-                if (__any_sync(0xffffffffu, resc)) {
-                    // O holds the steps before this one once PV of the last is complete
-                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.pv_done[t], (u - 1) & 1, abort_flag, dev_status, budget));
-                    if (!ok) break;
-                    tc_fence_after();
+                        for (int x = 3; x < 15; x += 2) mx[q] = max3f(mx[q], __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
+                        mx[q] = fmaxf(mx[q], __uint_as_float(y[15]));
+                    }
+                    return max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c_row;
+                };
+                // P of the step against m_used, over S; returns its sum
+                auto exponentiate = [&]() {
+                    // a row whose keys so far were all discarded exponentiates against 0
+                    const float ms = (kDrop && m_used == -INFINITY) ? 0.f : m_used;
+                    const uint64_t c2 = f2pack(c_row, c_row), nm2 = f2pack(-ms, -ms);
+                    uint64_t ls2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            float x0, x1;
+                            f2unpack(f2fma(f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1])), c2, nm2), x0, x1);
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                            ls2[(x >> 1) & 1] = f2add(ls2[(x >> 1) & 1], f2pack(p0, p1));
+                            __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
+                            pk[x >> 1] = *reinterpret_cast<uint32_t*>(&two);
+                        }
+                        tmem_st16(s_at + cc * 16, pk);
+                    }
+                    float l0, l1, l2, l3;
+                    f2unpack(ls2[0], l0, l1);
+                    f2unpack(ls2[1], l2, l3);
+                    return (l0 + l1) + (l2 + l3);
+                };
+                // P is taken against the maximum so far while this step's is found; only where that has
+                // grown past the threshold are O and the sum rescaled and P taken again.
+                if (u == 0) m_used = row_max();
+                float sum = exponentiate();
+                const float mt = row_max();
+                const bool grown = mt > m_used + kRescaleThreshold;
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float alpha = grown ? fast_exp2(m_used - mt) : 1.f;
+                    if (grown) m_used = mt;
+                    if (u > 0) {
+                        // O holds the steps before this one once PV of the last is complete
+                        ok = __all_sync(0xffffffffu, wait_bar(&ctl.pv_done[t], (u - 1) & 1, abort_flag, dev_status, budget));
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int q = 0; q < D / 8; ++q) {
-                        uint32_t o[8];
-                        tmem_ld8(lane_base + col_o(t) + q * 8, o);
-                        tmem_ld_wait();
+                        for (int q = 0; q < D / 8; ++q) {
+                            uint32_t o[8];
+                            tmem_ld8(lane_base + col_o(t) + q * 8, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                        tmem_st8(lane_base + col_o(t) + q * 8, o);
+                            for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                            tmem_st8(lane_base + col_o(t) + q * 8, o);
+                        }
+                        l_sum *= alpha;
                     }
-                    tmem_st_wait();
+                    sum = exponentiate();
                 }
-                // a row whose keys so far were all discarded exponentiates against 0
-                const float ms = (kDrop && m_used == -INFINITY) ? 0.f : m_used;
-                const uint64_t c2 = f2pack(c_row, c_row), nm2 = f2pack(-ms, -ms);
-                uint64_t ls2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-#pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        float x0, x1;
-                        f2unpack(f2fma(f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1])), c2, nm2), x0, x1);
-                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                        ls2[(x >> 1) & 1] = f2add(ls2[(x >> 1) & 1], f2pack(p0, p1));
-                        __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
-                        pk[x >> 1] = *reinterpret_cast<uint32_t*>(&two);
-                    }
-                    tmem_st16(s_at + cc * 16, pk);
-                }
-                float l0, l1, l2, l3;
-                f2unpack(ls2[0], l0, l1);
-                f2unpack(ls2[1], l2, l3);
-                l_sum = l_sum * alpha + ((l0 + l1) + (l2 + l3));
+                l_sum += sum;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -801,7 +816,7 @@ int prepare() {
         return ACACHE_ERR_CUDA;   // not cached: a later call may succeed
     }
     // the register split assumes the launch allocation; refuse to launch otherwise
-    const int rc = fa.numRegs * kThreads < 2 * 128 * kRegSoftmax + 128 * kRegIssue + 128 * kRegConv ? ACACHE_ERR_UNSUPPORTED
+    const int rc = fa.numRegs * kThreads < 128 * kRegSum ? ACACHE_ERR_UNSUPPORTED
                                                                                                  : ACACHE_OK;
     st.store(rc == ACACHE_OK ? 1 : rc, std::memory_order_release);
     return rc;

@@ -15,21 +15,18 @@ using bf16 = __nv_bfloat16;
 constexpr int kNoKey = INT32_MIN;           // read-slot entry of a key past the request's last
 constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles, abort path
 
-// Bounded wait for a phase.  A try that finds the phase incomplete suspends the warp for some 90 cycles;
-// what it issues between tries is taken from the working warps' slots.  kSlack: the waiter runs a
-// ring's depth ahead, so it sleeps between tries instead.
-template <bool kSlack = false>
+// Bounded wait for a phase.  A try that finds the phase incomplete suspends the warp until it completes, for
+// some 7,900 cycles at most (whatever limit it is given), so a loop of tries takes nothing from the
+// working warps.  kPolls (the rings' producers, which run ahead): a budget below that is kept by polling.
+constexpr long long kTryCycles = 1 << 13;
+template <bool kPolls = false>
 ACACHE_DEVFN bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_status,
                            long long budget) {
-    if (mbar_try_wait(bar, parity)) return true;
+    const bool poll = kPolls && budget < kTryCycles;
+    if (!poll && mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
-        if (kSlack) __nanosleep(100);
-        if (mbar_try_wait(bar, parity)) return true;
-        if (!kSlack) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if (mbar_try_wait(bar, parity)) return true;
-        }
+        if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (clock64() - t0 > budget) {
             *abort_flag = 1;
@@ -46,6 +43,12 @@ ACACHE_DEVFN uint64_t f2mul(uint64_t a, uint64_t b) {
 }
 ACACHE_DEVFN void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 32 bytes to a 32-byte aligned address
+ACACHE_DEVFN void st_global_v8(void* to, const uint32_t (&k)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(k[0]), "r"(k[1]), "r"(k[2]), "r"(k[3]),
+                 "r"(k[4]), "r"(k[5]), "r"(k[6]), "r"(k[7])
+                 : "memory");
 }
 // D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit float inputs, fp32 accumulate
 ACACHE_DEVFN void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {

@@ -293,6 +293,128 @@ def test_any_finite_softmax_scale(scale):
     assert_attention(out[0].double().cpu().numpy(), want, tol)
 
 
+@pytest.mark.parametrize("scale", [1e-10, 1e-30, 1e-42])
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("n_q", [1, 50, 300])
+def test_tiny_scales_and_empty_query_rows(dtype, d, n_q, scale):
+    """Every logit is next to zero, however small the factor that makes it so; masked keys stay out."""
+    hq, hkv, T = 2, 1, 100
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(1, n_q, hq, hkv, d, dtype, T, True, 13)
+    q[0, 0, 0], q[0, -1, 1] = 0.0, 1e-37
+    rs[0, :70] = -1
+    rs[0, 71] = 5
+    out = torch.empty(q.shape, dtype=dtype, device="cuda")
+    ac.acache_slot_attention_q8(_desc(hq, hkv, d, dtype, scale), 1, n_q, dev(q), T, dev(rs), dev(kc), dev(vc), dev(sc), ns, out,
+                                drop_none=True)
+    want, tol = attention(q[0], rs[0].numpy(), kv, vv, scale, True)
+    assert_attention(out[0].double().cpu().numpy(), want, tol)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("n_q", [1, 40, 300])
+def test_buffers_at_odd_16_byte_addresses(dtype, d, n_q):
+    """16 bytes is all the alignment that is asked for, and nothing before or behind a buffer is written."""
+    B, hq, hkv, T = 2, 4, 2, 333
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(B, n_q, hq, hkv, d, dtype, T, False, 17)
+
+    def at16(x, fill=0):
+        lead = 16 // x.element_size()
+        room = torch.full((x.numel() + 2 * lead,), fill, dtype=x.dtype, device="cuda")
+        assert room.data_ptr() % 32 == 0
+        view = room[lead:lead + x.numel()].view(x.shape)
+        view.copy_(x)
+        return view, room
+
+    (gq, _), (gk, _), (gv, _) = at16(q), at16(kc), at16(vc)
+    out, room = at16(torch.zeros_like(q), fill=7)
+    ac.acache_slot_attention_q8(_desc(hq, hkv, d, dtype), B, n_q, gq, T, dev(rs), gk, gv, dev(sc), ns, out)
+    lead = 16 // q.element_size()
+    assert (room[:lead] == 7).all() and (room[-lead:] == 7).all()
+    for b in range(B):
+        want, tol = attention(q[b], rs[b].numpy(), kv, vv, d ** -0.5)
+        assert_attention(out[b].double().cpu().numpy(), want, tol)
+    ko, kroom = at16(torch.zeros((B, T, hkv, d), dtype=dtype), fill=7)
+    vo, vroom = at16(torch.zeros((B, T, hkv, d), dtype=dtype), fill=7)
+    ac.acache_gather_slots_q8(_desc(hq, hkv, d, dtype), B, T, dev(rs), gk, gv, dev(sc), ns, ko, vo)
+    assert np.array_equal(ko.double().cpu().numpy(), kv[rs.numpy()]) and np.array_equal(vo.double().cpu().numpy(), vv[rs.numpy()])
+    assert all((x[:lead] == 7).all() and (x[-lead:] == 7).all() for x in (kroom, vroom))
+    # storing what was read back keeps the values
+    (nk, _), (nv, _) = at16(ko[0]), at16(vo[0])
+    (gk2, kroom), (gv2, vroom), s2 = at16(torch.zeros_like(kc), 9), at16(torch.zeros_like(vc), 9), torch.zeros_like(dev(sc))
+    ac.acache_write_slots_q8(_desc(hq, hkv, d, dtype), 1, T, dev(rs[:1]), nk[None], nv[None], gk2, gv2, s2, ns, 0)
+    at = rs[0].long()
+    assert np.array_equal(values(gk2.cpu()[at].numpy(), s2.cpu()[at, :, 0].numpy()), kv[at])
+    assert np.array_equal(values(gv2.cpu()[at].numpy(), s2.cpu()[at, :, 1].numpy()), vv[at])
+    assert all((x[:16] == 9).all() and (x[-16:] == 9).all() for x in (kroom, vroom))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n_q", [1, 40])
+def test_offsets_past_32_bits(dtype, n_q):
+    """A pool of 5 GB a side: slots on both sides of 2^32 bytes and of 2^31."""
+    hq, hkv, d, ns = 8, 8, 128, 5 << 20
+    g = torch.Generator().manual_seed(2)
+    near = [0, (1 << 21) - 1, 1 << 21, (1 << 22) - 1, 1 << 22, ns - 1]
+    slots = torch.tensor(near + list(range((1 << 22) + 7, (1 << 22) + 301)) + list(range(ns - 200, ns - 10)), dtype=torch.int32)
+    T = len(slots)
+    new = [torch.randn((1, T, hkv, d), generator=g).to(dtype) for _ in range(2)]
+    kc, vc = (torch.empty((ns, hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    sc = torch.empty((ns, hkv, 2), dtype=torch.uint8, device="cuda")
+    q = (1.5 * torch.randn((1, n_q, hq, d), generator=g)).to(dtype)
+    rs, desc, st = dev(slots[None]), _desc(hq, hkv, d, dtype), _status()
+    out = torch.empty(q.shape, dtype=dtype, device="cuda")
+    ac.acache_store_attend_q8(desc, 1, T, rs, dev(new[0]), dev(new[1]), kc, vc, sc, ns, 0, n_q, dev(q), T, rs, out, dev_status=st)
+    vals = []
+    for x in new:
+        c, e, _ = quantise(x[0])
+        vals.append(values(c, e))
+    want, tol = attention(q[0], np.arange(T), vals[0], vals[1], d ** -0.5)
+    assert_attention(out[0].double().cpu().numpy(), want, tol)
+    ko, vo = (torch.empty((1, T, hkv, d), dtype=dtype, device="cuda") for _ in range(2))
+    ac.acache_gather_slots_q8(desc, 1, T, rs, kc, vc, sc, ns, ko, vo, dev_status=st)
+    assert np.array_equal(ko[0].double().cpu().numpy(), vals[0]) and np.array_equal(vo[0].double().cpu().numpy(), vals[1])
+    assert st.item() == 0
+
+
+# clusters of 8 CTAs, with two row tiles each and with one (split keys); single CTAs.  Each has more key tiles
+# (of 128) than its K ring's 3 or 4, so that the ring's producer has to wait.
+@pytest.mark.parametrize("B,n_q,hq,hkv,T,d", [(2, 300, 4, 2, 5000, 128), (1, 100, 2, 2, 6000, 64), (4, 600, 16, 4, 700, 128)])
+def test_a_wait_that_runs_out_is_flagged_and_leaves_the_context_usable(B, n_q, hq, hkv, T, d):
+    """With a budget of a few hundred cycles that wait runs out on a healthy kernel: it flags the timeout and
+    exits; the same call then matches."""
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(B, n_q, hq, hkv, d, BF16, T, False, 41)
+    args = (_desc(hq, hkv, d, BF16), B, n_q, dev(q), T, dev(rs), dev(kc), dev(vc), dev(sc), ns)
+    out, st = torch.zeros(q.shape, dtype=BF16, device="cuda"), _status()
+    prev = ac.acache_wait_budget(300)
+    try:
+        ac.acache_slot_attention_q8(*args, out, dev_status=st)
+        torch.cuda.synchronize()
+    finally:
+        ac.acache_wait_budget(prev)
+    assert st.item() & _lib.DEV_TIMEOUT, f"device status {st.item()}"
+    st.zero_()
+    for _ in range(2):
+        ac.acache_slot_attention_q8(*args, out, dev_status=st)
+    assert st.item() == 0
+    want, tol = attention(q[0], rs[0].numpy(), kv, vv, d ** -0.5)
+    assert_attention(out[0].double().cpu().numpy(), want, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_an_empty_pool_holds_zero_rows(dtype):
+    """num_slots = 0: every entry is a bad slot, or with drop_none and no slot no key at all."""
+    hq, hkv, d, T, n_q = 2, 1, 64, 70, 3
+    kc = vc = torch.zeros((1, hkv, d), dtype=torch.uint8, device="cuda")
+    sc = torch.zeros((1, hkv, 2), dtype=torch.uint8, device="cuda")
+    q = torch.randn((1, n_q, hq, d)).to(dtype).cuda()
+    rs = torch.zeros((1, T), dtype=torch.int32, device="cuda")
+    for fill, drop, flags in ((0, False, _lib.DEV_BAD_SLOT), (-1, True, 0)):
+        rs.fill_(fill)
+        out, st = torch.full(q.shape, 3.0, dtype=dtype, device="cuda"), _status()
+        ac.acache_slot_attention_q8(_desc(hq, hkv, d, dtype), 1, n_q, q, T, rs, kc, vc, sc, 0, out, drop_none=drop, dev_status=st)
+        assert (out == 0).all() and st.item() == flags
+
+
 # ------------------------------------------------------------------------------------- ragged
 RAGGED = [
     ("mixed", BF16, 128, 8, 2, [(300, 700), (0, 50), (5, 1), (589, 1408), (128, 129)]),

@@ -5,7 +5,7 @@
 // 32); the 8-bit pool is this library's.
 //
 // Memory-bound: each (request, KV head) streams its keys' and values' codes once, 256 bytes a key
-// (d = 128), against at most 64 packed rows (queries x heads of the group).  What limits it is how many
+// (d = 128), against at most 32 packed rows (queries x heads of the group).  What limits it is how many
 // bytes are in flight and what a CTA costs besides its keys.  So a warp owns 8, 16 or 32 rows and works
 // alone: it brings 16 keys at a time into its own three-stage ring by cp.async, two chunks ahead of the
 // one it works on, and no barrier stands between a load and its use; two to four CTAs of four warps
@@ -65,16 +65,16 @@ struct DecParams {
 };
 
 // NR: rows of a warp
-template <int D, int NR, int RG>
+template <int D, int NR>
 struct Smem {
-    alignas(128) uint8_t q[RG * NR * D * 2];        // query rows in f16
+    alignas(128) uint8_t q[NR * D * 2];             // query rows in f16
     union {
         alignas(128) uint8_t ring[kWarps][kSt][2][kChunk * D];      // codes of K and V, a warp's own
-        alignas(16) float o[kWarps][NR * D];                        // partials, warp rg KG + kg
+        alignas(16) float o[kWarps][NR * D];                        // partials
     };
     float m[kWarps][NR], l[kWarps][NR];
-    float row_m[RG * NR], row_l[RG * NR];           // merged over the CTA's warps
-    float c_row[RG * NR];
+    float row_m[NR], row_l[NR];                     // merged over the CTA's warps
+    float c_row[NR];
 };
 
 ACACHE_DEVFN void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -120,10 +120,6 @@ ACACHE_DEVFN void ld_words(uint32_t addr, uint32_t (&r)[4]) { ld_shared_v4(addr,
 ACACHE_DEVFN void ld_words(uint32_t addr, uint32_t (&r)[2]) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
-// 16 bytes global -> shared through L1 (the warps of other row groups read the same keys)
-ACACHE_DEVFN void cp_async16_l1(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
 // Position of 16-byte piece c of row r in a chunk: a K operand is read by four lanes a row from two
 // neighbouring rows at a time, a V operand by two lanes a row from every other row.
 template <int D> ACACHE_DEVFN uint32_t k_piece(uint32_t r, uint32_t c) { return r * D + ((D == 128 ? c ^ ((r & 1u) << 2) : c) << 4); }
@@ -138,17 +134,15 @@ ACACHE_DEVFN void to_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
         : "r"(four));
 }
 
-// NB: groups of 8 rows to a warp; RG: row groups of the block, the KG = 4 / RG warps of a group share the
-// keys.
-template <int D, int NB, int RG>
+// NB: groups of 8 rows.  The warps share the block's rows and split its keys.
+template <int D, int NB>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NB))
 q8_decode_kernel(const DecParams p) {
     constexpr int NR = 8 * NB;
-    constexpr int KG = kWarps / RG;
     constexpr int H = D / 64;                        // 16-byte pieces of a key row per thread
     constexpr int NV = D / 8;                        // bytes of a value row per thread
     extern __shared__ __align__(128) uint8_t raw_smem[];
-    Smem<D, NR, RG>& sm = *reinterpret_cast<Smem<D, NR, RG>*>(raw_smem);
+    Smem<D, NR>& sm = *reinterpret_cast<Smem<D, NR>*>(raw_smem);
     const int cr = p.cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)p.cs);
     const int hk = p.cs == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)p.cs);
     const int b = (int)blockIdx.y;
@@ -164,14 +158,13 @@ q8_decode_kernel(const DecParams p) {
             return;
         }
     }
-    const int n_rows = n_q * p.g;                    // <= NR RG
+    const int n_rows = n_q * p.g;                    // <= NR
     if (n_rows == 0) return;
     const int n_ch = (T_len + kChunk - 1) / kChunk;
     const int cs = (n_ch + p.part - 1) / p.part;     // parts of this request's keys (<= p.cs)
     if (cr >= cs) return;
     const int ch0 = (int)((int64_t)cr * n_ch / cs), ch1 = (int)((int64_t)(cr + 1) * n_ch / cs);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rg = warp / KG, kg = warp % KG;
     const int g = lane >> 2, t = lane & 3;           // fragment coordinates
 
     // lanes 0-15 look after the keys of a chunk (16-31 repeat them)
@@ -182,11 +175,11 @@ q8_decode_kernel(const DecParams p) {
         return s;
     };
     // slots of the chunk at hand and the two after it (the maps are not written by a store)
-    int s0 = slot_of(ch0 + kg), s1 = slot_of(ch0 + kg + KG), s2 = slot_of(ch0 + kg + 2 * KG);
-    {   // query rows: each warp converts its share of its group's, 8 at least
-        constexpr int NC = NR / KG < 8 ? 8 : NR / KG;
-        const int f0 = rg * NR + kg * NC;
-        if (kg * NC < NR) {
+    int s0 = slot_of(ch0 + warp), s1 = slot_of(ch0 + warp + kWarps), s2 = slot_of(ch0 + warp + 2 * kWarps);
+    {   // query rows: 8 to a warp
+        constexpr int NC = 8;
+        const int f0 = warp * NC;
+        if (f0 < NR) {
             const int pr = f0 + (lane & (NC - 1)) < n_rows ? f0 + (lane & (NC - 1)) : 0, i = pr / p.g;
             const int64_t off = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * p.g)) * D;
             query_rows<D, NC>(p.q, off, smem_u32(&sm.q[f0 * D * 2]), lane, p.scale_log2, &sm.c_row[f0]);
@@ -223,13 +216,8 @@ q8_decode_kernel(const DecParams p) {
         for (int i = 0; i < NI; ++i) {               // (a key without a row is zeros)
             const uint64_t at = (uint64_t)(uint32_t)max(r[i], 0) * row_bytes;
             const uint32_t bytes = r[i] >= 0 ? 16u : 0u, row = (uint32_t)(i * RPI) + rr;
-            if (RG == 1) {
-                cp_async16(stage + k_piece<D>(row, pc), ksrc + at, bytes);
-                cp_async16(stage + kChunk * D + v_piece<D>(row, pc), vsrc + at, bytes);
-            } else {
-                cp_async16_l1(stage + k_piece<D>(row, pc), ksrc + at, bytes);
-                cp_async16_l1(stage + kChunk * D + v_piece<D>(row, pc), vsrc + at, bytes);
-            }
+            cp_async16(stage + k_piece<D>(row, pc), ksrc + at, bytes);
+            cp_async16(stage + kChunk * D + v_piece<D>(row, pc), vsrc + at, bytes);
         }
     };
     grid_dependency_wait();                          // store-then-attend: the pool is written now
@@ -241,7 +229,7 @@ q8_decode_kernel(const DecParams p) {
     __syncthreads();                                 // the query terms are there
     // the query operand: row g of group b, half x of the thread's piece h (NB = 4 reads it as it goes)
     auto load_q = [&](int b, int h, int x, uint32_t (&r)[4]) {
-        ld_shared_v4(smem_u32(&sm.q[0]) + (uint32_t)((rg * NR + 8 * b + g) * 2 * D + (t + 4 * h) * 32 + ((x ^ (g & 1)) * 16)), r);
+        ld_shared_v4(smem_u32(&sm.q[0]) + (uint32_t)((8 * b + g) * 2 * D + (t + 4 * h) * 32 + ((x ^ (g & 1)) * 16)), r);
     };
     constexpr bool kQRegs = NB <= 2;
     uint32_t qf[kQRegs ? NB : 1][H][2][4];
@@ -258,7 +246,7 @@ q8_decode_kernel(const DecParams p) {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            c[b][x] = sm.c_row[rg * NR + 8 * b + 2 * t + x];
+            c[b][x] = sm.c_row[8 * b + 2 * t + x];
             m[b][x] = kNoMax;
             l[b][x] = 0.f;
         }
@@ -271,7 +259,7 @@ q8_decode_kernel(const DecParams p) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[j][b][x] = 0.f;
     uint32_t at = 0, at2 = 2;                        // stages of the chunk at hand and of the one to bring
-    for (int ch = ch0 + kg; ch < ch1; ch += KG) {
+    for (int ch = ch0 + warp; ch < ch1; ch += kWarps) {
         bring(s2, ring + at2 * (2 * kChunk * D));
         cp_async_commit();
         sc2 = load_scale(s2);
@@ -282,7 +270,7 @@ q8_decode_kernel(const DecParams p) {
         s1 = s2;
         sc0 = sc1;
         sc1 = sc2;
-        s2 = slot_of(ch + 3 * KG);
+        s2 = slot_of(ch + 3 * kWarps);
         uint32_t fe[2];                              // of keys g and g + 8
 #pragma unroll
         for (int x = 0; x < 2; ++x) fe[x] = __shfl_sync(0xffffffffu, fe_own, g + 8 * x);
@@ -416,7 +404,7 @@ q8_decode_kernel(const DecParams p) {
             }
         }
     // float4 slot of a row, moved by row and by thread group so that the lanes spread over the banks
-    auto slot4 = [&](int r, int q4) { return (r & (NR - 1)) * D + 4 * (((q4 ^ (q4 / (NV / 4) & (NV / 4 - 1))) + (r & 7) * 2) & (D / 4 - 1)); };
+    auto slot4 = [&](int r, int q4) { return r * D + 4 * (((q4 ^ (q4 / (NV / 4) & (NV / 4 - 1))) + (r & 7) * 2) & (D / 4 - 1)); };
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -426,24 +414,24 @@ q8_decode_kernel(const DecParams p) {
                 *reinterpret_cast<float4*>(&sm.o[warp][slot4(8 * b + 2 * t + x, g * (NV / 4) + j)]) =
                     make_float4(o[2 * j][b][x], o[2 * j][b][2 + x], o[2 * j + 1][b][x], o[2 * j + 1][b][2 + x]);
     __syncthreads();
-    // First the warps of each row group, a thread taking 4 columns of a row.
+    // First the warps, a thread taking 4 columns of a row.
     const bool split = cs > 1;
     for (int it = (int)threadIdx.x; it < n_rows * (D / 4); it += kThreads) {
-        const int r = it / (D / 4), q4 = it % (D / 4), w0 = r / NR * KG;
-        float m[KG], M = kNoMax;
+        const int r = it / (D / 4), q4 = it % (D / 4);
+        float m[kWarps], M = kNoMax;
 #pragma unroll
-        for (int x = 0; x < KG; ++x) {
-            m[x] = sm.m[w0 + x][r & (NR - 1)];
+        for (int x = 0; x < kWarps; ++x) {
+            m[x] = sm.m[x][r];
             M = fmaxf(M, m[x]);
         }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float L = 0.f;
 #pragma unroll
-        for (int x = 0; x < KG; ++x) {
-            const float lv = sm.l[w0 + x][r & (NR - 1)];
+        for (int x = 0; x < kWarps; ++x) {
+            const float lv = sm.l[x][r];
             if (lv == 0.f) continue;                             // no key in this partial
             const float e = fast_exp2(m[x] - M);
-            const float4 f = *reinterpret_cast<const float4*>(&sm.o[w0 + x][slot4(r, q4)]);
+            const float4 f = *reinterpret_cast<const float4*>(&sm.o[x][slot4(r, q4)]);
             L = fmaf(e, lv, L);
             acc.x = fmaf(e, f.x, acc.x);
             acc.y = fmaf(e, f.y, acc.y);
@@ -455,7 +443,7 @@ q8_decode_kernel(const DecParams p) {
                 sm.row_m[r] = M;
                 sm.row_l[r] = L;
             }
-            *reinterpret_cast<float4*>(&sm.o[w0][slot4(r, q4)]) = acc;      // (only this thread reads or writes it)
+            *reinterpret_cast<float4*>(&sm.o[0][slot4(r, q4)]) = acc;      // (only this thread reads or writes it)
         } else {
             const float inv = L == 0.f ? 0.f : 1.f / L;
             const int i = r / p.g;
@@ -471,7 +459,7 @@ q8_decode_kernel(const DecParams p) {
     const uint32_t m_a = smem_u32(&sm.row_m[0]), l_a = smem_u32(&sm.row_l[0]);
     for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 4); it += cs * kThreads) {
         const int r = it / (D / 4), q4 = it % (D / 4);
-        const uint32_t at = smem_u32(&sm.o[r / NR * KG][slot4(r, q4)]);
+        const uint32_t at = smem_u32(&sm.o[0][slot4(r, q4)]);
         float m[kMaxCluster], l[kMaxCluster], M = kNoMax;
         float4 f[kMaxCluster];
 #pragma unroll
@@ -508,18 +496,18 @@ q8_decode_kernel(const DecParams p) {
     cluster_sync();                // no CTA may leave while another still reads its shared memory
 }
 
-std::atomic<int> g_prepared[8][64];   // the kernel's shared memory is allowed for, per device and variant
+std::atomic<int> g_prepared[6][64];   // the kernel's shared memory is allowed for, per device and variant
 
-template <int D, int NB, int RG>
+template <int D, int NB>
 int launch(const DecParams& prm, dim3 grid, cudaStream_t stream, bool pdl) {
-    auto kern = q8_decode_kernel<D, NB, RG>;
-    constexpr int smem = (int)sizeof(Smem<D, 8 * NB, RG>);
+    auto kern = q8_decode_kernel<D, NB>;
+    constexpr int smem = (int)sizeof(Smem<D, 8 * NB>);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
-    std::atomic<int>& st = g_prepared[(D == 128 ? 4 : 0) + NB / 2 + RG - 1][dev];
+    std::atomic<int>& st = g_prepared[(D == 128 ? 3 : 0) + NB / 2][dev];
     if (!st.load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
             (void)cudaGetLastError();
@@ -557,16 +545,17 @@ int launch(const DecParams& prm, dim3 grid, cudaStream_t stream, bool pdl) {
 
 template <int D>
 int dispatch(const DecParams& prm, int rows, dim3 grid, cudaStream_t stream, bool pdl) {
-    if (rows <= 8) return launch<D, 1, 1>(prm, grid, stream, pdl);
-    if (rows <= 16) return launch<D, 2, 1>(prm, grid, stream, pdl);
-    if (rows <= 32) return launch<D, 4, 1>(prm, grid, stream, pdl);
-    return launch<D, 4, 2>(prm, grid, stream, pdl);
+    if (rows <= 8) return launch<D, 1>(prm, grid, stream, pdl);
+    if (rows <= 16) return launch<D, 2>(prm, grid, stream, pdl);
+    return launch<D, 4>(prm, grid, stream, pdl);
 }
 
 }  // namespace
 
+// 64 rows in two such groups took longer than the tcgen05 kernel except for the shortest calls: 8 requests x 64
+// rows x 4480 keys (32 heads) 162 us against 118, 64 x 16000 (8 heads) 64 against 38, 64 x 500 (4 heads) 15 against 19.
 bool q8_decode_supported(const AttnArgs& a, int n_q) {
-    return q8_tc_supported(a) && (int64_t)n_q * (a.hq / a.hkv) <= 64;
+    return q8_tc_supported(a) && (int64_t)n_q * (a.hq / a.hkv) <= 32;
 }
 
 int launch_q8_decode_attention(const Q8Attn& c) {
@@ -595,15 +584,15 @@ int launch_q8_decode_attention(const Q8Attn& c) {
     // longest request only: parts until that one no longer outlasts the others, taken as an eighth as
     // long.
     constexpr int kFix = 6, kMerge = 2;
-    const int rows = c.n_q * g, kgs = rows <= 32 ? 4 : 2;
+    const int rows = c.n_q * g;
     const int n_ch = (c.T_len + kChunk - 1) / kChunk;
     const int64_t units = (int64_t)c.B * hkv, slots = (int64_t)sm_count() * ctas_per_sm(rows <= 8 ? 1 : rows <= 16 ? 2 : 4);
     prm.cs = 1;
     int64_t best = 0;
     for (int cs = 1; cs <= kMaxCluster && cs <= n_ch; cs *= 2) {
-        const int64_t per = (n_ch + cs * kgs - 1) / (cs * kgs) + kFix + (cs > 1 ? kMerge : 0);
+        const int64_t per = (n_ch + cs * kWarps - 1) / (cs * kWarps) + kFix + (cs > 1 ? kMerge : 0);
         int64_t est = ((units * cs + slots - 1) / slots) * per;
-        if (c.q_start) est = std::max(per, (units * (n_ch / (8 * kgs) + kFix + (cs > 1 ? kMerge : 0)) + slots - 1) / slots);
+        if (c.q_start) est = std::max(per, (units * (n_ch / (8 * kWarps) + kFix + (cs > 1 ? kMerge : 0)) + slots - 1) / slots);
         if (cs == 1 || est < best) {
             best = est;
             prm.cs = cs;

@@ -735,38 +735,61 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 }
             }
             cluster_sync();
-            // rank w finalises the (row, 32-column) items w, w + cs, ...
+            // Rank w finalises the (row, 16-column) items w, w + cs, ...  What bounds it is the latency of the
+            // other ranks' shared memory: the loads of four ranks are in flight at a time.
             const uint32_t m_a = smem_u32(&ctl.part_m[0]), l_a = smem_u32(&ctl.part_l[0]), f_a = smem_u32(&ctl.failed);
-            bool all = true;
-            for (int w = 0; w < cs; ++w) all = all && ld_cluster_f32(mapa_shared(f_a, w)) == 0.f;
-            if (all)
-                for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 32); it += cs * 2 * kBM) {
-                    const int rr = it / (D / 32), c4 = it % (D / 32);
-                    float M = -INFINITY;
-                    for (int w = 0; w < cs; ++w) M = fmaxf(M, ld_cluster_f32(mapa_shared(m_a + 4u * rr, w)));
-                    float acc[32], L = 0.f;
+            float lost = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) acc[x] = 0.f;
-                    for (int w = 0; w < cs; ++w) {
-                        const float mw = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
-                        const float lw = ld_cluster_f32(mapa_shared(l_a + 4u * rr, w));
-                        if (mw == -INFINITY && lw == 0.f) continue;       // no key in this part
-                        const float e = fast_exp2(mw - M);
-                        L = fmaf(e, lw, L);
+            for (int w = 0; w < kMaxCluster; ++w)
+                if (w < cs) lost += ld_cluster_f32(mapa_shared(f_a, w));
+            constexpr int kItems = D / 16;                 // per row
+            if (lost == 0.f)
+                for (int it = cr + cs * (int)threadIdx.x; it < n_rows * kItems; it += cs * 2 * kBM) {
+                    const int rr = it / kItems, c4 = it % kItems * 4;
+                    float mw[kMaxCluster], lw[kMaxCluster], M = -INFINITY, L = 0.f;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const float4 f = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, c4 * 8 + x), w));
-                            acc[4 * x] = fmaf(e, f.x, acc[4 * x]);
-                            acc[4 * x + 1] = fmaf(e, f.y, acc[4 * x + 1]);
-                            acc[4 * x + 2] = fmaf(e, f.z, acc[4 * x + 2]);
-                            acc[4 * x + 3] = fmaf(e, f.w, acc[4 * x + 3]);
+                    for (int w = 0; w < kMaxCluster; ++w) {
+                        mw[w] = -INFINITY;
+                        lw[w] = 0.f;
+                        if (w < cs) {
+                            mw[w] = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
+                            lw[w] = ld_cluster_f32(mapa_shared(l_a + 4u * rr, w));
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < kMaxCluster; ++w) M = fmaxf(M, mw[w]);
+                    float acc[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) acc[x] = 0.f;
+#pragma unroll
+                    for (int w0 = 0; w0 < kMaxCluster; w0 += 4) {
+                        if (w0 >= cs) break;
+                        float4 f[4][4];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (w0 + w < cs) f[w][x] = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, c4 + x), w0 + w));
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const float m1 = mw[w0 + w], l1 = lw[w0 + w];
+                            if (w0 + w >= cs || (m1 == -INFINITY && l1 == 0.f)) continue;       // no key in this part
+                            const float e = fast_exp2(m1 - M);
+                            L = fmaf(e, l1, L);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                acc[4 * x] = fmaf(e, f[w][x].x, acc[4 * x]);
+                                acc[4 * x + 1] = fmaf(e, f[w][x].y, acc[4 * x + 1]);
+                                acc[4 * x + 2] = fmaf(e, f[w][x].z, acc[4 * x + 2]);
+                                acc[4 * x + 3] = fmaf(e, f[w][x].w, acc[4 * x + 3]);
+                            }
                         }
                     }
                     const float inv = L == 0.f ? 0.f : kUnshift / L;
                     const uint32_t pr = (uint32_t)(row0 + rr), i = pr / (uint32_t)p.g;
-                    bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D + c4 * 32;
+                    bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D + c4 * 4;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2; ++x) {
                         uint32_t k[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
@@ -847,6 +870,37 @@ int launch(const Q8Params& prm, dim3 grid, cudaStream_t stream, bool pdl) {
     return launch_status();
 }
 
+// CTAs of the kernel that run at once in clusters of 2^i: a cluster stays within a group of SMs, and the groups
+// are no multiples of 4 or 8 (152, 152, 144 and 120 CTAs).
+std::atomic<int> g_slots[4][64];
+int cluster_slots(int i) {
+    int dev = 0;
+    if (i == 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
+    std::atomic<int>& known = g_slots[i][dev];
+    int n = known.load(std::memory_order_relaxed);
+    if (n) return n;
+    n = sm_count();
+    if (prepare<128, false>() == ACACHE_OK) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1u << i;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1u << i);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Geo<128>::kBytes;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, q8_attn_kernel<128, false>, &cfg) == cudaSuccess && clusters > 0)
+            n = clusters << i;
+        else
+            (void)cudaGetLastError();
+    }
+    known.store(n, std::memory_order_relaxed);
+    return n;
+}
+
 }  // namespace
 
 bool q8_tc_supported(const AttnArgs& a) {
@@ -881,14 +935,19 @@ int launch_q8_tc_attention(const Q8Attn& c) {
     prm.g = g;
     prm.scale_log2 = c.a.scale * kLog2e;
     prm.budget = wait_budget();
-    // Parts of the key range: waves x (tiles per part + the fixed cost of a CTA, about 4 tiles, and
-    // of a merge, about 2).
+    // Parts of the key range: waves x what a CTA takes, in thirds of a key tile against two row tiles (1.9 us at
+    // d = 128; against one, two thirds of that).  A CTA costs 16 (12) besides its keys, the launch and the merge
+    // of a cluster 8 (5) a doubling and once more.  (Measured: 600 rows x 3000 keys, 8 heads over 2: 56,
+    // 44, 38 and 72 us for 1, 2, 4 and 8 parts; 300 x 700, 4 heads: 23, 25, 27, 27; 100 x 2000, 16 heads: 31, 25, 23, 42.)
     const int n_all = (c.T_len + kBN - 1) / kBN;
-    const int64_t units = (int64_t)c.B * hkv * n_rb, nsm = sm_count();
+    const int64_t units = (int64_t)c.B * hkv * n_rb;
+    const bool two = (int64_t)c.n_q * g > kBM;
     prm.cs = 1;
     int64_t best = 0;
-    for (int cs = 1; cs <= kMaxCluster && cs <= n_all; cs *= 2) {
-        const int64_t est = ((units * cs + nsm - 1) / nsm) * ((n_all + cs - 1) / cs + 4 + (cs > 1 ? 2 : 0));
+    for (int i = 0, cs = 1; cs <= kMaxCluster && cs <= n_all; ++i, cs *= 2) {
+        const int64_t slots = cluster_slots(i);
+        const int64_t cta = (two ? 3 : 2) * ((n_all + cs - 1) / cs) + (two ? 16 : 12) + (i ? (two ? 8 : 5) * (i + 1) : 0);
+        const int64_t est = (units * cs + slots - 1) / slots * cta;
         if (cs == 1 || est < best) {
             best = est;
             prm.cs = cs;

@@ -46,6 +46,11 @@ ACACHE_DEVFN uint32_t q8_encode2(float a, float b) {
     return r;
 }
 
+// A ragged request with rows that is not computed: counts outside the call's bounds, or rows outside q.
+ACACHE_DEVFN bool q8_bad_lengths(int n_q, int max_q, int T_len, int max_T, int64_t q_at, int total_q, int64_t kv_at) {
+    return n_q < 0 || n_q > max_q || T_len < 1 || T_len > max_T || q_at < 0 || q_at + n_q > total_q || kv_at < 0;
+}
+
 // The attention over an 8-bit pool as the launchers take it.  q_start / kv_start: ragged batches
 // (then n_q and T_len bound the per-request counts and q holds total_q rows), else null.
 struct Q8Attn {
@@ -73,7 +78,7 @@ int launch_q8_simt_attention(const Q8Attn& c);
 // True when the tcgen05 kernel covers the call: bf16 and a positive softmax scale.
 bool q8_tc_supported(const AttnArgs& a);
 int launch_q8_tc_attention(const Q8Attn& c);
-// ... and the one for few rows per (request, KV head): at most 64 packed rows (queries x group).
+// ... and the one for few rows per (request, KV head): at most 32 packed rows (queries x group).
 bool q8_decode_supported(const AttnArgs& a, int n_q);
 int launch_q8_decode_attention(const Q8Attn& c);
 

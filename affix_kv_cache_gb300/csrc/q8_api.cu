@@ -13,10 +13,16 @@ bool pool_ok(const void* k_cache, const void* v_cache, const void* kv_scale) {
     return k_cache && v_cache && kv_scale && aligned16(k_cache) && aligned16(v_cache) && aligned2(kv_scale);
 }
 
+// What the attention's grids and tensor maps hold (clusters of up to 8 CTAs a head along x).
+bool fits(const AttnArgs& a, int batch, int n_q, int64_t num_slots) {
+    return batch <= 65535 && (int64_t)n_q * (a.hq / a.hkv) <= 65535LL * 64 && a.hkv <= 0x7fffffff / 8 &&
+           num_slots < 0x7fffffffLL / a.hkv;
+}
+
 // Fixed and ragged attention after their own scalar checks (q_start null: fixed).
 int attend(const Q8Attn& c) {
     if (!c.q || !c.read_slot || !c.out || !aligned16(c.q) || !aligned16(c.out) ||
-        !pool_ok(c.k_cache, c.v_cache, c.kv_scale))
+        !pool_ok(c.k_cache, c.v_cache, c.kv_scale) || !fits(c.a, c.B, c.n_q, c.num_slots))
         return ACACHE_ERR_INVALID_ARG;
     // (an empty pool: every key is a zero row, and there is no row for a tensor map to start at)
     if (c.num_slots == 0 || !q8_tc_supported(c.a)) return launch_q8_simt_attention(c);
@@ -125,7 +131,7 @@ int acache_store_attend_q8(const acache_attn_desc* desc, int batch, int rows, co
     const bool store = rows > 0, attends = n_q > 0;
     if (store && (!write_slot || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)))
         return ACACHE_ERR_INVALID_ARG;
-    if (attends && (seq_len == 0 || !q || !read_slot || !out || !aligned16(q) || !aligned16(out)))
+    if (attends && (seq_len == 0 || !q || !read_slot || !out || !aligned16(q) || !aligned16(out) || !fits(a, batch, n_q, num_slots)))
         return ACACHE_ERR_INVALID_ARG;
     if ((store || attends) && !pool_ok(k_cache, v_cache, kv_scale)) return ACACHE_ERR_INVALID_ARG;
     if (store)

@@ -58,7 +58,7 @@ struct DecParams {
     bf16* out;
     int32_t* dev_status;
     int64_t num_slots;
-    int n_q, T_len, Hq, Hkv, g;
+    int n_q, total_q, T_len, Hq, Hkv, g;
     int cs, part;                   // CTAs per cluster; chunks per part
     int drop;
     float scale_log2;
@@ -153,7 +153,7 @@ q8_decode_kernel(const DecParams p) {
         kbase = p.kv_start[b];
         n_q = (int)(p.q_start[b + 1] - qbase);
         T_len = (int)(p.kv_start[b + 1] - kbase);
-        if (n_q != 0 && (n_q < 0 || n_q > p.n_q || T_len < 1 || T_len > p.T_len)) {
+        if (n_q != 0 && q8_bad_lengths(n_q, p.n_q, T_len, p.T_len, qbase, p.total_q, kbase)) {
             if (threadIdx.x == 0 && blockIdx.x == 0) flag(p.dev_status, ACACHE_DEV_BAD_LENGTH);
             return;
         }
@@ -560,7 +560,6 @@ bool q8_decode_supported(const AttnArgs& a, int n_q) {
 
 int launch_q8_decode_attention(const Q8Attn& c) {
     const int d = c.a.d, hkv = c.a.hkv, g = c.a.hq / hkv;
-    if (c.B > 65535 || (int64_t)hkv * kMaxCluster > 0x7fffffff) return ACACHE_ERR_INVALID_ARG;
     DecParams prm{};
     prm.q = (const bf16*)c.q;
     prm.k_cache = c.k_cache;
@@ -573,6 +572,7 @@ int launch_q8_decode_attention(const Q8Attn& c) {
     prm.dev_status = c.dev_status;
     prm.num_slots = c.num_slots;
     prm.n_q = c.n_q;
+    prm.total_q = c.total_q;
     prm.T_len = c.T_len;
     prm.Hq = c.a.hq;
     prm.Hkv = hkv;

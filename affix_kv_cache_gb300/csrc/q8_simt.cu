@@ -26,7 +26,7 @@ struct SimtParams {
     void* out;
     int32_t* dev_status;
     int64_t num_slots;
-    int n_q, T_len, Hq, Hkv, g, cs;
+    int n_q, total_q, T_len, Hq, Hkv, g, cs;
     bool drop_none;
     float scale_log2;
 };
@@ -57,7 +57,7 @@ q8_simt_kernel(const SimtParams p) {
         kbase = p.kv_start[b];
         n_q = (int)(p.q_start[b + 1] - qbase);
         T_len = (int)(p.kv_start[b + 1] - kbase);
-        if (n_q != 0 && (n_q < 0 || n_q > p.n_q || T_len < 1 || T_len > p.T_len)) {
+        if (n_q != 0 && q8_bad_lengths(n_q, p.n_q, T_len, p.T_len, qbase, p.total_q, kbase)) {
             if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) flag(p.dev_status, ACACHE_DEV_BAD_LENGTH);
             return;
         }
@@ -293,7 +293,6 @@ int launch(const SimtParams& prm, dim3 grid, cudaStream_t stream) {
 int launch_q8_simt_attention(const Q8Attn& c) {
     const int g = c.a.hq / c.a.hkv;
     const int64_t n_rb = ((int64_t)c.n_q * g + kBM - 1) / kBM;
-    if (c.B > 65535 || n_rb > 65535) return ACACHE_ERR_INVALID_ARG;
     SimtParams prm{};
     prm.q = c.q;
     prm.k_cache = c.k_cache;
@@ -306,6 +305,7 @@ int launch_q8_simt_attention(const Q8Attn& c) {
     prm.dev_status = c.dev_status;
     prm.num_slots = c.num_slots;
     prm.n_q = c.n_q;
+    prm.total_q = c.total_q;
     prm.T_len = c.T_len;
     prm.Hq = c.a.hq;
     prm.Hkv = c.a.hkv;
@@ -316,7 +316,6 @@ int launch_q8_simt_attention(const Q8Attn& c) {
     const int64_t units = (int64_t)c.B * c.a.hkv * n_rb, tiles = (c.T_len + kBN - 1) / kBN;
     prm.cs = 1;
     while (prm.cs < kMaxCluster && units * prm.cs * 2 <= 2 * (int64_t)sm_count() && tiles >= 4 * prm.cs) prm.cs *= 2;
-    if ((int64_t)c.a.hkv * prm.cs > 0x7fffffff) return ACACHE_ERR_INVALID_ARG;
     const dim3 grid((unsigned)(c.a.hkv * prm.cs), (unsigned)c.B, (unsigned)n_rb);
     if (c.a.dtype == ACACHE_F32)
         return c.a.d == 64 ? launch<float, 64>(prm, grid, c.stream) : launch<float, 128>(prm, grid, c.stream);

@@ -101,7 +101,7 @@ struct Q8Params {
     int32_t* dev_status;
     int64_t num_slots;
     int oob_row;           // a pool row outside the tensor (reads zeros)
-    int n_q, T_len, Hq, Hkv, g;
+    int n_q, total_q, T_len, Hq, Hkv, g;
     int cs, part;          // CTAs per cluster; key tiles per part
     float scale_log2;
     long long budget;      // cycles a pipeline wait may take before it gives up
@@ -180,7 +180,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         kbase = p.kv_start[b];
         n_q = (int)(p.q_start[b + 1] - qbase);
         T_len = (int)(p.kv_start[b + 1] - kbase);
-        if (n_q != 0 && (n_q < 0 || n_q > p.n_q || T_len < 1 || T_len > p.T_len)) {
+        if (n_q != 0 && q8_bad_lengths(n_q, p.n_q, T_len, p.T_len, qbase, p.total_q, kbase)) {
             if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) flag(p.dev_status, ACACHE_DEV_BAD_LENGTH);
             return;
         }
@@ -909,14 +909,12 @@ bool q8_tc_supported(const AttnArgs& a) {
 
 int launch_q8_tc_attention(const Q8Attn& c) {
     const int d = c.a.d, hkv = c.a.hkv, g = c.a.hq / hkv;
-    if (c.num_slots * hkv >= 0x7fffffffLL) return ACACHE_ERR_INVALID_ARG;
     const int64_t n_rb = ((int64_t)c.n_q * g + kQT * kBM - 1) / (kQT * kBM);
-    if (c.B > 65535 || n_rb > 65535 || (int64_t)hkv * kMaxCluster > 0x7fffffff) return ACACHE_ERR_INVALID_ARG;
     Q8Params prm{};
     const uint64_t rows[2] = {(uint64_t)d, (uint64_t)(c.num_slots * hkv)};
     const uint64_t pool[3] = {(uint64_t)d, (uint64_t)hkv, (uint64_t)c.num_slots};
     const uint32_t one[2] = {(uint32_t)d, 1}, box[3] = {(uint32_t)d, 1, kBN};
-    if (!make_map_u8(&prm.tm_k, c.k_cache, 2, rows, one, true) || !make_map_u8(&prm.tm_kbox, c.k_cache, 3, pool, box, true))
+    if (!make_map_u8(&prm.tm_k, c.k_cache, 2, rows, one) || !make_map_u8(&prm.tm_kbox, c.k_cache, 3, pool, box))
         return ACACHE_ERR_CUDA;
     prm.q = (const bf16*)c.q;
     prm.v_cache = c.v_cache;
@@ -929,6 +927,7 @@ int launch_q8_tc_attention(const Q8Attn& c) {
     prm.num_slots = c.num_slots;
     prm.oob_row = (int)(c.num_slots * hkv) + (c.num_slots == 0);
     prm.n_q = c.n_q;
+    prm.total_q = c.total_q;
     prm.T_len = c.T_len;
     prm.Hq = c.a.hq;
     prm.Hkv = hkv;

@@ -15,10 +15,9 @@ bool make_map_box(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dim
 bool make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, int row_dim,
               uint32_t box_rows);
 
-// 8-bit tensor of `rank` dims (innermost first), contiguous; box[0] = 64 or 128 bytes, in
-// shared memory swizzled over that span or row after row; out-of-range elements read as zero.
-bool make_map_u8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint32_t* box,
-                 bool swizzle);
+// 8-bit tensor of `rank` dims (innermost first), contiguous; box[0] = 64 or 128 bytes, the span of the
+// swizzle in shared memory; out-of-range elements read as zero.
+bool make_map_u8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint32_t* box);
 
 // True when the tcgen05 kernels cover this geometry (bf16, head_dim 128).
 bool tc_supported(const AttnArgs& a);

@@ -51,8 +51,7 @@ bool make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, i
     return make_map_box(m, ptr, rank, dims, box);
 }
 
-bool make_map_u8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint32_t* box,
-                 bool swizzle) {
+bool make_map_u8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint32_t* box) {
     auto enc = encode_fn();
     if (!enc || rank < 1 || rank > 5 || (box[0] != 64 && box[0] != 128)) return false;
     cuuint64_t gdim[5], gstride[4];
@@ -67,7 +66,7 @@ bool make_map_u8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims
     }
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(ptr), gdim, gstride, bx, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE,
-               !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

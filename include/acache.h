@@ -389,7 +389,10 @@ ACACHE_API int acache_gather_slots(const acache_attn_desc* a, int batch, int seq
  * is exact, and storing a read-back row again keeps its values.  A row with a NaN, an infinity or a
  * value above 448 * 2^38 is stored as scale byte 255 and zero codes and flags ACACHE_DEV_BAD_VALUE: it
  * reads as NaN, and so does every query row that attends to it.  Bytes of 166 to 254 read as NaN too; a
- * pool set to zero bytes reads as zeros.
+ * pool set to zero bytes reads as zeros.  Pools not written by these calls keep to that format: codes 0x7f
+ * and 0xff, and bytes of 1 to 76, are not defined here.  An attention call takes up to 65,535
+ * requests, 65,535 tiles of 64 rows (queries x heads of a group) and a pool below 2^31 rows (slots x
+ * heads); more is ACACHE_ERR_INVALID_ARG.
  * The descriptor's dtype is that of the fresh K/V, the queries and the outputs.
  * ------------------------------------------------------------------------------- */
 
@@ -419,7 +422,8 @@ ACACHE_API int acache_slot_attention_q8(const acache_attn_desc* a, int batch, in
                           int drop_none, int32_t* dev_status, void* stream);
 
 /* (4b'') The same over a ragged batch: acache_slot_attention_varlen on an 8-bit pool (a serving
- * batch of single tokens, prompts, or both).  Arguments and errors as there. */
+ * batch of single tokens, prompts, or both).  Arguments and errors as there; a request whose rows lie
+ * outside the total_q_rows rows of q is skipped and flagged as well. */
 ACACHE_API int acache_slot_attention_varlen_q8(const acache_attn_desc* a, int batch,
                           const int32_t* q_start, int max_q_rows, int total_q_rows, const void* q,
                           const int32_t* kv_start, int max_seq_len, const int32_t* read_slot,

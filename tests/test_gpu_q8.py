@@ -471,6 +471,28 @@ def test_ragged_bad_lengths_are_skipped_and_flagged(dtype, d):
     assert_attention(got[:40], want, tol)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("max_q", [20, 60])
+def test_ragged_rows_outside_q_are_skipped_and_flagged(dtype, d, max_q):
+    """Only the first total_q_rows rows of q and out are the call's."""
+    rows, total = [15, 4, 11], 25                               # the last request's rows reach past them
+    g = torch.Generator().manual_seed(6)
+    kc, vc, sc, kv, vv = random_pool(200, 1, d, g)
+    q = torch.randn((sum(rows), 2, d), generator=g).to(dtype)
+    rs = torch.randint(0, 200, (3 * 100,), generator=g, dtype=torch.int32)
+    qs = torch.tensor([0] + list(np.cumsum(rows)), dtype=torch.int32)
+    ks = torch.tensor([0, 100, 200, 300], dtype=torch.int32)
+    out, st = torch.full(q.shape, 9.0, dtype=dtype, device="cuda"), _status()
+    ac.acache_slot_attention_varlen_q8(_desc(2, 1, d, dtype), 3, dev(qs), max_q, total, dev(q), dev(ks), 100, dev(rs), dev(kc),
+                                       dev(vc), dev(sc), 200, out, dev_status=st)
+    got = out.double().cpu().numpy()
+    assert st.item() == _lib.DEV_BAD_LENGTH and (got[19:] == 9).all()
+    for b in range(2):
+        at = slice(int(qs[b]), int(qs[b + 1]))
+        want, tol = attention(q[at], rs[100 * b:100 * b + 100].numpy(), kv, vv, d ** -0.5)
+        assert_attention(got[at], want, tol)
+
+
 # ------------------------------------------------------------------------------- store and attend
 def _step(B, rows, n_q, hq, hkv, d, dtype, T, seed):
     g = torch.Generator().manual_seed(seed)

@@ -80,6 +80,16 @@ def test_scalar_refusals_and_noops():
     assert _both(d, rows=0, n_q=0, slot=None, kn=None, vn=None, q=None, rs=None, out=None, **none) == 0
 
 
+def test_sizes_past_the_launch_limits_are_refused():
+    """Before anything is launched: a store in the same call would write through these pointers."""
+    for call in (_attend, _both):
+        assert call(_desc(), batch=65536) == E
+        assert call(_desc(), ns=(2 ** 31 - 1) // 2) == E
+        assert call(_desc(), n_q=65535 * 64 // 2 + 1) == E
+    assert _varlen(_desc(), batch=65536) == E and _varlen(_desc(), ns=2 ** 30) == E
+    assert _varlen(_desc(), mq=65535 * 32 + 1) == E
+
+
 def test_binding_raises():
     with pytest.raises(ac.AcacheError) as e:
         ac.acache_slot_attention_q8(_desc(), 1, 4, None, 4, None, None, None, None, 8, None)

@@ -7,10 +7,10 @@
 // Both are bound by memory.  The store's item is 16 consecutive elements of one (row, head), of K and of
 // V: a lane reads an item of each matrix with 16-byte loads, the d/16 lanes of a head agree on the
 // largest magnitude with shuffles, and one lane writes the head's two exponents as one 16-bit
-// word (measured 76 us for 16 x 1,205 rows of 32 heads, d = 128, bf16: 0.92 of the copy bandwidth).
-// The read-back's item is one 16-byte piece of the output.  Items are numbered across rows, so every
-// lane has work whatever the head count is, and a thread keeps several items in flight; a step of the
-// grid advances (row, item) by a constant pair, so the only division is at a thread's start.
+// word (measured 76 us for 16 x 1,205 rows of 32 heads, d = 128, bf16: 0.92 of the copy bandwidth); a
+// thread keeps two items in flight.  The read-back's item is one 16-byte piece of the output.  Items are
+// numbered across rows, so every lane has work whatever the head count is; a step of the grid advances
+// (row, item) by a constant pair, so the only division is at a thread's start.
 #include "q8.cuh"
 #include "ptx.cuh"
 
@@ -118,7 +118,10 @@ q8_write_kernel(const int32_t* __restrict__ write_slot, int64_t nrows, int ipr, 
 
 // One 16-byte piece of the output: 4 float32 or 8 bf16 from as many codes, so that the lanes of a warp
 // write whole lines (with 16 codes to a lane, as in the store, a lane's pieces of the output are 32
-// or 64 bytes apart from the next lane's: 55 us where this takes 24, float32, 147 MB written).
+// or 64 bytes apart from the next lane's: twice the time).  One piece at a time: few registers, so all the
+// warps an SM holds are there to keep loads in flight, and what they write stays close together: 29 us
+// for 8 x 4,480 rows of 8 heads (d = 128, float32, 147 MB written: 0.79 of the copy bandwidth), 37 with
+// four pieces; 57 us for 32 heads in bf16 (0.83), 70 with four.
 template <typename T> struct Piece;
 template <> struct Piece<float> {
     using Codes = uint32_t;
@@ -139,8 +142,6 @@ template <> struct Piece<__nv_bfloat16> {
     }
 };
 
-constexpr int kReadUnroll = 4;
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 q8_gather_kernel(const int32_t* __restrict__ read_slot, int64_t nrows, int ipr, int64_t step_r, int step_c,
@@ -152,41 +153,22 @@ q8_gather_kernel(const int32_t* __restrict__ read_slot, int64_t nrows, int ipr, 
     int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / ipr;
     int c = (int)(((int64_t)blockIdx.x * kThreads + threadIdx.x) - r * ipr);
     while (r < nrows) {
-        Codes k[kReadUnroll], v[kReadUnroll];
-        uint32_t s2[kReadUnroll];
-        int64_t src[kReadUnroll], dst[kReadUnroll];
-#pragma unroll
-        for (int u = 0; u < kReadUnroll; ++u) {      // the slots first: then all loads of the codes at once
-            src[u] = -1;
-            dst[u] = r * ipr + c;
-            if (r < nrows) {
-                const int64_t s = read_slot[r];
-                if (s < 0 || s >= num_slots) {
-                    if (c == 0) flag(dev_status, ACACHE_DEV_BAD_SLOT);
-                } else {
-                    src[u] = s * ipr + c;
-                }
-            }
-            r += step_r;
-            c += step_c;
-            if (c >= ipr) {
-                c -= ipr;
-                ++r;
-            }
+        const int64_t s = read_slot[r];
+        if (s >= 0 && s < num_slots) {
+            const int64_t src = s * ipr + c, dst = r * ipr + c;
+            const Codes k = __ldg(reinterpret_cast<const Codes*>(k_cache) + src), v = __ldg(reinterpret_cast<const Codes*>(v_cache) + src);
+            const uint32_t s2 = __ldg(reinterpret_cast<const uint16_t*>(kv_scale) + src / kPer);
+            __stcs(reinterpret_cast<uint4*>(k_out) + dst, Piece<T>::make(k, q8_factor(s2 & 0xffu)));
+            __stcs(reinterpret_cast<uint4*>(v_out) + dst, Piece<T>::make(v, q8_factor(s2 >> 8)));
+        } else if (c == 0) {
+            flag(dev_status, ACACHE_DEV_BAD_SLOT);
         }
-#pragma unroll
-        for (int u = 0; u < kReadUnroll; ++u)
-            if (src[u] >= 0) {
-                k[u] = __ldg(reinterpret_cast<const Codes*>(k_cache) + src[u]);
-                v[u] = __ldg(reinterpret_cast<const Codes*>(v_cache) + src[u]);
-                s2[u] = __ldg(reinterpret_cast<const uint16_t*>(kv_scale) + src[u] / kPer);
-            }
-#pragma unroll
-        for (int u = 0; u < kReadUnroll; ++u)
-            if (src[u] >= 0) {
-                __stcs(reinterpret_cast<uint4*>(k_out) + dst[u], Piece<T>::make(k[u], q8_factor(s2[u] & 0xffu)));
-                __stcs(reinterpret_cast<uint4*>(v_out) + dst[u], Piece<T>::make(v[u], q8_factor(s2[u] >> 8)));
-            }
+        r += step_r;
+        c += step_c;
+        if (c >= ipr) {
+            c -= ipr;
+            ++r;
+        }
     }
 }
 
@@ -240,7 +222,7 @@ int launch_q8_gather(int dtype, int batch, int seq_len, int hkv, int d, const in
                      void* k_out, void* v_out, int32_t* dev_status, cudaStream_t stream) {
     const int64_t nrows = (int64_t)batch * seq_len;
     if (nrows == 0) return ACACHE_OK;
-    const Shape s = item_shape(nrows, hkv * (d / (dtype == ACACHE_F32 ? 4 : 8)), kReadUnroll);
+    const Shape s = item_shape(nrows, hkv * (d / (dtype == ACACHE_F32 ? 4 : 8)), 1);
     ACACHE_Q8_DISPATCH(dtype, d, {
         q8_gather_kernel<T, D><<<s.grid, kThreads, 0, stream>>>(read_slot, nrows, s.ipr, s.step_r, s.step_c, k_cache,
                                                                 v_cache, kv_scale, num_slots, (T*)k_out, (T*)v_out,

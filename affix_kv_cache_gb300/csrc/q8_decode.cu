@@ -26,6 +26,10 @@
 // The warps of a CTA, the CTAs of a cluster (up to 8, where that fills the SMs better) share the keys; partial
 // (maximum, sum, O) are merged in a fixed order through (distributed) shared memory.
 //
+// Measured: 8 requests x 32 rows x 4,480 keys (32 heads, d = 128) 85 us, 0.21 of the time to read the pool's bytes:
+// bound by the latency between the products of a chunk (32 rows take 8 warps to an SM); 48 single tokens of 1 to
+// 16,000 keys (32 heads over 8) 53 us, 0.42: the longest request's parts, 2,000 keys each, take most of that.
+//
 // The register-operand products run at a quarter of tcgen05's rate, which few rows do not need: 128 keys
 // against 16 rows are 525 cycles of an SM's matrix pipes, and reading them at the memory's rate takes
 // 1400.  The tcgen05 form of this kernel (rows replicated over the 128 TMEM lanes, f16 V through shared

@@ -8,8 +8,8 @@
 // Mathematics.  out = softmax(scale q . k) v with k = 2^ek kc, v = 2^ev vc, codes kc and vc in e4m3.
 //   * S: the keys' codes are an operand as they lie in the pool.  A bf16 query row has 8
 //     significant bits, twice e4m3's 4: scaled by a power of two so that its largest element lies in
-//     [128, 256), q' = hi + lo with hi = e4m3(q') and lo = e4m3(q' - hi) is exact for elements within
-//     2^-10 of the largest and off by at most 2^-17 of the largest below.  S = hi kc + lo kc: two
+//     [128, 256), q' = hi + lo with hi = q' cut to 4 bits and lo = e4m3(q' - hi) is exact for elements
+//     within 2^-9 of the largest and off by some 2^-17 of the largest below.  S = hi kc + lo kc: two
 //     8-bit MMA passes at twice the bf16 rate, so no key is ever converted and the K ring takes
 //     half the shared memory.  2^ek multiplies S per key (float32), the row's power of two joins the
 //     softmax scale.
@@ -33,6 +33,17 @@
 //   A CTA with one row tile (few rows: decoding) splits its keys between the chains and merges
 //   them at the end.  When there are few blocks the key range is also split over a cluster of cs
 //   CTAs, whose partial (maximum, sum, O) are merged through distributed shared memory, in rank order.
+//
+// What bounds it.  16 requests x 986 rows x 2,624 keys, 28 heads over 4, d = 128: 555 us, 1,070 TFLOP/s, 0.55 of the
+// measured bf16 rate.  A step of 64 keys takes both chains some 1,800 cycles; their MMAs alone take 1,260
+// (2 x 385 for S, whose 64-key products read 6 KB of shared memory in the 32 cycles they need 4 KB's worth
+// of, and 2 x 257 for PV).  No pipe is full (ALU 0.38, FMA 0.27, MUFU 0.21, shared memory 0.30 besides the
+// MMAs' reads): two softmax warps per scheduler do not cover their own latencies, and whatever a softmax
+// warp waits for on its own account shows -- a barrier for the keys' factors cost 7 %, per-lane arrivals
+// 1 %.  A block costs some 15,000 cycles besides its steps (launch and set-up 4,000, the query terms 6,000, first
+// S 2,000, drain and epilogue 4,000).  Slower were: S of 128 keys at a time, which needs only 512 cycles, into one
+// buffer (692 us where this form took 617); the chains taking turns (+2 to 5 %); four softmax warpgroups
+// (+13 %); V's codes through a raw ring in shared memory; the keys' factors read before S is waited for (+20 %).
 //
 // Every mbarrier wait is bounded; a wait that gives up raises a CTA-wide abort flag and
 // ACACHE_DEV_TIMEOUT, roles leave their loops, MMAs in flight are drained, TMA loads issued before
@@ -58,9 +69,8 @@ constexpr int kMmaWarp = 8;
 constexpr int kProdWarp = 10, kProd = 2;    // K producer warps
 constexpr int kConvWarp = 12, kConv = 4;    // V converter warps
 constexpr int kThreads = 512;
-// Registers: 512 x 128 at launch = 65536; 2 x 128 x 168 + 128 x 56 + 128 x 120 = 65536.
-// Registers per thread of the warpgroups.  The producers of a call with discarded keys carry their masks:
-// with 56 they spill, and a long ragged batch takes 76 us instead of 72.
+// Registers per thread of the warpgroups, 512 x 128 in all.  The producers of a call with discarded keys carry
+// their masks: with 56 they spill, and a long ragged batch takes 76 us instead of 72.
 constexpr int kRegSoftmax = 168;
 template <bool kDrop>
 constexpr int kRegIssue = kDrop ? 64 : 56;
@@ -450,7 +460,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
         } else {
             // ------------------------------------------------------------------ MMA issuers
             // The whole warp walks the steps, so addresses and descriptors stay in uniform registers, and
-            // one lane issues: with the walk inside a one-lane branch each MMA took some 80 cycles to issue.
+            // one lane issues.
             const int t = __shfl_sync(0xffffffffu, warp, 0) - kMmaWarp;         // chain
             if (t < n_ch) {
                 const bool leader = elect_one();

@@ -457,11 +457,12 @@ q8_decode_kernel(const DecParams p) {
         }
     }
     if (!split) return;
-    // Then the parts: rank x finalises the (row, 4-column) items x, x + cs, ...
+    // Then the parts: a warp finalises 32 neighbouring (row, 4-column) items at a time, so that a load takes whole
+    // lines of the other SM's shared memory.
     __syncwarp();
     cluster_sync();
     const uint32_t m_a = smem_u32(&sm.row_m[0]), l_a = smem_u32(&sm.row_l[0]);
-    for (int it = cr + cs * (int)threadIdx.x; it < n_rows * (D / 4); it += cs * kThreads) {
+    for (int it = 32 * (cr + cs * warp) + lane; it < n_rows * (D / 4); it += cs * kThreads) {
         const int r = it / (D / 4), q4 = it % (D / 4);
         const uint32_t at = smem_u32(&sm.o[0][slot4(r, q4)]);
         float m[kMaxCluster], l[kMaxCluster], M = kNoMax;
@@ -470,6 +471,7 @@ q8_decode_kernel(const DecParams p) {
         for (int x = 0; x < kMaxCluster; ++x) {
             m[x] = kNoMax;
             l[x] = 0.f;
+            f[x] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (x < cs) {
                 m[x] = ld_cluster_f32(mapa_shared(m_a + 4u * r, x));
                 l[x] = ld_cluster_f32(mapa_shared(l_a + 4u * r, x));
@@ -482,13 +484,15 @@ q8_decode_kernel(const DecParams p) {
         float L = 0.f;
 #pragma unroll
         for (int x = 0; x < kMaxCluster; ++x) {
-            if (l[x] == 0.f) continue;                           // no key in this part
+            // (no key in this part: nothing to add; but every value loaded is used, so none is still on its way when
+            // the ranks part)
+            const bool none = l[x] == 0.f;
             const float e = fast_exp2(m[x] - M);
-            L = fmaf(e, l[x], L);
-            acc.x = fmaf(e, f[x].x, acc.x);
-            acc.y = fmaf(e, f[x].y, acc.y);
-            acc.z = fmaf(e, f[x].z, acc.z);
-            acc.w = fmaf(e, f[x].w, acc.w);
+            L = none ? L : fmaf(e, l[x], L);
+            acc.x = none ? acc.x : fmaf(e, f[x].x, acc.x);
+            acc.y = none ? acc.y : fmaf(e, f[x].y, acc.y);
+            acc.z = none ? acc.z : fmaf(e, f[x].z, acc.z);
+            acc.w = none ? acc.w : fmaf(e, f[x].w, acc.w);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const int i = r / p.g;

@@ -745,70 +745,52 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 }
             }
             cluster_sync();
-            // Rank w finalises the (row, 16-column) items w, w + cs, ...  What bounds it is the latency of the
-            // other ranks' shared memory: the loads of four ranks are in flight at a time.
+            // A warp finalises 32 neighbouring (row, 4-column) items at a time, all ranks' loads in flight: a load
+            // takes whole lines of the other SM's shared memory.  (16 columns to a lane, so lanes on 16 different
+            // rows: 12 us for 256 rows from four ranks.)  Every value loaded is used, so none is still on its way
+            // when the ranks part.
             const uint32_t m_a = smem_u32(&ctl.part_m[0]), l_a = smem_u32(&ctl.part_l[0]), f_a = smem_u32(&ctl.failed);
             float lost = 0.f;
 #pragma unroll
             for (int w = 0; w < kMaxCluster; ++w)
                 if (w < cs) lost += ld_cluster_f32(mapa_shared(f_a, w));
-            constexpr int kItems = D / 16;                 // per row
-            if (lost == 0.f)
-                for (int it = cr + cs * (int)threadIdx.x; it < n_rows * kItems; it += cs * 2 * kBM) {
-                    const int rr = it / kItems, c4 = it % kItems * 4;
-                    float mw[kMaxCluster], lw[kMaxCluster], M = -INFINITY, L = 0.f;
+            constexpr int kItems = D / 4;                  // per row
+            const int n_items = lost == 0.f ? n_rows * kItems : 0;
+#pragma unroll 1
+            for (int it = 32 * (cr + cs * warp) + lane; it < n_items; it += 32 * cs * 2 * (kBM / 32)) {
+                const int rr = it / kItems, q4 = it % kItems;
+                float mw[kMaxCluster], lw[kMaxCluster], M = -INFINITY, L = 0.f;
+                float4 f[kMaxCluster];
 #pragma unroll
-                    for (int w = 0; w < kMaxCluster; ++w) {
-                        mw[w] = -INFINITY;
-                        lw[w] = 0.f;
-                        if (w < cs) {
-                            mw[w] = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
-                            lw[w] = ld_cluster_f32(mapa_shared(l_a + 4u * rr, w));
-                        }
-                    }
-#pragma unroll
-                    for (int w = 0; w < kMaxCluster; ++w) M = fmaxf(M, mw[w]);
-                    float acc[16];
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) acc[x] = 0.f;
-#pragma unroll
-                    for (int w0 = 0; w0 < kMaxCluster; w0 += 4) {
-                        if (w0 >= cs) break;
-                        float4 f[4][4];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                if (w0 + w < cs) f[w][x] = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, c4 + x), w0 + w));
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const float m1 = mw[w0 + w], l1 = lw[w0 + w];
-                            if (w0 + w >= cs || (m1 == -INFINITY && l1 == 0.f)) continue;       // no key in this part
-                            const float e = fast_exp2(m1 - M);
-                            L = fmaf(e, l1, L);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                acc[4 * x] = fmaf(e, f[w][x].x, acc[4 * x]);
-                                acc[4 * x + 1] = fmaf(e, f[w][x].y, acc[4 * x + 1]);
-                                acc[4 * x + 2] = fmaf(e, f[w][x].z, acc[4 * x + 2]);
-                                acc[4 * x + 3] = fmaf(e, f[w][x].w, acc[4 * x + 3]);
-                            }
-                        }
-                    }
-                    const float inv = L == 0.f ? 0.f : kUnshift / L;
-                    const uint32_t pr = (uint32_t)(row0 + rr), i = pr / (uint32_t)p.g;
-                    bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D + c4 * 4;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t k[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            __nv_bfloat162 two = __floats2bfloat162_rn(acc[8 * x + 2 * y] * inv, acc[8 * x + 2 * y + 1] * inv);
-                            k[y] = *reinterpret_cast<uint32_t*>(&two);
-                        }
-                        reinterpret_cast<uint4*>(o)[x] = make_uint4(k[0], k[1], k[2], k[3]);
+                for (int w = 0; w < kMaxCluster; ++w) {
+                    mw[w] = -INFINITY;
+                    lw[w] = 0.f;
+                    f[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w < cs) {
+                        mw[w] = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
+                        lw[w] = ld_cluster_f32(mapa_shared(l_a + 4u * rr, w));
+                        f[w] = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, q4), w));
                     }
                 }
+#pragma unroll
+                for (int w = 0; w < kMaxCluster; ++w) M = fmaxf(M, mw[w]);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kMaxCluster; ++w) {
+                    const bool none = mw[w] == -INFINITY && lw[w] == 0.f;        // no key in this part
+                    const float e = none ? 0.f : fast_exp2(mw[w] - M);
+                    L = fmaf(e, lw[w], L);
+                    acc.x = none ? acc.x : fmaf(e, f[w].x, acc.x);
+                    acc.y = none ? acc.y : fmaf(e, f[w].y, acc.y);
+                    acc.z = none ? acc.z : fmaf(e, f[w].z, acc.z);
+                    acc.w = none ? acc.w : fmaf(e, f[w].w, acc.w);
+                }
+                const float inv = L == 0.f ? 0.f : kUnshift / L;
+                const uint32_t pr = (uint32_t)(row0 + rr), i = pr / (uint32_t)p.g;
+                bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D + q4 * 4;
+                __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
+            }
             __syncwarp();
             cluster_sync();        // no CTA may leave while another still reads its shared memory
         }

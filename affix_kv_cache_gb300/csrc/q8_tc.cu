@@ -53,6 +53,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "q8_tc.cuh"
 
@@ -745,10 +746,10 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 }
             }
             cluster_sync();
-            // A warp finalises 32 neighbouring (row, 4-column) items at a time, all ranks' loads in flight: a load
-            // takes whole lines of the other SM's shared memory.  (16 columns to a lane, so lanes on 16 different
-            // rows: 12 us for 256 rows from four ranks.)  Every value loaded is used, so none is still on its way
-            // when the ranks part.
+            // A lane finalises (row, 4-column) items, a warp 32 neighbouring ones, so that a load takes whole lines
+            // of the other SM's shared memory (16 columns to a lane, lanes on 16 different rows: 12 us for 256
+            // rows from four ranks).  Eight items' and ranks' loads are in flight.  Every value loaded is used,
+            // so none is still on its way when the ranks part.
             const uint32_t m_a = smem_u32(&ctl.part_m[0]), l_a = smem_u32(&ctl.part_l[0]), f_a = smem_u32(&ctl.failed);
             float lost = 0.f;
 #pragma unroll
@@ -756,41 +757,57 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 if (w < cs) lost += ld_cluster_f32(mapa_shared(f_a, w));
             constexpr int kItems = D / 4;                  // per row
             const int n_items = lost == 0.f ? n_rows * kItems : 0;
+            auto finalise = [&](auto ranks) {
+                constexpr int W = decltype(ranks)::value, N = kMaxCluster / W;
+                const int step = 32 * cs * 2 * (kBM / 32);
 #pragma unroll 1
-            for (int it = 32 * (cr + cs * warp) + lane; it < n_items; it += 32 * cs * 2 * (kBM / 32)) {
-                const int rr = it / kItems, q4 = it % kItems;
-                float mw[kMaxCluster], lw[kMaxCluster], M = -INFINITY, L = 0.f;
-                float4 f[kMaxCluster];
+                for (int it = 32 * (cr + cs * warp) + lane; it < n_items; it += N * step) {
+                    float mw[N][W], lw[N][W];
+                    float4 f[N][W];
 #pragma unroll
-                for (int w = 0; w < kMaxCluster; ++w) {
-                    mw[w] = -INFINITY;
-                    lw[w] = 0.f;
-                    f[w] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (w < cs) {
-                        mw[w] = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
-                        lw[w] = ld_cluster_f32(mapa_shared(l_a + 4u * rr, w));
-                        f[w] = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, q4), w));
+                    for (int n = 0; n < N; ++n)
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            mw[n][w] = -INFINITY;
+                            lw[n][w] = 0.f;
+                            f[n][w] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            const int at = it + n * step, rr = at / kItems;
+                            if (w < cs && at < n_items) {
+                                mw[n][w] = ld_cluster_f32(mapa_shared(m_a + 4u * rr, w));
+                                lw[n][w] = ld_cluster_f32(mapa_shared(l_a + 4u * rr, w));
+                                f[n][w] = ld_cluster_v4(mapa_shared(base + G::kRing + part_off<D>(rr, at % kItems), w));
+                            }
+                        }
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        const int at = it + n * step, rr = at / kItems;
+                        float M = -INFINITY, L = 0.f;
+#pragma unroll
+                        for (int w = 0; w < W; ++w) M = fmaxf(M, mw[n][w]);
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            const bool none = mw[n][w] == -INFINITY && lw[n][w] == 0.f;        // no key in this part
+                            const float e = none ? 0.f : fast_exp2(mw[n][w] - M);
+                            L = fmaf(e, lw[n][w], L);
+                            acc.x = none ? acc.x : fmaf(e, f[n][w].x, acc.x);
+                            acc.y = none ? acc.y : fmaf(e, f[n][w].y, acc.y);
+                            acc.z = none ? acc.z : fmaf(e, f[n][w].z, acc.z);
+                            acc.w = none ? acc.w : fmaf(e, f[n][w].w, acc.w);
+                        }
+                        const float inv = L == 0.f ? 0.f : kUnshift / L;
+                        const uint32_t pr = (uint32_t)(row0 + rr), i = pr / (uint32_t)p.g;
+                        __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                        if (at < n_items) {
+                            bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D + at % kItems * 4;
+                            *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
+                        }
                     }
                 }
-#pragma unroll
-                for (int w = 0; w < kMaxCluster; ++w) M = fmaxf(M, mw[w]);
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kMaxCluster; ++w) {
-                    const bool none = mw[w] == -INFINITY && lw[w] == 0.f;        // no key in this part
-                    const float e = none ? 0.f : fast_exp2(mw[w] - M);
-                    L = fmaf(e, lw[w], L);
-                    acc.x = none ? acc.x : fmaf(e, f[w].x, acc.x);
-                    acc.y = none ? acc.y : fmaf(e, f[w].y, acc.y);
-                    acc.z = none ? acc.z : fmaf(e, f[w].z, acc.z);
-                    acc.w = none ? acc.w : fmaf(e, f[w].w, acc.w);
-                }
-                const float inv = L == 0.f ? 0.f : kUnshift / L;
-                const uint32_t pr = (uint32_t)(row0 + rr), i = pr / (uint32_t)p.g;
-                bf16* o = p.out + ((qbase + i) * p.Hq + (int64_t)hk * p.g + (pr - i * (uint32_t)p.g)) * D + q4 * 4;
-                __nv_bfloat162 a2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-                *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<uint32_t*>(&a2), *reinterpret_cast<uint32_t*>(&b2));
-            }
+            };
+            if (cs <= 2) finalise(std::integral_constant<int, 2>{});
+            else if (cs <= 4) finalise(std::integral_constant<int, 4>{});
+            else finalise(std::integral_constant<int, 8>{});
             __syncwarp();
             cluster_sync();        // no CTA may leave while another still reads its shared memory
         }
@@ -927,9 +944,10 @@ int launch_q8_tc_attention(const Q8Attn& c) {
     prm.scale_log2 = c.a.scale * kLog2e;
     prm.budget = wait_budget();
     // Parts of the key range: waves x what a CTA takes, in thirds of a key tile against two row tiles (1.9 us at
-    // d = 128; against one, two thirds of that).  A CTA costs 16 (12) besides its keys, the launch and the merge
-    // of a cluster 8 (5) a doubling and once more.  (Measured: 600 rows x 3000 keys, 8 heads over 2: 56,
-    // 44, 38 and 72 us for 1, 2, 4 and 8 parts; 300 x 700, 4 heads: 23, 25, 27, 27; 100 x 2000, 16 heads: 31, 25, 23, 42.)
+    // d = 128; against one, two thirds of that).  A CTA costs 16 (12) besides its keys, a cluster's merge 11 (7).
+    // (Measured for 1, 2, 4 and 8 parts: 600 rows x 3000 keys, 8 heads over 2: 56, 41, 29 and 42 us; 300 x 700,
+    // 4 heads: 23, 23, 21, 21; 200 x 500, 2 requests, 32 heads over 8: 21, 23, 35, 35; 100 x 2000, 16 heads:
+    // 31, 25, 19, 29.)
     const int n_all = (c.T_len + kBN - 1) / kBN;
     const int64_t units = (int64_t)c.B * hkv * n_rb;
     const bool two = (int64_t)c.n_q * g > kBM;
@@ -937,7 +955,7 @@ int launch_q8_tc_attention(const Q8Attn& c) {
     int64_t best = 0;
     for (int i = 0, cs = 1; cs <= kMaxCluster && cs <= n_all; ++i, cs *= 2) {
         const int64_t slots = cluster_slots(i);
-        const int64_t cta = (two ? 3 : 2) * ((n_all + cs - 1) / cs) + (two ? 16 : 12) + (i ? (two ? 8 : 5) * (i + 1) : 0);
+        const int64_t cta = (two ? 3 : 2) * ((n_all + cs - 1) / cs) + (two ? 16 : 12) + (cs == 1 ? 0 : two ? 11 : 7);
         const int64_t est = (units * cs + slots - 1) / slots * cta;
         if (cs == 1 || est < best) {
             best = est;

@@ -597,7 +597,7 @@ int launch_q8_decode_attention(const Q8Attn& c) {
     const int64_t units = (int64_t)c.B * hkv, slots = (int64_t)sm_count() * ctas_per_sm(rows <= 8 ? 1 : rows <= 16 ? 2 : 4);
     prm.cs = 1;
     int64_t best = 0;
-    for (int cs = 1; cs <= kMaxCluster && cs <= n_ch; cs *= 2) {
+    for (int cs = 1; cs <= kMaxCluster && cs <= n_ch; ++cs) {
         const int64_t per = (n_ch + cs * kWarps - 1) / (cs * kWarps) + kFix + (cs > 1 ? kMerge : 0);
         int64_t est = ((units * cs + slots - 1) / slots) * per;
         if (c.q_start) est = std::max(per, (units * (n_ch / (8 * kWarps) + kFix + (cs > 1 ? kMerge : 0)) + slots - 1) / slots);

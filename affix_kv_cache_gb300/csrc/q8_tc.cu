@@ -879,30 +879,30 @@ int launch(const Q8Params& prm, dim3 grid, cudaStream_t stream, bool pdl) {
     return launch_status();
 }
 
-// CTAs of the kernel that run at once in clusters of 2^i: a cluster stays within a group of SMs, and the groups
-// are no multiples of 4 or 8 (152, 152, 144 and 120 CTAs).
-std::atomic<int> g_slots[4][64];
-int cluster_slots(int i) {
+// CTAs of the kernel that run at once in clusters of cs: a cluster stays within a group of SMs, and the groups are
+// no multiples of most sizes (152 SMs hold 152, 144 and 120 CTAs in clusters of 2, 4 and 8).
+std::atomic<int> g_slots[kMaxCluster + 1][64];
+int cluster_slots(int cs) {
     int dev = 0;
-    if (i == 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
-    std::atomic<int>& known = g_slots[i][dev];
+    if (cs == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
+    std::atomic<int>& known = g_slots[cs][dev];
     int n = known.load(std::memory_order_relaxed);
     if (n) return n;
     n = sm_count();
     if (prepare<128, false>() == ACACHE_OK) {
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 1u << i;
+        attr.val.clusterDim.x = (unsigned)cs;
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(1u << i);
+        cfg.gridDim = dim3((unsigned)cs);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = Geo<128>::kBytes;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int clusters = 0;
         if (cudaOccupancyMaxActiveClusters(&clusters, q8_attn_kernel<128, false>, &cfg) == cudaSuccess && clusters > 0)
-            n = clusters << i;
+            n = clusters * cs;
         else
             (void)cudaGetLastError();
     }
@@ -953,8 +953,8 @@ int launch_q8_tc_attention(const Q8Attn& c) {
     const bool two = (int64_t)c.n_q * g > kBM;
     prm.cs = 1;
     int64_t best = 0;
-    for (int i = 0, cs = 1; cs <= kMaxCluster && cs <= n_all; ++i, cs *= 2) {
-        const int64_t slots = cluster_slots(i);
+    for (int cs = 1; cs <= kMaxCluster && cs <= n_all; ++cs) {
+        const int64_t slots = cluster_slots(cs);
         const int64_t cta = (two ? 3 : 2) * ((n_all + cs - 1) / cs) + (two ? 16 : 12) + (cs == 1 ? 0 : two ? 11 : 7);
         const int64_t est = (units * cs + slots - 1) / slots * cta;
         if (cs == 1 || est < best) {

@@ -36,10 +36,10 @@
 //
 // What bounds it.  16 requests x 986 rows x 2,624 keys, 28 heads over 4, d = 128: 555 us, 1,070 TFLOP/s, 0.55 of the
 // measured bf16 rate.  A step of 64 keys takes both chains some 1,800 cycles; their MMAs alone take 1,260
-// (2 x 385 for S, whose 64-key products read 6 KB of shared memory in the 32 cycles they need 4 KB's worth
-// of, and 2 x 257 for PV).  No pipe is full (ALU 0.38, FMA 0.27, MUFU 0.21); what comes nearest is shared memory: the
+// (2 x 385 for S, whose 64-key MMAs read 6 KB of shared memory, 48 cycles, for 32 cycles of products, and
+// 2 x 257 for PV).  No pipe is full (ALU 0.38, FMA 0.27, MUFU 0.21); what comes nearest is shared memory: the
 // MMAs' operands, the keys' factors (every softmax warp reads all of them), V's tiles and K's take some
-// 1,700 of the 1,800 cycles between them, so two softmax warps per scheduler cannot cover their waits, and
+// 1,700 of the 1,800 cycles by count, so two softmax warps per scheduler cannot cover their waits, and
 // whatever a softmax warp waits for on its own account shows -- a barrier for the keys' factors cost 7 %,
 // per-lane arrivals 1 %.  A block costs some 15,000 cycles besides its steps (launch and set-up 4,000, the
 // query terms 6,000, first S 2,000, drain and epilogue 4,000).  Slower were: S of 128 keys at a time, which needs

@@ -249,6 +249,25 @@ def test_masked_bad_and_poisoned_keys(dtype, d, n_q, T):
     assert_attention(got[1], want, tol, "beside a poisoned request")
 
 
+# few rows, so that the keys are split over as many CTAs as there are tiles of 128 (or chunks of 64), up to 8
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q", [1, 70, 150])
+@pytest.mark.parametrize("T", [129, 330, 600, 750, 890, 1100])
+@pytest.mark.parametrize("drop", [False, True])
+def test_any_number_of_parts(d, n_q, T, drop):
+    hq, hkv = 1, 1
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(1, n_q, hq, hkv, d, BF16, T, drop, 7 * T + n_q)
+    if drop:
+        rs[0, 128:256] = -1                                     # a part that may hold no key at all
+    args = (_desc(hq, hkv, d, BF16), 1, n_q, dev(q), T, dev(rs), dev(kc), dev(vc), dev(sc), ns)
+    out, again = (torch.empty(q.shape, dtype=BF16, device="cuda") for _ in range(2))
+    for o in (out, again):
+        ac.acache_slot_attention_q8(*args, o, drop_none=drop)
+    want, tol = attention(q[0], rs[0].numpy(), kv, vv, d ** -0.5, drop)
+    assert_attention(out[0].double().cpu().numpy(), want, tol)
+    assert torch.equal(out, again)                              # parts are merged in a fixed order
+
+
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
 @pytest.mark.parametrize("n_q", [1, 40, 300])
 def test_a_poisoned_key_among_discarded_ones_is_not_lost(dtype, d, n_q):

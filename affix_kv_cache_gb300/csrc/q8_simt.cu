@@ -6,8 +6,11 @@
 // group share one pass over the keys -- and per part of the key range: 64-key tiles are decoded to
 // float32 in shared memory, S = Q K^T and O += P V run as 4 x 4 and 4 x d/16 register tiles, and
 // the softmax keeps a running maximum and sum per row in base 2.  Bound by FFMA issue and the
-// shared-memory reads that feed it; two CTAs per SM.  When there are few blocks the key range is
-// split over a cluster of up to 8 CTAs, which merge their partial (maximum, sum, O) through
+// shared-memory reads that feed it; two CTAs per SM.  With at most 32 or 16 rows to a (request, KV
+// head) a CTA takes that many, with as many fewer threads: the products of 64 rows would be mostly of
+// rows that are not there (8 single tokens over 4,000 keys, 32 heads over 8, d = 128, float32: 142 us, 308 in
+// tiles of 64; 4 x 32 rows over 1,408 keys, 8 heads: 48 and 115).  When there are few blocks the key range
+// is split over a cluster of up to 8 CTAs, which merge their partial (maximum, sum, O) through
 // distributed shared memory in rank order.
 #include "q8.cuh"
 #include "ptx.cuh"
@@ -15,8 +18,7 @@
 namespace acache {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBM = 64, kBN = 64;
+constexpr int kBN = 64;                     // keys per tile; 4 threads to a row
 constexpr int kMaxCluster = 8;
 
 struct SimtParams {
@@ -31,7 +33,7 @@ struct SimtParams {
     float scale_log2;
 };
 
-template <int D>
+template <int D, int kBM>
 struct SimtSmem {
     float q[D][kBM];          // transposed; the partial O of a split key range afterwards
     float k[D][kBN];          // transposed
@@ -42,11 +44,12 @@ struct SimtSmem {
     float m[kBM], l[kBM];
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int D, int kBM>
+__global__ void __launch_bounds__(4 * kBM)
 q8_simt_kernel(const SimtParams p) {
+    constexpr int kThreads = 4 * kBM;
     extern __shared__ __align__(16) uint8_t raw[];
-    SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
+    SimtSmem<D, kBM>& sm = *reinterpret_cast<SimtSmem<D, kBM>*>(raw);
     constexpr int NC = D / 64;                          // 4-column chunks of O per thread
     const int cr = (int)(blockIdx.x % (unsigned)p.cs), hk = (int)(blockIdx.x / (unsigned)p.cs);
     const int b = (int)blockIdx.y;
@@ -86,28 +89,33 @@ q8_simt_kernel(const SimtParams p) {
 #pragma unroll
         for (int x = 0; x < NC * 4; ++x) acc[y][x] = 0.f;
     }
+    // slots and exponents of a tile's keys, looked up a tile ahead
+    int64_t row = -2;
+    uint32_t two = 0;
+    auto look_up = [&](int j) {
+        const int t = j * kBN + tid;
+        row = -2;
+        two = 0;
+        if (j < j1 && tid < kBN && t < T_len) {
+            const int64_t s = p.read_slot[kbase + t];
+            if (s >= 0 && s < p.num_slots) {
+                row = s * p.Hkv + hk;
+                two = reinterpret_cast<const uint16_t*>(p.kv_scale)[row];
+            } else if (!(p.drop_none && s == ACACHE_SLOT_NONE)) {
+                row = -1;
+                flag(p.dev_status, ACACHE_DEV_BAD_SLOT);
+            }
+        }
+    };
+    look_up(j0);
     for (int j = j0; j < j1; ++j) {
         __syncthreads();                                // the last tile has been read
         if (tid < kBN) {
-            const int t = j * kBN + tid;
-            int64_t row = -2;
-            float ks = 0.f, vs = 0.f;
-            if (t < T_len) {
-                const int64_t s = p.read_slot[kbase + t];
-                if (s >= 0 && s < p.num_slots) {
-                    row = s * p.Hkv + hk;
-                    const uint32_t two = reinterpret_cast<const uint16_t*>(p.kv_scale)[row];
-                    ks = q8_factor(two & 0xffu);
-                    vs = q8_factor(two >> 8);
-                } else if (!(p.drop_none && s == ACACHE_SLOT_NONE)) {
-                    row = -1;
-                    flag(p.dev_status, ACACHE_DEV_BAD_SLOT);
-                }
-            }
             sm.row[tid] = row;
-            sm.ks[tid] = ks;
-            sm.vs[tid] = vs;
+            sm.ks[tid] = row >= 0 ? q8_factor(two & 0xffu) : 0.f;
+            sm.vs[tid] = row >= 0 ? q8_factor(two >> 8) : 0.f;
         }
+        look_up(j + 1);
         __syncthreads();
 #pragma unroll
         for (int it = 0; it < kBN * D / 16 / kThreads; ++it) {
@@ -261,17 +269,17 @@ q8_simt_kernel(const SimtParams p) {
     ptx::cluster_sync();       // no CTA may leave while another still reads its shared memory
 }
 
-template <typename T, int D>
+template <typename T, int D, int kBM>
 int launch(const SimtParams& prm, dim3 grid, cudaStream_t stream) {
-    auto kern = q8_simt_kernel<T, D>;
-    constexpr int smem = (int)sizeof(SimtSmem<D>);
+    auto kern = q8_simt_kernel<T, D, kBM>;
+    constexpr int smem = (int)sizeof(SimtSmem<D, kBM>);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(4 * kBM);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -288,11 +296,18 @@ int launch(const SimtParams& prm, dim3 grid, cudaStream_t stream) {
     return launch_status();
 }
 
+template <typename T, int D>
+int launch(const SimtParams& prm, int bm, dim3 grid, cudaStream_t stream) {
+    return bm == 16 ? launch<T, D, 16>(prm, grid, stream) : bm == 32 ? launch<T, D, 32>(prm, grid, stream) : launch<T, D, 64>(prm, grid, stream);
+}
+
 }  // namespace
 
 int launch_q8_simt_attention(const Q8Attn& c) {
     const int g = c.a.hq / c.a.hkv;
-    const int64_t n_rb = ((int64_t)c.n_q * g + kBM - 1) / kBM;
+    const int64_t rows = (int64_t)c.n_q * g;
+    const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    const int64_t n_rb = (rows + bm - 1) / bm;
     SimtParams prm{};
     prm.q = c.q;
     prm.k_cache = c.k_cache;
@@ -312,15 +327,16 @@ int launch_q8_simt_attention(const Q8Attn& c) {
     prm.g = g;
     prm.drop_none = c.drop_none;
     prm.scale_log2 = c.a.scale * kLog2e;
-    // split the keys while the parts still fit in one wave (two CTAs per SM) and have two tiles each
+    // split the keys while the parts still fit in one wave (two CTAs per SM: their tiles of K and V take 64 KB
+    // whatever the rows) and have two tiles each
     const int64_t units = (int64_t)c.B * c.a.hkv * n_rb, tiles = (c.T_len + kBN - 1) / kBN;
     prm.cs = 1;
     while (prm.cs < kMaxCluster && units * prm.cs * 2 <= 2 * (int64_t)sm_count() && tiles >= 4 * prm.cs) prm.cs *= 2;
     const dim3 grid((unsigned)(c.a.hkv * prm.cs), (unsigned)c.B, (unsigned)n_rb);
     if (c.a.dtype == ACACHE_F32)
-        return c.a.d == 64 ? launch<float, 64>(prm, grid, c.stream) : launch<float, 128>(prm, grid, c.stream);
-    return c.a.d == 64 ? launch<__nv_bfloat16, 64>(prm, grid, c.stream)
-                       : launch<__nv_bfloat16, 128>(prm, grid, c.stream);
+        return c.a.d == 64 ? launch<float, 64>(prm, bm, grid, c.stream) : launch<float, 128>(prm, bm, grid, c.stream);
+    return c.a.d == 64 ? launch<__nv_bfloat16, 64>(prm, bm, grid, c.stream)
+                       : launch<__nv_bfloat16, 128>(prm, bm, grid, c.stream);
 }
 
 }  // namespace acache

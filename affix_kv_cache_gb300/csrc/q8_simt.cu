@@ -12,6 +12,9 @@
 // tiles of 64; 4 x 32 rows over 1,408 keys, 8 heads: 48 and 115).  When there are few blocks the key range
 // is split over a cluster of up to 8 CTAs, which merge their partial (maximum, sum, O) through
 // distributed shared memory in rank order.
+#include <algorithm>
+#include <atomic>
+
 #include "q8.cuh"
 #include "ptx.cuh"
 
@@ -245,19 +248,30 @@ q8_simt_kernel(const SimtParams p) {
     const uint32_t m_a = ptx::smem_u32(&sm.m[0]), l_a = ptx::smem_u32(&sm.l[0]), o_a = ptx::smem_u32(part);
     for (int x = tid; x < ((rows - cr + cs - 1) / cs) * (D / 4); x += kThreads) {
         const int r = cr + (x / (D / 4)) * cs, c = x % (D / 4);
-        float M = -INFINITY;
-        for (int w = 0; w < cs; ++w) M = fmaxf(M, ptx::ld_cluster_f32(ptx::mapa_shared(m_a + 4u * r, w)));
+        float pm[kMaxCluster], pl[kMaxCluster], M = -INFINITY, L = 0.f;
+        float4 po[kMaxCluster], O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kMaxCluster; ++w) {                 // all ranks' loads in flight
+            pm[w] = -INFINITY;
+            pl[w] = 0.f;
+            po[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w < cs) {
+                pm[w] = ptx::ld_cluster_f32(ptx::mapa_shared(m_a + 4u * r, w));
+                pl[w] = ptx::ld_cluster_f32(ptx::mapa_shared(l_a + 4u * r, w));
+                po[w] = ptx::ld_cluster_v4(ptx::mapa_shared(o_a + (uint32_t)(r * D + 4 * c) * 4u, w));
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < kMaxCluster; ++w) M = fmaxf(M, pm[w]);
         const float ref = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < cs; ++w) {
-            const float e = fast_exp2(ptx::ld_cluster_f32(ptx::mapa_shared(m_a + 4u * r, w)) - ref);
-            const float4 o = ptx::ld_cluster_v4(ptx::mapa_shared(o_a + (uint32_t)(r * D + 4 * c) * 4u, w));
-            L = fmaf(e, ptx::ld_cluster_f32(ptx::mapa_shared(l_a + 4u * r, w)), L);
-            O.x = fmaf(e, o.x, O.x);
-            O.y = fmaf(e, o.y, O.y);
-            O.z = fmaf(e, o.z, O.z);
-            O.w = fmaf(e, o.w, O.w);
+#pragma unroll
+        for (int w = 0; w < kMaxCluster; ++w) {
+            const float e = fast_exp2(pm[w] - ref);
+            L = fmaf(e, pl[w], L);
+            O.x = fmaf(e, po[w].x, O.x);
+            O.y = fmaf(e, po[w].y, O.y);
+            O.z = fmaf(e, po[w].z, O.z);
+            O.w = fmaf(e, po[w].w, O.w);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         T* o = (T*)p.out + q_off(r) + 4 * c;
@@ -269,25 +283,55 @@ q8_simt_kernel(const SimtParams p) {
     ptx::cluster_sync();       // no CTA may leave while another still reads its shared memory
 }
 
+// CTAs of a variant that run at once in clusters of cs (a cluster stays within a group of SMs), per device.
+std::atomic<int> g_slots[2][3][kMaxCluster + 1][64];
+
 template <typename T, int D, int kBM>
-int launch(const SimtParams& prm, dim3 grid, cudaStream_t stream) {
+int launch(SimtParams prm, const Q8Attn& c) {
     auto kern = q8_simt_kernel<T, D, kBM>;
     constexpr int smem = (int)sizeof(SimtSmem<D, kBM>);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
     cfg.blockDim = dim3(4 * kBM);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
+    cfg.stream = c.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)prm.cs;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // Parts of the key range: waves x (tiles of a part, a CTA's own cost of about one and as much for a merge)
+    const int64_t n_rb = ((int64_t)c.n_q * prm.g + kBM - 1) / kBM, units = (int64_t)c.B * prm.Hkv * n_rb;
+    const int tiles = (c.T_len + kBN - 1) / kBN;
+    int64_t best = 0;
+    for (int cs = 1; cs <= kMaxCluster && cs <= tiles; ++cs) {
+        std::atomic<int>& known = g_slots[D == 128][kBM == 16 ? 0 : kBM == 32 ? 1 : 2][cs][dev];
+        int slots = known.load(std::memory_order_relaxed);
+        if (!slots) {
+            int clusters = 0;
+            cfg.gridDim = dim3((unsigned)cs);
+            attr[0].val.clusterDim.x = (unsigned)cs;
+            if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
+                (void)cudaGetLastError();
+                clusters = std::max(1, sm_count() / cs);
+            }
+            slots = clusters * cs;
+            known.store(slots, std::memory_order_relaxed);
+        }
+        const int64_t est = (units * cs + slots - 1) / slots * ((tiles + cs - 1) / cs + 1 + (cs > 1));
+        if (cs == 1 || est < best) {
+            best = est;
+            prm.cs = cs;
+        }
+    }
+    cfg.gridDim = dim3((unsigned)(prm.Hkv * prm.cs), (unsigned)c.B, (unsigned)n_rb);
+    attr[0].val.clusterDim.x = (unsigned)prm.cs;
     cfg.numAttrs = prm.cs > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kern, prm) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -297,17 +341,15 @@ int launch(const SimtParams& prm, dim3 grid, cudaStream_t stream) {
 }
 
 template <typename T, int D>
-int launch(const SimtParams& prm, int bm, dim3 grid, cudaStream_t stream) {
-    return bm == 16 ? launch<T, D, 16>(prm, grid, stream) : bm == 32 ? launch<T, D, 32>(prm, grid, stream) : launch<T, D, 64>(prm, grid, stream);
+int launch(const SimtParams& prm, const Q8Attn& c) {
+    const int64_t rows = (int64_t)c.n_q * prm.g;
+    return rows <= 16 ? launch<T, D, 16>(prm, c) : rows <= 32 ? launch<T, D, 32>(prm, c) : launch<T, D, 64>(prm, c);
 }
 
 }  // namespace
 
 int launch_q8_simt_attention(const Q8Attn& c) {
     const int g = c.a.hq / c.a.hkv;
-    const int64_t rows = (int64_t)c.n_q * g;
-    const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    const int64_t n_rb = (rows + bm - 1) / bm;
     SimtParams prm{};
     prm.q = c.q;
     prm.k_cache = c.k_cache;
@@ -327,16 +369,8 @@ int launch_q8_simt_attention(const Q8Attn& c) {
     prm.g = g;
     prm.drop_none = c.drop_none;
     prm.scale_log2 = c.a.scale * kLog2e;
-    // split the keys while the parts still fit in one wave (two CTAs per SM: their tiles of K and V take 64 KB
-    // whatever the rows) and have two tiles each
-    const int64_t units = (int64_t)c.B * c.a.hkv * n_rb, tiles = (c.T_len + kBN - 1) / kBN;
-    prm.cs = 1;
-    while (prm.cs < kMaxCluster && units * prm.cs * 2 <= 2 * (int64_t)sm_count() && tiles >= 4 * prm.cs) prm.cs *= 2;
-    const dim3 grid((unsigned)(c.a.hkv * prm.cs), (unsigned)c.B, (unsigned)n_rb);
-    if (c.a.dtype == ACACHE_F32)
-        return c.a.d == 64 ? launch<float, 64>(prm, bm, grid, c.stream) : launch<float, 128>(prm, bm, grid, c.stream);
-    return c.a.d == 64 ? launch<__nv_bfloat16, 64>(prm, bm, grid, c.stream)
-                       : launch<__nv_bfloat16, 128>(prm, bm, grid, c.stream);
+    if (c.a.dtype == ACACHE_F32) return c.a.d == 64 ? launch<float, 64>(prm, c) : launch<float, 128>(prm, c);
+    return c.a.d == 64 ? launch<__nv_bfloat16, 64>(prm, c) : launch<__nv_bfloat16, 128>(prm, c);
 }
 
 }  // namespace acache

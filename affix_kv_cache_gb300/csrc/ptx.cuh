@@ -335,8 +335,11 @@ ACACHE_DEVFN float4 ld_cluster_v4(uint32_t addr) {
     return v;
 }
 // Every thread of every CTA of the cluster executes both halves (release / acquire order the
-// shared-memory writes before the barrier with the remote reads after it).
+// shared-memory writes before the barrier with the remote reads after it).  The aligned form is a
+// whole warp's instruction, so the warp comes together first: callers reach this behind loops whose
+// trip counts differ between lanes.
 ACACHE_DEVFN void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -679,3 +679,22 @@ def test_a_tensor_off_the_current_device_is_refused():
     out = torch.empty(q.shape, dtype=BF16, device="cuda")
     with pytest.raises(ValueError, match="current device"):
         ac.acache_slot_attention_q8(_desc(4, 2, 128, BF16), 1, 6, dev(q), 130, dev(rs), kc, vc, sc, ns, out)
+
+
+@pytest.mark.parametrize("dtype,scale", [(F32, None), (BF16, -0.125)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q", [1, 3, 5, 17, 33])
+def test_merges_whose_lanes_take_different_numbers_of_turns(dtype, scale, d, n_q):
+    """CUDA-core kernel, keys split over a cluster, an odd number of rows: in the merge some lanes of a
+    warp finalise one item more than the others before the whole warp reaches the cluster's barrier."""
+    hq, hkv, T = 1, 1, 1100
+    scale = d ** -0.5 if scale is None else scale
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(2, n_q, hq, hkv, d, dtype, T, False, 3 * n_q + d)
+    args = (_desc(hq, hkv, d, dtype, scale), 2, n_q, dev(q), T, dev(rs), dev(kc), dev(vc), dev(sc), ns)
+    outs = [torch.empty(q.shape, dtype=dtype, device="cuda") for _ in range(3)]
+    for o in outs:
+        ac.acache_slot_attention_q8(*args, o)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    for b in range(2):
+        want, tol = attention(q[b], rs[b].numpy(), kv, vv, scale)
+        assert_attention(outs[0][b].double().cpu().numpy(), want, tol, f"request {b}")

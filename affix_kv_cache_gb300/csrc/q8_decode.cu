@@ -54,6 +54,8 @@ constexpr float kPHead = 3.0f;              // P of the used maximum is 2^3 ...
 constexpr float kRescaleThreshold = 12.0f;  // ... and never above 2^15
 constexpr float kNoMax = -1e38f;            // maximum before any key; a key that takes no part lies below it
 constexpr uint32_t kNoEv = 0xff610000u;     // bf16 -2.99e38: its ev
+constexpr uint32_t kZeroEv = 0xc2480000u;   // bf16 -50: ev of a row of zeros
+static_assert(kQ8MinExp == -50, "kZeroEv");
 
 struct DecParams {
     const bf16* q;
@@ -204,7 +206,9 @@ q8_decode_kernel(const DecParams p) {
             return (k > kQ8MaxByte ? 0x7fffu : k << 7) | (ev & 0xffff0000u);
         }
         if (slot == kNoKey || (p.drop && slot == ACACHE_SLOT_NONE)) return kNoEv;
-        return 0x3f80u;                              // outside the pool: a zero row that counts
+        // outside the pool: a zero row that counts, with the exponent a stored one has (a larger one would raise
+        // the maximum of s + ev over the rows that hold something, and their P would lose its bits)
+        return 0x3f80u | kZeroEv;
     };
     auto load_scale = [&](int slot) -> uint32_t {
         uint32_t sc = 0;

@@ -698,3 +698,26 @@ def test_merges_whose_lanes_take_different_numbers_of_turns(dtype, scale, d, n_q
     for b in range(2):
         want, tol = attention(q[b], rs[b].numpy(), kv, vv, scale)
         assert_attention(outs[0][b].double().cpu().numpy(), want, tol, f"request {b}")
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("n_q", [1, 32, 40, 300])
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e-6, 1e-12])
+def test_bad_slots_beside_small_values(dtype, d, n_q, size):
+    """A zero row has no size: however small the other rows' values are, it takes only its share of the
+    softmax."""
+    hq, hkv, T, ns = 2, 1, 70, 200
+    g = torch.Generator().manual_seed(23)
+    x = [torch.randn((ns, hkv, d), generator=g) * f for f in (1.0, size)]
+    (kc, ks, _), (vc, vs, _) = quantise(x[0]), quantise(x[1])
+    kv, vv = values(kc, ks), values(vc, vs)
+    sc = torch.from_numpy(np.stack((ks, vs), -1)).contiguous()
+    q = (1.5 * torch.randn((1, n_q, hq, d), generator=g)).to(dtype)
+    rs = torch.randperm(ns, generator=g)[None, :T].to(torch.int32)
+    rs[0, [0, 17, 40, T - 1]] = torch.tensor([-1, ns, -9, 2 ** 31 - 1], dtype=torch.int32)
+    out, st = torch.empty(q.shape, dtype=dtype, device="cuda"), _status()
+    ac.acache_slot_attention_q8(_desc(hq, hkv, d, dtype), 1, n_q, dev(q), T, dev(rs), dev(torch.from_numpy(kc)),
+                                dev(torch.from_numpy(vc)), dev(sc), ns, out, dev_status=st)
+    want, tol = attention(q[0], rs[0].numpy(), kv, vv, d ** -0.5)
+    assert_attention(out[0].double().cpu().numpy(), want, tol)
+    assert st.item() == _lib.DEV_BAD_SLOT

@@ -176,7 +176,7 @@ q8_decode_kernel(const DecParams p) {
     // lanes 0-15 look after the keys of a chunk (16-31 repeat them)
     auto slot_of = [&](int ch) -> int {
         const int key = ch * kChunk + (lane & 15);
-        int s = kNoKey;
+        int s = -1;
         if (ch < ch1 && key < T_len) s = p.read_slot[kbase + key];
         return s;
     };
@@ -197,15 +197,15 @@ q8_decode_kernel(const DecParams p) {
     const uint8_t* ksrc = p.k_cache + (int64_t)hk * D + pc * 16;
     const uint8_t* vsrc = p.v_cache + (int64_t)hk * D + pc * 16;
     const uint32_t ring = smem_u32(&sm.ring[warp][0][0][0]);
-    // 2^ek as bf16 with ev as bf16 above it, of this lane's key
-    auto factors = [&](int slot, uint32_t sc) -> uint32_t {
+    // 2^ek as bf16 with ev as bf16 above it, of this lane's key; past: it lies behind the request's last
+    auto factors = [&](int slot, uint32_t sc, bool past) -> uint32_t {
         if (slot >= 0 && slot < p.num_slots) {
             const uint32_t k = sc & 0xffu, v = sc >> 8;
             const uint32_t ev = v > kQ8MaxByte ? 0x7fff0000u
                                                : __float_as_uint((float)((int)max(v, (uint32_t)(kQ8MinExp + 127)) - 127));
             return (k > kQ8MaxByte ? 0x7fffu : k << 7) | (ev & 0xffff0000u);
         }
-        if (slot == kNoKey || (p.drop && slot == ACACHE_SLOT_NONE)) return kNoEv;
+        if (past || (p.drop && slot == ACACHE_SLOT_NONE)) return kNoEv;
         // outside the pool: a zero row that counts, with the exponent a stored one has (a larger one would raise
         // the maximum of s + ev over the rows that hold something, and their P would lose its bits)
         return 0x3f80u | kZeroEv;
@@ -271,8 +271,9 @@ q8_decode_kernel(const DecParams p) {
         bring(s2, ring + at2 * (2 * kChunk * D));
         cp_async_commit();
         sc2 = load_scale(s2);
-        const uint32_t fe_own = factors(s0, sc0);
-        if (s0 != kNoKey && (s0 < 0 || s0 >= p.num_slots) && !(p.drop && s0 == ACACHE_SLOT_NONE))
+        const bool past = ch * kChunk + (lane & 15) >= T_len;
+        const uint32_t fe_own = factors(s0, sc0, past);
+        if (!past && (s0 < 0 || s0 >= p.num_slots) && !(p.drop && s0 == ACACHE_SLOT_NONE))
             flag(p.dev_status, ACACHE_DEV_BAD_SLOT);
         s0 = s1;
         s1 = s2;

@@ -371,22 +371,23 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             auto load_slots = [&](int e, int (&raw)[4]) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    raw[u] = kNoKey;
+                    raw[u] = -1;
                     if (e < n_kv) {
                         const int t = (kt0 + sch.entry_tile(e)) * kBN + 4 * lane + u;
                         if (t < T_len) raw[u] = p.read_slot[kbase + t];
                     }
                 }
             };
-            auto resolve = [&](const int (&raw)[4], int (&rows)[4], int& slot0, uint32_t& gone) -> bool {
+            auto resolve = [&](int e, const int (&raw)[4], int (&rows)[4], int& slot0, uint32_t& gone) -> bool {
                 int sl[4];
+                const int left = T_len - (kt0 + sch.entry_tile(e)) * kBN - 4 * lane;   // keys from the lane's first on
                 gone = 0;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const bool in = raw[u] >= 0 && raw[u] < p.num_slots;
                     sl[u] = in ? raw[u] : -1;
                     if (kDrop && raw[u] == ACACHE_SLOT_NONE) gone |= 1u << u;
-                    else if (!in && raw[u] != kNoKey && pi == 0) flag(dev_status, ACACHE_DEV_BAD_SLOT);
+                    else if (!in && u < left && pi == 0) flag(dev_status, ACACHE_DEV_BAD_SLOT);
                 }
                 bool run = sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
                 const int after = __shfl_down_sync(0xffffffffu, sl[0], 1);
@@ -414,7 +415,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
             int raw[4], rows[4], slot0;
             uint32_t sc[4], gone;
             load_slots(0, raw);
-            bool box = resolve(raw, rows, slot0, gone);
+            bool box = resolve(0, raw, rows, slot0, gone);
             load_slots(1, raw);
             grid_dependency_wait();
             load_scales(rows, sc);
@@ -448,7 +449,7 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.k_full[s]);
                 if (e + 1 < n_kv) {
-                    box = resolve(raw, rows, slot0, gone);
+                    box = resolve(e + 1, raw, rows, slot0, gone);
                     load_scales(rows, sc);
                     load_slots(e + 2, raw);
                 }

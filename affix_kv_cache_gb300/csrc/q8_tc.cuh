@@ -12,7 +12,6 @@ namespace q8 {
 using namespace ptx;
 using bf16 = __nv_bfloat16;
 
-constexpr int kNoKey = INT32_MIN;           // read-slot entry of a key past the request's last
 constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles, abort path
 
 // Bounded wait for a phase.  A try that finds the phase incomplete suspends the warp until it completes, for

@@ -721,3 +721,30 @@ def test_bad_slots_beside_small_values(dtype, d, n_q, size):
     want, tol = attention(q[0], rs[0].numpy(), kv, vv, d ** -0.5)
     assert_attention(out[0].double().cpu().numpy(), want, tol)
     assert st.item() == _lib.DEV_BAD_SLOT
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("n_q", [1, 32, 40, 300])
+@pytest.mark.parametrize("drop", [False, True])
+@pytest.mark.parametrize("slot", [-2 ** 31, -2 ** 31 + 1, -2, 2 ** 31 - 1])
+def test_every_value_outside_the_pool_is_a_flagged_zero_row(dtype, d, n_q, drop, slot):
+    """Nine keys, so that one key too few in a softmax shows; also the last of them, next to the keys that
+    are past the end."""
+    hq, hkv, T = 2, 1, 9
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(2, n_q, hq, hkv, d, dtype, T, False, 19)
+    rs[0, 3], rs[0, 8], rs[1, 0] = slot, slot, slot
+    if drop:
+        rs[0, 5] = -1
+    desc, pool = _desc(hq, hkv, d, dtype), (dev(kc), dev(vc), dev(sc), ns)
+    starts = [torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda") for n in (n_q, T)]
+    for ragged in (False, True):
+        out, st = torch.empty(q.shape, dtype=dtype, device="cuda"), _status()
+        if ragged:
+            ac.acache_slot_attention_varlen_q8(desc, 2, starts[0], n_q, 2 * n_q, dev(q), starts[1], T, dev(rs), *pool, out,
+                                               drop_none=drop, dev_status=st)
+        else:
+            ac.acache_slot_attention_q8(desc, 2, n_q, dev(q), T, dev(rs), *pool, out, drop_none=drop, dev_status=st)
+        for b in range(2):
+            want, tol = attention(q[b], rs[b].numpy(), kv, vv, d ** -0.5, drop)
+            assert_attention(out[b].double().cpu().numpy(), want, tol, f"request {b}")
+        assert st.item() == _lib.DEV_BAD_SLOT

@@ -51,7 +51,7 @@
 // Every mbarrier wait is bounded; a wait that gives up raises a CTA-wide abort flag and
 // ACACHE_DEV_TIMEOUT, roles leave their loops, MMAs in flight are drained, TMA loads issued before
 // it are waited for (bounded), TMEM is freed, the cluster barriers are reached on every path, and
-// no output of the block is written.
+// no output row is written that its steps have not all reached.
 #include <cuda.h>
 
 #include <algorithm>
@@ -660,7 +660,9 @@ q8_attn_kernel(const __grid_constant__ Q8Params p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.p_full[t][h]);
             }
-            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget));
+            // An issuer that gave up commits its drain too: only without an abort do all the steps stand behind it.
+            if (ok)
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget) && !*abort_flag);
         }
         // Split keys: chain A merges the two partial states (weight 0 for a chain without keys)
         float w_a = 1.f, w_b = 0.f;

@@ -95,8 +95,8 @@ ACACHE_API int acache_version(void);
  * Failure detection: the budget of the kernels' bounded waits (host, thread-safe).
  * Every wait of a tensor-core kernel's pipeline (a TMA load, an MMA, another role's hand-off)
  * gives up after `budget` SM clock cycles: the kernel then sets ACACHE_DEV_TIMEOUT in
- * dev_status, stops its work (its outputs are not written), lets the copies and MMAs it had
- * issued finish, releases its tensor memory and exits, so the context stays usable.  The
+ * dev_status, stops its work (output rows it has not finished are not written), lets the copies
+ * and MMAs it had issued finish, releases its tensor memory and exits, so the context stays usable.  The
  * page has no counterpart: this is the library's own watchdog.
  * cycles > 0 sets the budget of kernels launched after the call; cycles <= 0 only reads it.
  * Returns the budget in force before the call (default 2^31 cycles, about 1 s at 2.07 GHz).

@@ -695,8 +695,9 @@ tc_attn_kernel(const __grid_constant__ AttnParams p) {
             mbar_arrive(&ctl.p_full[t]);
             if (pingpong) mbar_arrive(&ctl.turn[t ^ 1]);
         }
-        // drain[t] is committed after the last PV of this chain
-        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget));
+        // drain[t] is committed after the last PV of this chain, and by an MMA thread that gave up: only without an
+        // abort do all the tiles stand behind it
+        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget) && !*abort_flag);
         // Split keys: chain B hands its row maximum and row sum to chain A, which merges the two
         // partial states -- O = O_A 2^(m_A - m) + O_B 2^(m_B - m) with m = max(m_A, m_B), the
         // sums alike -- and stores the rows.  A chain whose keys so far were all discarded has
@@ -1279,8 +1280,10 @@ tc_slot_persist_kernel(const __grid_constant__ AttnParams p) {
                 if (cfg >> 31) mbar_arrive(&ctl.turn[t ^ 1]);
             }
             // drain[t] is committed after the chain's last MMA of the unit (once per unit, also
-            // when the chain has no tile); then Q buffer t is free
-            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], (su >> 3) & 1u, &ctl.abort, p.dev_status, p.budget));
+            // when the chain has no tile); then Q buffer t is free.  (An MMA thread that gave up commits it too.)
+            if (ok)
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], (su >> 3) & 1u, &ctl.abort, p.dev_status, p.budget) &&
+                                                 !*abort_flag);
             // the unit's indices again (recomputed rather than held through the tile loop)
             int u2 = (int)(su >> 5);
             asm volatile("" : "+r"(u2));
@@ -1294,8 +1297,8 @@ tc_slot_persist_kernel(const __grid_constant__ AttnParams p) {
                     ctl.split_l[r] = l_sum;
                     mbar_arrive(&ctl.split_ready);
                 } else if (ok) {
-                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.split_ready, (su >> 4) & 1u, &ctl.abort, p.dev_status, p.budget)) &&
-                         !*abort_flag &&
+                    ok = __all_sync(0xffffffffu, wait_bar(&ctl.split_ready, (su >> 4) & 1u, &ctl.abort, p.dev_status, p.budget) &&
+                                                     !*abort_flag) &&
                          __all_sync(0xffffffffu, wait_bar(&ctl.drain[1], (su >> 3) & 1u, &ctl.abort, p.dev_status, p.budget));
                     if (ok) {
                         const float mb = ctl.split_m[r], lb = ctl.split_l[r];

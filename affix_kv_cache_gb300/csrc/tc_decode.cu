@@ -426,7 +426,8 @@ tc_decode_kernel(const __grid_constant__ DecParams p) {
             tc_fence_before();
             mbar_arrive(&ctl.p_full[sb]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain, 0, abort_flag, dev_status, budget));
+        // an issuer that gave up commits its drain too: only without an abort do all the tiles stand behind it
+        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain, 0, abort_flag, dev_status, budget) && !*abort_flag);
         if (ok) {
             tc_fence_after();
             if (REP == 1 && cs == 1) {
@@ -484,7 +485,11 @@ tc_decode_kernel(const __grid_constant__ DecParams p) {
     // Row r of the block has REP x cs partials: replica w of cluster rank q sits at lane
     // w*G + r of CTA q.  CTA q finalises the (row, 32-column chunk) items it = q (mod cs).
     if (cs > 1) cluster_sync(); else __syncthreads();
-    if (wg == 0 && !*abort_flag) {
+    // Nothing is written when a CTA of the cluster gave up: its partials are missing.
+    bool lost = *abort_flag != 0;
+    if (wg == 0 && cs > 1)
+        lost = __any_sync(0xffffffffu, lane < cs && __float_as_uint(ld_cluster_f32(mapa_shared(smem_u32(&ctl.abort), (uint32_t)lane))) != 0u);
+    if (wg == 0 && !lost) {
         const uint32_t part_base = base + kTileBytes;
         const uint32_t m_base = smem_u32(&ctl.part_m[0]), l_base = smem_u32(&ctl.part_l[0]);
         for (int it = cr + cs * (int)threadIdx.x; it < rows_valid * 4; it += cs * 128) {

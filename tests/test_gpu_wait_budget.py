@@ -115,3 +115,33 @@ def test_block_decode_waits_that_run_out_flag_timeout():
     assert st2.item() == 0
     ref = oracle.slot_attention(q, rs, kc, vc, scale=d ** -0.5)
     assert_out_close(out2.float().cpu().numpy(), ref, "bf16", "block decode after a timeout")
+
+
+# (B, n_q, T, Hq, Hkv): one wave of two-tile blocks; lone query
+# tiles with split keys; several waves (persistent kernel), also with lone tiles; block decoding in clusters
+@pytest.mark.parametrize("shape", [(2, 300, 700, 4, 2), (2, 100, 1500, 4, 4), (4, 600, 700, 32, 8), (8, 330, 400, 32, 8),
+                                   (2, 32, 1408, 8, 4), (1, 32, 3000, 28, 4)])
+def test_no_unfinished_row_is_written_after_a_timeout(shape):
+    """Waits that run out at any stage of a kernel: a row of the output has the bits of an undisturbed run, or
+    it is as it was."""
+    B, n_q, T, hq, hkv, d, num_slots, kc, vc, q, rs = _case(*shape)
+    args = (ac.attn_desc(hq, hkv, d, d ** -0.5, "bf16"), B, n_q, dev(q), T, dev(rs), dev(kc), dev(vc), num_slots)
+    want, out, st = torch.empty(q.shape, dtype=q.dtype, device="cuda"), torch.empty(q.shape, dtype=q.dtype, device="cuda"), status_tensor()
+    ac.acache_slot_attention(*args, want, dev_status=st)
+    assert st.item() == 0
+    assert_out_close(want.float().cpu().numpy(), oracle.slot_attention(q, rs, kc, vc, scale=d ** -0.5), "bf16", "undisturbed")
+    seen = 0
+    for budget in [300] * 8 + list(range(1000, 40000, 1500)):
+        out.fill_(9.0)
+        st.zero_()
+        prev = ac.acache_wait_budget(budget)
+        try:
+            ac.acache_slot_attention(*args, out, dev_status=st)
+            torch.cuda.synchronize()
+        finally:
+            ac.acache_wait_budget(prev)
+        left, right = (out == 9).all(-1), (out == want).all(-1)
+        assert (left | right).all(), f"budget {budget}: {(~(left | right)).sum().item()} rows"
+        assert st.item() in (0, ac._lib.DEV_TIMEOUT) and (st.item() or right.all())
+        seen += st.item() != 0
+    assert seen

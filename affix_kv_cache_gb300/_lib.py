@@ -150,11 +150,22 @@ def _stream(stream):
     return stream
 
 
-def _stream_of(t, stream):
-    """_stream, for a call on tensor `t`: the tensors of a call live on the current device."""
-    if torch.cuda.is_initialized() and isinstance(t, torch.Tensor) and t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"tensor on {t.device}, current device is cuda:{torch._C._cuda_getDevice()}")
-    return _stream(stream)
+def _current_device():
+    """The device that every tensor of a call lives on; before torch has touched CUDA there is none."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
+
+
+def _on(device, t):
+    """_p, for a call on `device`."""
+    if t is None:
+        return None
+    try:
+        at = t.data_ptr()
+        if at and t.get_device() != device:
+            raise ValueError(f"tensor on {t.device}, not on the current device")
+        return at or None
+    except AttributeError:       # a plain address
+        return t or None
 
 
 def _check(fn, status):
@@ -342,27 +353,30 @@ def acache_rerotate_keys(desc, rows, k_in, k_out, delta_pos, rope_theta, interle
 def acache_write_slots_q8(desc, batch, rows, write_slot, k_new, v_new, k_cache, v_cache, kv_scale, num_slots,
                           private_begin, dev_status=None, stream=None, check=True):
     """The store step into an 8-bit pool: quantises as it writes."""
-    st = lib().acache_write_slots_q8(ctypes.byref(desc), batch, rows, _p(write_slot), _p(k_new), _p(v_new),
-                                     _p(k_cache), _p(v_cache), _p(kv_scale), num_slots, private_begin,
-                                     _p(dev_status), _stream_of(k_cache, stream))
+    dev = _current_device()
+    st = lib().acache_write_slots_q8(ctypes.byref(desc), batch, rows, _on(dev, write_slot), _on(dev, k_new),
+                                     _on(dev, v_new), _on(dev, k_cache), _on(dev, v_cache), _on(dev, kv_scale),
+                                     num_slots, private_begin, _on(dev, dev_status), _stream(stream))
     return _check("acache_write_slots_q8", st) if check else st
 
 
 def acache_gather_slots_q8(desc, batch, seq_len, read_slot, k_cache, v_cache, kv_scale, num_slots, k_out, v_out,
                            dev_status=None, stream=None, check=True):
     """The logical K/V view of an 8-bit pool, in the descriptor's dtype."""
-    st = lib().acache_gather_slots_q8(ctypes.byref(desc), batch, seq_len, _p(read_slot), _p(k_cache), _p(v_cache),
-                                      _p(kv_scale), num_slots, _p(k_out), _p(v_out), _p(dev_status),
-                                      _stream_of(k_cache, stream))
+    dev = _current_device()
+    st = lib().acache_gather_slots_q8(ctypes.byref(desc), batch, seq_len, _on(dev, read_slot), _on(dev, k_cache),
+                                      _on(dev, v_cache), _on(dev, kv_scale), num_slots, _on(dev, k_out),
+                                      _on(dev, v_out), _on(dev, dev_status), _stream(stream))
     return _check("acache_gather_slots_q8", st) if check else st
 
 
 def acache_slot_attention_q8(desc, batch, n_q, q, seq_len, read_slot, k_cache, v_cache, kv_scale, num_slots, out,
                              drop_none=False, dev_status=None, stream=None, check=True):
     """Read-slot attention over an 8-bit pool; with drop_none, SLOT_NONE entries are discarded keys."""
-    st = lib().acache_slot_attention_q8(ctypes.byref(desc), batch, n_q, _p(q), seq_len, _p(read_slot), _p(k_cache),
-                                        _p(v_cache), _p(kv_scale), num_slots, _p(out), int(bool(drop_none)),
-                                        _p(dev_status), _stream_of(k_cache, stream))
+    dev = _current_device()
+    st = lib().acache_slot_attention_q8(ctypes.byref(desc), batch, n_q, _on(dev, q), seq_len, _on(dev, read_slot),
+                                        _on(dev, k_cache), _on(dev, v_cache), _on(dev, kv_scale), num_slots,
+                                        _on(dev, out), int(bool(drop_none)), _on(dev, dev_status), _stream(stream))
     return _check("acache_slot_attention_q8", st) if check else st
 
 
@@ -371,10 +385,12 @@ def acache_slot_attention_varlen_q8(desc, batch, q_start, max_q_rows, total_q_ro
                                     dev_status=None, stream=None, check=True):
     """Read-slot attention over a ragged batch and an 8-bit pool (offsets as in
     acache_slot_attention_varlen)."""
-    st = lib().acache_slot_attention_varlen_q8(ctypes.byref(desc), batch, _p(q_start), max_q_rows, total_q_rows,
-                                               _p(q), _p(kv_start), max_seq_len, _p(read_slot), _p(k_cache),
-                                               _p(v_cache), _p(kv_scale), num_slots, _p(out), int(bool(drop_none)),
-                                               _p(dev_status), _stream_of(k_cache, stream))
+    dev = _current_device()
+    st = lib().acache_slot_attention_varlen_q8(ctypes.byref(desc), batch, _on(dev, q_start), max_q_rows,
+                                               total_q_rows, _on(dev, q), _on(dev, kv_start), max_seq_len,
+                                               _on(dev, read_slot), _on(dev, k_cache), _on(dev, v_cache),
+                                               _on(dev, kv_scale), num_slots, _on(dev, out), int(bool(drop_none)),
+                                               _on(dev, dev_status), _stream(stream))
     return _check("acache_slot_attention_varlen_q8", st) if check else st
 
 
@@ -382,10 +398,11 @@ def acache_store_attend_q8(desc, batch, rows, write_slot, k_new, v_new, k_cache,
                            private_begin, n_q, q, seq_len, read_slot, out, drop_none=False, dev_status=None,
                            stream=None, check=True):
     """Store step into an 8-bit pool, then read-slot attention over it, in one call."""
-    st = lib().acache_store_attend_q8(ctypes.byref(desc), batch, rows, _p(write_slot), _p(k_new), _p(v_new),
-                                      _p(k_cache), _p(v_cache), _p(kv_scale), num_slots, private_begin, n_q, _p(q),
-                                      seq_len, _p(read_slot), _p(out), int(bool(drop_none)), _p(dev_status),
-                                      _stream_of(k_cache, stream))
+    dev = _current_device()
+    st = lib().acache_store_attend_q8(ctypes.byref(desc), batch, rows, _on(dev, write_slot), _on(dev, k_new),
+                                      _on(dev, v_new), _on(dev, k_cache), _on(dev, v_cache), _on(dev, kv_scale),
+                                      num_slots, private_begin, n_q, _on(dev, q), seq_len, _on(dev, read_slot),
+                                      _on(dev, out), int(bool(drop_none)), _on(dev, dev_status), _stream(stream))
     return _check("acache_store_attend_q8", st) if check else st
 
 

@@ -9,6 +9,7 @@ from affix_kv_cache_gb300 import _lib
 
 from gpu_helpers import dev
 from q8_reference import assert_attention, attention, quantise, random_pool, values
+from test_q8_host import CALLS, TENSORS
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -777,3 +778,12 @@ def test_no_unfinished_row_is_written_after_a_timeout(B, n_q, hq, hkv, T, d):
         assert st.item() in (0, _lib.DEV_TIMEOUT) and (st.item() or right.all())
         seen += st.item() != 0
     assert seen
+
+
+@pytest.mark.parametrize("call,name", TENSORS)
+def test_a_host_tensor_beside_device_tensors_is_refused(call, name):
+    """Raised before the library is called: nothing is launched."""
+    host, there = torch.zeros(64), torch.zeros(64, device="cuda")
+    args = [host if a == name else there if isinstance(a, str) else a for a in CALLS[call]]
+    with pytest.raises(ValueError, match="current device"):
+        getattr(ac, call)(_desc(4, 2, 128, BF16), *args, dev_status=host if name == "dev_status" else there)

@@ -116,3 +116,23 @@ def test_reference_scales_at_their_borders():
     assert s.tolist() == [127, 128, 119, 77, 77, 165, 165, 255, 255, 255]
     assert bad.tolist() == [False] * 7 + [True] * 3
     assert np.isnan(values(c, s)[-1]).all()
+
+
+CALLS = {  # the arguments of each call behind the descriptor, in order; tensors by name
+    "acache_write_slots_q8": (1, 4, "write_slot", "k_new", "v_new", "k_cache", "v_cache", "kv_scale", 10, 0),
+    "acache_gather_slots_q8": (1, 4, "read_slot", "k_cache", "v_cache", "kv_scale", 10, "k_out", "v_out"),
+    "acache_slot_attention_q8": (1, 4, "q", 4, "read_slot", "k_cache", "v_cache", "kv_scale", 10, "out"),
+    "acache_slot_attention_varlen_q8": (1, "q_start", 4, 4, "q", "kv_start", 4, "read_slot", "k_cache", "v_cache", "kv_scale", 10,
+                                        "out"),
+    "acache_store_attend_q8": (1, 4, "write_slot", "k_new", "v_new", "k_cache", "v_cache", "kv_scale", 10, 0, 4, "q", 4,
+                               "read_slot", "out")}
+TENSORS = [(c, a) for c, args in CALLS.items() for a in args + ("dev_status",) if isinstance(a, str)]
+
+
+@pytest.mark.parametrize("call,name", TENSORS)
+def test_a_host_tensor_in_any_argument_is_refused(call, name):
+    """It would reach a kernel as an address.  (The other arguments are plain addresses, which are the caller's.)"""
+    host = torch.zeros(64)
+    args = [host if a == name else BOGUS if isinstance(a, str) else a for a in CALLS[call]]
+    with pytest.raises(ValueError, match="current device"):
+        getattr(ac, call)(_desc(), *args, dev_status=host if name == "dev_status" else None)

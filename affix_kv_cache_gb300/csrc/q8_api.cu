@@ -13,16 +13,19 @@ bool pool_ok(const void* k_cache, const void* v_cache, const void* kv_scale) {
     return k_cache && v_cache && kv_scale && aligned16(k_cache) && aligned16(v_cache) && aligned2(kv_scale);
 }
 
-// What the attention's grids and tensor maps hold (clusters of up to 8 CTAs a head along x).
-bool fits(const AttnArgs& a, int batch, int n_q, int64_t num_slots) {
-    return batch <= 65535 && (int64_t)n_q * (a.hq / a.hkv) <= 65535LL * 64 && a.hkv <= 0x7fffffff / 8 &&
-           num_slots < 0x7fffffffLL / a.hkv;
+// Head counts whose items (16-byte pieces of a row) and row bytes are numbered in 32 bits.
+bool heads_fit(const AttnArgs& a) { return a.hkv <= 1 << 24; }
+// What the attention's grids and tensor maps hold (clusters of up to 8 CTAs a head along x), and keys whose indices,
+// rounded up to whole tiles and looked up a few tiles ahead, stay in 32 bits.
+bool fits(const AttnArgs& a, int batch, int n_q, int T_len, int64_t num_slots) {
+    return batch <= 65535 && (int64_t)n_q * (a.hq / a.hkv) <= 65535LL * 64 && heads_fit(a) &&
+           T_len <= 0x7fffffff - 1023 && num_slots < 0x7fffffffLL / a.hkv;
 }
 
 // Fixed and ragged attention after their own scalar checks (q_start null: fixed).
 int attend(const Q8Attn& c) {
     if (!c.q || !c.read_slot || !c.out || !aligned16(c.q) || !aligned16(c.out) ||
-        !pool_ok(c.k_cache, c.v_cache, c.kv_scale) || !fits(c.a, c.B, c.n_q, c.num_slots))
+        !pool_ok(c.k_cache, c.v_cache, c.kv_scale) || !fits(c.a, c.B, c.n_q, c.T_len, c.num_slots))
         return ACACHE_ERR_INVALID_ARG;
     // (an empty pool: every key is a zero row, and there is no row for a tensor map to start at)
     if (c.num_slots == 0 || !q8_tc_supported(c.a)) return launch_q8_simt_attention(c);
@@ -62,7 +65,7 @@ int acache_write_slots_q8(const acache_attn_desc* desc, int batch, int rows, con
     if (batch < 0 || rows < 0 || num_slots < 0 || private_begin < 0 || private_begin > num_slots)
         return ACACHE_ERR_INVALID_ARG;
     if (batch == 0 || rows == 0) return ACACHE_OK;
-    if (!write_slot || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) ||
+    if (!write_slot || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || !heads_fit(a) ||
         !pool_ok(k_cache, v_cache, kv_scale))
         return ACACHE_ERR_INVALID_ARG;
     return launch_q8_write(a.dtype, batch, rows, a.hkv, a.d, write_slot, k_new, v_new, (uint8_t*)k_cache,
@@ -76,7 +79,7 @@ int acache_gather_slots_q8(const acache_attn_desc* desc, int batch, int seq_len,
     if (int rc = check_desc(desc, &a)) return rc;
     if (batch < 0 || seq_len < 0 || num_slots < 0) return ACACHE_ERR_INVALID_ARG;
     if (batch == 0 || seq_len == 0) return ACACHE_OK;
-    if (!read_slot || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) ||
+    if (!read_slot || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || !heads_fit(a) ||
         !pool_ok(k_cache, v_cache, kv_scale))
         return ACACHE_ERR_INVALID_ARG;
     return launch_q8_gather(a.dtype, batch, seq_len, a.hkv, a.d, read_slot, (const uint8_t*)k_cache,
@@ -129,9 +132,10 @@ int acache_store_attend_q8(const acache_attn_desc* desc, int batch, int rows, co
         return ACACHE_ERR_INVALID_ARG;
     if (batch == 0) return ACACHE_OK;
     const bool store = rows > 0, attends = n_q > 0;
-    if (store && (!write_slot || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)))
+    if (store && (!write_slot || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || !heads_fit(a)))
         return ACACHE_ERR_INVALID_ARG;
-    if (attends && (seq_len == 0 || !q || !read_slot || !out || !aligned16(q) || !aligned16(out) || !fits(a, batch, n_q, num_slots)))
+    if (attends && (seq_len == 0 || !q || !read_slot || !out || !aligned16(q) || !aligned16(out) ||
+                    !fits(a, batch, n_q, seq_len, num_slots)))
         return ACACHE_ERR_INVALID_ARG;
     if ((store || attends) && !pool_ok(k_cache, v_cache, kv_scale)) return ACACHE_ERR_INVALID_ARG;
     if (store)

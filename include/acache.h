@@ -390,9 +390,9 @@ ACACHE_API int acache_gather_slots(const acache_attn_desc* a, int batch, int seq
  * value above 448 * 2^38 is stored as scale byte 255 and zero codes and flags ACACHE_DEV_BAD_VALUE: it
  * reads as NaN, and so does every query row that attends to it.  Bytes of 166 to 254 read as NaN too; a
  * pool set to zero bytes reads as zeros.  Pools not written by these calls keep to that format: codes 0x7f
- * and 0xff, and bytes of 1 to 76, are not defined here.  An attention call takes up to 65,535
- * requests, 65,535 tiles of 64 rows (queries x heads of a group) and a pool below 2^31 rows (slots x
- * heads); more is ACACHE_ERR_INVALID_ARG.
+ * and 0xff, and bytes of 1 to 76, are not defined here.  A call takes up to 2^24 KV heads, an
+ * attention call up to 65,535 requests, 65,535 tiles of 64 rows (queries x heads of a group), 2^31 - 1024
+ * keys of a request and a pool below 2^31 rows (slots x heads); more is ACACHE_ERR_INVALID_ARG.
  * The descriptor's dtype is that of the fresh K/V, the queries and the outputs.
  * ------------------------------------------------------------------------------- */
 

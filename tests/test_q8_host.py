@@ -136,3 +136,22 @@ def test_a_host_tensor_in_any_argument_is_refused(call, name):
     args = [host if a == name else BOGUS if isinstance(a, str) else a for a in CALLS[call]]
     with pytest.raises(ValueError, match="current device"):
         getattr(ac, call)(_desc(), *args, dev_status=host if name == "dev_status" else None)
+
+
+def test_sizes_past_32_bit_indices_are_refused():
+    """Their tile and item numbers would wrap: keys were rounded up to a negative number of tiles, and the
+    call returned without an output or a status.  (One less passes the checks and reaches a host without a
+    GPU.)"""
+    longest = 2 ** 31 - 1024
+    for call, name in ((_attend, "T"), (_both, "T"), (_varlen, "mt")):
+        for n in (longest + 1, 2 ** 31 - 1):
+            assert call(_desc(), **{name: n}) == E
+        if not torch.cuda.is_available():
+            assert call(_desc(), **{name: longest}) == _lib.ACACHE_ERR_CUDA
+    wide = 2 ** 24 + 1
+    for call in (_write, _gather, _attend, _varlen):
+        assert call(_desc(hq=wide, hkv=wide), ns=1) == E
+    assert _both(_desc(hq=wide, hkv=wide), ns=1, n_q=0) == E and _both(_desc(hq=wide, hkv=wide), ns=1, rows=0) == E
+    if not torch.cuda.is_available():
+        for call in (_write, _gather):
+            assert call(_desc(hq=2 ** 24, hkv=2 ** 24), ns=1) == _lib.ACACHE_ERR_CUDA

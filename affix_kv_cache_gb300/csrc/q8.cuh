@@ -46,6 +46,12 @@ ACACHE_DEVFN uint32_t q8_encode2(float a, float b) {
     return r;
 }
 
+// Rows or keys of ragged request b, from the offsets.  One behind the other's start is no count, however far: the
+// difference of two offsets need not fit 32 bits.  (With a negative start, which is refused too, it may be anything.)
+ACACHE_DEVFN int q8_count(const int32_t* start, int b) {
+    const int32_t a = start[b], z = start[b + 1];
+    return z < a ? -1 : (int)((uint32_t)z - (uint32_t)a);
+}
 // A ragged request with rows that is not computed: counts outside the call's bounds, or rows outside q.
 ACACHE_DEVFN bool q8_bad_lengths(int n_q, int max_q, int T_len, int max_T, int64_t q_at, int total_q, int64_t kv_at) {
     return n_q < 0 || n_q > max_q || T_len < 1 || T_len > max_T || q_at < 0 || q_at + n_q > total_q || kv_at < 0;

@@ -61,8 +61,8 @@ q8_simt_kernel(const SimtParams p) {
     if (p.q_start) {
         qbase = p.q_start[b];
         kbase = p.kv_start[b];
-        n_q = (int)(p.q_start[b + 1] - qbase);
-        T_len = (int)(p.kv_start[b + 1] - kbase);
+        n_q = q8_count(p.q_start, b);
+        T_len = q8_count(p.kv_start, b);
         if (n_q != 0 && q8_bad_lengths(n_q, p.n_q, T_len, p.T_len, qbase, p.total_q, kbase)) {
             if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) flag(p.dev_status, ACACHE_DEV_BAD_LENGTH);
             return;

@@ -787,3 +787,24 @@ def test_a_host_tensor_beside_device_tensors_is_refused(call, name):
     args = [host if a == name else there if isinstance(a, str) else a for a in CALLS[call]]
     with pytest.raises(ValueError, match="current device"):
         getattr(ac, call)(_desc(4, 2, 128, BF16), *args, dev_status=host if name == "dev_status" else there)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("max_q", [1, 60])
+def test_ragged_counts_that_wrap_32_bits_are_skipped_and_flagged(dtype, d, max_q):
+    """Offsets whose difference is -(2^32 - 1): cut to 32 bits that is a count of one."""
+    g = torch.Generator().manual_seed(8)
+    kc, vc, sc, kv, vv = random_pool(50, 1, d, g)
+    q = torch.randn((3, 2, d), generator=g).to(dtype)
+    rs = torch.randint(0, 50, (40,), generator=g, dtype=torch.int32)
+    top, low = 2 ** 31 - 1, -2 ** 31
+    for qs, ks, right in (((0, 1, 2), (0, 40, low), 1), ((0, 1, 2), (top, low, 3), 0), ((top, low, 2), (0, 40, 40), 0)):
+        out, st = torch.full(q.shape, 9.0, dtype=dtype, device="cuda"), _status()
+        qs, ks = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (qs, ks))
+        ac.acache_slot_attention_varlen_q8(_desc(2, 1, d, dtype), 2, qs, max_q, 3, dev(q), ks, 40, dev(rs), dev(kc), dev(vc), dev(sc),
+                                           50, out, dev_status=st)
+        got = out.double().cpu().numpy()
+        assert st.item() == _lib.DEV_BAD_LENGTH and (got[right:] == 9).all()
+        if right:
+            want, tol = attention(q[:1], rs.numpy(), kv, vv, d ** -0.5)
+            assert_attention(got[:1], want, tol)

@@ -808,3 +808,52 @@ def test_ragged_counts_that_wrap_32_bits_are_skipped_and_flagged(dtype, d, max_q
         if right:
             want, tol = attention(q[:1], rs.numpy(), kv, vv, d ** -0.5)
             assert_attention(got[:1], want, tol)
+
+
+def _counted_keys(T, hkv, d, g):
+    """A pool of T slots whose attention outputs are counts: head h's key t has logit 0 or, for a random half,
+    one that no weight is left of; and a value row that is zero but for one element of one head."""
+    t = torch.arange(T)
+    alive = torch.rand(T, generator=g) < 0.5
+    alive[torch.tensor([0, T - 1])] = True
+    k, v = torch.zeros((T, hkv, d)), torch.zeros((T, hkv, d))
+    k[:, :, 0] = torch.where(alive, 0.0, -64.0)[:, None]
+    v[t, t % hkv, t // hkv % d] = 1.0
+    return k, v, alive
+
+
+@pytest.mark.parametrize("dtype,hkv,d", [(BF16, 8, 128), (BF16, 16, 64), (F32, 8, 128)])
+@pytest.mark.parametrize("n_q", [1, 9, 32, 40, 300])
+@pytest.mark.parametrize("T", [4097, 9000])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_every_key_of_a_long_context_counts_once(dtype, hkv, d, n_q, T, ragged):
+    """Weights are 1 or 0, so an output element is a number of keys over the number of all: one key lost or
+    read twice, anywhere, changes it by far more than its rounding."""
+    g = torch.Generator().manual_seed(T + n_q)
+    k, v, alive = _counted_keys(T, hkv, d, g)
+    n, count = int(alive.sum()), v[alive].sum(0).double().numpy()         # [hkv][d]
+    want = count / n
+    rel = {BF16: 2.0 ** -8, F32: 2.0 ** -20}[dtype] + 2.0 ** -20          # the output's rounding; exp2, sum and 1/sum
+    for other in ((count - 1) / (n - 1), (count + 1) / (n + 1)):
+        changed = np.abs(other - want)[count > 0]
+        assert (changed > 2.5 * rel * want[count > 0]).all()
+    slots = torch.randperm(T, generator=g)
+    slots[: T // 2] = torch.sort(slots[: T // 2]).values                  # (runs of neighbours as well)
+    kc, vc = (torch.empty((T, hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    sc = torch.empty((T, hkv, 2), dtype=torch.uint8, device="cuda")
+    desc, rs = _desc(hkv, hkv, d, dtype, 1.0), slots.to(torch.int32).cuda()[None]
+    ac.acache_write_slots_q8(desc, 1, T, rs, dev(k.to(dtype))[None], dev(v.to(dtype))[None], kc, vc, sc, T, 0)
+    q = torch.zeros((1, n_q, hkv, d), dtype=dtype, device="cuda")
+    q[..., 0] = 8.0
+    out, st = torch.empty_like(q), _status()
+    if ragged:                              # behind a request of one key and before an idle one
+        qs, ks = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ((0, 1, n_q + 1, n_q + 1), (0, 1, T + 1, T + 1)))
+        q, rs = torch.cat((q[0, :1], q[0])), torch.cat((rs[0, :1], rs[0]))
+        o = torch.empty_like(q)
+        ac.acache_slot_attention_varlen_q8(desc, 3, qs, n_q, n_q + 1, q, ks, T, rs, kc, vc, sc, T, o, dev_status=st)
+        out = o[1:][None]
+    else:
+        ac.acache_slot_attention_q8(desc, 1, n_q, q, T, rs, kc, vc, sc, T, out, dev_status=st)
+    got = out[0].double().cpu().numpy()
+    assert st.item() == 0
+    assert (np.abs(got - want) <= rel * want).all(), np.abs(got / np.maximum(want, 1e-30) - (want > 0)).max()

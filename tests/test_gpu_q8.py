@@ -857,3 +857,25 @@ def test_every_key_of_a_long_context_counts_once(dtype, hkv, d, n_q, T, ragged):
     got = out[0].double().cpu().numpy()
     assert st.item() == 0
     assert (np.abs(got - want) <= rel * want).all(), np.abs(got / np.maximum(want, 1e-30) - (want > 0)).max()
+
+
+@pytest.mark.parametrize("B,rows,n_q,hq,hkv,d,dtype,T", [
+    (2, 300, 300, 4, 4, 128, BF16, 700), (3, 32, 32, 8, 4, 128, BF16, 600), (2, 1, 1, 8, 2, 128, BF16, 1500),
+    (2, 33, 40, 4, 2, 64, BF16, 300), (2, 40, 40, 2, 2, 64, F32, 150)])
+def test_store_attend_with_discarded_keys(B, rows, n_q, hq, hkv, d, dtype, T):
+    kc, vc, sc, ns, priv0, ws, rs, kn, vn, q = _step(B, rows, n_q, hq, hkv, d, dtype, T, rows + 2 * T)
+    rs[(torch.rand(rs.shape, generator=torch.Generator().manual_seed(T)) < 0.4) & (rs < priv0)] = -1
+    rs[1] = -1                                                  # stored, and nothing to attend to
+    pool, st = [dev(x) for x in (kc, vc, sc)], _status()
+    out = torch.full(q.shape, 9.0, dtype=dtype, device="cuda")
+    ac.acache_store_attend_q8(_desc(hq, hkv, d, dtype), B, rows, dev(ws), dev(kn), dev(vn), *pool, ns, priv0, n_q, dev(q), T,
+                              dev(rs), out, drop_none=True, dev_status=st)
+    k, v, s = [x.cpu().numpy() for x in pool]
+    at = ws.view(-1).numpy()
+    for i, (c, x) in enumerate(((k, kn), (v, vn))):
+        codes, scale, _ = quantise(x.view((-1,) + x.shape[2:]))
+        assert np.array_equal(c[at], codes) and np.array_equal(s[at, :, i], scale)
+    for b in range(B):
+        want, tol = attention(q[b], rs[b].numpy(), values(k, s[..., 0]), values(v, s[..., 1]), d ** -0.5, True)
+        assert_attention(out[b].double().cpu().numpy(), want, tol, f"request {b}")
+    assert (out[1] == 0).all() and st.item() == 0

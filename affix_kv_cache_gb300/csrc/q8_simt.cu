@@ -41,11 +41,15 @@ struct SimtSmem {
     float q[D][kBM];          // transposed; the partial O of a split key range afterwards
     float k[D][kBN];          // transposed
     float v[kBN][D];
-    float p[kBN][kBM];        // transposed
+    union {
+        float p[kBN][kBM];    // transposed
+        float ml[2][kBM];     // maximum and sum of a split key range afterwards
+    };
     float ks[kBN], vs[kBN];
     int64_t row[kBN];         // pool row, or -1 (zero row), or -2 (no key)
-    float m[kBM], l[kBM];
 };
+// two CTAs to an SM (228 KB, of which a CTA takes 1 KB more than it asks for)
+static_assert(2 * (sizeof(SimtSmem<128, 64>) + 1024) <= 228 * 1024, "shared memory of two CTAs");
 
 template <typename T, int D, int kBM>
 __global__ void __launch_bounds__(4 * kBM)
@@ -236,8 +240,8 @@ q8_simt_kernel(const SimtParams p) {
     for (int y = 0; y < 4; ++y) {
         const int r = 4 * ty + y;
         if (tx == 0) {
-            sm.m[r] = m[y];
-            sm.l[r] = l[y];
+            sm.ml[0][r] = m[y];
+            sm.ml[1][r] = l[y];
         }
 #pragma unroll
         for (int n = 0; n < NC; ++n)
@@ -245,7 +249,7 @@ q8_simt_kernel(const SimtParams p) {
                 make_float4(acc[y][n * 4], acc[y][n * 4 + 1], acc[y][n * 4 + 2], acc[y][n * 4 + 3]);
     }
     ptx::cluster_sync();
-    const uint32_t m_a = ptx::smem_u32(&sm.m[0]), l_a = ptx::smem_u32(&sm.l[0]), o_a = ptx::smem_u32(part);
+    const uint32_t m_a = ptx::smem_u32(&sm.ml[0][0]), l_a = ptx::smem_u32(&sm.ml[1][0]), o_a = ptx::smem_u32(part);
     for (int x = tid; x < ((rows - cr + cs - 1) / cs) * (D / 4); x += kThreads) {
         const int r = cr + (x / (D / 4)) * cs, c = x % (D / 4);
         float pm[kMaxCluster], pl[kMaxCluster], M = -INFINITY, L = 0.f;

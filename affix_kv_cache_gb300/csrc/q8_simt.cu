@@ -12,6 +12,8 @@
 // tiles of 64; 4 x 32 rows over 1,408 keys, 8 heads: 48 and 115).  When there are few blocks the key range
 // is split over a cluster of up to 8 CTAs, which merge their partial (maximum, sum, O) through
 // distributed shared memory in rank order.
+#include <cfloat>
+
 #include <algorithm>
 #include <atomic>
 
@@ -88,6 +90,7 @@ q8_simt_kernel(const SimtParams p) {
         const int r = x / D, c = x % D;
         sm.q[c][r] = r < rows ? to_f32(((const T*)p.q)[q_off(r) + c]) : 0.f;
     }
+    bool any = false;                                   // a key of this thread's columns is there
     float m[4], l[4], acc[4][NC * 4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
@@ -170,7 +173,10 @@ q8_simt_kernel(const SimtParams p) {
         }
         bool gone[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) gone[x] = sm.row[4 * tx + x] == -2;
+        for (int x = 0; x < 4; ++x) {
+            gone[x] = sm.row[4 * tx + x] == -2;
+            any = any || !gone[x];
+        }
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
             float mt = -INFINITY;
@@ -218,6 +224,11 @@ q8_simt_kernel(const SimtParams p) {
     for (int y = 0; y < 4; ++y)
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) l[y] += __shfl_xor_sync(0xffffffffu, l[y], o);
+    // A row has a maximum if it has a key, be its logit -infinity: then a sum of 0 is 0 / 0, not an empty row.
+    any = __any_sync(0xffffffffu, any);
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+        if (any) m[y] = fmaxf(m[y], -FLT_MAX);
     if (cs == 1) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -225,7 +236,7 @@ q8_simt_kernel(const SimtParams p) {
             if (r >= rows) continue;
             T* o = (T*)p.out + q_off(r);
             // a row without keys gives zeros (a NaN sum is carried into the output)
-            const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
+            const float inv = m[y] == -INFINITY && l[y] == 0.f ? 0.f : 1.f / l[y];
 #pragma unroll
             for (int n = 0; n < NC; ++n)
 #pragma unroll
@@ -277,7 +288,7 @@ q8_simt_kernel(const SimtParams p) {
             O.z = fmaf(e, po[w].z, O.z);
             O.w = fmaf(e, po[w].w, O.w);
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
         T* o = (T*)p.out + q_off(r) + 4 * c;
         o[0] = from_f32<T>(O.x * inv);
         o[1] = from_f32<T>(O.y * inv);

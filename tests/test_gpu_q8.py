@@ -879,3 +879,38 @@ def test_store_attend_with_discarded_keys(B, rows, n_q, hq, hkv, d, dtype, T):
         want, tol = attention(q[b], rs[b].numpy(), values(k, s[..., 0]), values(v, s[..., 1]), d ** -0.5, True)
         assert_attention(out[b].double().cpu().numpy(), want, tol, f"request {b}")
     assert (out[1] == 0).all() and st.item() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 128), (F32, 64)])
+@pytest.mark.parametrize("n_q", [1, 20, 40, 300])
+def test_logits_of_minus_infinity(dtype, d, n_q):
+    """A row whose every logit is -infinity has no softmax: NaN, not the zeros of a row without keys.  Beside one
+    finite logit, wherever it is, they weigh nothing."""
+    hq, hkv, T = 2, 1, 2000
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(2, n_q, hq, hkv, d, dtype, T, False, 33)
+    kc[:, :, 0], sc[..., 0] = 0x60, 127                         # element 0 of every key: 2^5
+    free = ns - 1
+    kc[free] = 0
+    rs[rs == free] = 0
+    desc, pool = _desc(hq, hkv, d, dtype, 1.0), (dev(kc), dev(vc), dev(sc), ns)
+
+    def run(q, rs, drop=True):
+        out = torch.full(q.shape, 9.0, dtype=dtype, device="cuda")
+        ac.acache_slot_attention_q8(desc, 2, n_q, dev(q), T, dev(rs), *pool, out, drop_none=drop)
+        return out.double().cpu().numpy()
+
+    q[..., 0] = -float("inf")
+    one = torch.full_like(rs, -1)
+    one[:, 900] = rs[:, 900]
+    for r in (rs, one):
+        assert np.isnan(run(q, r)).all()
+    assert np.isnan(run(q, rs, drop=False)).all()
+    if dtype == F32:
+        assert (run(q, torch.full_like(rs, -1)) == 0).all()
+        # products that overflow to -infinity
+        q[..., 0] = -3e38
+        for at in (0, 700, T - 1):
+            r = rs.clone()
+            r[:, at] = free
+            got, want = run(q, r), vv[free, 0]
+            assert np.abs(got - want).max() <= 2.0 ** -20 * np.abs(want).max()

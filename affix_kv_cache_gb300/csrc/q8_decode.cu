@@ -266,6 +266,7 @@ q8_decode_kernel(const DecParams p) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[j][b][x] = 0.f;
+    bool any = false;                                // a key of this lane's takes part
     uint32_t at = 0, at2 = 2;                        // stages of the chunk at hand and of the one to bring
     for (int ch = ch0 + warp; ch < ch1; ch += kWarps) {
         bring(s2, ring + at2 * (2 * kChunk * D));
@@ -273,6 +274,7 @@ q8_decode_kernel(const DecParams p) {
         sc2 = load_scale(s2);
         const bool past = ch * kChunk + (lane & 15) >= T_len;
         const uint32_t fe_own = factors(s0, sc0, past);
+        any = any || fe_own != kNoEv;
         if (!past && (s0 < 0 || s0 >= p.num_slots) && !(p.drop && s0 == ACACHE_SLOT_NONE))
             flag(p.dev_status, ACACHE_DEV_BAD_SLOT);
         s0 = s1;
@@ -399,6 +401,7 @@ q8_decode_kernel(const DecParams p) {
         __syncwarp();                                // the next chunk but two lands in this stage
     }
     cp_async_wait<0>();
+    any = __any_sync(0xffffffffu, any);
     __syncthreads();                                 // the partials go over the rings
     // -------------------------------------------------------------------------- merge
 #pragma unroll
@@ -409,7 +412,7 @@ q8_decode_kernel(const DecParams p) {
             for (int i = 4; i < 32; i <<= 1) l[b][x] += __shfl_xor_sync(0xffffffffu, l[b][x], i);
             if (g == 0) {
                 sm.m[warp][8 * b + 2 * t + x] = m[b][x];
-                sm.l[warp][8 * b + 2 * t + x] = l[b][x];
+                sm.l[warp][8 * b + 2 * t + x] = any ? l[b][x] : 0.f;   // (a row that is not finite: NaN even so)
             }
         }
     // float4 slot of a row, moved by row and by thread group so that the lanes spread over the banks

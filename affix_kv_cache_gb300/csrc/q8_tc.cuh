@@ -108,9 +108,10 @@ ACACHE_DEVFN uint32_t cut_codes(uint32_t a, uint32_t b) {
 }
 // Then the terms, in place, row `lane` by its lane: whole rows pass through its registers, so the row's
 // largest needs no exchange.  Returns the row's factor: its logits are S times the keys' factors times it
-// (scale_log2 times the power of two the row was divided by; NaN for a row that is not finite, which is
-// carried as zeros).  The factor stays a normal number: a logit that the raise would change is below
-// 2^-60, and 0 times a masked key's -infinity would be NaN.
+// (scale_log2 times the power of two the row was divided by).  A row that is not finite has NaN for all its
+// terms, so that S is NaN, and 1 for its factor: a discarded key, masked after S, must stay out.  The factor
+// stays a normal number: a logit that the raise would change is below 2^-60, and 0 times a masked key's
+// -infinity would be NaN.
 // hi is q' cut to 4 significant bits and lo the rest, rounded to e4m3's subnormal step where it is longer.
 template <int D>
 ACACHE_DEVFN float query_terms(uint32_t hi, uint32_t lo, int lane, float scale_log2) {
@@ -127,7 +128,7 @@ ACACHE_DEVFN float query_terms(uint32_t hi, uint32_t lo, int lane, float scale_l
     top = max(top & 0xffffu, top >> 16);
     const uint32_t E = max(top >> 7, 8u);                     // biased exponent of the row's largest
     const bool finite = E != 255u;
-    const uint32_t keep = finite ? 0xffffffffu : 0u;
+    const uint32_t nan2 = finite ? 0u : 0x7fff7fffu;
     const uint32_t up2 = (261u - E) << 7 | (261u - E) << 23;  // 2^(134 - E), twice: the largest goes to [128, 256)
     constexpr uint32_t kDown2 = 0x03800380u;                  // 2^-120, twice
 #pragma unroll
@@ -138,7 +139,7 @@ ACACHE_DEVFN float query_terms(uint32_t hi, uint32_t lo, int lane, float scale_l
             uint32_t x[2], r[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t v = w[c + (y >> 2)][(y & 3) + j] & keep;
+                const uint32_t v = w[c + (y >> 2)][(y & 3) + j] | nan2;
                 asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x[j]) : "r"(v), "r"(up2));
                 asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x[j]) : "r"(x[j]), "r"(kDown2));
                 asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r[j]) : "r"(x[j]), "r"(x[j] & 0xfff0fff0u));
@@ -150,7 +151,7 @@ ACACHE_DEVFN float query_terms(uint32_t hi, uint32_t lo, int lane, float scale_l
         st_shared_v4(hi + o, h[0], h[1], h[2], h[3]);
         st_shared_v4(lo + o, l[0], l[1], l[2], l[3]);
     }
-    return finite ? fmaxf(scale_log2 * __uint_as_float((E - 7u) << 23), 0x1p-126f) : __uint_as_float(0x7fffffffu);
+    return finite ? fmaxf(scale_log2 * __uint_as_float((E - 7u) << 23), 0x1p-126f) : 1.f;
 }
 
 }  // namespace q8

@@ -914,3 +914,26 @@ def test_logits_of_minus_infinity(dtype, d, n_q):
             r[:, at] = free
             got, want = run(q, r), vv[free, 0]
             assert np.abs(got - want).max() <= 2.0 ** -20 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("n_q", [1, 12, 40, 300])
+def test_non_finite_queries_without_a_key_give_zeros(dtype, d, n_q):
+    """The rows of a padded request may hold anything; a query row with a key is NaN if it is not finite, however
+    many parts of the keys hold none."""
+    B, hq, hkv, T = 4, 2, 1, 2000
+    (kc, vc, sc, kv, vv), q, rs, ns = _attend_case(B, n_q, hq, hkv, d, dtype, T, False, 27)
+    q[:, -1, 0, 3], q[:, 0, 1, 0] = float("nan"), -float("inf")
+    rs[0], rs[1:3] = -1, -1
+    rs[1, 700], rs[2, T - 1] = 5, 6
+    out, st = torch.full(q.shape, 9.0, dtype=dtype, device="cuda"), _status()
+    ac.acache_slot_attention_q8(_desc(hq, hkv, d, dtype), B, n_q, dev(q), T, dev(rs), dev(kc), dev(vc), dev(sc), ns, out,
+                                drop_none=True, dev_status=st)
+    got = out.double().cpu().numpy()
+    assert st.item() == 0 and (got[0] == 0).all()
+    gone = ~torch.isfinite(q).all(-1).numpy()
+    assert gone.any() and np.isnan(got[1:][gone[1:]]).all()
+    q[~torch.isfinite(q)] = 0.0
+    for b in range(1, B):
+        want, tol = attention(q[b], rs[b].numpy(), kv, vv, d ** -0.5, True)
+        assert_attention(got[b][~gone[b]], want[~gone[b]], tol[~gone[b]], f"request {b}")

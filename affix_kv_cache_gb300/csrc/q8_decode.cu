@@ -26,14 +26,17 @@
 // The warps of a CTA, the CTAs of a cluster (up to 8, where that fills the SMs better) share the keys; partial
 // (maximum, sum, O) are merged in a fixed order through (distributed) shared memory.
 //
-// Measured: 8 requests x 32 rows x 4,480 keys (32 heads, d = 128) 85 us, 0.21 of the time to read the pool's bytes:
-// bound by the latency between the products of a chunk (32 rows take 8 warps to an SM); 48 single tokens of 1 to
-// 16,000 keys (32 heads over 8) 53 us, 0.42: the longest request's parts, 2,000 keys each, take most of that.
+// Measured: 8 requests x 32 rows x 4,480 keys (32 heads, d = 128) 86 us with their store, 0.21 of the rate at which the
+// pool's bytes could be read: bound by the latency between the products of a chunk (32 rows take 8 warps to an SM;
+// a warp waits for fixed latencies in half of its cycles, the tensor pipe is busy in 0.42 of them); 48 single tokens of
+// 1 to 16,000 keys (32 heads over 8) 54 us, 0.41: the longest request's parts, 2,000 keys each, take most of that; 16 tokens
+// over 4,000 keys each 26.5 us, 0.60: launch, the first loads and the merges, some 7 us, stand beside 16 us of reading.
 //
 // The register-operand products run at a quarter of tcgen05's rate, which few rows do not need: 128 keys
 // against 16 rows are 525 cycles of an SM's matrix pipes, and reading them at the memory's rate takes
 // 1400.  The tcgen05 form of this kernel (rows replicated over the 128 TMEM lanes, f16 V through shared
-// memory) took 2300 cycles a tile of 128 keys, 1600 of them its M = 128 products of mostly unused rows.
+// memory) took 2300 cycles a tile of 128 keys, 1600 of them its M = 128 products of mostly unused rows.  (With the keys
+// as the 128 rows of S^T and the query rows as its columns nothing would be unused: not built.)
 #include <algorithm>
 #include <atomic>
 

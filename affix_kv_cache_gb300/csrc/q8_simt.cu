@@ -1,15 +1,17 @@
-// q8_simt.cu -- read-slot attention over an 8-bit pool on CUDA cores: float32 queries and outputs
-// (tensor cores have no float32 mode that keeps them) and shapes the tensor-core kernel does not
-// cover.
+// q8_simt.cu -- read-slot attention over an 8-bit pool on CUDA cores: float32 queries and outputs, and
+// calls that the tensor-core kernels do not cover (a softmax scale that is not positive, an empty pool).
+// (One pass of a tensor-core product would cut float32 queries and probabilities to 8 or 11 bits.  The codes are
+// exact in bf16, so passes over three bf16 terms of the float32 operand would keep them: not built.)
 //
 // One CTA per 64 packed rows -- (query, query head of the KV head's group), so the heads of a
 // group share one pass over the keys -- and per part of the key range: 64-key tiles are decoded to
 // float32 in shared memory, S = Q K^T and O += P V run as 4 x 4 and 4 x d/16 register tiles, and
 // the softmax keeps a running maximum and sum per row in base 2.  Bound by FFMA issue and the
-// shared-memory reads that feed it; two CTAs per SM.  With at most 32 or 16 rows to a (request, KV
-// head) a CTA takes that many, with as many fewer threads: the products of 64 rows would be mostly of
-// rows that are not there (8 single tokens over 4,000 keys, 32 heads over 8, d = 128, float32: 142 us, 308 in
-// tiles of 64; 4 x 32 rows over 1,408 keys, 8 heads: 48 and 115).  When there are few blocks the key range
+// shared-memory reads that feed it; at least two CTAs per SM (4 x 589 rows over 1,408 keys, 8 heads, d = 128,
+// float32: 478 us, 28 TFLOP/s; 560 with one).  With at most 32 or 16 rows to a (request, KV head) a CTA takes that
+// many, with as many fewer threads: the products of 64 rows would be mostly of rows that are not there (8 single
+// tokens over 4,000 keys, 32 heads over 8, d = 128, float32: 137 us where they share the keys and 183 where each has its
+// own, 265 and 284 in tiles of 64; 4 x 32 rows over 1,408 keys, 8 heads: 45 and 63).  When there are few blocks the key range
 // is split over a cluster of up to 8 CTAs, which merge their partial (maximum, sum, O) through
 // distributed shared memory in rank order.
 #include <cfloat>

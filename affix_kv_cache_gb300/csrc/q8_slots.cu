@@ -7,7 +7,7 @@
 // Both are bound by memory.  The store's item is 16 consecutive elements of one (row, head), of K and of
 // V: a lane reads an item of each matrix with 16-byte loads, the d/16 lanes of a head agree on the
 // largest magnitude with shuffles, and one lane writes the head's two exponents as one 16-bit
-// word (measured 76 us for 16 x 1,205 rows of 32 heads, d = 128, bf16: 0.92 of the copy bandwidth); a
+// word (16 x 1,205 rows of 32 heads, d = 128: 76 us in bf16, 123 us in float32, 0.92 and 0.95 of the copy bandwidth); a
 // thread keeps two items in flight.  The read-back's item is one 16-byte piece of the output.  Items are
 // numbered across rows, so every lane has work whatever the head count is; a step of the grid advances
 // (row, item) by a constant pair, so the only division is at a thread's start.
@@ -119,9 +119,9 @@ q8_write_kernel(const int32_t* __restrict__ write_slot, int64_t nrows, int ipr, 
 // One 16-byte piece of the output: 4 float32 or 8 bf16 from as many codes, so that the lanes of a warp
 // write whole lines (with 16 codes to a lane, as in the store, a lane's pieces of the output are 32
 // or 64 bytes apart from the next lane's: twice the time).  One piece at a time: few registers, so all the
-// warps an SM holds are there to keep loads in flight, and what they write stays close together: 29 us
-// for 8 x 4,480 rows of 8 heads (d = 128, float32, 147 MB written: 0.79 of the copy bandwidth), 37 with
-// four pieces; 57 us for 32 heads in bf16 (0.83), 70 with four.
+// warps an SM holds are there to keep loads in flight, and what they write stays close together: 26.4 us
+// for 8 x 4,480 rows of 8 heads (d = 64, float32, 147 MB written: 0.86 of the copy bandwidth) and 119 us for 32 heads
+// (d = 128, bf16, 587 MB: 0.80); with four pieces at a time 1.2 to 1.3 times that.
 template <typename T> struct Piece;
 template <> struct Piece<float> {
     using Codes = uint32_t;

@@ -35,7 +35,7 @@
 //   CTAs, whose partial (maximum, sum, O) are merged through distributed shared memory, in rank order.
 //
 // What bounds it.  16 requests x 986 rows x 2,624 keys, 28 heads over 4, d = 128: 555 us, 1,070 TFLOP/s, 0.55 of the
-// measured bf16 rate.  A step of 64 keys takes both chains some 1,800 cycles; their MMAs alone take 1,260
+// measured bf16 rate.  A step of 64 keys takes both chains some 1,800 cycles; their MMAs alone take 1,280
 // (2 x 385 for S, whose 64-key MMAs read 6 KB of shared memory, 48 cycles, for 32 cycles of products, and
 // 2 x 257 for PV).  No pipe is full (ALU 0.38, FMA 0.27, MUFU 0.21); what comes nearest is shared memory: the
 // MMAs' operands, the keys' factors (every softmax warp reads all of them), V's tiles and K's take some

@@ -394,6 +394,12 @@ ACACHE_API int acache_gather_slots(const acache_attn_desc* a, int batch, int seq
  * attention call up to 65,535 requests, 65,535 tiles of 64 rows (queries x heads of a group), 2^31 - 1024
  * keys of a request and a pool below 2^31 rows (slots x heads); more is ACACHE_ERR_INVALID_ARG.
  * The descriptor's dtype is that of the fresh K/V, the queries and the outputs.
+ * Roundings: logits, maxima, sums of weights and O are float32 in every kernel (exponentials to 2^-22), and a float32
+ * call rounds nothing further.  In a bf16 call with a positive softmax scale the weights are rounded before the
+ * product with V, not in their sum, and the query row is carried in two terms or in f16.  With more than 32 rows
+ * (queries x heads of a group) to a request and KV head: weights to bf16, a query element off by at most 2^-17 of the
+ * row's largest.  With up to 32: weights times the V row's power of two to f16 (11 bits; fewer below 2^-17 of the
+ * largest, none below 2^-27), a query element off by at most 2^-32 of the row's largest.
  * ------------------------------------------------------------------------------- */
 
 /* (4a) Store step of one layer: acache_write_slots into an 8-bit pool, quantising as it writes.

@@ -14,5 +14,8 @@ from ._lib import (AcacheError, AttnDesc, attn_desc, acache_build_slot_maps,  # 
                    acache_rerotate_keys, acache_store_attend, acache_store_attend_layers, acache_topk_anchors, Pool,
                    acache_wait_budget, acache_write_slots,
                    acache_write_slots_q8, acache_gather_slots_q8, acache_slot_attention_q8,
-                   acache_slot_attention_varlen_q8, acache_store_attend_q8, lib,
+                   acache_slot_attention_varlen_q8, acache_store_attend_q8,
+                   Rope, rope_desc, rope_desc_frequencies, acache_rotate_qk, acache_rotate_store,
+                   acache_rotate_store_q8, acache_slot_attention_masked, acache_slot_attention_masked_varlen,
+                   acache_token_scores, lib,
                    status_string, version)

@@ -32,6 +32,9 @@ SLOT_NONE = -1
 DEV_BAD_SLOT, DEV_SHARED_WRITE, DEV_BAD_ROW, DEV_BAD_ANCHOR, DEV_NAN, DEV_TIMEOUT = 1, 2, 4, 8, 16, 32
 DEV_BAD_LENGTH = 64
 DEV_BAD_VALUE = 128
+DEV_BAD_TOKEN = 256
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = 0, 1, 2, 3, 4
+MAX_ALTERNATIVES = 32
 
 EXPORTS = ("acache_status_string", "acache_version", "acache_wait_budget", "acache_probe_workspace_bytes",
            "acache_probe_scores", "acache_probe_scores_layers", "acache_probe_scores_noalloc", "acache_topk_anchors", "acache_build_slot_maps",
@@ -43,7 +46,10 @@ EXPORTS = ("acache_status_string", "acache_version", "acache_wait_budget", "acac
            "acache_pool_register_affix", "acache_pool_release_affix", "acache_pool_alloc_private",
            "acache_pool_free_private", "acache_pool_stats",
            "acache_write_slots_q8", "acache_gather_slots_q8", "acache_slot_attention_q8",
-           "acache_slot_attention_varlen_q8", "acache_store_attend_q8")
+           "acache_slot_attention_varlen_q8", "acache_store_attend_q8",
+           "acache_rope_init", "acache_rope_init_frequencies", "acache_rotate_qk", "acache_rotate_store",
+           "acache_rotate_store_q8", "acache_slot_attention_masked", "acache_slot_attention_masked_varlen",
+           "acache_token_scores")
 
 
 class AcacheError(RuntimeError):
@@ -56,6 +62,16 @@ class AttnDesc(ctypes.Structure):
     _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("dtype", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("phase", ctypes.c_uint64 * 64)]
+
+
+class Mask(ctypes.Structure):
+    _fields_ = [("row_range", ctypes.c_void_p), ("q_pos", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
+                ("softcap", ctypes.c_float), ("drop_none", ctypes.c_int32)]
 
 
 def attn_desc(hq: int, hkv: int, d: int, scale: float, dtype) -> AttnDesc:
@@ -78,7 +94,8 @@ def lib() -> ctypes.CDLL:
                                "run `python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(LIB_PATH)
         P, I, I64, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-        D = ctypes.POINTER(AttnDesc)
+        D, R, M = ctypes.POINTER(AttnDesc), ctypes.POINTER(Rope), ctypes.POINTER(Mask)
+        F = ctypes.c_float
         sig = {
             "acache_status_string": (ctypes.c_char_p, [I]),
             "acache_version": (I, []),
@@ -104,6 +121,17 @@ def lib() -> ctypes.CDLL:
             "acache_slot_attention_q8": (I, [D, I, I, P, I, P, P, P, P, I64, P, I, P, P]),
             "acache_slot_attention_varlen_q8": (I, [D, I, P, I, I, P, P, I, P, P, P, P, I64, P, I, P, P]),
             "acache_store_attend_q8": (I, [D, I, I, P, P, P, P, P, P, I64, I64, I, P, I, P, P, I, P, P]),
+            "acache_rope_init": (I, [ctypes.POINTER(Rope), I, I, ctypes.c_double, I, ctypes.c_double, I64,
+                                     ctypes.c_double, ctypes.c_double]),
+            "acache_rope_init_frequencies": (I, [ctypes.POINTER(Rope), I, I, ctypes.POINTER(ctypes.c_double),
+                                                 ctypes.c_float]),
+            "acache_rotate_qk": (I, [D, R, I64, P, P, I64, P, I64, P, P, F, P, I64, P, I64, P]),
+            "acache_rotate_store": (I, [D, R, I, I, P, P, P, I64, P, I64, P, I64, P, P, F, P, P, P, I64, I64, P, P]),
+            "acache_rotate_store_q8": (I, [D, R, I, I, P, P, P, I64, P, I64, P, I64, P, P, F, P, P, P, P, I64, I64,
+                                           P, P]),
+            "acache_slot_attention_masked": (I, [D, M, I, I, P, I, P, P, P, I64, P, P, P]),
+            "acache_slot_attention_masked_varlen": (I, [D, M, I, P, I, I, P, P, I, P, P, P, I64, P, P, P]),
+            "acache_token_scores": (I, [I, I64, I, P, I64, F, P, P, P, I, P, P, P, P]),
             "acache_pool_create": (I, [I64, I64, ctypes.c_int32, ctypes.POINTER(P)]),
             "acache_pool_destroy": (None, [P]),
             "acache_pool_register_affix": (I, [P, ctypes.c_uint64, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
@@ -404,6 +432,138 @@ def acache_store_attend_q8(desc, batch, rows, write_slot, k_new, v_new, k_cache,
                                       num_slots, private_begin, n_q, _on(dev, q), seq_len, _on(dev, read_slot),
                                       _on(dev, out), int(bool(drop_none)), _on(dev, dev_status), _stream(stream))
     return _check("acache_store_attend_q8", st) if check else st
+
+
+# ---- the steps around the attention, and attention under a mask (see include/acache.h)
+_SCALINGS = {"none": ROPE_NONE, "linear": ROPE_LINEAR, "ntk": ROPE_NTK, "yarn": ROPE_YARN, "bands": ROPE_BANDS}
+
+
+def rope_desc(rotary_dim, theta=10000.0, interleaved=False, scaling="none", factor=1.0, trained_len=0, turns_low=0.0,
+              turns_high=0.0, amplitude=None) -> Rope:
+    """The rotation of a head's first rotary_dim elements, to be kept and passed to the calls below."""
+    r = Rope()
+    _check("acache_rope_init", lib().acache_rope_init(
+        ctypes.byref(r), rotary_dim, int(bool(interleaved)), float(theta), _SCALINGS.get(scaling, scaling), float(factor),
+        int(trained_len), float(turns_low), float(turns_high)))
+    if amplitude is not None:
+        r.amplitude = amplitude
+    return r
+
+
+def rope_desc_frequencies(frequencies, interleaved=False, amplitude=1.0) -> Rope:
+    """The same from a sequence of angles per position, one per pair."""
+    f = [float(x) for x in frequencies]
+    r = Rope()
+    _check("acache_rope_init_frequencies", lib().acache_rope_init_frequencies(
+        ctypes.byref(r), 2 * len(f), int(bool(interleaved)), (ctypes.c_double * max(len(f), 1))(*f), float(amplitude)))
+    return r
+
+
+def _row_stride(t, heads, d):
+    """Elements from one row [heads][d] of a tensor [..., heads, d] to the next; rows must be evenly spaced."""
+    if not isinstance(t, torch.Tensor) or t.is_contiguous():
+        return heads * d
+    shape, stride = t.shape, t.stride()
+    if t.dim() < 3 or stride[-1] != 1 or (shape[-2] > 1 and stride[-2] != shape[-1]):
+        raise ValueError("the heads of a row have to follow one another")
+    step, n = None, 1
+    for size, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if size != 1:
+            if step is None:
+                step = st
+            elif st != step * n:
+                raise ValueError("the rows have to be evenly spaced")
+            n *= size
+    return heads * d if step is None else step
+
+
+def acache_rotate_qk(desc, rope, rows, positions, q, k, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6,
+                     stream=None, check=True):
+    """Norm (with a weight) and rotary position of query and key rows [..., heads, d], which may be slices
+    of a wider row; rope=None rotates nothing, q or k None is left out."""
+    dev = _current_device()
+    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    st = lib().acache_rotate_qk(
+        ctypes.byref(desc), None if rope is None else ctypes.byref(rope), rows, _on(dev, positions), _on(dev, q),
+        _row_stride(q, hq, d), _on(dev, k), _row_stride(k, hkv, d), _on(dev, q_weight), _on(dev, k_weight), eps,
+        _on(dev, q_out), _row_stride(q_out, hq, d), _on(dev, k_out), _row_stride(k_out, hkv, d), _stream(stream))
+    return _check("acache_rotate_qk", st) if check else st
+
+
+def _new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight, k_weight, eps, q_out, k_cache,
+              v_cache):
+    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    return (ctypes.byref(desc), None if rope is None else ctypes.byref(rope), batch, rows, _on(dev, positions),
+            _on(dev, write_slot), _on(dev, q), _row_stride(q, hq, d), _on(dev, k), _row_stride(k, hkv, d), _on(dev, v),
+            _row_stride(v, hkv, d), _on(dev, q_weight), _on(dev, k_weight), eps, _on(dev, q_out), _on(dev, k_cache),
+            _on(dev, v_cache))
+
+
+def acache_rotate_store(desc, rope, batch, rows, positions, write_slot, q, k, v, q_out, k_cache, v_cache, num_slots,
+                        private_begin, q_weight=None, k_weight=None, eps=1e-6, dev_status=None, stream=None,
+                        check=True):
+    """acache_rotate_qk with the rotated keys and the values stored to their slots."""
+    dev = _current_device()
+    st = lib().acache_rotate_store(*_new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight,
+                                              k_weight, eps, q_out, k_cache, v_cache),
+                                   num_slots, private_begin, _on(dev, dev_status), _stream(stream))
+    return _check("acache_rotate_store", st) if check else st
+
+
+def acache_rotate_store_q8(desc, rope, batch, rows, positions, write_slot, q, k, v, q_out, k_cache, v_cache, kv_scale,
+                           num_slots, private_begin, q_weight=None, k_weight=None, eps=1e-6, dev_status=None,
+                           stream=None, check=True):
+    """The same into an 8-bit pool."""
+    dev = _current_device()
+    st = lib().acache_rotate_store_q8(*_new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight,
+                                                 k_weight, eps, q_out, k_cache, v_cache),
+                                      _on(dev, kv_scale), num_slots, private_begin, _on(dev, dev_status),
+                                      _stream(stream))
+    return _check("acache_rotate_store_q8", st) if check else st
+
+
+def acache_slot_attention_masked(desc, batch, n_q, q, seq_len, read_slot, k_cache, v_cache, num_slots, out,
+                                 row_range=None, q_pos=None, slopes=None, softcap=0.0, drop_none=False,
+                                 dev_status=None, stream=None, check=True):
+    """Read-slot attention whose rows see a range of keys (row_range [B, n_q, 2]), with capped scores and a
+    bias of -slopes[h] * |q_pos - t|."""
+    dev = _current_device()
+    mask = Mask(_on(dev, row_range), _on(dev, q_pos), _on(dev, slopes), softcap, int(bool(drop_none)))
+    st = lib().acache_slot_attention_masked(ctypes.byref(desc), ctypes.byref(mask), batch, n_q, _on(dev, q), seq_len,
+                                            _on(dev, read_slot), _on(dev, k_cache), _on(dev, v_cache), num_slots,
+                                            _on(dev, out), _on(dev, dev_status), _stream(stream))
+    return _check("acache_slot_attention_masked", st) if check else st
+
+
+def acache_slot_attention_masked_varlen(desc, batch, q_start, max_q_rows, total_q_rows, q, kv_start, max_seq_len,
+                                        read_slot, k_cache, v_cache, num_slots, out, row_range=None, q_pos=None,
+                                        slopes=None, softcap=0.0, drop_none=False, dev_status=None, stream=None,
+                                        check=True):
+    """The same over a ragged batch (offsets as in acache_slot_attention_varlen)."""
+    dev = _current_device()
+    mask = Mask(_on(dev, row_range), _on(dev, q_pos), _on(dev, slopes), softcap, int(bool(drop_none)))
+    st = lib().acache_slot_attention_masked_varlen(
+        ctypes.byref(desc), ctypes.byref(mask), batch, _on(dev, q_start), max_q_rows, total_q_rows, _on(dev, q),
+        _on(dev, kv_start), max_seq_len, _on(dev, read_slot), _on(dev, k_cache), _on(dev, v_cache), num_slots,
+        _on(dev, out), _on(dev, dev_status), _stream(stream))
+    return _check("acache_slot_attention_masked_varlen", st) if check else st
+
+
+def acache_token_scores(rows, vocab, logits, tokens=None, token_logprob=None, entropy=None, top_tokens=None,
+                        top_logprob=None, temperature=1.0, k=None, dev_status=None, stream=None, check=True):
+    """Log probabilities of given tokens, entropy and the likeliest tokens (k = the last dimension of top_tokens)
+    of logits [rows, vocab] in bf16 or float32, whose rows may lie apart."""
+    dtype = {torch.float32: ACACHE_F32, torch.bfloat16: ACACHE_BF16}.get(logits.dtype, -1)
+    if logits.dim() < 1 or (vocab > 1 and logits.stride(-1) != 1):
+        raise ValueError("the logits of a row have to follow one another")
+    dev = _current_device()
+    stride = vocab if logits.is_contiguous() else _row_stride(logits.unsqueeze(-2), 1, vocab)
+    if k is None:
+        k = 0 if top_tokens is None else top_tokens.shape[-1]
+    st = lib().acache_token_scores(dtype, rows, vocab, _on(dev, logits), stride, temperature, _on(dev, tokens),
+                                   _on(dev, token_logprob), _on(dev, entropy), k, _on(dev, top_tokens),
+                                   _on(dev, top_logprob), _on(dev, dev_status), _stream(stream))
+    return _check("acache_token_scores", st) if check else st
 
 
 class Pool:

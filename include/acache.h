@@ -67,7 +67,8 @@ enum {
     ACACHE_DEV_NAN = 16,          /* a NaN importance score reached Top-K                  */
     ACACHE_DEV_TIMEOUT = 32,      /* a bounded wait inside a kernel gave up                */
     ACACHE_DEV_BAD_LENGTH = 64,   /* a ragged-batch request length outside its bounds     */
-    ACACHE_DEV_BAD_VALUE = 128    /* a K or V value an 8-bit pool cannot hold was stored  */
+    ACACHE_DEV_BAD_VALUE = 128,   /* a K or V value an 8-bit pool cannot hold was stored  */
+    ACACHE_DEV_BAD_TOKEN = 256    /* a token outside the vocabulary was to be scored      */
 };
 
 /* Read-slot map entry of a logical position whose K/V was discarded (the page's DropNA
@@ -461,6 +462,169 @@ ACACHE_API int acache_store_attend_q8(const acache_attn_desc* a, int batch, int 
 ACACHE_API int acache_rerotate_keys(const acache_attn_desc* a, int64_t rows, const void* k_in,
                         void* k_out, int32_t delta_pos, double rope_theta, int interleaved,
                         void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Rotary positions.  Page: Sec. 4 and Limitations (the cache is kept after the rotation); the
+ * pages leave the rotation itself to the model, here it is part of the path.
+ *
+ * An acache_rope (host memory, read during a call only) describes the rotation of a head's first
+ * rotary_dim elements: pair i at position p turns by the angle p * f_i and is multiplied by
+ * `amplitude`; elements from rotary_dim on pass unchanged.  Pairs as in acache_rerotate_keys
+ * (interleaved = 0: (x_i, x_{i + rotary_dim/2}); 1: (x_{2i}, x_{2i+1})).  phase[i] is f_i / 2 pi
+ * modulo one turn in units of 2^-64 turns: the product with a 32-bit position is exact modulo
+ * whole turns, so far positions lose nothing (the angle is off by at most 2^-33 turns from the
+ * frequency's own rounding, and by 2^-24 of itself, taken within half a turn, in float32).
+ *
+ * acache_rope_init fills one with f_i = theta^(-2i/rotary_dim), changed for long contexts by
+ *   ACACHE_ROPE_NONE    nothing
+ *   ACACHE_ROPE_LINEAR  f / factor
+ *   ACACHE_ROPE_NTK     theta * factor^(r/(r-2)) in place of theta, r = rotary_dim (r > 2)
+ *   ACACHE_ROPE_YARN    with c(n) = r ln(trained_len / (2 pi n)) / (2 ln theta), the pair at which n
+ *                       turns fit the trained length (theta > 1), a = max(floor c(turns_high), 0) and
+ *                       b = min(ceil c(turns_low), r - 1): f where i <= a, f / factor where i >= b,
+ *                       linear in i between; amplitude = 0.1 ln(factor) + 1 (factor > 1)
+ *                       (YaRN, arXiv 2309.00071)
+ *   ACACHE_ROPE_BANDS   by the turns n = f trained_len / 2 pi: f where n >= turns_high, f / factor
+ *                       where n <= turns_low, linear in n between
+ * with 0 < turns_low < turns_high (0, 0: 1 and 32 with YARN, 1 and 4 with BANDS).  amplitude is 1
+ * except as stated; a caller may change it afterwards.  acache_rope_init_frequencies takes the
+ * f_i (radians per position, finite) from the caller.
+ * Both are host functions: ACACHE_ERR_INVALID_ARG for a rotary_dim that is odd or outside 2..128,
+ * theta or factor not finite and positive, or what the list above rules out.
+ * ------------------------------------------------------------------------------- */
+enum {
+    ACACHE_ROPE_NONE = 0,
+    ACACHE_ROPE_LINEAR = 1,
+    ACACHE_ROPE_NTK = 2,
+    ACACHE_ROPE_YARN = 3,
+    ACACHE_ROPE_BANDS = 4
+};
+typedef struct {
+    int32_t rotary_dim;     /* even, at most the head dim of the call                 */
+    int32_t interleaved;
+    float amplitude;
+    int32_t reserved;       /* 0                                                      */
+    uint64_t phase[64];     /* the first rotary_dim / 2 are used                      */
+} acache_rope;
+ACACHE_API int acache_rope_init(acache_rope* out, int rotary_dim, int interleaved, double theta,
+                        int scaling, double factor, int64_t trained_len, double turns_low,
+                        double turns_high);
+ACACHE_API int acache_rope_init_frequencies(acache_rope* out, int rotary_dim, int interleaved,
+                        const double* frequencies, float amplitude);
+
+/* ---------------------------------------------------------------------------------
+ * Norm and rotary position of query and key rows, as a probe or an attention takes them.
+ * For each row and head: x' = x / sqrt(mean of x^2 over the head + eps) * weight (with a weight;
+ * else x' = x), then the rotation at positions[row].  Everything is float32 between the load and
+ * the one rounding to the storage type.
+ *   positions    [rows] int32 (any value; may be NULL with rope = NULL: no rotation)
+ *   q, k         rows of [Hq][d] / [Hkv][d], contiguous within a row; q_stride / k_stride elements
+ *                from one row to the next (so slices of a fused projection need no copy).  Either
+ *                may be NULL: that matrix is left out
+ *   q_weight, k_weight  [d] of the descriptor's dtype, or NULL: no norm
+ *   q_out, k_out rows at their own strides.  An output may be its own input (same pointer and
+ *                stride); otherwise it must not overlap an input
+ * Pointers 16-byte aligned, strides >= a row and multiples of 16 bytes; eps >= 0.
+ * ------------------------------------------------------------------------------- */
+ACACHE_API int acache_rotate_qk(const acache_attn_desc* a, const acache_rope* rope, int64_t rows,
+                        const int32_t* positions, const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const void* q_weight, const void* k_weight, float eps,
+                        void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                        void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * (4a) Store step with norm and rotary position on the way, one layer: acache_rotate_qk of the
+ * B * rows rows with q_out [B][rows][Hq][d], and the rotated keys and the values go straight to
+ * their slots as acache_write_slots puts them (no rotated copy of the keys is written or read).
+ *   positions, write_slot [B][rows] int32 -- write_pos and the private slots of
+ *            acache_build_slot_maps are what a recompute point passes
+ *   q may be NULL (then q_out is not used); v rows at v_stride
+ * A row whose slot is outside the pool or shared stores nothing (flags as acache_write_slots);
+ * its query is rotated all the same.  The slots of one call must differ from one another.
+ * rows = 0 is a no-op.
+ * ------------------------------------------------------------------------------- */
+ACACHE_API int acache_rotate_store(const acache_attn_desc* a, const acache_rope* rope, int batch,
+                        int rows, const int32_t* positions, const int32_t* write_slot,
+                        const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const void* q_weight,
+                        const void* k_weight, float eps, void* q_out, void* k_cache,
+                        void* v_cache, int64_t num_slots, int64_t private_begin,
+                        int32_t* dev_status, void* stream);
+/* The same into an 8-bit pool: codes and exponents as acache_write_slots_q8 writes them, from the
+ * float32 rows (a key is rounded once, not to the storage type first). */
+ACACHE_API int acache_rotate_store_q8(const acache_attn_desc* a, const acache_rope* rope, int batch,
+                        int rows, const int32_t* positions, const int32_t* write_slot,
+                        const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const void* q_weight,
+                        const void* k_weight, float eps, void* q_out, void* k_cache,
+                        void* v_cache, uint8_t* kv_scale, int64_t num_slots,
+                        int64_t private_begin, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * (4b) Read-slot attention under a mask, one layer.  The page's attention is bidirectional over
+ * all keys; models that are causal, block-causal, windowed, prefix- or document-masked, that cap
+ * their scores or bias them by distance take this form over the same pool and maps.
+ * Row i of request b, query head h and logical key t:
+ *   s = scale * q.k;  s = softcap * tanh(s / softcap) if softcap > 0;
+ *   s -= slopes[h] * |q_pos[b][i] - t| with slopes
+ * and the softmax runs over the keys t with row_range[b][i][0] <= t < row_range[b][i][1] (and, with
+ * drop_none, whose read-slot entry is not ACACHE_SLOT_NONE).  Nothing of a key that a row does not
+ * see reaches that row, whatever the pool holds there (infinities and NaN included).  A row that
+ * sees no key outputs zeros.
+ *   acache_mask (host memory; its pointers are device pointers, NULL where not used):
+ *     row_range  [B][n_q][2] int32, clamped to [0, T]; NULL: every row sees all keys
+ *     q_pos      [B][n_q] int32 logical positions (needed with slopes)
+ *     slopes     [Hq] float
+ *     softcap    0 (none) or positive
+ * mask = NULL is no mask at all.  Other arguments, layouts and errors as acache_slot_attention;
+ * a bad slot of a key that no row sees may go unflagged.  In the ragged form row_range and q_pos are
+ * flat like q ([total_q_rows][2], [total_q_rows]), their keys count from the request's first;
+ * its lengths, skips and flags are those of acache_slot_attention_varlen_q8.
+ * Tensor cores: bf16 (head dim 64 and 128) with a positive scale; otherwise CUDA cores.
+ * Limits: B <= 65,535, pools below 2^31 rows (slots x heads), T <= 2^31 - 1024,
+ * n_q * Hq / Hkv < 2^22; more is ACACHE_ERR_INVALID_ARG.
+ * Roundings: logits, maxima, sums and O are float32 (exponentials to 2^-22, tanh to 2^-22
+ * absolute); in a bf16 call the weights are rounded to bf16 before the product with V, not in
+ * their sum.
+ * ------------------------------------------------------------------------------- */
+typedef struct {
+    const int32_t* row_range;
+    const int32_t* q_pos;
+    const float* slopes;
+    float softcap;
+    int32_t drop_none;
+} acache_mask;
+ACACHE_API int acache_slot_attention_masked(const acache_attn_desc* a, const acache_mask* mask,
+                        int batch, int n_q, const void* q, int seq_len, const int32_t* read_slot,
+                        const void* k_cache, const void* v_cache, int64_t num_slots, void* out,
+                        int32_t* dev_status, void* stream);
+ACACHE_API int acache_slot_attention_masked_varlen(const acache_attn_desc* a, const acache_mask* mask,
+                        int batch, const int32_t* q_start, int max_q_rows, int total_q_rows,
+                        const void* q, const int32_t* kv_start, int max_seq_len,
+                        const int32_t* read_slot, const void* k_cache, const void* v_cache,
+                        int64_t num_slots, void* out, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Scores of tokens from logits: what decoding decides by.  Page: Sec. 5 (generation with a
+ * confidence threshold: the masked positions whose likeliest token is probable enough are kept).
+ * Per row, with y = logits / temperature and log p = y - log sum exp y:
+ *   token_logprob [rows] float  log p of tokens[row] (both NULL: left out).  A token outside
+ *                 [0, vocab) leaves its entry as it was and flags ACACHE_DEV_BAD_TOKEN
+ *   entropy       [rows] float  - sum p log p, tokens with p = 0 counting nothing (or NULL)
+ *   top_tokens [rows][k] int32, top_logprob [rows][k] float (or NULL): the k largest logits in
+ *                 descending order, ties to the lower token; -0.0 counts as +0.0, NaN ranks below
+ *                 every number
+ * 0 <= k <= min(vocab, ACACHE_MAX_ALTERNATIVES); dtype is that of the logits, row_stride (>= vocab)
+ * counts elements; rows need no alignment beyond their element's.  Logits of -infinity are tokens
+ * that cannot be chosen.  A row with a NaN or +infinity has NaN as every log probability and
+ * entropy and flags ACACHE_DEV_NAN; one that is -infinity throughout has NaN too, unflagged.
+ * Logits are read once (a few candidates' again); sums are float32, in a fixed order.
+ * ------------------------------------------------------------------------------- */
+#define ACACHE_MAX_ALTERNATIVES (32)
+ACACHE_API int acache_token_scores(int dtype, int64_t rows, int vocab, const void* logits,
+                        int64_t row_stride, float temperature, const int32_t* tokens,
+                        float* token_logprob, float* entropy, int k, int32_t* top_tokens,
+                        float* top_logprob, int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------------
  * Admission runtime (host only; no device memory is touched).  Page: Sec. 4.1-4.2 -- the

@@ -1,0 +1,790 @@
+// masked_tc.cu -- read-slot attention under a mask on the tensor cores (tcgen05 + TMEM, TMA-fed): bf16, head
+// dim 64 or 128, a positive scale.
+//
+// Page: "Affix Cache for Diffusion Large Language Models", Sec. 4.3 and App. C.1 (attention through the read-slot
+// map); ranges, caps and distance biases are this library's (include/acache.h, acache_slot_attention_masked).
+//
+//   s = scale q.k, capped by c tanh(s / c), biased by -slope |pos - t|; softmax over the row's keys [lo, hi)
+//
+// One CTA per (request, KV head, query block): two Q tiles A and B of 128 rows, a row being a (query, head of the
+// group) pair, so that all heads of a group share one K/V stream and a causal block spans few positions.
+//   WG0, WG1   softmax + epilogue of tile A / B, thread r owning row r = TMEM lane r: a tile of scores is read
+//              into registers, capped, biased, masked, exponentiated in base 2 against a lazily raised
+//              maximum, and written back over the scores as bf16 for the product with V.  The two take turns.
+//   WG2        warps 8 and 9 issue the MMAs of A and B (S = Q K^T from shared memory, O += P V with P from TMEM)
+//   warps 10-19  TMA producers of a 3-stage K ring and a 2-stage V ring: a tile of 128 consecutive slots is tiled
+//              box loads of the pool, any other gather4 loads of four rows each.
+// A block left with one Q tile splits its keys between the two chains and merges them at the end.
+// The CTA streams only keys from the first that one of its rows sees to the last: the window [min lo, max hi),
+// which need not start at a whole tile.  Inside it a row's range is a bit mask per 32 keys; tiles that every row of a warp sees
+// whole skip it.  Blocks run from the last to the first, so that a causal call starts its longest first.
+// What a masked key holds cannot reach a row through its score (replaced by -infinity), but 0 x NaN is NaN in
+// the product with V: a row whose output is not finite while its sum of weights is, is computed again by its
+// warp over its own keys alone.
+//
+// Every mbarrier wait is bounded (acache_wait_budget); a wait that gives up raises a CTA-wide abort flag and
+// ACACHE_DEV_TIMEOUT, roles leave their loops, MMAs and loads in flight are waited for (bounded), and TMEM is
+// freed before the CTA exits.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+#include "q8.cuh"
+#include "step.cuh"
+#include "tc_attn.cuh"
+
+namespace acache {
+namespace {
+
+using namespace ptx;
+using bf16 = __nv_bfloat16;
+
+constexpr int kBM = 128;                    // rows of a Q tile
+constexpr int kQT = 2;                      // Q tiles to a CTA
+constexpr int kBN = 128;                    // keys of a tile
+constexpr int kKStages = 3, kVStages = 2;
+constexpr int kMmaWarp = 8, kProdWarp = 10, kProdPerRing = 5;
+constexpr int kThreads = (kProdWarp + 2 * kProdPerRing) * 32;
+// Registers: 640 threads x 96 at launch; the softmax warpgroups grow to 168, the others shrink to 48
+constexpr int kRegLaunch = 65536 / kThreads / 8 * 8, kRegSoftmax = 168, kRegOther = 48;
+static_assert(2 * 128 * kRegSoftmax + (kThreads - 256) * kRegOther <= kThreads * kRegLaunch, "register split");
+constexpr uint32_t kRegion = kBN * 128;     // 64 columns of a 128-row tile
+__host__ __device__ constexpr uint32_t tile_bytes(int D) { return (uint32_t)(D / 64) * kRegion; }
+__host__ __device__ constexpr uint32_t smem_bytes(int D) { return tile_bytes(D) * (kQT + kKStages + kVStages) + 1024; }
+constexpr uint32_t kTmemCols = 512;         // S_A, S_B, O_A, O_B
+__host__ __device__ constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
+__host__ __device__ constexpr uint32_t col_o(int t) { return 256u + (uint32_t)t * 128u; }
+constexpr float kRescaleThreshold = 8.0f;   // log2 units: weights stay below 2^8
+constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles: the abort path's own waits
+
+struct MaskParams {
+    CUtensorMap tm_q;     // fixed: 4-D [B][n_q][Hq][d], box {64, g, qpt, 1}; ragged: 3-D [total_q][Hq][d], box {64, g, qpt}
+    CUtensorMap tm_o;     // output, laid out as tm_q
+    CUtensorMap tm_kg;    // 2-D pool rows [num_slots * Hkv][d], box {64, 1} (gather4)
+    CUtensorMap tm_vg;
+    CUtensorMap tm_kb;    // 3-D pool [num_slots][Hkv][d], box {64, 1, 128} (consecutive slots)
+    CUtensorMap tm_vb;
+    const bf16 *q, *k_cache, *v_cache;
+    bf16* out;
+    const int32_t *read_slot, *q_start, *kv_start, *row_range, *q_pos;
+    const float* slopes;
+    int32_t* dev_status;
+    int64_t num_slots;
+    int n_rows, total_q, T_len, Hq, Hkv, g;
+    int qpt;              // queries of a tile: floor(128 / g)
+    int drop;
+    float scale_log2;     // > 0
+    float cap_in;         // 2 log2e scale / softcap: 2^(cap_in q.k) = e^(2 s / softcap)
+    float cap_log2;       // softcap log2e
+    long long budget;
+};
+
+struct MaskCtl {
+    uint64_t q_full;
+    uint64_t k_full[kKStages], k_empty[kKStages];
+    uint64_t v_full[kVStages + 1], v_empty[kVStages + 1];   // + the stage in the free Q buffer (split keys)
+    uint64_t s_full[kQT], p_half[kQT], p_full[kQT], drain[kQT], turn[kQT];
+    uint32_t tmem_base;
+    int abort;
+    int unlanded;         // abort path: some load issued before the abort may not have landed
+    int split_ok;
+    int win_lo[8], win_hi[8];
+    float split_m[kBM], split_l[kBM];
+};
+
+static_assert(kKStages == 3 && kVStages == 2, "ring sizes 2 and 3");
+ACACHE_DEVFN int ring_lap(int e, int n) { return n == 2 ? (e >> 1) : e / 3; }
+ACACHE_DEVFN int ring_stage(int e, int n) { return e - ring_lap(e, n) * n; }
+
+// Ring entry e is the e-th tile loaded; chain t reads its i-th tile from entry(t, i).  Unsplit: every chain
+// reads every tile.  Split: chain 0 tiles [0, n0), chain 1 the rest, entries alternating.
+struct KeySchedule {
+    bool split;
+    int n_kv, n0;
+    ACACHE_DEVFN int n_tiles(int t) const { return split ? (t == 0 ? n0 : n_kv - n0) : n_kv; }
+    ACACHE_DEVFN int tile(int t, int i) const { return (split && t == 1) ? n0 + i : i; }
+    ACACHE_DEVFN int entry(int t, int i) const {
+        if (!split) return i;
+        const int n1 = n_kv - n0;
+        return i < n1 ? 2 * i + t : n1 + i;
+    }
+    ACACHE_DEVFN int entry_tile(int e) const {
+        if (!split) return e;
+        const int n1 = n_kv - n0;
+        if (e < 2 * n1) return (e & 1) ? n0 + (e >> 1) : (e >> 1);
+        return e - n1;
+    }
+};
+
+ACACHE_DEVFN bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_status, long long budget) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > budget) {
+            *abort_flag = 1;
+            flag(dev_status, ACACHE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// bits [max(n, 0), 32), none from 32 on (the instruction clamps its shift)
+ACACHE_DEVFN uint32_t bits_from(int n) {
+    uint32_t r;
+    asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(r) : "r"(max(n, 0)));
+    return r;
+}
+ACACHE_DEVFN float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// c tanh(s / c) in log2 units from the product q.k: tanh y = 1 - 2 / (1 + e^2y), within 2^-22 c of it
+// (infinities of e^2y give the limits)
+ACACHE_DEVFN float capped(float dot, float cap_in, float cap_log2) {
+    return fmaf(-2.f * cap_log2, fast_rcp(1.f + fast_exp2(dot * cap_in)), cap_log2);
+}
+
+// One row over its own keys [lo, hi), by a warp: for rows whose product with V met a masked key that is not
+// finite.  q and out: the row; rs: the request's read-slot entries.
+template <int D, bool kCap, bool kBias>
+ACACHE_DEVFN void masked_row(const MaskParams& p, const bf16* q, bf16* out, const int32_t* rs, int lo, int hi, int hk,
+                                        float slope_log2, int64_t pos, int lane) {
+    constexpr int kPer = D / 32;
+    float m = -INFINITY, l = 0.f, acc[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+    for (int t0 = lo; t0 < hi; t0 += 32) {
+        const int t = t0 + lane;
+        float s = -INFINITY;
+        int64_t at = -1;
+        if (t < hi) {
+            const int slot = rs[t];
+            if (!(p.drop && slot == ACACHE_SLOT_NONE)) {
+                float dot = 0.f;
+                if (slot >= 0 && slot < p.num_slots) {
+                    at = ((int64_t)slot * p.Hkv + hk) * D;
+#pragma unroll 4
+                    for (int c = 0; c < D; ++c) dot = fmaf(to_f32(q[c]), to_f32(p.k_cache[at + c]), dot);
+                }
+                s = kCap ? capped(dot, p.cap_in, p.cap_log2) : dot * p.scale_log2;
+                if (kBias) s = fmaf(-slope_log2, fabsf((float)(pos - t)), s);
+            }
+        }
+        const float m_new = fmaxf(m, warp_max(s)), m_ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = fast_exp2(m - m_ref), w = fast_exp2(s - m_ref);
+        l = l * alpha + warp_sum(w);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) acc[x] *= alpha;
+        for (int u = 0; u < min(32, hi - t0); ++u) {
+            const float wu = __shfl_sync(0xffffffffu, w, u);
+            const int64_t au = __shfl_sync(0xffffffffu, at, u);
+            if (au < 0) continue;
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) acc[x] = fmaf(wu, to_f32(p.v_cache[au + lane + 32 * x]), acc[x]);
+        }
+        m = m_new;
+    }
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) out[lane + 32 * x] = from_f32<bf16>(l == 0.f ? 0.f : acc[x] / l);
+}
+
+template <int D, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+masked_tc_kernel(const __grid_constant__ MaskParams p) {
+    constexpr uint32_t kTileBytes = tile_bytes(D);
+    constexpr int kHalves = D / 64;                    // 64-column regions of a tile
+    extern __shared__ uint8_t dsm[];
+    __shared__ MaskCtl ctl;
+    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+    auto sQ = [&](int t) { return base + kTileBytes * (uint32_t)t; };
+    auto sK = [&](int s) { return base + kTileBytes * (uint32_t)(kQT + s); };
+    auto sV = [&](int s) { return base + kTileBytes * (uint32_t)(kQT + kKStages + s); };
+    const int hk = (int)blockIdx.x, b = (int)blockIdx.y, qb = (int)(gridDim.z - 1 - blockIdx.z);
+    int n_rows = p.n_rows, T_len = p.T_len;
+    int64_t qbase = (int64_t)b * p.n_rows, kbase = (int64_t)b * p.T_len;
+    if (p.q_start) {
+        qbase = p.q_start[b];
+        kbase = p.kv_start[b];
+        n_rows = q8_count(p.q_start, b);
+        T_len = q8_count(p.kv_start, b);
+        if (n_rows != 0 && q8_bad_lengths(n_rows, p.n_rows, T_len, p.T_len, qbase, p.total_q, kbase)) {
+            if (threadIdx.x == 0 && qb == 0 && hk == 0) flag(p.dev_status, ACACHE_DEV_BAD_LENGTH);
+            return;
+        }
+    }
+    const int qpt = p.qpt;
+    const int q0 = qb * kQT * qpt;
+    if (q0 >= n_rows) return;
+    const int n_qt = q0 + qpt < n_rows ? 2 : 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
+    volatile int* abort_flag = &ctl.abort;
+    int32_t* dev_status = p.dev_status;
+    const long long budget = p.budget;
+
+    // Row `at` of Q tile `t`: its query of the request and its keys [lo, hi) (lo = hi = 0: none, or no row).
+    auto row_keys = [&](int t, int at, int& lo, int& hi) -> bool {
+        const int qi = q0 + t * qpt + at / p.g;
+        lo = hi = 0;
+        if (at >= qpt * p.g || qi >= n_rows) return false;
+        hi = T_len;
+        if (p.row_range) {
+            lo = max(p.row_range[2 * (qbase + qi)], 0);
+            hi = min(p.row_range[2 * (qbase + qi) + 1], T_len);
+        }
+        if (lo >= hi) lo = hi = 0;
+        return true;
+    };
+    if (wg < kQT) {
+        int lo, hi;
+        row_keys(wg, threadIdx.x & 127, lo, hi);
+        const int a = __reduce_min_sync(0xffffffffu, lo < hi ? lo : 0x7fffffff), z = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            ctl.win_lo[warp] = a;
+            ctl.win_hi[warp] = z;
+        }
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(&ctl.q_full, 1);
+        for (int t = 0; t < kQT; ++t) {
+            mbar_init(&ctl.s_full[t], 1);
+            mbar_init(&ctl.p_half[t], 128);
+            mbar_init(&ctl.p_full[t], 128);
+            mbar_init(&ctl.drain[t], 1);
+            mbar_init(&ctl.turn[t], 128);
+        }
+        ctl.abort = 0;
+        ctl.unlanded = 0;
+        ctl.split_ok = 1;
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(n_qt * kHalves * 128 * p.g * qpt));
+        for (int t = 0; t < n_qt; ++t)
+            for (int x = 0; x < kHalves; ++x) {
+                if (p.q_start) tma_load_3d(sQ(t) + x * kRegion, &p.tm_q, 64 * x, hk * p.g, (int)qbase + q0 + t * qpt, &ctl.q_full);
+                else tma_load_4d(sQ(t) + x * kRegion, &p.tm_q, 64 * x, hk * p.g, q0 + t * qpt, b, &ctl.q_full);
+            }
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ctl.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    __syncthreads();
+    // The window of keys that the CTA streams.
+    int w_lo = 0x7fffffff, w_hi = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        w_lo = min(w_lo, ctl.win_lo[x]);
+        w_hi = max(w_hi, ctl.win_hi[x]);
+    }
+    if (w_lo > w_hi) w_lo = w_hi = 0;
+    const int T_win = w_hi - w_lo;
+    const int n_kv = (T_win + kBN - 1) / kBN;
+    const int32_t* rs = p.read_slot + kbase + w_lo;
+    const bool split = n_qt == 1 && n_kv >= 2;
+    const int n_ch = split ? 2 : n_qt;
+    const KeySchedule ks{split, n_kv, split ? (n_kv + 1) / 2 : n_kv};
+    const int n_vst = split ? kVStages + 1 : kVStages;
+    auto sVs = [&](int s) { return s < kVStages ? sV(s) : sQ(1); };
+    if (threadIdx.x == 0) {
+        const int readers = split ? 1 : n_qt;
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(&ctl.k_full[s], kProdPerRing);
+            mbar_init(&ctl.k_empty[s], readers);
+        }
+        for (int s = 0; s < kVStages + 1; ++s) {
+            mbar_init(&ctl.v_full[s], kProdPerRing);
+            mbar_init(&ctl.v_empty[s], readers);
+        }
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+
+    if (wg >= 2) {
+        setmaxnreg_dec<kRegOther>();
+        if (warp >= kProdWarp) {
+            // -------------------------------------------------------------- TMA producers
+            if (warp == kProdWarp && lane == 0) {
+                tma_prefetch_desc(&p.tm_o);
+                tma_prefetch_desc(&p.tm_kg);
+                tma_prefetch_desc(&p.tm_vg);
+                tma_prefetch_desc(&p.tm_kb);
+                tma_prefetch_desc(&p.tm_vb);
+            }
+            const bool flagger = warp == kProdWarp;
+            const bool is_v = warp >= kProdWarp + kProdPerRing;
+            const int pi = warp - kProdWarp - (is_v ? kProdPerRing : 0);
+            const int nst = is_v ? n_vst : kKStages;
+            uint64_t* full = is_v ? ctl.v_full : ctl.k_full;
+            uint64_t* empty = is_v ? ctl.v_empty : ctl.k_empty;
+            const CUtensorMap* tm_g = is_v ? &p.tm_vg : &p.tm_kg;
+            const CUtensorMap* tm_b = is_v ? &p.tm_vb : &p.tm_kb;
+            const bool leader = pi == 0 && lane == 0;
+            const int oob_row = (int)(p.num_slots * p.Hkv);
+            // this lane's gather x of a tile: 4-row group x / kHalves, column region x % kHalves
+            const int x = kProdPerRing * lane + pi;
+            const bool gathers = x < 32 * kHalves;
+            const int grp = x / kHalves, half = x % kHalves;
+            // Tile j, resolved one entry ahead: lane l reads the slots of keys 4 l .. 4 l + 3; whether the tile's 128
+            // slots are consecutive, its first slot, and the pool rows of this lane's gather.  A slot outside
+            // the pool, a discarded key and a place behind the window read zeros.
+            auto resolve = [&](int j, int (&rows)[4], int& slot0) -> bool {
+                int sl[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int t = j * kBN + 4 * lane + u;
+                    sl[u] = -1;
+                    if (j < n_kv && t < T_win) {
+                        const int slot = __ldg(rs + t);
+                        if (slot >= 0 && slot < p.num_slots) sl[u] = slot;
+                        else if (flagger && !(p.drop && slot == ACACHE_SLOT_NONE)) flag(dev_status, ACACHE_DEV_BAD_SLOT);
+                    }
+                }
+                bool run = sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[2] == sl[0] + 2 && sl[3] == sl[0] + 3;
+                const int after = __shfl_down_sync(0xffffffffu, sl[0], 1);
+                if (lane < 31) run = run && after == sl[0] + 4;
+                slot0 = __shfl_sync(0xffffffffu, sl[0], 0);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int sv = __shfl_sync(0xffffffffu, sl[u], grp & 31);
+                    rows[u] = (gathers && sv >= 0) ? sv * p.Hkv + hk : oob_row;
+                }
+                return __all_sync(0xffffffffu, run);
+            };
+            int next[4], next_slot0;
+            bool next_box = resolve(n_kv > 0 ? ks.entry_tile(0) : 0, next, next_slot0);
+            int armed = -1;
+            for (int e = 0; e < n_kv; ++e) {
+                const int s = ring_stage(e, nst);
+                const uint32_t dst = is_v ? sVs(s) : sK(s);
+                int rows[4] = {next[0], next[1], next[2], next[3]};
+                const int slot0 = next_slot0;
+                const bool box = next_box;
+                next_box = resolve(e + 1 < n_kv ? ks.entry_tile(e + 1) : n_kv, next, next_slot0);
+                if (e >= nst &&
+                    !__all_sync(0xffffffffu, wait_bar(&empty[s], (ring_lap(e, nst) - 1) & 1, abort_flag, dev_status, budget)))
+                    break;
+                // one arrival per warp of the ring, also where the first warp loads alone: no warp can then fall
+                // two phases behind a stage's barrier
+                if (leader) mbar_arrive_expect_tx(&full[s], kTileBytes);
+                else if (lane == 0) mbar_arrive(&full[s]);
+                armed = e;
+                __syncwarp();
+                if (box) {
+                    if (leader) {
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * kRegion, tm_b, 64 * h, hk, slot0, &full[s]);
+                    }
+                } else if (gathers) {
+                    tma_gather4(dst + (uint32_t)half * kRegion + (uint32_t)grp * 512u, tm_g, half * 64, rows[0], rows[1], rows[2],
+                                rows[3], &full[s]);
+                }
+            }
+            if (*abort_flag && armed >= 0) {
+                bool landed = true;
+                for (int e = max(0, armed - nst + 1); e <= armed; ++e)
+                    landed = mbar_wait(&full[ring_stage(e, nst)], (uint32_t)ring_lap(e, nst) & 1u, kLandBudget) && landed;
+                if (!__all_sync(0xffffffffu, landed) && lane == 0) ctl.unlanded = 1;
+            }
+        } else {
+            // ------------------------------------------------------------------ MMA issuers
+            const int t = warp - kMmaWarp;
+            if (t < n_ch && lane == 0) {
+                const uint32_t idS = idesc_bf16(kBM, kBN, false, false);
+                const uint32_t idO = idesc_bf16(kBM, D, false, true);
+                const uint32_t d_s = tmem + col_s(t), d_o = tmem + col_o(t);
+                const uint64_t dq = sdesc_sw128(sQ(split ? 0 : t), 16, 1024);
+                const int nt = ks.n_tiles(t);
+                auto issue_s = [&](int e) {
+                    const uint64_t dk = sdesc_sw128(sK(e % kKStages), 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t ko = ((uint64_t)(k >> 2) * kRegion + (uint64_t)(k & 3) * 32u) >> 4;
+                        umma_ss(d_s, dq + ko, dk + ko, idS, k > 0);
+                    }
+                    umma_commit(&ctl.s_full[t]);
+                    umma_commit(&ctl.k_empty[e % kKStages]);
+                };
+                auto issue_pv_half = [&](int e, bool acc, int h) {
+                    const uint64_t dv = sdesc_sw128(sVs(ring_stage(e, n_vst)), kRegion, 1024);
+#pragma unroll
+                    for (int k = 4 * h; k < 4 * h + 4; ++k)
+                        umma_ts(d_o, d_s + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (acc || k > 0));
+                };
+                // (also without a key: the Q tiles have landed before the CTA goes on)
+                bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget);
+                if (ok && nt > 0) {
+                    const int e0 = ks.entry(t, 0);
+                    ok = wait_bar(&ctl.k_full[e0 % kKStages], (e0 / kKStages) & 1, abort_flag, dev_status, budget);
+                    if (ok) {
+                        tc_fence_after();
+                        issue_s(e0);
+                    }
+                }
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int e = ks.entry(t, i);
+                    ok = wait_bar(&ctl.v_full[ring_stage(e, n_vst)], ring_lap(e, n_vst) & 1, abort_flag, dev_status, budget) &&
+                         wait_bar(&ctl.p_half[t], i & 1, abort_flag, dev_status, budget);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv_half(e, i > 0, 0);
+                    ok = wait_bar(&ctl.p_full[t], i & 1, abort_flag, dev_status, budget);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv_half(e, i > 0, 1);
+                    umma_commit(&ctl.v_empty[ring_stage(e, n_vst)]);
+                    if (i + 1 < nt) {
+                        const int en = ks.entry(t, i + 1);
+                        ok = wait_bar(&ctl.k_full[en % kKStages], (en / kKStages) & 1, abort_flag, dev_status, budget);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(en);
+                    }
+                }
+                umma_commit(&ctl.drain[t]);
+                mbar_wait(&ctl.drain[t], 0, kDrainBudget);
+            }
+            __syncwarp();
+        }
+    } else {
+        setmaxnreg_inc<kRegSoftmax>();
+        if (wg < n_ch) {
+        // ------------------------------------------------------------------ softmax + epilogue
+        const int t = wg;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int r = threadIdx.x & 127;
+        const int rt = split ? 0 : t;                      // (with split keys both chains work on tile A's rows)
+        int a_lo, a_hi;
+        const bool mine = row_keys(rt, r, a_lo, a_hi);
+        a_lo -= w_lo;                                      // from the window's start
+        a_hi -= w_lo;
+        float slope = 0.f;
+        int64_t away = 0;                                  // the row's position from the window's start
+        if (kBias && mine) {
+            slope = p.slopes[hk * p.g + r % p.g] * kLog2e;
+            away = (int64_t)p.q_pos[qbase + q0 + rt * qpt + r / p.g] - w_lo;
+        }
+        const bool pingpong = n_ch > 1;
+        const int nt = ks.n_tiles(t);
+        float m_used = -INFINITY, l_sum = 0.f;
+        bool ok = true;
+        for (int i = 0; i < nt; ++i) {
+            const int j = ks.tile(t, i);
+            // the row's keys of the tile, one bit each, before the wait for its scores
+            uint32_t see[4];
+            const int f_lo = a_lo - j * kBN, f_hi = a_hi - j * kBN;
+            bool whole = f_lo <= 0 && f_hi >= kBN;         // (a row that is none does not count)
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) see[cc] = bits_from(f_lo - 32 * cc) & ~bits_from(f_hi - 32 * cc);
+            if (p.drop) {
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    const int tk = j * kBN + cc * 32 + lane;
+                    const uint32_t gone = __ballot_sync(0xffffffffu, tk < T_win && rs[tk] == ACACHE_SLOT_NONE);
+                    see[cc] &= ~gone;
+                    whole = whole && gone == 0u;
+                }
+            }
+            whole = __all_sync(0xffffffffu, whole || !mine);
+            ok = __all_sync(0xffffffffu, wait_bar(&ctl.s_full[t], i & 1, abort_flag, dev_status, budget));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t v[4][32];
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) tmem_ld32(lane_base + col_s(t) + cc * 32, v[cc]);
+            tmem_ld_wait();
+            if (pingpong && (t == 1 || i > 0))
+                ok = __all_sync(0xffffffffu, wait_bar(&ctl.turn[t], (t == 0 ? i - 1 : i) & 1, abort_flag, dev_status, budget));
+            if (!ok) break;
+            if constexpr (kCap) {
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        v[cc][x] = __float_as_uint(capped(__uint_as_float(v[cc][x]), p.cap_in, p.cap_log2));
+            }
+            if constexpr (kBias) {
+                // -slope |d - x| for key x of the tile, d = position - tile start: linear on either side
+                const int64_t d = away - j * kBN;
+                const float c = kCap ? 1.f : p.scale_log2;
+                if (__any_sync(0xffffffffu, d > 0 && d < kBN - 1)) {
+                    const float df = (float)d;
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            v[cc][x] = __float_as_uint(fmaf(__uint_as_float(v[cc][x]), c, -slope * fabsf(df - (float)(32 * cc + x))));
+                } else {
+                    const float sg = d > 0 ? slope : -slope, b0 = -sg * (float)d;
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            v[cc][x] = __float_as_uint(fmaf(__uint_as_float(v[cc][x]), c, fmaf(sg, (float)(32 * cc + x), b0)));
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (!((see[cc] >> x) & 1u)) v[cc][x] = __float_as_uint(-INFINITY);
+            }
+            // from here on scores count in log2 units with the factor c
+            const float c = (kCap || kBias) ? 1.f : p.scale_log2;
+            float mx[4];
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+                mx[cc] = max3f(__uint_as_float(v[cc][0]), __uint_as_float(v[cc][1]), __uint_as_float(v[cc][2]));
+#pragma unroll
+                for (int x = 3; x < 31; x += 2)
+                    mx[cc] = max3f(mx[cc], __uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
+                mx[cc] = fmaxf(mx[cc], __uint_as_float(v[cc][31]));
+            }
+            const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c;
+            float alpha = 1.f;
+            bool resc = false;
+            if (i == 0) {
+                m_used = mt;
+            } else if (mt > m_used + kRescaleThreshold) {
+                alpha = fast_exp2(m_used - mt);
+                m_used = mt;
+                resc = true;
+            }
+            if (__any_sync(0xffffffffu, resc)) {
+                // S(j) completed after the product before it: O is final up to there; 8 columns at a time
+#pragma unroll 1
+                for (int q = 0; q < D / 8; ++q) {
+                    uint32_t o[8];
+                    tmem_ld8(lane_base + col_o(t) + q * 8, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                    tmem_st8(lane_base + col_o(t) + q * 8, o);
+                }
+                tmem_st_wait();
+            }
+            // a row that has seen no key exponentiates against 0 (every score is -infinity)
+            const float ms = m_used == -INFINITY ? 0.f : m_used;
+            const uint64_t c2 = f2pack(c, c), nm2 = f2pack(-ms, -ms);
+            uint64_t ls2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    float x0, x1;
+                    const uint64_t two_s = f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
+                    f2unpack((kCap || kBias) ? f2add(two_s, nm2) : f2fma(two_s, c2, nm2), x0, x1);
+                    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                    ls2[(x >> 1) & 1] = f2add(ls2[(x >> 1) & 1], f2pack(p0, p1));
+                    // the weights' one rounding: bf16, the type of V (the sum takes them unrounded)
+                    __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
+                    pk[x >> 1] = *reinterpret_cast<uint32_t*>(&two);
+                }
+                tmem_st16(lane_base + col_s(t) + cc * 16, pk);
+                if (cc == 1) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&ctl.p_half[t]);
+                }
+            }
+            float l0, l1, l2, l3;
+            f2unpack(ls2[0], l0, l1);
+            f2unpack(ls2[1], l2, l3);
+            l_sum = l_sum * alpha + ((l0 + l1) + (l2 + l3));
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&ctl.p_full[t]);
+            if (pingpong) mbar_arrive(&ctl.turn[t ^ 1]);
+        }
+        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget) && !*abort_flag);
+        // Split keys: chain B's maximum and sum go to chain A, which merges the two and stores the rows.
+        float w_a = 1.f, w_b = 0.f;
+        if (split) {
+            if (t == 1) {
+                ctl.split_m[r] = m_used;
+                ctl.split_l[r] = l_sum;
+                if (!ok) ctl.split_ok = 0;
+            }
+            named_barrier_sync<1>(2 * kBM);
+            if (t == 1) {
+                ok = false;
+            } else if (ok) {
+                ok = ctl.split_ok && __all_sync(0xffffffffu, wait_bar(&ctl.drain[1], 0, abort_flag, dev_status, budget));
+                const float mb = ctl.split_m[r], lb = ctl.split_l[r];
+                const float m = fmaxf(m_used, mb);
+                w_a = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m);
+                w_b = mb == -INFINITY ? 0.f : fast_exp2(mb - m);
+                // (a sum that is NaN stays: its weight 0 times NaN)
+                l_sum = l_sum * w_a + lb * w_b;
+            }
+        }
+        const bool writer = !split || t == 0;
+        const uint32_t stage = sQ(t);
+        bool fix = false;
+        const bool boxed = !(p.q_start && q0 + (t + 1) * qpt > n_rows);   // else a box would reach the next request's rows
+        const int64_t row_at = ((qbase + q0 + rt * qpt + r / p.g) * p.Hq + hk * p.g + r % p.g) * D;
+        if (ok) {
+            tc_fence_after();
+            const float inv_l = 1.f / l_sum;
+            const bool none = l_sum == 0.f;                // no key: zeros, whatever the accumulator holds
+            float chk = 0.f;                               // NaN once a column is not finite
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t o[32];
+                tmem_ld32(lane_base + col_o(t) + cc * 32, o);
+                tmem_ld_wait();
+                if (split) {
+                    uint32_t ob[32];
+                    tmem_ld32(lane_base + col_o(1) + cc * 32, ob);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        o[x] = __float_as_uint(fmaf(__uint_as_float(o[x]), w_a, __uint_as_float(ob[x]) * w_b));
+                }
+                uint32_t pkd[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float y0 = none ? 0.f : __uint_as_float(o[2 * x]) * inv_l, y1 = none ? 0.f : __uint_as_float(o[2 * x + 1]) * inv_l;
+                    chk = fmaf(y0, 0.f, fmaf(y1, 0.f, chk));
+                    __nv_bfloat162 two = __floats2bfloat162_rn(y0, y1);
+                    pkd[x] = *reinterpret_cast<uint32_t*>(&two);
+                }
+                // 16-byte chunk k of row r: region k / 8, swizzled position (k % 8) ^ (r % 8)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int k = 4 * cc + x;
+                    st_shared_v4(stage + (uint32_t)(k >> 3) * kRegion + (uint32_t)r * 128u + ((uint32_t)((k & 7) ^ (r & 7)) << 4),
+                                 pkd[4 * x], pkd[4 * x + 1], pkd[4 * x + 2], pkd[4 * x + 3]);
+                }
+            }
+            fix = mine && chk != chk && l_sum == l_sum;
+        }
+        if (writer) {
+            fence_proxy_async_smem();
+            // the rows leave as a box when all of them are right; every thread of the warpgroup arrives
+            const bool clean = t == 0 ? named_barrier_and<2>(kBM, ok && boxed && !fix) : named_barrier_and<3>(kBM, ok && boxed && !fix);
+            if (clean) {
+                if (r == 0) {
+#pragma unroll
+                    for (int x = 0; x < kHalves; ++x) {
+                        if (p.q_start) tma_store_3d(&p.tm_o, stage + x * kRegion, 64 * x, hk * p.g, (int)qbase + q0 + t * qpt);
+                        else tma_store_4d(&p.tm_o, stage + x * kRegion, 64 * x, hk * p.g, q0 + t * qpt, b);
+                    }
+                    bulk_commit_group();
+                    bulk_wait_group_read0();
+                }
+            } else if (ok) {                               // (uniform over the warp)
+                if (mine && !fix) {
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k) {
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(stage + (uint32_t)(k >> 3) * kRegion + (uint32_t)r * 128u + ((uint32_t)((k & 7) ^ (r & 7)) << 4))
+                                     : "memory");
+                        reinterpret_cast<uint4*>(p.out + row_at)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                for (uint32_t todo = __ballot_sync(0xffffffffu, fix); todo; todo &= todo - 1) {
+                    const int l0 = __ffs(todo) - 1;
+                    const int64_t at = __shfl_sync(0xffffffffu, row_at, l0);
+                    masked_row<D, kCap, kBias>(p, p.q + at, p.out + at, rs, __shfl_sync(0xffffffffu, a_lo, l0),
+                                               __shfl_sync(0xffffffffu, a_hi, l0), hk, __shfl_sync(0xffffffffu, slope, l0),
+                                               __shfl_sync(0xffffffffu, away, l0), lane);
+                }
+            }
+        }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag) {
+        if (threadIdx.x == 0 && !mbar_wait(&ctl.q_full, 0, kLandBudget)) ctl.unlanded = 1;
+        __syncthreads();
+        settle_after_abort(ctl.unlanded != 0);
+    }
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, bool kCap, bool kBias>
+int launch(const MaskParams& prm, dim3 grid, cudaStream_t stream) {
+    auto kern = masked_tc_kernel<D, kCap, kBias>;
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(D)) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, kern) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ACACHE_ERR_CUDA;
+    }
+    if (fa.numRegs < kRegLaunch) return ACACHE_ERR_UNSUPPORTED;   // the register split assumes the launch allocation
+    kern<<<grid, kThreads, smem_bytes(D), stream>>>(prm);
+    return launch_status();
+}
+
+template <int D>
+int dispatch(const MaskParams& prm, bool cap, bool bias, dim3 grid, cudaStream_t stream) {
+    if (cap) return bias ? launch<D, true, true>(prm, grid, stream) : launch<D, true, false>(prm, grid, stream);
+    return bias ? launch<D, false, true>(prm, grid, stream) : launch<D, false, false>(prm, grid, stream);
+}
+
+}  // namespace
+
+bool masked_tc_supported(const MaskedAttn& c) {
+    return c.a.dtype == ACACHE_BF16 && c.a.scale > 0.f && c.a.hq / c.a.hkv <= kBM && c.num_slots > 0;
+}
+
+int launch_masked_tc(const MaskedAttn& c) {
+    const int d = c.a.d, g = c.a.hq / c.a.hkv;
+    MaskParams prm{};
+    prm.qpt = kBM / g;
+    const int64_t n_qb = (c.n_q + 2LL * prm.qpt - 1) / (2LL * prm.qpt);
+    if (n_qb > 65535) return ACACHE_ERR_INVALID_ARG;
+    const uint64_t dq4[4] = {(uint64_t)d, (uint64_t)c.a.hq, (uint64_t)c.n_q, (uint64_t)c.B};
+    const uint64_t dq3[3] = {(uint64_t)d, (uint64_t)c.a.hq, (uint64_t)c.total_q};
+    const uint32_t bq[4] = {64u, (uint32_t)g, (uint32_t)prm.qpt, 1u};
+    const uint64_t d2[2] = {(uint64_t)d, (uint64_t)c.num_slots * c.a.hkv};
+    const uint64_t d3[3] = {(uint64_t)d, (uint64_t)c.a.hkv, (uint64_t)c.num_slots};
+    const uint64_t* dq = c.q_start ? dq3 : dq4;
+    const int rank = c.q_start ? 3 : 4;
+    if (!make_map_box(&prm.tm_q, c.q, rank, dq, bq) || !make_map_box(&prm.tm_o, c.out, rank, dq, bq) ||
+        !make_map(&prm.tm_kg, c.k_cache, 2, d2, 1, 1) || !make_map(&prm.tm_vg, c.v_cache, 2, d2, 1, 1) ||
+        !make_map(&prm.tm_kb, c.k_cache, 3, d3, 2, kBN) || !make_map(&prm.tm_vb, c.v_cache, 3, d3, 2, kBN))
+        return ACACHE_ERR_CUDA;
+    prm.q = (const bf16*)c.q;
+    prm.k_cache = (const bf16*)c.k_cache;
+    prm.v_cache = (const bf16*)c.v_cache;
+    prm.out = (bf16*)c.out;
+    prm.read_slot = c.read_slot;
+    prm.q_start = c.q_start;
+    prm.kv_start = c.kv_start;
+    prm.row_range = c.mask.row_range;
+    prm.q_pos = c.mask.q_pos;
+    prm.slopes = c.mask.slopes;
+    prm.dev_status = c.dev_status;
+    prm.num_slots = c.num_slots;
+    prm.n_rows = c.n_q;
+    prm.total_q = c.total_q;
+    prm.T_len = c.T_len;
+    prm.Hq = c.a.hq;
+    prm.Hkv = c.a.hkv;
+    prm.g = g;
+    prm.drop = c.mask.drop_none != 0;
+    prm.scale_log2 = c.a.scale * kLog2e;
+    const bool cap = c.mask.softcap > 0.f;
+    if (cap) {
+        prm.cap_in = 2.f * kLog2e * (c.a.scale / c.mask.softcap);
+        prm.cap_log2 = c.mask.softcap * kLog2e;
+    }
+    prm.budget = wait_budget();
+    const dim3 grid((unsigned)c.a.hkv, (unsigned)c.B, (unsigned)n_qb);
+    const bool bias = c.mask.slopes != nullptr;
+    return d == 64 ? dispatch<64>(prm, cap, bias, grid, c.stream) : dispatch<128>(prm, cap, bias, grid, c.stream);
+}
+
+}  // namespace acache

@@ -43,6 +43,9 @@ struct MaskedAttn {
     cudaStream_t stream;
 };
 int launch_masked_simt(const MaskedAttn& c);
+// True when the tcgen05 kernel covers the call: bf16, a positive scale, at most 128 heads to a group, a pool with a row.
+bool masked_tc_supported(const MaskedAttn& c);
+int launch_masked_tc(const MaskedAttn& c);
 
 struct ScoreCall {
     int dtype;

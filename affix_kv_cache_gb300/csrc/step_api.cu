@@ -111,7 +111,7 @@ int attend(const MaskedAttn& c) {
     if (!c.q || !c.read_slot || !c.out || !c.k_cache || !c.v_cache || !aligned16(c.q) || !aligned16(c.out) ||
         !aligned16(c.k_cache) || !aligned16(c.v_cache))
         return ACACHE_ERR_INVALID_ARG;
-    return launch_masked_simt(c);
+    return masked_tc_supported(c) ? launch_masked_tc(c) : launch_masked_simt(c);
 }
 
 MaskedAttn masked_call(const AttnArgs& a, const acache_mask* mask, int batch, int n_q, const void* q, int seq_len,

@@ -29,6 +29,7 @@
 
 #include <algorithm>
 
+#include "masked.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
 #include "step.cuh"
@@ -73,7 +74,7 @@ struct MaskParams {
     int64_t num_slots;
     int n_rows, total_q, T_len, Hq, Hkv, g;
     int qpt;              // queries of a tile: floor(128 / g)
-    int drop;
+    int drop, wide;       // wide: a cap above kWideCap
     float scale_log2;     // > 0
     float cap_in;         // 2 log2e scale / softcap: 2^(cap_in q.k) = e^(2 s / softcap)
     float cap_log2;       // softcap log2e
@@ -137,61 +138,6 @@ ACACHE_DEVFN uint32_t bits_from(int n) {
     asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(r) : "r"(max(n, 0)));
     return r;
 }
-ACACHE_DEVFN float fast_rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// c tanh(s / c) in log2 units from the product q.k: tanh y = 1 - 2 / (1 + e^2y), within 2^-22 c of it
-// (infinities of e^2y give the limits)
-ACACHE_DEVFN float capped(float dot, float cap_in, float cap_log2) {
-    return fmaf(-2.f * cap_log2, fast_rcp(1.f + fast_exp2(dot * cap_in)), cap_log2);
-}
-
-// One row over its own keys [lo, hi), by a warp: for rows whose product with V met a masked key that is not
-// finite.  q and out: the row; rs: the request's read-slot entries.
-template <int D, bool kCap, bool kBias>
-ACACHE_DEVFN void masked_row(const MaskParams& p, const bf16* q, bf16* out, const int32_t* rs, int lo, int hi, int hk,
-                                        float slope_log2, int64_t pos, int lane) {
-    constexpr int kPer = D / 32;
-    float m = -INFINITY, l = 0.f, acc[kPer];
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-    for (int t0 = lo; t0 < hi; t0 += 32) {
-        const int t = t0 + lane;
-        float s = -INFINITY;
-        int64_t at = -1;
-        if (t < hi) {
-            const int slot = rs[t];
-            if (!(p.drop && slot == ACACHE_SLOT_NONE)) {
-                float dot = 0.f;
-                if (slot >= 0 && slot < p.num_slots) {
-                    at = ((int64_t)slot * p.Hkv + hk) * D;
-#pragma unroll 4
-                    for (int c = 0; c < D; ++c) dot = fmaf(to_f32(q[c]), to_f32(p.k_cache[at + c]), dot);
-                }
-                s = kCap ? capped(dot, p.cap_in, p.cap_log2) : dot * p.scale_log2;
-                if (kBias) s = fmaf(-slope_log2, fabsf((float)(pos - t)), s);
-            }
-        }
-        const float m_new = fmaxf(m, warp_max(s)), m_ref = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = fast_exp2(m - m_ref), w = fast_exp2(s - m_ref);
-        l = l * alpha + warp_sum(w);
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) acc[x] *= alpha;
-        for (int u = 0; u < min(32, hi - t0); ++u) {
-            const float wu = __shfl_sync(0xffffffffu, w, u);
-            const int64_t au = __shfl_sync(0xffffffffu, at, u);
-            if (au < 0) continue;
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) acc[x] = fmaf(wu, to_f32(p.v_cache[au + lane + 32 * x]), acc[x]);
-        }
-        m = m_new;
-    }
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) out[lane + 32 * x] = from_f32<bf16>(l == 0.f ? 0.f : acc[x] / l);
-}
-
 template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
 masked_tc_kernel(const __grid_constant__ MaskParams p) {
@@ -502,11 +448,19 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 ok = __all_sync(0xffffffffu, wait_bar(&ctl.turn[t], (t == 0 ? i - 1 : i) & 1, abort_flag, dev_status, budget));
             if (!ok) break;
             if constexpr (kCap) {
+                if (p.wide) {
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc)
+                    for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        v[cc][x] = __float_as_uint(capped(__uint_as_float(v[cc][x]), p.cap_in, p.cap_log2));
+                        for (int x = 0; x < 32; ++x)
+                            v[cc][x] = __float_as_uint(capped_wide(__uint_as_float(v[cc][x]), p.cap_in, p.cap_log2));
+                } else {
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            v[cc][x] = __float_as_uint(capped(__uint_as_float(v[cc][x]), p.cap_in, p.cap_log2));
+                }
             }
             if constexpr (kBias) {
                 // -slope |d - x| for key x of the tile, d = position - tile start: linear on either side
@@ -694,9 +648,10 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 for (uint32_t todo = __ballot_sync(0xffffffffu, fix); todo; todo &= todo - 1) {
                     const int l0 = __ffs(todo) - 1;
                     const int64_t at = __shfl_sync(0xffffffffu, row_at, l0);
-                    masked_row<D, kCap, kBias>(p, p.q + at, p.out + at, rs, __shfl_sync(0xffffffffu, a_lo, l0),
-                                               __shfl_sync(0xffffffffu, a_hi, l0), hk, __shfl_sync(0xffffffffu, slope, l0),
-                                               __shfl_sync(0xffffffffu, away, l0), lane);
+                    masked_row<D>(MaskedPool{p.k_cache, p.v_cache, rs, p.num_slots, p.Hkv, p.drop, p.wide != 0, p.scale_log2, kCap ? p.cap_in : 0.f,
+                                             p.cap_log2},
+                                  p.q + at, p.out + at, __shfl_sync(0xffffffffu, a_lo, l0), __shfl_sync(0xffffffffu, a_hi, l0), hk,
+                                  __shfl_sync(0xffffffffu, slope, l0), __shfl_sync(0xffffffffu, away, l0), lane);
                 }
             }
         }
@@ -780,6 +735,7 @@ int launch_masked_tc(const MaskedAttn& c) {
     if (cap) {
         prm.cap_in = 2.f * kLog2e * (c.a.scale / c.mask.softcap);
         prm.cap_log2 = c.mask.softcap * kLog2e;
+        prm.wide = c.mask.softcap > kWideCap;
     }
     prm.budget = wait_budget();
     const dim3 grid((unsigned)c.a.hkv, (unsigned)c.B, (unsigned)n_qb);

@@ -46,6 +46,9 @@ int launch_masked_simt(const MaskedAttn& c);
 // True when the tcgen05 kernel covers the call: bf16, a positive scale, at most 128 heads to a group, a pool with a row.
 bool masked_tc_supported(const MaskedAttn& c);
 int launch_masked_tc(const MaskedAttn& c);
+// ... and the one for few rows per (request, KV head): at most 32 (queries x heads of a group).
+bool masked_decode_supported(const MaskedAttn& c);
+int launch_masked_decode(const MaskedAttn& c);
 
 struct ScoreCall {
     int dtype;

@@ -103,6 +103,8 @@ bool masked_ok(const AttnArgs& a, const acache_mask* m, int batch, int n_q, int 
     if (m && (!(m->softcap >= 0.f) || isinf(m->softcap) || (m->slopes && !m->q_pos) || !aligned(m->row_range, 4) ||
               !aligned(m->q_pos, 4) || !aligned(m->slopes, 4)))
         return false;
+    // (the capped score's constants have to be numbers)
+    if (m && m->softcap > 0.f && (!isfinite(2.f * kLog2e * (a.scale / m->softcap)) || !isfinite(m->softcap * kLog2e))) return false;
     return batch <= 65535 && (int64_t)n_q * (a.hq / a.hkv) < 1 << 22 && T_len <= 0x7fffffff - 1023 &&
            a.hkv <= 1 << 20 && num_slots < 0x7fffffffLL / a.hkv;
 }
@@ -111,6 +113,7 @@ int attend(const MaskedAttn& c) {
     if (!c.q || !c.read_slot || !c.out || !c.k_cache || !c.v_cache || !aligned16(c.q) || !aligned16(c.out) ||
         !aligned16(c.k_cache) || !aligned16(c.v_cache))
         return ACACHE_ERR_INVALID_ARG;
+    if (masked_decode_supported(c)) return launch_masked_decode(c);
     return masked_tc_supported(c) ? launch_masked_tc(c) : launch_masked_simt(c);
 }
 

@@ -575,7 +575,7 @@ ACACHE_API int acache_rotate_store_q8(const acache_attn_desc* a, const acache_ro
  *     row_range  [B][n_q][2] int32, clamped to [0, T]; NULL: every row sees all keys
  *     q_pos      [B][n_q] int32 logical positions (needed with slopes)
  *     slopes     [Hq] float
- *     softcap    0 (none) or positive
+ *     softcap    0 (none) or positive (its quotient with scale and both times 3 within float32)
  * mask = NULL is no mask at all.  Other arguments, layouts and errors as acache_slot_attention;
  * a bad slot of a key that no row sees may go unflagged.  In the ragged form row_range and q_pos are
  * flat like q ([total_q_rows][2], [total_q_rows]), their keys count from the request's first;
@@ -583,8 +583,8 @@ ACACHE_API int acache_rotate_store_q8(const acache_attn_desc* a, const acache_ro
  * Tensor cores: bf16 (head dim 64 and 128) with a positive scale; otherwise CUDA cores.
  * Limits: B <= 65,535, pools below 2^31 rows (slots x heads), T <= 2^31 - 1024,
  * n_q * Hq / Hkv < 2^22; more is ACACHE_ERR_INVALID_ARG.
- * Roundings: logits, maxima, sums and O are float32 (exponentials to 2^-22, tanh to 2^-22
- * absolute); in a bf16 call the weights are rounded to bf16 before the product with V, not in
+ * Roundings: logits, maxima, sums and O are float32 (exponentials to 2^-22, a capped
+ * score to 2^-22 of the cap, or from a cap of 512 on to 2^-20 of itself); in a bf16 call the weights are rounded to bf16 before the product with V, not in
  * their sum.
  * ------------------------------------------------------------------------------- */
 typedef struct {

@@ -102,10 +102,11 @@ def masked_attention(q, slots, k_pool, v_pool, scale, lo, hi, pos=None, slopes=N
                 s = cap * np.tanh(dot / cap) if cap > 0 else dot
                 size = np.abs(k) @ np.abs(q[i, h]) * abs(scale)
                 # products of d terms in float32 (an MMA's additions may cut instead of round), the scale's
-                # and the base's roundings; the cap's quotient, its tanh (2^-22) and product
+                # and the base's roundings
                 ds = 2 * d * U * size.max() + 4 * U * np.abs(dot).max()
                 if cap > 0:
-                    ds = ds + 10 * U * cap
+                    # its quotient, tanh and product: 2^-22 of the cap, above 512 2^-20 of itself
+                    ds = ds + (10 * U * cap if cap <= 512 else 20 * U * np.abs(dot).max())
                 if slopes is not None:
                     bias = float(slopes[h]) * np.abs(float(pos[i]) - t)
                     s = s - bias

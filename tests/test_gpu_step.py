@@ -344,6 +344,14 @@ def test_masked_attention_caps_biases_and_discarded_keys(dtype, hq, hkv, d, kind
     _attend_case(dtype, hq, hkv, d, 2, n, T, kind, cap=cap, bias=bias, drop=drop, seed=3)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("cap", [0.01, 511.0, 513.0, 2e5, 1e12])
+def test_masked_attention_with_small_and_large_caps(dtype, n, cap):
+    """Up to a cap of 512 the score is off by 2^-22 of the cap, above by 2^-20 of itself."""
+    _attend_case(dtype, 4, 2, 128, 1, n, 160, "causal", cap=cap, seed=6)
+
+
 @pytest.mark.parametrize("n", [1, 40, 130])
 @pytest.mark.parametrize("scale", [-0.1, 0.0])
 def test_masked_attention_with_a_scale_that_is_not_positive(n, scale):

@@ -57,6 +57,11 @@ constexpr uint32_t kTmemCols = 512;         // S_A, S_B, O_A, O_B
 __host__ __device__ constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + (uint32_t)t * 128u; }
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: weights stay below 2^8
+// Scores within +-50 need no running maximum: weights e^s between 2e-22 and 6e21 are ordinary float32 and bf16 numbers, and so
+// are sums of 2^31 of them.  (Products with V beyond float32 give a row that is not finite, which is computed again.)
+constexpr float kBoundedCap = 50.f;
+// tanh y / y = 1 + c1 y^2 + c2 y^4 + c3 y^6 within 2^-20.5 of itself up to y = 1/2 (relative minimax fit)
+constexpr float kTanhNear = 0.5f, kTanh1 = -0.33328159f, kTanh2 = 0.1320536f, kTanh3 = -0.04475064f;
 constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles: the abort path's own waits
 
 struct MaskParams {
@@ -75,9 +80,12 @@ struct MaskParams {
     int n_rows, total_q, T_len, Hq, Hkv, g;
     int qpt;              // queries of a tile: floor(128 / g)
     int drop, wide;       // wide: a cap above kWideCap
+    int bounded;          // a cap of at most kBoundedCap
     float scale_log2;     // > 0
     float cap_in;         // 2 log2e scale / softcap: 2^(cap_in q.k) = e^(2 s / softcap)
     float cap_log2;       // softcap log2e
+    float cap_near;       // |q.k| of a score of half the cap ...
+    float cap_k[4];       // ... up to which the capped score in log2 units is q.k times this polynomial in (q.k)^2
     long long budget;
 };
 
@@ -85,7 +93,9 @@ struct MaskCtl {
     uint64_t q_full;
     uint64_t k_full[kKStages], k_empty[kKStages];
     uint64_t v_full[kVStages + 1], v_empty[kVStages + 1];   // + the stage in the free Q buffer (split keys)
-    uint64_t s_full[kQT], p_half[kQT], p_full[kQT], drain[kQT], turn[kQT];
+    uint64_t s_full[kQT], p_half[kQT], p_full[kQT];
+    uint64_t drain[kQT];  // chain t's MMAs are complete
+    uint64_t fin;         // ... and all of them, on every path
     uint32_t tmem_base;
     int abort;
     int unlanded;         // abort path: some load issued before the abort may not have landed
@@ -200,8 +210,8 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             mbar_init(&ctl.p_half[t], 128);
             mbar_init(&ctl.p_full[t], 128);
             mbar_init(&ctl.drain[t], 1);
-            mbar_init(&ctl.turn[t], 128);
         }
+        mbar_init(&ctl.fin, 1);
         ctl.abort = 0;
         ctl.unlanded = 0;
         ctl.split_ok = 1;
@@ -338,62 +348,69 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 if (!__all_sync(0xffffffffu, landed) && lane == 0) ctl.unlanded = 1;
             }
         } else {
-            // ------------------------------------------------------------------ MMA issuers
-            const int t = warp - kMmaWarp;
-            if (t < n_ch && lane == 0) {
+            // ------------------------------------------------------------------ MMA issuer
+            // One thread issues both chains' MMAs, A's and B's in turn: PV(i) in two halves of the tile as the softmax
+            // publishes them, then S(i + 1).  A chain's MMAs then run as one burst, and the chains fall into
+            // step, one in its softmax while the other's MMAs run.  (Two issuing threads interleaved their MMAs: both
+            // chains' bursts took twice as long and ended together, and neither softmax overlapped an MMA.)
+            if (warp == kMmaWarp && lane == 0) {
                 const uint32_t idS = idesc_bf16(kBM, kBN, false, false);
                 const uint32_t idO = idesc_bf16(kBM, D, false, true);
-                const uint32_t d_s = tmem + col_s(t), d_o = tmem + col_o(t);
-                const uint64_t dq = sdesc_sw128(sQ(split ? 0 : t), 16, 1024);
-                const int nt = ks.n_tiles(t);
-                auto issue_s = [&](int e) {
+                auto issue_s = [&](int t, int e) {
+                    const uint64_t dq = sdesc_sw128(sQ(split ? 0 : t), 16, 1024);
                     const uint64_t dk = sdesc_sw128(sK(e % kKStages), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t ko = ((uint64_t)(k >> 2) * kRegion + (uint64_t)(k & 3) * 32u) >> 4;
-                        umma_ss(d_s, dq + ko, dk + ko, idS, k > 0);
+                        umma_ss(tmem + col_s(t), dq + ko, dk + ko, idS, k > 0);
                     }
                     umma_commit(&ctl.s_full[t]);
                     umma_commit(&ctl.k_empty[e % kKStages]);
                 };
-                auto issue_pv_half = [&](int e, bool acc, int h) {
+                auto issue_pv_half = [&](int t, int e, bool acc, int h) {
                     const uint64_t dv = sdesc_sw128(sVs(ring_stage(e, n_vst)), kRegion, 1024);
 #pragma unroll
                     for (int k = 4 * h; k < 4 * h + 4; ++k)
-                        umma_ts(d_o, d_s + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (acc || k > 0));
+                        umma_ts(tmem + col_o(t), tmem + col_s(t) + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (acc || k > 0));
                 };
                 // (also without a key: the Q tiles have landed before the CTA goes on)
                 bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget);
-                if (ok && nt > 0) {
+                for (int t = 0; ok && t < n_ch && n_kv > 0; ++t) {
                     const int e0 = ks.entry(t, 0);
                     ok = wait_bar(&ctl.k_full[e0 % kKStages], (e0 / kKStages) & 1, abort_flag, dev_status, budget);
-                    if (ok) {
-                        tc_fence_after();
-                        issue_s(e0);
-                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(t, e0);
                 }
-                for (int i = 0; ok && i < nt; ++i) {
+                const int steps = ks.n_tiles(0);                // chain 0 has as many as chain 1, or one more
+                for (int it = 0; ok && it < steps * n_ch; ++it) {
+                    const int t = n_ch == 2 ? it & 1 : 0, i = n_ch == 2 ? it >> 1 : it;
+                    const int nt = ks.n_tiles(t);
+                    if (i >= nt) continue;
                     const int e = ks.entry(t, i);
                     ok = wait_bar(&ctl.v_full[ring_stage(e, n_vst)], ring_lap(e, n_vst) & 1, abort_flag, dev_status, budget) &&
                          wait_bar(&ctl.p_half[t], i & 1, abort_flag, dev_status, budget);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_pv_half(e, i > 0, 0);
+                    issue_pv_half(t, e, i > 0, 0);
                     ok = wait_bar(&ctl.p_full[t], i & 1, abort_flag, dev_status, budget);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_pv_half(e, i > 0, 1);
+                    issue_pv_half(t, e, i > 0, 1);
                     umma_commit(&ctl.v_empty[ring_stage(e, n_vst)]);
                     if (i + 1 < nt) {
                         const int en = ks.entry(t, i + 1);
                         ok = wait_bar(&ctl.k_full[en % kKStages], (en / kKStages) & 1, abort_flag, dev_status, budget);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_s(en);
+                        issue_s(t, en);
+                    } else {
+                        umma_commit(&ctl.drain[t]);             // the chain's last
                     }
                 }
-                umma_commit(&ctl.drain[t]);
-                mbar_wait(&ctl.drain[t], 0, kDrainBudget);
+                // no MMA may still run when TMEM is released
+                umma_commit(&ctl.fin);
+                mbar_wait(&ctl.fin, 0, kDrainBudget);
             }
             __syncwarp();
         }
@@ -415,9 +432,9 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             slope = p.slopes[hk * p.g + r % p.g] * kLog2e;
             away = (int64_t)p.q_pos[qbase + q0 + rt * qpt + r / p.g] - w_lo;
         }
-        const bool pingpong = n_ch > 1;
         const int nt = ks.n_tiles(t);
-        float m_used = -INFINITY, l_sum = 0.f;
+        // (bounded: scores within the cap need no maximum)
+        float m_used = kCap && !kBias && p.bounded ? 0.f : -INFINITY, l_sum = 0.f;
         bool ok = true;
         for (int i = 0; i < nt; ++i) {
             const int j = ks.tile(t, i);
@@ -444,11 +461,30 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) tmem_ld32(lane_base + col_s(t) + cc * 32, v[cc]);
             tmem_ld_wait();
-            if (pingpong && (t == 1 || i > 0))
-                ok = __all_sync(0xffffffffu, wait_bar(&ctl.turn[t], (t == 0 ? i - 1 : i) & 1, abort_flag, dev_status, budget));
-            if (!ok) break;
             if constexpr (kCap) {
-                if (p.wide) {
+                // |s| up to half the cap in the whole warp: s times a polynomial in s^2, two elements to an instruction
+                float am[4];
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    am[cc] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2)
+                        am[cc] = max3abs(am[cc], __uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
+                }
+                if (!__any_sync(0xffffffffu, max3f(am[0], am[1], fmaxf(am[2], am[3])) > p.cap_near)) {
+                    const uint64_t k0 = f2pack(p.cap_k[0], p.cap_k[0]), k1 = f2pack(p.cap_k[1], p.cap_k[1]),
+                                   k2 = f2pack(p.cap_k[2], p.cap_k[2]), k3 = f2pack(p.cap_k[3], p.cap_k[3]);
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            const uint64_t d = f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1])), z = f2mul(d, d);
+                            float y0, y1;
+                            f2unpack(f2mul(d, f2fma(f2fma(f2fma(k3, z, k2), z, k1), z, k0)), y0, y1);
+                            v[cc][x] = __float_as_uint(y0);
+                            v[cc][x + 1] = __float_as_uint(y1);
+                        }
+                } else if (p.wide) {
 #pragma unroll
                     for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
@@ -491,6 +527,8 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             }
             // from here on scores count in log2 units with the factor c
             const float c = (kCap || kBias) ? 1.f : p.scale_log2;
+            float alpha = 1.f;
+            if (!(kCap && !kBias) || !p.bounded) {
             float mx[4];
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
@@ -501,7 +539,6 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 mx[cc] = fmaxf(mx[cc], __uint_as_float(v[cc][31]));
             }
             const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c;
-            float alpha = 1.f;
             bool resc = false;
             if (i == 0) {
                 m_used = mt;
@@ -522,6 +559,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                     tmem_st8(lane_base + col_o(t) + q * 8, o);
                 }
                 tmem_st_wait();
+            }
             }
             // a row that has seen no key exponentiates against 0 (every score is -infinity)
             const float ms = m_used == -INFINITY ? 0.f : m_used;
@@ -555,9 +593,10 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&ctl.p_full[t]);
-            if (pingpong) mbar_arrive(&ctl.turn[t ^ 1]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget) && !*abort_flag);
+        if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget) && !*abort_flag);
+        // (without a key the rows wait for the Q tiles, whose place they are stored from)
+        if (ok && nt == 0) ok = __all_sync(0xffffffffu, wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget));
         // Split keys: chain B's maximum and sum go to chain A, which merges the two and stores the rows.
         float w_a = 1.f, w_b = 0.f;
         if (split) {
@@ -736,6 +775,15 @@ int launch_masked_tc(const MaskedAttn& c) {
         prm.cap_in = 2.f * kLog2e * (c.a.scale / c.mask.softcap);
         prm.cap_log2 = c.mask.softcap * kLog2e;
         prm.wide = c.mask.softcap > kWideCap;
+        prm.bounded = c.mask.softcap <= kBoundedCap;
+        const double y = (double)c.a.scale / c.mask.softcap, k = prm.scale_log2;      // y: of q.k = 1
+        prm.cap_near = (float)(kTanhNear / y);
+        const double k4[4] = {k, k * kTanh1 * y * y, k * kTanh2 * y * y * y * y, k * kTanh3 * y * y * y * y * y * y};
+        for (int i = 0; i < 4; ++i) {
+            prm.cap_k[i] = (float)k4[i];
+            if (!(fabs(k4[i]) > 1e-37 && fabs(k4[i]) < 1e38)) prm.cap_near = -1.f;    // a cap far from the scale: not this way
+        }
+        prm.cap_near = std::min(prm.cap_near, 1e18f);
     }
     prm.budget = wait_budget();
     const dim3 grid((unsigned)c.a.hkv, (unsigned)c.B, (unsigned)n_qb);

@@ -353,63 +353,69 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             // publishes them, then S(i + 1).  A chain's MMAs then run as one burst, and the chains fall into
             // step, one in its softmax while the other's MMAs run.  (Two issuing threads interleaved their MMAs: both
             // chains' bursts took twice as long and ended together, and neither softmax overlapped an MMA.)
-            if (warp == kMmaWarp && lane == 0) {
-                const uint32_t idS = idesc_bf16(kBM, kBN, false, false);
-                const uint32_t idO = idesc_bf16(kBM, D, false, true);
-                auto issue_s = [&](int t, int e) {
-                    const uint64_t dq = sdesc_sw128(sQ(split ? 0 : t), 16, 1024);
-                    const uint64_t dk = sdesc_sw128(sK(e % kKStages), 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t ko = ((uint64_t)(k >> 2) * kRegion + (uint64_t)(k & 3) * 32u) >> 4;
-                        umma_ss(tmem + col_s(t), dq + ko, dk + ko, idS, k > 0);
-                    }
-                    umma_commit(&ctl.s_full[t]);
-                    umma_commit(&ctl.k_empty[e % kKStages]);
+            // The whole warp walks the steps, so addresses and descriptors stay in uniform registers, and one lane
+            // issues (one lane alone took 80 to 100 cycles to issue an MMA of 64).
+            if (warp == kMmaWarp) {
+                const bool leader = elect_one();
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                const int nk = __shfl_sync(0xffffffffu, n_kv, 0);
+                const bool two = __shfl_sync(0xffffffffu, n_ch, 0) == 2, halved = __shfl_sync(0xffffffffu, (int)split, 0) != 0;
+                const KeySchedule us{halved, nk, halved ? (nk + 1) / 2 : nk};
+                const int vst = halved ? kVStages + 1 : kVStages;
+                constexpr uint32_t idS = idesc_bf16(kBM, kBN, false, false);
+                constexpr uint32_t idO = idesc_bf16(kBM, D, false, true);
+                auto wait = [&](uint64_t* bar, int phase) {
+                    return __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)phase & 1u, abort_flag, dev_status, budget));
                 };
-                auto issue_pv_half = [&](int t, int e, bool acc, int h) {
-                    const uint64_t dv = sdesc_sw128(sVs(ring_stage(e, n_vst)), kRegion, 1024);
+                auto issue_s = [&](int t, int e) -> bool {
+                    const int st = e % kKStages;
+                    if (!wait(&ctl.k_full[st], e / kKStages)) return false;
+                    tc_fence_after();
+                    const uint64_t dq = sdesc_sw128(sQ(halved ? 0 : t), 16, 1024);
+                    const uint64_t dk = sdesc_sw128(sK(st), 16, 1024);
+                    if (leader) {
 #pragma unroll
-                    for (int k = 4 * h; k < 4 * h + 4; ++k)
-                        umma_ts(tmem + col_o(t), tmem + col_s(t) + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (acc || k > 0));
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t ko = ((uint64_t)(k >> 2) * kRegion + (uint64_t)(k & 3) * 32u) >> 4;
+                            umma_ss(tm + col_s(t), dq + ko, dk + ko, idS, k > 0);
+                        }
+                        umma_commit(&ctl.s_full[t]);
+                        umma_commit(&ctl.k_empty[st]);
+                    }
+                    return true;
                 };
                 // (also without a key: the Q tiles have landed before the CTA goes on)
-                bool ok = wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget);
-                for (int t = 0; ok && t < n_ch && n_kv > 0; ++t) {
-                    const int e0 = ks.entry(t, 0);
-                    ok = wait_bar(&ctl.k_full[e0 % kKStages], (e0 / kKStages) & 1, abort_flag, dev_status, budget);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_s(t, e0);
-                }
-                const int steps = ks.n_tiles(0);                // chain 0 has as many as chain 1, or one more
-                for (int it = 0; ok && it < steps * n_ch; ++it) {
-                    const int t = n_ch == 2 ? it & 1 : 0, i = n_ch == 2 ? it >> 1 : it;
-                    const int nt = ks.n_tiles(t);
+                bool ok = wait(&ctl.q_full, 0);
+                if (ok && nk > 0) ok = issue_s(0, us.entry(0, 0));
+                if (ok && nk > 0 && two) ok = issue_s(1, us.entry(1, 0));
+                const int steps = us.n_tiles(0) * (two ? 2 : 1);    // chain 0 has as many tiles as chain 1, or one more
+                for (int it = 0; ok && it < steps; ++it) {
+                    const int t = two ? it & 1 : 0, i = two ? it >> 1 : it;
+                    const int nt = us.n_tiles(t);
                     if (i >= nt) continue;
-                    const int e = ks.entry(t, i);
-                    ok = wait_bar(&ctl.v_full[ring_stage(e, n_vst)], ring_lap(e, n_vst) & 1, abort_flag, dev_status, budget) &&
-                         wait_bar(&ctl.p_half[t], i & 1, abort_flag, dev_status, budget);
+                    const int e = us.entry(t, i), st = ring_stage(e, vst);
+                    ok = wait(&ctl.v_full[st], ring_lap(e, vst)) && wait(&ctl.p_half[t], i);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_pv_half(t, e, i > 0, 0);
-                    ok = wait_bar(&ctl.p_full[t], i & 1, abort_flag, dev_status, budget);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv_half(t, e, i > 0, 1);
-                    umma_commit(&ctl.v_empty[ring_stage(e, n_vst)]);
-                    if (i + 1 < nt) {
-                        const int en = ks.entry(t, i + 1);
-                        ok = wait_bar(&ctl.k_full[en % kKStages], (en / kKStages) & 1, abort_flag, dev_status, budget);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_s(t, en);
-                    } else {
-                        umma_commit(&ctl.drain[t]);             // the chain's last
+                    const uint64_t dv = sdesc_sw128(sVs(st), kRegion, 1024);
+                    const uint32_t d_o = tm + col_o(t), d_p = tm + col_s(t);
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) umma_ts(d_o, d_p + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, (i > 0 || k > 0));
                     }
+                    ok = wait(&ctl.p_full[t], i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 4; k < 8; ++k) umma_ts(d_o, d_p + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, 1);
+                        umma_commit(&ctl.v_empty[st]);
+                        if (i + 1 == nt) umma_commit(&ctl.drain[t]);    // the chain's last
+                    }
+                    if (i + 1 < nt) ok = issue_s(t, us.entry(t, i + 1));
                 }
                 // no MMA may still run when TMEM is released
-                umma_commit(&ctl.fin);
+                if (leader) umma_commit(&ctl.fin);
                 mbar_wait(&ctl.fin, 0, kDrainBudget);
             }
             __syncwarp();

@@ -9,8 +9,8 @@
 // One CTA per (request, KV head, query block): two Q tiles A and B of 128 rows, a row being a (query, head of the
 // group) pair, so that all heads of a group share one K/V stream and a causal block spans few positions.
 //   WG0, WG1   softmax + epilogue of tile A / B, thread r owning row r = TMEM lane r: a tile of scores is read
-//              into registers, capped, biased, masked, exponentiated in base 2 against a lazily raised
-//              maximum, and written back over the scores as bf16 for the product with V.  The two take turns.
+//              into registers, capped, biased, masked, exponentiated in base 2 against a reference that
+//              follows the sums of weights, and written back over the scores as bf16 for the product with V.  The two take turns.
 //   WG2        warps 8 and 9 issue the MMAs of A and B (S = Q K^T from shared memory, O += P V with P from TMEM)
 //   warps 10-19  TMA producers of a 3-stage K ring and a 2-stage V ring: a tile of 128 consecutive slots is tiled
 //              box loads of the pool, any other gather4 loads of four rows each.
@@ -28,6 +28,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "masked.cuh"
 #include "ptx.cuh"
@@ -56,12 +57,12 @@ __host__ __device__ constexpr uint32_t smem_bytes(int D) { return tile_bytes(D) 
 constexpr uint32_t kTmemCols = 512;         // S_A, S_B, O_A, O_B
 __host__ __device__ constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + (uint32_t)t * 128u; }
-constexpr float kRescaleThreshold = 8.0f;   // log2 units: weights stay below 2^8
 // Scores within +-50 need no running maximum: weights e^s between 2e-22 and 6e21 are ordinary float32 and bf16 numbers, and so
 // are sums of 2^31 of them.  (Products with V beyond float32 give a row that is not finite, which is computed again.)
 constexpr float kBoundedCap = 50.f;
-// tanh y / y = 1 + c1 y^2 + c2 y^4 + c3 y^6 within 2^-20.5 of itself up to y = 1/2 (relative minimax fit)
-constexpr float kTanhNear = 0.5f, kTanh1 = -0.33328159f, kTanh2 = 0.1320536f, kTanh3 = -0.04475064f;
+// tanh y / y = 1 + c1 y^2 + c2 y^4 + c3 y^6 within 2^-20.5 of itself up to y = 1/2 (relative minimax fit).  (A level of one term
+// less up to y = 1/4 made the call slower: most tiles hold a larger score.)
+constexpr double kTanhHalf[4] = {1, -0.33328159, 0.1320536, -0.04475064};
 constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles: the abort path's own waits
 
 struct MaskParams {
@@ -80,7 +81,6 @@ struct MaskParams {
     int n_rows, total_q, T_len, Hq, Hkv, g;
     int qpt;              // queries of a tile: floor(128 / g)
     int drop, wide;       // wide: a cap above kWideCap
-    int bounded;          // a cap of at most kBoundedCap
     float scale_log2;     // > 0
     float cap_in;         // 2 log2e scale / softcap: 2^(cap_in q.k) = e^(2 s / softcap)
     float cap_log2;       // softcap log2e
@@ -148,7 +148,8 @@ ACACHE_DEVFN uint32_t bits_from(int n) {
     asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(r) : "r"(max(n, 0)));
     return r;
 }
-template <int D, bool kCap, bool kBias>
+// kCap: scores are capped; kBounded: by so little that they need no maximum (then there is no bias).
+template <int D, bool kCap, bool kBounded, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
 masked_tc_kernel(const __grid_constant__ MaskParams p) {
     constexpr uint32_t kTileBytes = tile_bytes(D);
@@ -439,9 +440,9 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             away = (int64_t)p.q_pos[qbase + q0 + rt * qpt + r / p.g] - w_lo;
         }
         const int nt = ks.n_tiles(t);
-        // (bounded: scores within the cap need no maximum)
-        float m_used = kCap && !kBias && p.bounded ? 0.f : -INFINITY, l_sum = 0.f;
-        bool ok = true;
+        float m_used = kBounded ? 0.f : -INFINITY, l_sum = 0.f;
+        int up = 0;                                        // powers of two by which the next tile raises the reference
+        bool lost = false, ok = true;
         for (int i = 0; i < nt; ++i) {
             const int j = ks.tile(t, i);
             // the row's keys of the tile, one bit each, before the wait for its scores
@@ -533,39 +534,52 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             }
             // from here on scores count in log2 units with the factor c
             const float c = (kCap || kBias) ? 1.f : p.scale_log2;
-            float alpha = 1.f;
-            if (!(kCap && !kBias) || !p.bounded) {
-            float mx[4];
+            if constexpr (!kBounded) {
+                // The first tile that a row sees something of sets its reference, its maximum there.  Later tiles take
+                // the reference as it stands; where a tile's weights sum to more than 2^8, the next one raises it.
+                // (Under a bias by distance scores grow by more from tile to tile than weights have room for: there every
+                // tile's maximum is found, and the reference raised by it before the weights are.)
+                float alpha = 1.f;
+                bool raise = false;
+                if (kBias || __any_sync(0xffffffffu, m_used == -INFINITY)) {
+                    float mx[4];
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-                mx[cc] = max3f(__uint_as_float(v[cc][0]), __uint_as_float(v[cc][1]), __uint_as_float(v[cc][2]));
+                    for (int cc = 0; cc < 4; ++cc) {
+                        mx[cc] = max3f(__uint_as_float(v[cc][0]), __uint_as_float(v[cc][1]), __uint_as_float(v[cc][2]));
 #pragma unroll
-                for (int x = 3; x < 31; x += 2)
-                    mx[cc] = max3f(mx[cc], __uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
-                mx[cc] = fmaxf(mx[cc], __uint_as_float(v[cc][31]));
-            }
-            const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c;
-            bool resc = false;
-            if (i == 0) {
-                m_used = mt;
-            } else if (mt > m_used + kRescaleThreshold) {
-                alpha = fast_exp2(m_used - mt);
-                m_used = mt;
-                resc = true;
-            }
-            if (__any_sync(0xffffffffu, resc)) {
-                // S(j) completed after the product before it: O is final up to there; 8 columns at a time
-#pragma unroll 1
-                for (int q = 0; q < D / 8; ++q) {
-                    uint32_t o[8];
-                    tmem_ld8(lane_base + col_o(t) + q * 8, o);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                    tmem_st8(lane_base + col_o(t) + q * 8, o);
+                        for (int x = 3; x < 31; x += 2)
+                            mx[cc] = max3f(mx[cc], __uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
+                        mx[cc] = fmaxf(mx[cc], __uint_as_float(v[cc][31]));
+                    }
+                    const float mt = max3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c;
+                    if (m_used == -INFINITY) {
+                        m_used = mt;
+                        // (what a row that has seen no key has in O so far: zeros, or what masked rows of V made of them)
+                    } else if (kBias && mt > m_used + 8.f) {
+                        alpha = fast_exp2(m_used - mt);
+                        m_used = mt;
+                        raise = true;
+                    }
                 }
-                tmem_st_wait();
-            }
+                if (!kBias && up > 0) {
+                    alpha = __uint_as_float((uint32_t)(127 - up) << 23);
+                    m_used += (float)up;
+                    raise = true;
+                }
+                if (__any_sync(0xffffffffu, raise)) {
+                    l_sum *= alpha;
+                    // S(j) completed after the product before it: O is final up to there; 8 columns at a time
+#pragma unroll 1
+                    for (int q = 0; q < D / 8; ++q) {
+                        uint32_t o[8];
+                        tmem_ld8(lane_base + col_o(t) + q * 8, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                        tmem_st8(lane_base + col_o(t) + q * 8, o);
+                    }
+                    tmem_st_wait();
+                }
             }
             // a row that has seen no key exponentiates against 0 (every score is -infinity)
             const float ms = m_used == -INFINITY ? 0.f : m_used;
@@ -578,7 +592,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 for (int x = 0; x < 32; x += 2) {
                     float x0, x1;
                     const uint64_t two_s = f2pack(__uint_as_float(v[cc][x]), __uint_as_float(v[cc][x + 1]));
-                    f2unpack((kCap || kBias) ? f2add(two_s, nm2) : f2fma(two_s, c2, nm2), x0, x1);
+                    f2unpack(kBounded ? two_s : (kCap || kBias) ? f2add(two_s, nm2) : f2fma(two_s, c2, nm2), x0, x1);
                     const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
                     ls2[(x >> 1) & 1] = f2add(ls2[(x >> 1) & 1], f2pack(p0, p1));
                     // the weights' one rounding: bf16, the type of V (the sum takes them unrounded)
@@ -595,7 +609,13 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             float l0, l1, l2, l3;
             f2unpack(ls2[0], l0, l1);
             f2unpack(ls2[1], l2, l3);
-            l_sum = l_sum * alpha + ((l0 + l1) + (l2 + l3));
+            const float sum = (l0 + l1) + (l2 + l3);
+            l_sum += sum;
+            if constexpr (!kBounded && !kBias) {
+                // (sums of 2^127 and beyond: the reference was that far off; such a row is computed again)
+                up = sum > 256.f ? min((int)(__float_as_uint(sum) >> 23) - 127, 126) : 0;
+                lost = lost || sum == INFINITY;
+            }
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&ctl.p_full[t]);
@@ -608,7 +628,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
         if (split) {
             if (t == 1) {
                 ctl.split_m[r] = m_used;
-                ctl.split_l[r] = l_sum;
+                ctl.split_l[r] = lost ? -1.f : l_sum;
                 if (!ok) ctl.split_ok = 0;
             }
             named_barrier_sync<1>(2 * kBM);
@@ -622,6 +642,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 w_b = mb == -INFINITY ? 0.f : fast_exp2(mb - m);
                 // (a sum that is NaN stays: its weight 0 times NaN)
                 l_sum = l_sum * w_a + lb * w_b;
+                lost = lost || lb == -1.f;
             }
         }
         const bool writer = !split || t == 0;
@@ -663,7 +684,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                                  pkd[4 * x], pkd[4 * x + 1], pkd[4 * x + 2], pkd[4 * x + 3]);
                 }
             }
-            fix = mine && chk != chk && l_sum == l_sum;
+            fix = mine && (lost || (chk != chk && l_sum == l_sum));
         }
         if (writer) {
             fence_proxy_async_smem();
@@ -713,24 +734,34 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kCap, bool kBias>
+template <int D, bool kCap, bool kBounded, bool kBias>
 int launch(const MaskParams& prm, dim3 grid, cudaStream_t stream) {
-    auto kern = masked_tc_kernel<D, kCap, kBias>;
-    cudaFuncAttributes fa;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(D)) != cudaSuccess ||
-        cudaFuncGetAttributes(&fa, kern) != cudaSuccess) {
+    auto kern = masked_tc_kernel<D, kCap, kBounded, kBias>;
+    static std::atomic<int> prepared[64];             // per device: the launch is allowed for
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
-    if (fa.numRegs < kRegLaunch) return ACACHE_ERR_UNSUPPORTED;   // the register split assumes the launch allocation
+    if (!prepared[dev].load(std::memory_order_acquire)) {
+        cudaFuncAttributes fa;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(D)) != cudaSuccess ||
+            cudaFuncGetAttributes(&fa, kern) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return ACACHE_ERR_CUDA;
+        }
+        if (fa.numRegs < kRegLaunch) return ACACHE_ERR_UNSUPPORTED;   // the register split assumes the launch allocation
+        prepared[dev].store(1, std::memory_order_release);
+    }
     kern<<<grid, kThreads, smem_bytes(D), stream>>>(prm);
     return launch_status();
 }
 
 template <int D>
-int dispatch(const MaskParams& prm, bool cap, bool bias, dim3 grid, cudaStream_t stream) {
-    if (cap) return bias ? launch<D, true, true>(prm, grid, stream) : launch<D, true, false>(prm, grid, stream);
-    return bias ? launch<D, false, true>(prm, grid, stream) : launch<D, false, false>(prm, grid, stream);
+int dispatch(const MaskParams& prm, bool cap, bool bounded, bool bias, dim3 grid, cudaStream_t stream) {
+    if (cap && bias) return launch<D, true, false, true>(prm, grid, stream);
+    if (cap) return bounded ? launch<D, true, true, false>(prm, grid, stream) : launch<D, true, false, false>(prm, grid, stream);
+    return bias ? launch<D, false, false, true>(prm, grid, stream) : launch<D, false, false, false>(prm, grid, stream);
 }
 
 }  // namespace
@@ -781,20 +812,19 @@ int launch_masked_tc(const MaskedAttn& c) {
         prm.cap_in = 2.f * kLog2e * (c.a.scale / c.mask.softcap);
         prm.cap_log2 = c.mask.softcap * kLog2e;
         prm.wide = c.mask.softcap > kWideCap;
-        prm.bounded = c.mask.softcap <= kBoundedCap;
-        const double y = (double)c.a.scale / c.mask.softcap, k = prm.scale_log2;      // y: of q.k = 1
-        prm.cap_near = (float)(kTanhNear / y);
-        const double k4[4] = {k, k * kTanh1 * y * y, k * kTanh2 * y * y * y * y, k * kTanh3 * y * y * y * y * y * y};
-        for (int i = 0; i < 4; ++i) {
-            prm.cap_k[i] = (float)k4[i];
-            if (!(fabs(k4[i]) > 1e-37 && fabs(k4[i]) < 1e38)) prm.cap_near = -1.f;    // a cap far from the scale: not this way
+        const double y = (double)c.a.scale / c.mask.softcap;         // of q.k = 1
+        double k = prm.scale_log2;
+        prm.cap_near = (float)std::min(0.5 / y, 1e18);
+        for (int i = 0; i < 4; ++i, k *= y * y) {
+            prm.cap_k[i] = (float)(k * kTanhHalf[i]);
+            if (!(k > 1e-36 && k < 1e36)) prm.cap_near = -1.f;   // a cap far from the scale: not this way
         }
-        prm.cap_near = std::min(prm.cap_near, 1e18f);
     }
     prm.budget = wait_budget();
     const dim3 grid((unsigned)c.a.hkv, (unsigned)c.B, (unsigned)n_qb);
     const bool bias = c.mask.slopes != nullptr;
-    return d == 64 ? dispatch<64>(prm, cap, bias, grid, c.stream) : dispatch<128>(prm, cap, bias, grid, c.stream);
+    const bool bounded = cap && !bias && c.mask.softcap <= kBoundedCap;
+    return d == 64 ? dispatch<64>(prm, cap, bounded, bias, grid, c.stream) : dispatch<128>(prm, cap, bounded, bias, grid, c.stream);
 }
 
 }  // namespace acache

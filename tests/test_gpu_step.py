@@ -754,3 +754,30 @@ def test_tensors_on_the_host_are_refused():
         ac.acache_slot_attention_masked(d, 1, 2, x, 2, pos, k, k, 2, x, row_range=torch.zeros((1, 2, 2), dtype=torch.int32))
     with pytest.raises(ValueError):
         ac.acache_token_scores(2, 128, x[:, 0].float(), entropy=torch.zeros(2))
+
+
+@pytest.mark.parametrize("n", [40, 300])
+@pytest.mark.parametrize("size", [4.0, 30.0, 300.0])
+def test_scores_that_jump_between_tiles(n, size):
+    """Scores that rise by up to hundreds from one tile of keys to the next, and rows whose first key is far below
+    the others: what the softmax is taken against has to keep up."""
+    g = torch.Generator().manual_seed(int(size))
+    hq, hkv, d, T = 2, 1, 128, 700
+    q = torch.randn((1, n, hq, d), generator=g)
+    q[..., 0] = 1.0 * d ** 0.5
+    kp, vp = (torch.randn((T, hkv, d), generator=g) * 0.2 for _ in range(2))
+    t = torch.arange(T)
+    kp[:, 0, 0] = size * torch.tensor([-1.0, 0.0, 1.0, -0.5, 2.0, 0.5])[t // 128]
+    kp[0, 0, 0] = -2 * size
+    kp[127, 0, 0] = -2 * size
+    q, kp, vp = q.to(BF16), kp.to(BF16), vp.to(BF16)
+    lo = torch.randint(0, 3, (n,), generator=g) * 127
+    hi = torch.randint(200, T + 1, (n,), generator=g)
+    out, st = torch.empty((1, n, hq, d), dtype=BF16, device="cuda"), _status()
+    rs = t.to(torch.int32)[None]
+    ac.acache_slot_attention_masked(_desc(hq, hkv, d, BF16), 1, n, dev(q), T, dev(rs), dev(kp), dev(vp), T, out,
+                                    row_range=dev(torch.stack((lo, hi), -1).to(torch.int32)[None]), dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    want, tol = masked_attention(q[0], rs[0].numpy(), kp, vp, d ** -0.5, lo, hi)
+    assert_attention(_np(out[0]), want, tol)

@@ -40,11 +40,37 @@ struct ScoreParams {
     float to_log2, to_ln;                   // log2e / temperature, 1 / temperature
 };
 
+ACACHE_DEVFN float max_nan(float a, float b) {
+    float c;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+    return c;
+}
+ACACHE_DEVFN uint64_t f2mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 template <typename T> struct Piece;
 template <> struct Piece<float> {
     static constexpr int kN = 4;
     ACACHE_DEVFN static float at(const uint4& w, int i) { return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w); }
     ACACHE_DEVFN static float top(const uint4& w) { return fmaxf(fmaxf(at(w, 0), at(w, 1)), fmaxf(at(w, 2), at(w, 3))); }
+    template <int B> ACACHE_DEVFN static float top(const uint4 (&w)[B]) {
+        float m = top(w[0]);
+#pragma unroll
+        for (int u = 1; u < B; ++u) m = fmaxf(m, top(w[u]));
+        return m;
+    }
+    // Elements e, e + 1; weights' exponents are bounded from below one by one.
+    struct Floor {};
+    ACACHE_DEVFN static Floor floor_of(float, float) { return {}; }
+    ACACHE_DEVFN static bool bounds(Floor) { return true; }
+    ACACHE_DEVFN static uint64_t pair(const uint4& w, int e, Floor) { return f2pack(at(w, e), at(w, e + 1)); }
+    ACACHE_DEVFN static void bound(float& a, float& b) {
+        a = max_nan(a, kLowest);
+        b = max_nan(b, kLowest);
+    }
     ACACHE_DEVFN static void put(uint4& w, int i, float x) {
         const uint32_t u = __float_as_uint(x);
         if (i == 0) w.x = u;
@@ -64,6 +90,31 @@ template <> struct Piece<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
         return fmaxf(__low2float(m), __high2float(m));
     }
+    template <int B> ACACHE_DEVFN static float top(const uint4 (&w)[B]) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+        __nv_bfloat162 m[4] = {h[0], h[1], h[2], h[3]};
+#pragma unroll
+        for (int i = 4; i < 4 * B; ++i) m[i & 3] = __hmax2(m[i & 3], h[i]);
+        m[0] = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+        return fmaxf(__low2float(m[0]), __high2float(m[0]));
+    }
+    // Elements e, e + 1, raised to a floor below which a weight is zero all the same: two to an instruction.  The floor
+    // lies 300 in log2 units below the maximum, and by more than its rounding; 0: there is no such bf16 value.
+    using Floor = uint32_t;
+    ACACHE_DEVFN static Floor floor_of(float m, float to_log2) {
+        const float f = m - 300.f / to_log2 - fabsf(m) * 0.015625f;
+        if (!(f > -3.3e38f)) return 0u;
+        const uint32_t u = __float_as_uint(f) >> 16;         // (cut: a little more for negative ones, less for others)
+        return u | u << 16;
+    }
+    ACACHE_DEVFN static bool bounds(Floor f) { return f != 0u; }
+    ACACHE_DEVFN static uint64_t pair(const uint4& w, int e, Floor f) {
+        uint32_t v = e == 0 ? w.x : e == 2 ? w.y : e == 4 ? w.z : w.w;
+        const __nv_bfloat162 h = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&f));
+        v = *reinterpret_cast<const uint32_t*>(&h);
+        return f2pack(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+    ACACHE_DEVFN static void bound(float&, float&) {}
     ACACHE_DEVFN static void put(uint4& w, int i, float x) {
         const uint32_t u = __float_as_uint(x) >> 16;        // (the value is one of bf16)
         uint32_t& v = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
@@ -83,11 +134,6 @@ ACACHE_DEVFN float key_value(uint64_t key) {
     return __uint_as_float(o == 1u ? 0x7fffffffu : (o >> 31) ? o & 0x7fffffffu : ~o);
 }
 ACACHE_DEVFN uint64_t max_key(uint64_t a, uint64_t b) { return a > b ? a : b; }
-ACACHE_DEVFN float max_nan(float a, float b) {
-    float c;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
-    return c;
-}
 ACACHE_DEVFN uint64_t warp_max_key(uint64_t key) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
     const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
@@ -126,7 +172,7 @@ ACACHE_DEVFN uint64_t ld_cluster_u64(uint32_t addr) {
 
 // NT threads to a CTA, cs CTAs (a cluster) to a row.
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1)
 scores_kernel(const ScoreParams p) {
     using W = Piece<T>;
     constexpr int N = W::kN, kWarps = NT / 32;
@@ -158,10 +204,13 @@ scores_kernel(const ScoreParams p) {
     };
     Stat st{kNone, 0.f, 0.f};
     int best_piece = -1;
-    auto raise = [&](float m) {
-        st = moved(st, m, p.to_log2);
-    };
-    auto add = [&](const uint4& w) {
+    // One piece, or what there is of it, with every weight's exponent bounded from below on its own.
+    auto add = [&](const uint4& w, int i) {
+        const float m = W::top(w);
+        if (m > st.m) {
+            st = moved(st, m, p.to_log2);
+            best_piece = i;
+        }
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float d = max_nan((W::at(w, e) - st.m) * p.to_log2, kLowest), q = fast_exp2(d);
@@ -170,30 +219,49 @@ scores_kernel(const ScoreParams p) {
         }
     };
     int i = p0 + tid;
-    for (; i + (kBatch - 1) * NT < p1; i += kBatch * NT) {
+    if (i < p1 && !whole(i)) {              // a first piece that begins in front of the row
+        add(load(i), i);
+        i += NT;
+    }
+    const int z = whole(n_all - 1) || p1 < n_all ? p1 : p1 - 1;     // pieces from here on are not whole
+    typename W::Floor floor = W::floor_of(st.m, p.to_log2);
+    for (; i + (kBatch - 1) * NT < z; i += kBatch * NT) {
         uint4 w[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) w[u] = load(i + u * NT);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const float m = W::top(w[u]);
-            if (m > st.m) {
-                raise(m);
-                best_piece = i + u * NT;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) add(w[u]);
-    }
-    for (; i < p1; i += NT) {
-        const uint4 w = load(i);
+        for (int u = 0; u < kBatch; ++u) w[u] = __ldg(w0 + i + u * NT);
         const float m = W::top(w);
         if (m > st.m) {
-            raise(m);
-            best_piece = i;
+            st = moved(st, m, p.to_log2);
+            floor = W::floor_of(m, p.to_log2);
+#pragma unroll
+            for (int u = kBatch - 1; u >= 0; --u)
+                if (W::top(w[u]) == m) best_piece = i + u * NT;
         }
-        add(w);
+        if (!W::bounds(floor)) {            // (a maximum near the lowest value)
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) add(w[u], i + u * NT);
+        } else {
+            const uint64_t nm = f2pack(-st.m, -st.m), c2 = f2pack(p.to_log2, p.to_log2);
+            uint64_t s2 = f2pack(0.f, 0.f), u2 = s2;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    float d0, d1;
+                    f2unpack(f2mul(f2add(W::pair(w[u], e, floor), nm), c2), d0, d1);
+                    W::bound(d0, d1);
+                    const uint64_t q2 = f2pack(fast_exp2(d0), fast_exp2(d1));
+                    s2 = f2add(s2, q2);
+                    u2 = f2fma(q2, f2pack(d0, d1), u2);
+                }
+            float a0, a1;
+            f2unpack(s2, a0, a1);
+            st.s += a0 + a1;
+            f2unpack(u2, a0, a1);
+            st.u += a0 + a1;
+        }
     }
+    for (; i < p1; i += NT) add(load(i), i);
     // ---- the CTA's maximum, S and U
     {
         float m = warp_max(st.m);
@@ -389,9 +457,9 @@ int dispatch(ScoreParams& p, int64_t rows, cudaStream_t stream) {
     p.cs = 1;
     if (pieces <= 128) return launch<T, 32>(p, rows, stream);
     if (pieces <= 1024) return launch<T, 128>(p, rows, stream);
-    // rows that leave SMs idle are split over a cluster, two pieces a thread at least
-    while (p.cs < kMaxCluster && rows * p.cs * 2 <= 2LL * sm_count() && pieces >= 2LL * 512 * 2 * p.cs) p.cs *= 2;
-    return launch<T, 512>(p, rows, stream);
+    // rows that leave SMs idle are split over a cluster, four pieces a thread at least
+    while (p.cs < kMaxCluster && rows * p.cs < 4LL * sm_count() && pieces >= 4LL * 256 * 2 * p.cs) p.cs *= 2;
+    return launch<T, 256>(p, rows, stream);
 }
 
 }  // namespace

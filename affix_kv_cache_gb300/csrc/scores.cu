@@ -8,12 +8,12 @@
 //   log p(t) = (x_t - M) / temperature - ln S,   entropy = ln S - ln2 U / S
 //
 // Bound by memory.  A row's 16-byte pieces go round the threads of a CTA (or, with few rows, of a cluster);
-// every thread keeps its own running maximum, S and U, raised when a batch of pieces holds more.  Both
-// terms of the entropy are >= 0, so nothing cancels.
-// The k likeliest: candidates are compared by (value, lower token), all different.  A thread's best piece is
-// remembered by the way; the k threads with the best elements hold all of the row's k best (each
-// other thread's best is below k elements), so only their pieces are looked at again, against the k-th
-// best of the threads.
+// every thread keeps its own reference in place of M (within 2^6 of its maximum, so next to nothing cancels between the
+// terms of the entropy), S and U.
+// The k likeliest: candidates are compared by (value, lower token), all different.  The k-th best of the groups of threads,
+// each by its best logit, is a bound that k elements reach, so only threads whose best reaches it are looked at again, a
+// warp to the pieces of one, for the elements that do; these -- few more than k -- are ranked by comparing all
+// with all.
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,7 +28,9 @@ constexpr int kMaxCluster = 8;
 constexpr int kList = 1024;                 // candidates of a CTA
 constexpr float kNone = -3.402823466e38f;   // maximum before any logit (lowest finite value: as a logit it counts)
 constexpr float kLowest = -200.f;           // d from here on down is a weight of zero
+constexpr float kHead = 6.f, kFloor = 300.f;   // log2 units: how far a logit may pass the reference; where a floor under it lies
 constexpr int kBatch = 4;                   // pieces in flight
+constexpr int kCtas = 5;                    // CTAs of 256 threads to an SM
 
 struct ScoreParams {
     const void* logits;
@@ -38,6 +40,7 @@ struct ScoreParams {
     int32_t *top_tokens, *dev_status;
     int vocab, k, cs;
     float to_log2, to_ln;                   // log2e / temperature, 1 / temperature
+    float head, floor_gap;                  // kHead and kFloor in logits
 };
 
 ACACHE_DEVFN float max_nan(float a, float b) {
@@ -54,6 +57,7 @@ ACACHE_DEVFN uint64_t f2mul(uint64_t a, uint64_t b) {
 template <typename T> struct Piece;
 template <> struct Piece<float> {
     static constexpr int kN = 4;
+    static constexpr uint32_t kNegInf = 0xff800000u;
     ACACHE_DEVFN static float at(const uint4& w, int i) { return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w); }
     ACACHE_DEVFN static float top(const uint4& w) { return fmaxf(fmaxf(at(w, 0), at(w, 1)), fmaxf(at(w, 2), at(w, 3))); }
     template <int B> ACACHE_DEVFN static float top(const uint4 (&w)[B]) {
@@ -81,6 +85,7 @@ template <> struct Piece<float> {
 };
 template <> struct Piece<__nv_bfloat16> {
     static constexpr int kN = 8;
+    static constexpr uint32_t kNegInf = 0xff80ff80u;
     ACACHE_DEVFN static float at(const uint4& w, int i) {
         const uint32_t v = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
         return __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16);
@@ -99,10 +104,10 @@ template <> struct Piece<__nv_bfloat16> {
         return fmaxf(__low2float(m[0]), __high2float(m[0]));
     }
     // Elements e, e + 1, raised to a floor below which a weight is zero all the same: two to an instruction.  The floor
-    // lies 300 in log2 units below the maximum, and by more than its rounding; 0: there is no such bf16 value.
+    // lies kFloor in log2 units below the reference, and by more than its rounding; 0: there is no such bf16 value.
     using Floor = uint32_t;
-    ACACHE_DEVFN static Floor floor_of(float m, float to_log2) {
-        const float f = m - 300.f / to_log2 - fabsf(m) * 0.015625f;
+    ACACHE_DEVFN static Floor floor_of(float m, float gap) {
+        const float f = m - gap - fabsf(m) * 0.015625f;
         if (!(f > -3.3e38f)) return 0u;
         const uint32_t u = __float_as_uint(f) >> 16;         // (cut: a little more for negative ones, less for others)
         return u | u << 16;
@@ -122,17 +127,18 @@ template <> struct Piece<__nv_bfloat16> {
     }
 };
 
-// Order of candidates: by value, then the lower token; 0 is no candidate, NaN the lowest.
-ACACHE_DEVFN uint64_t make_key(float x, int token) {
-    const uint32_t b = __float_as_uint(x + 0.f);             // -0.0 counts as +0.0
-    const uint32_t o = x != x ? 1u : (b >> 31) ? ~b : b | 0x80000000u;
-    return (uint64_t)o << 32 | (uint32_t)~token;
+// Order of values as whole numbers (-0.0 as +0.0, NaN the lowest), and of candidates: by value, then the lower token; 0 is
+// no candidate.
+ACACHE_DEVFN uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return x != x ? 1u : (b >> 31) ? ~b : b | 0x80000000u;
 }
-ACACHE_DEVFN int key_token(uint64_t key) { return (int)~(uint32_t)key; }
-ACACHE_DEVFN float key_value(uint64_t key) {
-    const uint32_t o = (uint32_t)(key >> 32);
+ACACHE_DEVFN float value_of(uint32_t o) {
     return __uint_as_float(o == 1u ? 0x7fffffffu : (o >> 31) ? o & 0x7fffffffu : ~o);
 }
+ACACHE_DEVFN uint64_t make_key(float x, int token) { return (uint64_t)order_of(x) << 32 | (uint32_t)~token; }
+ACACHE_DEVFN int key_token(uint64_t key) { return (int)~(uint32_t)key; }
+ACACHE_DEVFN float key_value(uint64_t key) { return value_of((uint32_t)(key >> 32)); }
 ACACHE_DEVFN uint64_t max_key(uint64_t a, uint64_t b) { return a > b ? a : b; }
 ACACHE_DEVFN uint64_t warp_max_key(uint64_t key) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
@@ -153,15 +159,16 @@ ACACHE_DEVFN Stat moved(const Stat& b, float m, float to_log2) {
 
 template <int NT>
 struct Smem {
-    uint64_t keys[NT];
+    alignas(16) float val[NT];              // a thread's best
+    alignas(16) float group[NT / 2];
     uint64_t list[kList];
     uint64_t best[kMaxK];                   // of this CTA, in order; 0 behind the last
-    int cand[kMaxK];
-    uint64_t threshold;
+    int cand[NT];
+    uint32_t bound;
     uint64_t wkey[NT / 32];
     Stat part[NT / 32];
     Stat stat;
-    int n_list;
+    int n_list, n_cand;
 };
 
 ACACHE_DEVFN uint64_t ld_cluster_u64(uint32_t addr) {
@@ -172,10 +179,10 @@ ACACHE_DEVFN uint64_t ld_cluster_u64(uint32_t addr) {
 
 // NT threads to a CTA, cs CTAs (a cluster) to a row.
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 1)
+__global__ void __launch_bounds__(NT, NT == 256 ? kCtas : 1)
 scores_kernel(const ScoreParams p) {
     using W = Piece<T>;
-    constexpr int N = W::kN, kWarps = NT / 32;
+    constexpr int N = W::kN, kWarps = NT / 32, kGroups = NT == 32 ? 32 : NT / 2;
     __shared__ Smem<NT> sm;
     const int64_t row = blockIdx.x / (unsigned)p.cs;
     const int cr = (int)(blockIdx.x % (unsigned)p.cs);
@@ -198,19 +205,19 @@ scores_kernel(const ScoreParams p) {
         }
         return w;
     };
-    auto key_of = [&](const uint4& w, int i, int e) -> uint64_t {
-        const int64_t at = (int64_t)i * N + e - skip;
-        return at >= 0 && at < p.vocab ? make_key(W::at(w, e), (int)at) : 0ull;
-    };
+    // The reference st.m is the maximum of the thread's first batch and rises when a later one is 2^kHead times as
+    // likely; the best logit is kept beside it.
     Stat st{kNone, 0.f, 0.f};
-    int best_piece = -1;
+    float best = -INFINITY;
+    auto note = [&](float m) -> bool {
+        best = fmaxf(best, m);
+        const bool up = m > st.m + p.head;
+        if (up) st = moved(st, m, p.to_log2);
+        return up;
+    };
     // One piece, or what there is of it, with every weight's exponent bounded from below on its own.
-    auto add = [&](const uint4& w, int i) {
-        const float m = W::top(w);
-        if (m > st.m) {
-            st = moved(st, m, p.to_log2);
-            best_piece = i;
-        }
+    auto add = [&](const uint4& w) {
+        note(W::top(w));
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float d = max_nan((W::at(w, e) - st.m) * p.to_log2, kLowest), q = fast_exp2(d);
@@ -219,27 +226,25 @@ scores_kernel(const ScoreParams p) {
         }
     };
     int i = p0 + tid;
-    if (i < p1 && !whole(i)) {              // a first piece that begins in front of the row
-        add(load(i), i);
+    if (i == 0 && skip != 0) {              // a first piece that begins in front of the row
+        add(load(i));
         i += NT;
     }
     const int z = whole(n_all - 1) || p1 < n_all ? p1 : p1 - 1;     // pieces from here on are not whole
-    typename W::Floor floor = W::floor_of(st.m, p.to_log2);
-    for (; i + (kBatch - 1) * NT < z; i += kBatch * NT) {
-        uint4 w[kBatch];
+    typename W::Floor floor = W::floor_of(st.m, p.floor_gap);
+    const uint32_t none = W::kNegInf;
+    for (; i < z; i += kBatch * NT) {
+        uint4 w[kBatch];                    // (behind the last: -infinity, which adds nothing)
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) w[u] = __ldg(w0 + i + u * NT);
-        const float m = W::top(w);
-        if (m > st.m) {
-            st = moved(st, m, p.to_log2);
-            floor = W::floor_of(m, p.to_log2);
-#pragma unroll
-            for (int u = kBatch - 1; u >= 0; --u)
-                if (W::top(w[u]) == m) best_piece = i + u * NT;
+        for (int u = 0; u < kBatch; ++u) {
+            w[u] = make_uint4(none, none, none, none);
+            if (i + u * NT < z) w[u] = __ldg(w0 + i + u * NT);
         }
+        if (note(W::top(w))) floor = W::floor_of(st.m, p.floor_gap);
         if (!W::bounds(floor)) {            // (a maximum near the lowest value)
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) add(w[u], i + u * NT);
+            for (int u = 0; u < kBatch; ++u)
+                if (i + u * NT < z) add(w[u]);
         } else {
             const uint64_t nm = f2pack(-st.m, -st.m), c2 = f2pack(p.to_log2, p.to_log2);
             uint64_t s2 = f2pack(0.f, 0.f), u2 = s2;
@@ -261,7 +266,8 @@ scores_kernel(const ScoreParams p) {
             st.u += a0 + a1;
         }
     }
-    for (; i < p1; i += NT) add(load(i), i);
+    // a last piece that ends behind the row, by the thread whose turn it is
+    if (z < p1 && (z - p0) % NT == tid && (z > 0 || skip == 0)) add(load(z));
     // ---- the CTA's maximum, S and U
     {
         float m = warp_max(st.m);
@@ -269,30 +275,12 @@ scores_kernel(const ScoreParams p) {
         t.s = warp_sum(t.s);
         t.u = warp_sum(t.u);
         if (lane == 0) sm.part[warp] = t;
-        if (tid == 0) sm.n_list = 0;
+        sm.val[tid] = best;
+        if (tid == 0) {
+            sm.n_list = sm.n_cand = 0;
+            sm.bound = order_of(-INFINITY);
+        }
         if (tid < kMaxK) sm.best[tid] = 0ull;
-    }
-    // ---- candidates
-    uint64_t key = 0;
-    if (p.k > 0) {
-        if (best_piece >= 0) {
-            const uint4 w = load(best_piece);
-#pragma unroll
-            for (int e = N - 1; e >= 0; --e)
-                if (W::at(w, e) == st.m) key = key_of(w, best_piece, e);
-        } else {                            // nothing above the lowest value: each element as it is
-            for (int q = p0 + tid; q < p1; q += NT) {
-                const uint4 w = load(q);
-#pragma unroll
-                for (int e = 0; e < N; ++e) key = max_key(key, key_of(w, q, e));
-            }
-        }
-        if (p.k == 1) {
-            key = warp_max_key(key);
-            if (lane == 0) sm.wkey[warp] = key;
-        } else {
-            sm.keys[tid] = key;
-        }
     }
     __syncthreads();
     if (warp == 0) {
@@ -302,82 +290,105 @@ scores_kernel(const ScoreParams p) {
         t.s = warp_sum(t.s);
         t.u = warp_sum(t.u);
         if (lane == 0) sm.stat = Stat{m, t.s, t.u};
-        if (p.k == 1) {
-            const uint64_t top = warp_max_key(lane < kWarps ? sm.wkey[lane] : 0ull);
-            if (lane == 0) sm.best[0] = top;
-        } else if (p.k > 1) {
-            // the k best threads, one after the other
-            uint64_t mine[kWarps], top = 0, last = 0;
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) {
-                mine[q] = sm.keys[32 * q + lane];
-                top = max_key(top, mine[q]);
+    }
+    if (p.k > 0) {
+        // ---- candidates.  A bound that k elements reach: the k-th best of the groups of threads, each by its best.
+        float mine = best;
+        if constexpr (kGroups < NT) {
+            if (tid < kGroups) sm.group[tid] = mine = fmaxf(best, sm.val[tid + kGroups]);
+            __syncthreads();
+        }
+        const float* group = kGroups < NT ? sm.group : sm.val;
+        if (tid < kGroups) {
+            int reach = 0;
+#pragma unroll 8
+            for (int q = 0; q < kGroups; q += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(group + q);
+                reach += (v.x >= mine) + (v.y >= mine) + (v.z >= mine) + (v.w >= mine);
             }
-            for (int r = 0; r < p.k; ++r) {
-                last = warp_max_key(top);
-                if (top == last && last) {
-                    top = 0;
-                    int from = 0;
+            if (reach >= p.k) atomicMax(&sm.bound, order_of(mine));
+        }
+        __syncthreads();
+        const float bound = value_of(sm.bound);
+        const bool any = bound == -INFINITY;                 // (then NaN may be among them too)
+        if (any || best >= bound) sm.cand[atomicAdd(&sm.n_cand, 1)] = tid;
+        __syncthreads();
+        // Threads whose best reaches the bound: their pieces are looked at again, a warp to a thread's.
+        const int n_cand = sm.n_cand;
+        auto candidates = [&](float from, auto&& see) {
+            for (int c = warp; c < n_cand; c += kWarps)
+                for (int q = p0 + sm.cand[c] + lane * NT; q < p1; q += 32 * NT) {
+                    const uint4 w = load(q);
+                    if (W::top(w) < from) continue;
 #pragma unroll
-                    for (int q = 0; q < kWarps; ++q) {
-                        if (mine[q] == last) {
-                            from = 32 * q + lane;
-                            mine[q] = 0;
-                        }
-                        top = max_key(top, mine[q]);
-                    }
-                    sm.cand[r] = from;
+                    for (int e = 0; e < N; ++e) see(W::at(w, e), q * N + e - skip);
                 }
-                if (lane == 0 && !last) sm.cand[r] = -1;
+        };
+        auto append = [&](float x, int at) {
+            if (at < 0 || at >= p.vocab) return;
+            const int n = atomicAdd(&sm.n_list, 1);
+            if (n < kList) sm.list[n] = make_key(x, at);
+        };
+        candidates(bound, [&](float x, int at) { if (any || x >= bound) append(x, at); });
+        __syncthreads();
+        int n = sm.n_list;
+        if (n > kList) {
+            // More than the list holds, as where most logits are one and the same: those above the bound, then
+            // those at it from the front.
+            __syncthreads();
+            if (tid == 0) sm.n_list = 0;
+            __syncthreads();
+            candidates(bound, [&](float x, int at) { if (x > bound) append(x, at); });
+            __syncthreads();
+            const int above = sm.n_list;
+            __syncthreads();
+            if (above + 32 * N + kMaxK > kList) {            // one after the other
+                uint64_t last = ~0ull;
+                for (int r = 0; r < p.k; ++r) {
+                    uint64_t top = 0;
+                    candidates(bound, [&](float x, int at) {
+                        const uint64_t c = at >= 0 && at < p.vocab && (any || x >= bound) ? make_key(x, at) : 0ull;
+                        if (c < last) top = max_key(top, c);
+                    });
+                    top = warp_max_key(top);
+                    if (lane == 0) sm.wkey[warp] = top;
+                    __syncthreads();
+#pragma unroll
+                    for (int q = 0; q < kWarps; ++q) top = max_key(top, sm.wkey[q]);
+                    last = top;
+                    if (tid == 0) sm.best[r] = top;
+                    __syncthreads();
+                }
+                n = 0;
+            } else {
+                for (int nan = 0; nan < (any ? 2 : 1); ++nan)
+                    for (int q0 = p0; q0 < p1; q0 += 32) {
+                        if (warp != 0) break;
+                        int have = lane == 0 ? *(volatile int*)&sm.n_list : 0;
+                        have = __shfl_sync(0xffffffffu, have, 0);
+                        if (have >= above + p.k) break;
+                        if (q0 + lane < p1) {
+                            const uint4 w = load(q0 + lane);
+#pragma unroll
+                            for (int e = 0; e < N; ++e) {
+                                const float x = W::at(w, e);
+                                if (nan ? x != x : x == bound) append(x, (q0 + lane) * N + e - skip);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                __syncthreads();
+                n = sm.n_list;
             }
-            if (lane == 0) sm.threshold = last;
+        }
+        for (int a = tid; a < n; a += NT) {
+            const uint64_t c = sm.list[a];
+            int above = 0;
+            for (int q = 0; q < n; ++q) above += sm.list[q] > c;
+            if (above < p.k) sm.best[above] = c;
         }
     }
     __syncthreads();
-    if (p.k > 1) {
-        const uint64_t least = max_key(sm.threshold, 1);
-        const int per = (p1 - p0 + NT - 1) / NT;                // pieces of a thread, at most
-        auto candidates = [&](auto&& see) {
-            for (int64_t it = tid; it < (int64_t)p.k * per; it += NT) {
-                const int from = sm.cand[it / per], q = p0 + from + (int)(it % per) * NT;
-                if (from < 0 || q >= p1) continue;
-                const uint4 w = load(q);
-#pragma unroll
-                for (int e = 0; e < N; ++e) see(key_of(w, q, e));
-            }
-        };
-        candidates([&](uint64_t c) {
-            if (c >= least) {
-                const int at = atomicAdd(&sm.n_list, 1);
-                if (at < kList) sm.list[at] = c;
-            }
-        });
-        __syncthreads();
-        const int n = sm.n_list;
-        if (n <= kList) {
-            for (int a = tid; a < n; a += NT) {
-                const uint64_t c = sm.list[a];
-                int above = 0;
-                for (int q = 0; q < n; ++q) above += sm.list[q] > c;
-                if (above < p.k) sm.best[above] = c;
-            }
-        } else {                            // more than the list holds: one after the other
-            uint64_t last = ~0ull;
-            for (int r = 0; r < p.k; ++r) {
-                uint64_t top = 0;
-                candidates([&](uint64_t c) { if (c < last) top = max_key(top, c); });
-                top = warp_max_key(top);
-                if (lane == 0) sm.wkey[warp] = top;
-                __syncthreads();
-#pragma unroll
-                for (int q = 0; q < kWarps; ++q) top = max_key(top, sm.wkey[q]);
-                last = top;
-                if (tid == 0) sm.best[r] = top;
-                __syncthreads();
-            }
-        }
-        __syncthreads();
-    }
     // ---- the row's from its CTAs'
     Stat all = sm.stat;
     uint64_t mine = 0;                      // this thread's alternative, tid-th in order
@@ -385,7 +396,10 @@ scores_kernel(const ScoreParams p) {
         if (tid < p.k) mine = sm.best[tid];
     } else {
         ptx::cluster_sync();
-        if (cr == 0 && warp == 0) {
+        if (cr == 0) {
+            // every CTA's alternatives into one list, then each to its place
+            for (int a = tid; a < p.cs * p.k; a += NT)
+                sm.list[a] = ld_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sm.best[a % p.k]), (uint32_t)(a / p.k)));
             const uint32_t at = ptx::smem_u32(&sm.stat);
             Stat t{kNone, 0.f, 0.f};
             if (lane < p.cs) {
@@ -395,20 +409,15 @@ scores_kernel(const ScoreParams p) {
             const float m = warp_max(t.m);
             t = moved(t, m, p.to_log2);
             all = Stat{m, warp_sum(t.s), warp_sum(t.u)};
-            uint64_t c[kMaxCluster];        // lane's of each CTA
-#pragma unroll
-            for (int q = 0; q < kMaxCluster; ++q)
-                c[q] = q < p.cs && lane < p.k ? ld_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&sm.best[lane]), (uint32_t)q)) : 0ull;
-            for (int r = 0; r < p.k; ++r) {
-                uint64_t top = 0;
-#pragma unroll
-                for (int q = 0; q < kMaxCluster; ++q) top = max_key(top, c[q]);
-                top = warp_max_key(top);
-#pragma unroll
-                for (int q = 0; q < kMaxCluster; ++q)
-                    if (c[q] == top) c[q] = 0;
-                if (lane == r) mine = top;
+            __syncthreads();
+            for (int a = tid; a < p.cs * p.k; a += NT) {
+                const uint64_t c = sm.list[a];
+                int above = 0;
+                for (int q = 0; q < p.cs * p.k; ++q) above += sm.list[q] > c;
+                if (c && above < p.k) sm.best[above] = c;    // (its own alternatives are in the list)
             }
+            __syncthreads();
+            if (tid < p.k) mine = sm.best[tid];
         }
         ptx::cluster_sync();                // no CTA may leave while another still reads its shared memory
         if (cr != 0) return;
@@ -457,8 +466,8 @@ int dispatch(ScoreParams& p, int64_t rows, cudaStream_t stream) {
     p.cs = 1;
     if (pieces <= 128) return launch<T, 32>(p, rows, stream);
     if (pieces <= 1024) return launch<T, 128>(p, rows, stream);
-    // rows that leave SMs idle are split over a cluster, four pieces a thread at least
-    while (p.cs < kMaxCluster && rows * p.cs < 4LL * sm_count() && pieces >= 4LL * 256 * 2 * p.cs) p.cs *= 2;
+    // rows that leave SMs idle are split over a cluster, in one wave and with four pieces a thread at least
+    p.cs = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxCluster, (int64_t)kCtas * sm_count() / rows, pieces / (4 * 256)}));
     return launch<T, 256>(p, rows, stream);
 }
 
@@ -478,6 +487,8 @@ int launch_token_scores(const ScoreCall& c) {
     p.k = c.k;
     p.to_log2 = kLog2e / c.temperature;
     p.to_ln = 1.f / c.temperature;
+    p.head = kHead / p.to_log2;
+    p.floor_gap = kFloor / p.to_log2;
     return c.dtype == ACACHE_F32 ? dispatch<float>(p, c.rows, c.stream) : dispatch<__nv_bfloat16>(p, c.rows, c.stream);
 }
 

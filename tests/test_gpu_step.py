@@ -611,6 +611,29 @@ def test_candidates_of_one_thread_and_of_all(k):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [300, 5003, 130001])
+@pytest.mark.parametrize("k", [1, 5, 32])
+def test_few_tokens_left_and_many_alike(dtype, V, k):
+    """Rows of which a handful can be chosen (the rest -infinity, in front and behind), and rows with thousands of
+    logits at the k-th best value, few or many above it."""
+    g = torch.Generator().manual_seed(V + k)
+    x = torch.full((8, V), -INF)
+    x[0, [V // 2, V - 1, 3]] = torch.tensor([1.0, 2.0, 1.0])
+    x[1] = torch.randint(0, 2, (V,), generator=g).float()
+    x[2] = 1.0
+    x[2, torch.randint(0, V, (3,), generator=g)] = 2.0
+    x[3] = torch.randint(0, 200, (V,), generator=g).clamp_max(190).float()
+    x[4, V - 60:] = 4.0                                   # the alike lie at the end
+    x[5] = torch.where(torch.arange(V) % 3 == 0, 5.0, torch.randn(V, generator=g))
+    x[6, :40], x[6, 40:] = NAN, -INF
+    x[7, ::2] = NAN
+    x[7, V - 1] = 0.5
+    st = _lib.DEV_NAN
+    _check_scores(x.to(dtype), min(k, V), status=st)
+    _check_scores(x[:6].to(dtype).repeat(60, 1), min(k, V))      # many rows: no cluster
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("V", [9, 3000, 40000])
 def test_scores_of_what_is_not_finite(dtype, V):
     g = torch.Generator().manual_seed(V)

@@ -461,19 +461,23 @@ def rope_desc_frequencies(frequencies, interleaved=False, amplitude=1.0) -> Rope
 
 def _row_stride(t, heads, d):
     """Elements from one row [heads][d] of a tensor [..., heads, d] to the next; rows must be evenly spaced."""
-    if not isinstance(t, torch.Tensor) or t.is_contiguous():
+    if t is None or not hasattr(t, "stride") or t.is_contiguous():
         return heads * d
     shape, stride = t.shape, t.stride()
-    if t.dim() < 3 or stride[-1] != 1 or (shape[-2] > 1 and stride[-2] != shape[-1]):
+    n = len(shape)
+    if n == 4 and stride[3] == 1 and stride[2] == d and stride[0] == stride[1] * shape[1] and shape[1] > 1:
+        return stride[1]                     # slices of a batch of fused rows
+    if n < 3 or stride[-1] != 1 or (stride[-2] != shape[-1] and shape[-2] > 1):
         raise ValueError("the heads of a row have to follow one another")
-    step, n = None, 1
-    for size, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+    step, rows = None, 1
+    for i in range(n - 3, -1, -1):
+        size = shape[i]
         if size != 1:
             if step is None:
-                step = st
-            elif st != step * n:
+                step = stride[i]
+            elif stride[i] != step * rows:
                 raise ValueError("the rows have to be evenly spaced")
-            n *= size
+            rows *= size
     return heads * d if step is None else step
 
 

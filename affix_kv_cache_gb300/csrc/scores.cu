@@ -30,7 +30,7 @@ constexpr float kNone = -3.402823466e38f;   // maximum before any logit (lowest 
 constexpr float kLowest = -200.f;           // d from here on down is a weight of zero
 constexpr float kHead = 6.f, kFloor = 300.f;   // log2 units: how far a logit may pass the reference; where a floor under it lies
 constexpr int kBatch = 4;                   // pieces in flight
-constexpr int kCtas = 5;                    // CTAs of 256 threads to an SM
+constexpr int kCtas = 6;                    // CTAs of 256 threads to an SM
 
 struct ScoreParams {
     const void* logits;
@@ -467,7 +467,7 @@ int dispatch(ScoreParams& p, int64_t rows, cudaStream_t stream) {
     if (pieces <= 128) return launch<T, 32>(p, rows, stream);
     if (pieces <= 1024) return launch<T, 128>(p, rows, stream);
     // rows that leave SMs idle are split over a cluster, in one wave and with four pieces a thread at least
-    p.cs = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxCluster, (int64_t)kCtas * sm_count() / rows, pieces / (4 * 256)}));
+    p.cs = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxCluster, 4LL * sm_count() / rows, pieces / (4 * 256)}));
     return launch<T, 256>(p, rows, stream);
 }
 

@@ -37,22 +37,25 @@ ACACHE_DEVFN float capped_wide(float dot, float cap_in, float cap_log2) {
 // Up to here the plain form is off by at most 2^-13, a sixteenth of a weight's rounding to bf16.
 constexpr float kWideCap = 512.f;
 
+template <typename T>
 struct MaskedPool {
-    const __nv_bfloat16 *k_cache, *v_cache;
+    const T *k_cache, *v_cache;
     const int32_t* read_slot;       // of the request, from the first of the keys counted below
     int64_t num_slots;
     int hkv, drop;
     bool wide;                      // a cap above kWideCap
     float scale_log2, cap_in, cap_log2;   // cap_in = 0: no cap
+    float scale;                    // float32 rows: cap_in is the cap itself, and tanh the library's
 };
 
 // One row over its own keys [lo, hi), by a warp: for rows whose product with V met a masked key that is not
 // finite (0 x NaN is NaN).  pos counts as the keys do.
-template <int D>
-ACACHE_DEVFN void masked_row(const MaskedPool& p, const __nv_bfloat16* q, __nv_bfloat16* out, int lo, int hi, int hk,
-                             float slope_log2, int64_t pos, int lane) {
+template <typename T, int D>
+ACACHE_DEVFN void masked_row(const MaskedPool<T>& p, const T* q, T* out, int lo, int hi, int hk, float slope_log2, int64_t pos,
+                             int lane) {
     constexpr int kPer = D / 32;
     float m = -INFINITY, l = 0.f, acc[kPer];
+    bool any = false;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
 #pragma unroll 1
@@ -64,12 +67,16 @@ ACACHE_DEVFN void masked_row(const MaskedPool& p, const __nv_bfloat16* q, __nv_b
             const int slot = p.read_slot[t];
             if (!(p.drop && slot == ACACHE_SLOT_NONE)) {
                 float dot = 0.f;
+                any = true;
                 if (slot >= 0 && slot < p.num_slots) {
                     at = ((int64_t)slot * p.hkv + hk) * D;
 #pragma unroll 4
                     for (int c = 0; c < D; ++c) dot = fmaf(to_f32(q[c]), to_f32(p.k_cache[at + c]), dot);
                 }
-                s = p.cap_in > 0.f ? (p.wide ? capped_wide(dot, p.cap_in, p.cap_log2) : capped(dot, p.cap_in, p.cap_log2)) : dot * p.scale_log2;
+                if (p.scale != 0.f || p.scale_log2 == 0.f)
+                    s = p.cap_in > 0.f ? p.cap_in * tanhf(dot * p.scale / p.cap_in) * kLog2e : dot * p.scale * kLog2e;
+                else
+                    s = p.cap_in > 0.f ? (p.wide ? capped_wide(dot, p.cap_in, p.cap_log2) : capped(dot, p.cap_in, p.cap_log2)) : dot * p.scale_log2;
                 if (slope_log2 != 0.f) s = fmaf(-slope_log2, fabsf((float)(pos - t)), s);
             }
         }
@@ -88,8 +95,9 @@ ACACHE_DEVFN void masked_row(const MaskedPool& p, const __nv_bfloat16* q, __nv_b
         }
         m = m_new;
     }
+    any = __any_sync(0xffffffffu, any);
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) out[lane + 32 * x] = from_f32<__nv_bfloat16>(l == 0.f ? 0.f : acc[x] / l);
+    for (int x = 0; x < kPer; ++x) out[lane + 32 * x] = from_f32<T>(any ? acc[x] / l : 0.f);
 }
 
 }  // namespace acache

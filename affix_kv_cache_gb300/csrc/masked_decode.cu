@@ -216,6 +216,7 @@ masked_decode_kernel(const DecParams p) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[j][b][x] = 0.f;
+    uint32_t saw = 0;                                // bit 2 b + x: row 2 t + x of group b sees a key
     uint32_t at = 0, at2 = 2;                        // stages of the chunk at hand and of the one to bring
     for (int ch = ch0 + warp; ch < ch1; ch += kWarps) {
         bring(s2, ring + at2 * (2 * kMat));
@@ -268,7 +269,9 @@ masked_decode_kernel(const DecParams p) {
                     for (int i = 1; i < CH; ++i) d += s[b][i][2 * k + x];
                     float y = p.cap_in > 0.f ? (p.wide ? capped_wide(d, p.cap_in, p.cap_log2) : capped(d, p.cap_in, p.cap_log2)) : d * p.scale_log2;
                     if (p.slopes) y = fmaf(-sm.slope[8 * b + 2 * t + x], fabsf((float)(sm.pos[8 * b + 2 * t + x] - key)), y);
-                    u[b][2 * k + x] = in && key >= lo[b][x] && key < hi[b][x] ? y : -INFINITY;
+                    const bool see = in && key >= lo[b][x] && key < hi[b][x];
+                    saw |= (uint32_t)see << (2 * b + x);
+                    u[b][2 * k + x] = see ? y : -INFINITY;
                 }
         }
         bool grow = false;                           // (a maximum that is NaN -- every key of the row so far -- is left alone)
@@ -327,6 +330,15 @@ masked_decode_kernel(const DecParams p) {
         __syncwarp();                                // the next chunk but two lands in this stage
     }
     cp_async_wait<0>();
+    // The maximum of a row that sees no key stays -infinity; of one that sees some, be their scores all -infinity (then its
+    // sum of 0 makes it 0 / 0), it is a number.
+#pragma unroll
+    for (int i = 4; i < 32; i <<= 1) saw |= __shfl_xor_sync(0xffffffffu, saw, i);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if ((saw >> (2 * b + x)) & 1u) m[b][x] = fmaxf(m[b][x], -3.4e38f);
     __syncthreads();                                 // the partials go over the rings
     // -------------------------------------------------------------------------- merge
 #pragma unroll
@@ -348,11 +360,11 @@ masked_decode_kernel(const DecParams p) {
     __syncthreads();
     // A merged row's 4 columns at a time; a warp takes 32 neighbouring items.  Rows whose output is not finite while their sum
     // is are computed again.
-    auto finish = [&](int it, bool in, const float4& acc, float L) {
+    auto finish = [&](int it, bool in, const float4& acc, float M, float L) {
         const int r = in ? it / (D / 4) : 0, q4 = it % (D / 4), i = r / p.g;
         const int64_t row_at = ((qbase + i) * p.Hq + (int64_t)hk * p.g + (r - i * p.g)) * D;
         const float inv = 1.f / L;
-        const bool none = L == 0.f;                  // no key: zeros
+        const bool none = M == -INFINITY;            // no key: zeros
         const float y0 = none ? 0.f : acc.x * inv, y1 = none ? 0.f : acc.y * inv, y2 = none ? 0.f : acc.z * inv, y3 = none ? 0.f : acc.w * inv;
         const float chk = fmaf(y0, 0.f, fmaf(y1, 0.f, fmaf(y2, 0.f, y3 * 0.f)));
         if (in) {
@@ -367,7 +379,7 @@ masked_decode_kernel(const DecParams p) {
                 if (!((bad >> part) & (D == 128 ? 0xffffffffu : 0xffffu))) continue;
                 const int rw = __shfl_sync(0xffffffffu, r, part);
                 const int64_t ra = __shfl_sync(0xffffffffu, row_at, part);
-                masked_row<D>(MaskedPool{p.k_cache, p.v_cache, rs, p.num_slots, p.Hkv, p.drop, p.wide != 0, p.scale_log2, p.cap_in, p.cap_log2},
+                masked_row<bf16, D>(MaskedPool<bf16>{p.k_cache, p.v_cache, rs, p.num_slots, p.Hkv, p.drop, p.wide != 0, p.scale_log2, p.cap_in, p.cap_log2, 0.f},
                               p.q + ra, p.out + ra, sm.lo[rw], sm.hi[rw], hk, sm.slope[rw], sm.pos[rw], lane);
             }
         }
@@ -399,7 +411,7 @@ masked_decode_kernel(const DecParams p) {
             acc.w = fmaf(e, f.w, acc.w);
         }
         if (!split) {
-            finish(it, in, acc, L);
+            finish(it, in, acc, M, L);
         } else if (in) {
             if (q4 == 0) {
                 sm.row_m[r] = M;
@@ -446,7 +458,7 @@ masked_decode_kernel(const DecParams p) {
             acc.z = none ? acc.z : fmaf(e, f[x].z, acc.z);
             acc.w = none ? acc.w : fmaf(e, f[x].w, acc.w);
         }
-        finish(it, in, acc, L);
+        finish(it, in, acc, M, L);
     }
     cluster_sync();                // no CTA may leave while another still reads its shared memory
 }

@@ -442,7 +442,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
         const int nt = ks.n_tiles(t);
         float m_used = kBounded ? 0.f : -INFINITY, l_sum = 0.f;
         int up = 0;                                        // powers of two by which the next tile raises the reference
-        bool lost = false, ok = true;
+        bool lost = false, saw = false, ok = true;         // saw: the row sees a key
         for (int i = 0; i < nt; ++i) {
             const int j = ks.tile(t, i);
             // the row's keys of the tile, one bit each, before the wait for its scores
@@ -460,6 +460,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                     whole = whole && gone == 0u;
                 }
             }
+            saw = saw || (see[0] | see[1] | see[2] | see[3]) != 0u;
             whole = __all_sync(0xffffffffu, whole || !mine);
             ok = __all_sync(0xffffffffu, wait_bar(&ctl.s_full[t], i & 1, abort_flag, dev_status, budget));
             if (!ok) break;
@@ -623,6 +624,9 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
         if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[t], 0, abort_flag, dev_status, budget) && !*abort_flag);
         // (without a key the rows wait for the Q tiles, whose place they are stored from)
         if (ok && nt == 0) ok = __all_sync(0xffffffffu, wait_bar(&ctl.q_full, 0, abort_flag, dev_status, budget));
+        // The reference of a row that sees no key is -infinity; of one that sees some, be their scores all -infinity (then
+        // its sum of 0 makes it 0 / 0), it is a number.
+        m_used = saw ? fmaxf(m_used, -3.4e38f) : -INFINITY;
         // Split keys: chain B's maximum and sum go to chain A, which merges the two and stores the rows.
         float w_a = 1.f, w_b = 0.f;
         if (split) {
@@ -643,6 +647,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 // (a sum that is NaN stays: its weight 0 times NaN)
                 l_sum = l_sum * w_a + lb * w_b;
                 lost = lost || lb == -1.f;
+                m_used = m;
             }
         }
         const bool writer = !split || t == 0;
@@ -653,7 +658,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
         if (ok) {
             tc_fence_after();
             const float inv_l = 1.f / l_sum;
-            const bool none = l_sum == 0.f;                // no key: zeros, whatever the accumulator holds
+            const bool none = m_used == -INFINITY;         // no key: zeros, whatever the accumulator holds
             float chk = 0.f;                               // NaN once a column is not finite
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
@@ -714,8 +719,8 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 for (uint32_t todo = __ballot_sync(0xffffffffu, fix); todo; todo &= todo - 1) {
                     const int l0 = __ffs(todo) - 1;
                     const int64_t at = __shfl_sync(0xffffffffu, row_at, l0);
-                    masked_row<D>(MaskedPool{p.k_cache, p.v_cache, rs, p.num_slots, p.Hkv, p.drop, p.wide != 0, p.scale_log2, kCap ? p.cap_in : 0.f,
-                                             p.cap_log2},
+                    masked_row<bf16, D>(MaskedPool<bf16>{p.k_cache, p.v_cache, rs, p.num_slots, p.Hkv, p.drop, p.wide != 0, p.scale_log2, kCap ? p.cap_in : 0.f,
+                                                         p.cap_log2, 0.f},
                                   p.q + at, p.out + at, __shfl_sync(0xffffffffu, a_lo, l0), __shfl_sync(0xffffffffu, a_hi, l0), hk,
                                   __shfl_sync(0xffffffffu, slope, l0), __shfl_sync(0xffffffffu, away, l0), lane);
                 }

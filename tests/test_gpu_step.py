@@ -804,3 +804,24 @@ def test_scores_that_jump_between_tiles(n, size):
     assert st.item() == 0
     want, tol = masked_attention(q[0], rs[0].numpy(), kp, vp, d ** -0.5, lo, hi)
     assert_attention(_np(out[0]), want, tol)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 128)])
+@pytest.mark.parametrize("n", [1, 20, 150])
+def test_rows_whose_scores_are_all_minus_infinity(dtype, d, n):
+    """A softmax over keys that all score -infinity is 0 / 0; over no key it is zeros."""
+    g = torch.Generator().manual_seed(n)
+    T = 200
+    q = torch.rand((1, n, 2, d), generator=g).to(dtype) + 0.5
+    kp, vp = (torch.randn((T, 1, d), generator=g).to(dtype) for _ in range(2))
+    kp[:, 0, 0] = -INF
+    kp[150, 0, 0] = 1.0
+    lo = torch.zeros(n, dtype=torch.int32)
+    hi = torch.where(torch.arange(n) % 3 == 0, 150, torch.where(torch.arange(n) % 3 == 1, 200, 0)).to(torch.int32)
+    out = torch.empty((1, n, 2, d), dtype=dtype, device="cuda")
+    ac.acache_slot_attention_masked(_desc(2, 1, d, dtype), 1, n, dev(q), T, dev(torch.arange(T, dtype=torch.int32)[None]), dev(kp), dev(vp), T,
+                                    out, row_range=dev(torch.stack((lo, hi), -1)[None]))
+    torch.cuda.synchronize()
+    o = out[0].float().cpu()
+    assert o[::3].isnan().all()
+    assert torch.equal(o[1::3], vp[150].float().expand_as(o[1::3])) and (o[2::3] == 0).all()

@@ -30,7 +30,7 @@ using bf16 = __nv_bfloat16;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys a warp takes at a time
 constexpr int kSt = 3;                      // chunks in a warp's ring
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;             // (above 8: not on every GPU, but on the one this is for)
 constexpr int kCtasPerSm = 2;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: weights stay below 2^8
 
@@ -476,7 +476,8 @@ int launch(const DecParams& prm, dim3 grid, cudaStream_t stream) {
     }
     std::atomic<int>& st = g_prepared[(D == 128 ? 3 : 0) + NB / 2][dev];
     if (!st.load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
             (void)cudaGetLastError();
             return ACACHE_ERR_CUDA;
         }

@@ -165,7 +165,7 @@ masked_simt_kernel(const SimtParams p) {
             // K: consecutive lanes take consecutive keys, so the transposed stores do not conflict
             const int key = tid & (kBN - 1);
             const int64_t kr = sm.row[key];
-#pragma unroll 8
+#pragma unroll 4
             for (int it = 0; it < PPT; ++it) {
                 const int c = (tid / kBN) * PPT + it;
                 uint4 w = make_uint4(0u, 0u, 0u, 0u);
@@ -174,7 +174,7 @@ masked_simt_kernel(const SimtParams p) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) sm.k[c * N + i][key] = to_f32(e[i]);
             }
-#pragma unroll 8
+#pragma unroll 4
             for (int it = 0; it < PPT; ++it) {
                 const int x = it * kThreads + tid, vk = x / (D / N), c = x % (D / N);
                 const int64_t vr = sm.row[vk];

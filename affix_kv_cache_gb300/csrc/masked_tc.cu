@@ -128,11 +128,14 @@ struct KeySchedule {
     }
 };
 
+// Bounded wait that also leaves early once another role has aborted.  The hardware's suspending wait returns after a time
+// of its own, some microseconds: budgets below that are polled.
+constexpr long long kPatient = 1LL << 16;
 ACACHE_DEVFN bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_status, long long budget) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (budget >= kPatient ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (budget >= kPatient ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (clock64() - t0 > budget) {
             *abort_flag = 1;

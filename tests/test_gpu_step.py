@@ -825,3 +825,65 @@ def test_rows_whose_scores_are_all_minus_infinity(dtype, d, n):
     o = out[0].float().cpu()
     assert o[::3].isnan().all()
     assert torch.equal(o[1::3], vp[150].float().expand_as(o[1::3])) and (o[2::3] == 0).all()
+
+
+@pytest.mark.parametrize("n,cap", [(600, 0.0), (600, 30.0), (20, 0.0)])
+def test_masked_waits_that_run_out(n, cap):
+    """Waits of the tensor-core kernel that run out: flagged, no row is written that lacks a product, and the same call
+    with the default budget gives what it gave before."""
+    g = torch.Generator().manual_seed(n)
+    B, hq, hkv, d, T = 8, 32, 8, 128, 1500
+    q = torch.randn((B, n, hq, d), generator=g).to(BF16)
+    kp, vp = (torch.randn((T, hkv, d), generator=g).to(BF16) for _ in range(2))
+    rs = torch.randperm(T, generator=g).to(torch.int32).expand(B, T)
+    args = (_desc(hq, hkv, d, BF16), B, n, dev(q), T, dev(rs), dev(kp), dev(vp), T)
+    rr = torch.stack((torch.zeros(n, dtype=torch.int32), torch.arange(T - n + 1, T + 1, dtype=torch.int32)), -1)
+    rr = dev(rr.expand(B, n, 2))
+
+    def call():
+        out, st = torch.full((B, n, hq, d), 7.0, dtype=BF16, device="cuda"), _status()
+        ac.acache_slot_attention_masked(*args, out, row_range=rr, softcap=cap, dev_status=st)
+        torch.cuda.synchronize()
+        return out, st.item()
+
+    want, st = call()
+    assert st == 0
+    timed_out = 0
+    for budget in (1, 300, 1000, 2000, 4000, 8000):
+        prev = ac.acache_wait_budget(budget)
+        try:
+            out, st = call()
+        finally:
+            ac.acache_wait_budget(prev)
+        assert st in (0, _lib.DEV_TIMEOUT)
+        timed_out += st != 0
+        same = (out == want).all(-1)
+        assert (same | (out == 7.0).all(-1)).all()
+        assert st != 0 or same.all()
+    assert timed_out
+    out, st = call()
+    assert st == 0 and torch.equal(out, want)
+
+
+def test_calls_on_two_streams_at_once():
+    """The calls hold nothing between them: two streams in turn give what one gives."""
+    g = torch.Generator().manual_seed(21)
+    hq, hkv, d, T, n = 8, 2, 128, 600, 64
+    kp, vp = (torch.randn((T, hkv, d), generator=g).to(BF16).cuda() for _ in range(2))
+    rs = dev(torch.randperm(T, generator=g).to(torch.int32)[None])
+    qs = [torch.randn((1, n, hq, d), generator=g).to(BF16).cuda() for _ in range(4)]
+    xs = [torch.randn((40, 70001), generator=g).cuda() for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    results = []
+    for two in (False, True):
+        torch.cuda.synchronize()
+        got = []
+        for i in range(4):
+            with torch.cuda.stream(streams[i & 1] if two else streams[0]):
+                o, tt, tl = torch.empty_like(qs[i]), torch.empty((40, 20), dtype=torch.int32, device="cuda"), torch.empty((40, 20), device="cuda")
+                ac.acache_slot_attention_masked(_desc(hq, hkv, d, BF16), 1, n, qs[i], T, rs, kp, vp, T, o, softcap=9.0)
+                ac.acache_token_scores(40, 70001, xs[i], top_tokens=tt, top_logprob=tl)
+                got += [o, tt, tl]
+        torch.cuda.synchronize()
+        results.append(got)
+    assert all(torch.equal(a, b) for a, b in zip(*results))

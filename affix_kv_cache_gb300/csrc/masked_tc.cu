@@ -10,8 +10,8 @@
 // group) pair, so that all heads of a group share one K/V stream and a causal block spans few positions.
 //   WG0, WG1   softmax + epilogue of tile A / B, thread r owning row r = TMEM lane r: a tile of scores is read
 //              into registers, capped, biased, masked, exponentiated in base 2 against a reference that
-//              follows the sums of weights, and written back over the scores as bf16 for the product with V.  The two take turns.
-//   WG2        warps 8 and 9 issue the MMAs of A and B (S = Q K^T from shared memory, O += P V with P from TMEM)
+//              follows the sums of weights, and written back over the scores as bf16 for the product with V.
+//   warp 8     issues the MMAs of both (S = Q K^T from shared memory, O += P V with P from TMEM), A's and B's in turn
 //   warps 10-19  TMA producers of a 3-stage K ring and a 2-stage V ring: a tile of 128 consecutive slots is tiled
 //              box loads of the pool, any other gather4 loads of four rows each.
 // A block left with one Q tile splits its keys between the two chains and merges them at the end.
@@ -21,6 +21,14 @@
 // What a masked key holds cannot reach a row through its score (replaced by -infinity), but 0 x NaN is NaN in
 // the product with V: a row whose output is not finite while its sum of weights is, is computed again by its
 // warp over its own keys alone.
+//
+// Measured (2,070 MHz): causal prompts of 2 x 4,096 (32 heads over 8, d = 128) 249 us, 1,100 TFLOP/s over the keys that rows see;
+// block-causal capped point of 16 x 986 rows over 2,624 keys (28 over 4) 524 us, 925 TFLOP/s.  A step of both chains takes 3,600
+// cycles (capped: 4,300) where its MMAs need 2,150: the MMAs of a chain wait for barriers some 700 cycles a tile, a capped
+// softmax (2,700 cycles, two of them at a time) for issue.  Set-up, the first tile's loads and the epilogue take 14,000 cycles of a
+// CTA's 60,000.  What was tried: two issuing warps (their MMAs interleave and both chains end together), waits
+// merged or tested ahead (slower by 2 to 9 %), polling instead of suspended waits (7 to 9 %), chains that take turns (no
+// difference, or 8 % slower).
 //
 // Every mbarrier wait is bounded (acache_wait_budget); a wait that gives up raises a CTA-wide abort flag and
 // ACACHE_DEV_TIMEOUT, roles leave their loops, MMAs and loads in flight are waited for (bounded), and TMEM is
@@ -209,6 +217,16 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
     }
     if (threadIdx.x == 0) {
         mbar_init(&ctl.q_full, 1);
+        // stages fill with one arrival per producer warp of the ring, and are free with the MMAs of the last chain that
+        // reads them
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(&ctl.k_full[s], kProdPerRing);
+            mbar_init(&ctl.k_empty[s], 1);
+        }
+        for (int s = 0; s < kVStages + 1; ++s) {
+            mbar_init(&ctl.v_full[s], kProdPerRing);
+            mbar_init(&ctl.v_empty[s], 1);
+        }
         for (int t = 0; t < kQT; ++t) {
             mbar_init(&ctl.s_full[t], 1);
             mbar_init(&ctl.p_half[t], 128);
@@ -231,7 +249,9 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
         tmem_alloc(&ctl.tmem_base, kTmemCols);
         tmem_relinquish();
     }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     // The window of keys that the CTA streams.
     int w_lo = 0x7fffffff, w_hi = 0;
 #pragma unroll
@@ -248,21 +268,6 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
     const KeySchedule ks{split, n_kv, split ? (n_kv + 1) / 2 : n_kv};
     const int n_vst = split ? kVStages + 1 : kVStages;
     auto sVs = [&](int s) { return s < kVStages ? sV(s) : sQ(1); };
-    if (threadIdx.x == 0) {
-        const int readers = split ? 1 : n_qt;
-        for (int s = 0; s < kKStages; ++s) {
-            mbar_init(&ctl.k_full[s], kProdPerRing);
-            mbar_init(&ctl.k_empty[s], readers);
-        }
-        for (int s = 0; s < kVStages + 1; ++s) {
-            mbar_init(&ctl.v_full[s], kProdPerRing);
-            mbar_init(&ctl.v_empty[s], readers);
-        }
-        fence_mbar_init();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
 
     if (wg >= 2) {
@@ -384,7 +389,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                             umma_ss(tm + col_s(t), dq + ko, dk + ko, idS, k > 0);
                         }
                         umma_commit(&ctl.s_full[t]);
-                        umma_commit(&ctl.k_empty[st]);
+                        if (halved || !two || t == 1) umma_commit(&ctl.k_empty[st]);
                     }
                     return true;
                 };
@@ -413,7 +418,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                     if (leader) {
 #pragma unroll
                         for (int k = 4; k < 8; ++k) umma_ts(d_o, d_p + k * 8, dv + (uint64_t)(k * 2048 / 16), idO, 1);
-                        umma_commit(&ctl.v_empty[st]);
+                        if (halved || !two || t == 1) umma_commit(&ctl.v_empty[st]);
                         if (i + 1 == nt) umma_commit(&ctl.drain[t]);    // the chain's last
                     }
                     if (i + 1 < nt) ok = issue_s(t, us.entry(t, i + 1));

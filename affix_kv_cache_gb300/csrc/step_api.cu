@@ -105,7 +105,7 @@ bool masked_ok(const AttnArgs& a, const acache_mask* m, int batch, int n_q, int 
         return false;
     // (the capped score's constants have to be numbers)
     if (m && m->softcap > 0.f && (!isfinite(2.f * kLog2e * (a.scale / m->softcap)) || !isfinite(m->softcap * kLog2e))) return false;
-    return batch <= 65535 && (int64_t)n_q * (a.hq / a.hkv) < 1 << 22 && T_len <= 0x7fffffff - 1023 &&
+    return batch <= 65535 && (int64_t)n_q * (a.hq / a.hkv) <= 65535LL * 64 && T_len <= 0x7fffffff - 1023 &&
            a.hkv <= 1 << 20 && num_slots < 0x7fffffffLL / a.hkv;
 }
 

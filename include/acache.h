@@ -582,7 +582,7 @@ ACACHE_API int acache_rotate_store_q8(const acache_attn_desc* a, const acache_ro
  * its lengths, skips and flags are those of acache_slot_attention_varlen_q8.
  * Tensor cores: bf16 (head dim 64 and 128) with a positive scale; otherwise CUDA cores.
  * Limits: B <= 65,535, pools below 2^31 rows (slots x heads), T <= 2^31 - 1024,
- * n_q * Hq / Hkv < 2^22; more is ACACHE_ERR_INVALID_ARG.
+ * n_q * Hq / Hkv <= 65,535 * 64; more is ACACHE_ERR_INVALID_ARG.
  * Roundings: logits, maxima, sums and O are float32 (exponentials to 2^-22, a capped
  * score to 2^-22 of the cap, or from a cap of 512 on to 2^-20 of itself); in a bf16 call the weights are rounded to bf16 before the product with V, not in
  * their sum.

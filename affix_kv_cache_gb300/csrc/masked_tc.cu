@@ -12,7 +12,7 @@
 //              into registers, capped, biased, masked, exponentiated in base 2 against a reference that
 //              follows the sums of weights, and written back over the scores as bf16 for the product with V.
 //   warp 8     issues the MMAs of both (S = Q K^T from shared memory, O += P V with P from TMEM), A's and B's in turn
-//   warps 10-19  TMA producers of a 3-stage K ring and a 2-stage V ring: a tile of 128 consecutive slots is tiled
+//   warps 10-15  TMA producers of a 3-stage K ring and a 2-stage V ring: a tile of 128 consecutive slots is tiled
 //              box loads of the pool, any other gather4 loads of four rows each.
 // A block left with one Q tile splits its keys between the two chains and merges them at the end.
 // The CTA streams only keys from the first that one of its rows sees to the last: the window [min lo, max hi),
@@ -22,13 +22,15 @@
 // the product with V: a row whose output is not finite while its sum of weights is, is computed again by its
 // warp over its own keys alone.
 //
-// Measured (2,070 MHz): causal prompts of 2 x 4,096 (32 heads over 8, d = 128) 249 us, 1,100 TFLOP/s over the keys that rows see;
-// block-causal capped point of 16 x 986 rows over 2,624 keys (28 over 4) 524 us, 925 TFLOP/s.  A step of both chains takes 3,600
-// cycles (capped: 4,300) where its MMAs need 2,150: the MMAs of a chain wait for barriers some 700 cycles a tile, a capped
-// softmax (2,700 cycles, two of them at a time) for issue.  Set-up, the first tile's loads and the epilogue take 14,000 cycles of a
-// CTA's 60,000.  What was tried: two issuing warps (their MMAs interleave and both chains end together), waits
-// merged or tested ahead (slower by 2 to 9 %), polling instead of suspended waits (7 to 9 %), chains that take turns (no
-// difference, or 8 % slower).
+// Measured: causal prompts of 2 x 4,096 (32 heads over 8, d = 128) 241 us, 1,140 TFLOP/s over the keys that rows see;
+// block-causal capped point of 16 x 986 rows over 2,624 keys (28 over 4) 502 us, 970 TFLOP/s.  A step of both chains takes
+// some 3,500 cycles (capped: 4,100) where its MMAs need 2,150: the MMAs of a chain wait for barriers some 700 cycles a
+// tile, a capped softmax (2,700 cycles, two of them at a time) for issue.  Set-up, the first tile's loads and the
+// epilogue take 14,000 cycles of a CTA's 60,000.  What was tried: two issuing warps (their MMAs interleave and both chains
+// end together), waits merged or tested ahead (slower by 2 to 9 %), polling instead of suspended waits (7 to 9 %), chains
+// that take turns (no difference, or 8 % slower), CTAs that stay and take block after block, the next one's Q and
+// K loaded under the last's epilogue (uncapped 1 % faster, capped 14 % slower: the store of rows straight to memory and
+// a longer loop ate what it hid).
 //
 // Every mbarrier wait is bounded (acache_wait_budget); a wait that gives up raises a CTA-wide abort flag and
 // ACACHE_DEV_TIMEOUT, roles leave their loops, MMAs and loads in flight are waited for (bounded), and TMEM is
@@ -54,10 +56,11 @@ constexpr int kBM = 128;                    // rows of a Q tile
 constexpr int kQT = 2;                      // Q tiles to a CTA
 constexpr int kBN = 128;                    // keys of a tile
 constexpr int kKStages = 3, kVStages = 2;
-constexpr int kMmaWarp = 8, kProdWarp = 10, kProdPerRing = 5;
+constexpr int kMmaWarp = 8, kProdWarp = 10, kProdPerRing = 3;
 constexpr int kThreads = (kProdWarp + 2 * kProdPerRing) * 32;
-// Registers: 640 threads x 96 at launch; the softmax warpgroups grow to 168, the others shrink to 48
-constexpr int kRegLaunch = 65536 / kThreads / 8 * 8, kRegSoftmax = 168, kRegOther = 48;
+// Registers: 512 threads x 128 at launch; the softmax warpgroups grow to 208, which hold a tile's scores without spilling,
+// the others shrink to 48.  (640 threads leave them 168: 3 to 7 % slower.)
+constexpr int kRegLaunch = 65536 / kThreads / 8 * 8, kRegSoftmax = 208, kRegOther = 48;
 static_assert(2 * 128 * kRegSoftmax + (kThreads - 256) * kRegOther <= kThreads * kRegLaunch, "register split");
 constexpr uint32_t kRegion = kBN * 128;     // 64 columns of a 128-row tile
 __host__ __device__ constexpr uint32_t tile_bytes(int D) { return (uint32_t)(D / 64) * kRegion; }
@@ -245,6 +248,13 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 else tma_load_4d(sQ(t) + x * kRegion, &p.tm_q, 64 * x, hk * p.g, q0 + t * qpt, b, &ctl.q_full);
             }
     }
+    // Rows of a Q tile that no (query, head) pair fills are zeros: scores out of what lay there could send their warp the
+    // long ways through a cap or a raised reference (measured: an otherwise equal call took 720 us for 574).
+    const int n_fill = (kBM - qpt * p.g) * 8;              // 16-byte pieces of a region
+    for (int x = threadIdx.x; x < kQT * kHalves * n_fill; x += kThreads)
+        *reinterpret_cast<uint4*>(dsm + (base - smem_u32(dsm)) + (x / n_fill) * kRegion + qpt * p.g * 128 + (x % n_fill) * 16) =
+            make_uint4(0, 0, 0, 0);
+    if (n_fill > 0) fence_proxy_async_smem();
     if (warp == kMmaWarp) {
         tmem_alloc(&ctl.tmem_base, kTmemCols);
         tmem_relinquish();

@@ -33,7 +33,8 @@ constexpr float kNone = -3.402823466e38f;   // maximum before any logit (lowest 
 constexpr float kLowest = -200.f;           // d from here on down is a weight of zero
 constexpr float kHead = 6.f, kFloor = 300.f;   // log2 units: how far a logit may pass the reference; where a floor under it lies
 constexpr int kBatch = 4;                   // pieces in flight
-constexpr int kCtas = 6;                    // CTAs of 256 threads to an SM
+// CTAs to an SM: 1,536 threads (40 registers), at most 32 CTAs
+constexpr int ctas(int nt) { return nt >= 48 ? 1536 / nt : 32; }
 
 struct ScoreParams {
     const void* logits;
@@ -163,7 +164,7 @@ ACACHE_DEVFN Stat moved(const Stat& b, float m, float to_log2) {
 template <int NT>
 struct Smem {
     alignas(16) float val[NT];              // a thread's best
-    alignas(16) float group[NT / 2];
+    alignas(16) float group[NT];
     uint64_t list[kList];
     uint64_t best[kMaxK];                   // of this CTA, in order; 0 behind the last
     int cand[NT];
@@ -180,12 +181,13 @@ ACACHE_DEVFN uint64_t ld_cluster_u64(uint32_t addr) {
     return v;
 }
 
-// NT threads to a CTA, cs CTAs (a cluster) to a row.
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT, NT == 256 ? kCtas : 1)
+// NT threads to a CTA, cs CTAs (a cluster) to a row; candidates are bounded by kGroups groups of threads.
+template <typename T, int NT, int kGroups>
+__global__ void __launch_bounds__(NT, ctas(NT))
 scores_kernel(const ScoreParams p) {
     using W = Piece<T>;
-    constexpr int N = W::kN, kWarps = NT / 32, kGroups = NT == 32 ? 32 : NT / 2;
+    constexpr int N = W::kN, kWarps = NT / 32;
+    static_assert(kGroups == NT || kGroups == NT / 2);
     __shared__ Smem<NT> sm;
     const int64_t row = blockIdx.x / (unsigned)p.cs;
     const int cr = (int)(blockIdx.x % (unsigned)p.cs);
@@ -443,7 +445,7 @@ scores_kernel(const ScoreParams p) {
     }
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int kGroups = NT == 32 ? 32 : NT / 2>
 int launch(const ScoreParams& p, int64_t rows, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * p.cs));
@@ -456,7 +458,7 @@ int launch(const ScoreParams& p, int64_t rows, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cs > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, scores_kernel<T, NT>, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, scores_kernel<T, NT, kGroups>, p) != cudaSuccess) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
@@ -467,8 +469,15 @@ template <typename T>
 int dispatch(ScoreParams& p, int64_t rows, cudaStream_t stream) {
     const int64_t pieces = ((int64_t)p.vocab * sizeof(T) + 15) / 16;
     p.cs = 1;
+    // A row's phases behind its loads (sums, candidates, their order) wait, so that CTAs of fewer threads, more of them to an
+    // SM, are the faster the shorter the rows -- where there are rows to fill the SMs with.  bf16, one alternative, us: 16,400 rows
+    // of 2,000: 40 of 64 threads, 58 of 128, 101 of 256; of 8,000: 74, 78, 117; of 16,000: 120, 113, 154; of 32,000: 214, 185, 223;
+    // 4,100 of 50,000: 121, 99, 97.  300 of 8,000: 13, 10.9.  With many alternatives 64 threads need 64 groups
+    // (20 of 2,000: 89, with 32 groups 103; one: 44, with 32 groups 40).
     if (pieces <= 128) return launch<T, 32>(p, rows, stream);
-    if (pieces <= 1024) return launch<T, 128>(p, rows, stream);
+    if (pieces <= 1024 && rows > (int64_t)ctas(128) * sm_count())
+        return p.k <= 8 ? launch<T, 64, 32>(p, rows, stream) : launch<T, 64, 64>(p, rows, stream);
+    if (pieces <= 1024 || (pieces <= 4096 && rows > (int64_t)ctas(256) * sm_count())) return launch<T, 128>(p, rows, stream);
     // rows that leave SMs idle are split over a cluster, in one wave and with four pieces a thread at least
     p.cs = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxCluster, 4LL * sm_count() / rows, pieces / (4 * 256)}));
     return launch<T, 256>(p, rows, stream);

@@ -558,6 +558,30 @@ def test_scores(dtype, V, R, k):
     _check_scores(x, min(k, V), seed=V)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("R,V", [(1900, 1100), (1900, 4003), (1900, 8190), (930, 8200), (930, 16385), (930, 32760)])
+@pytest.mark.parametrize("k", [0, 1, 8, 9, 32])
+def test_scores_of_many_short_rows(dtype, R, V, k):
+    """Enough rows to fill the SMs with small CTAs."""
+    V = V if dtype == BF16 else V // 2
+    g = torch.Generator().manual_seed(V + k)
+    few = (3 * torch.randn((24, V), generator=g)).to(dtype)
+    few[1] = (few[1] * 0.5).round()                       # many alike
+    few[2, 7:] = -INF
+    few[3] = 1.0
+    few[4, V - 60:] = 40.0
+    x = few.repeat((R + 23) // 24, 1)[:R]
+    lp, H, tt, tl, st = _score(x, torch.arange(R, dtype=torch.int32) % 7, k)
+    assert st == 0
+    wl, wh, order, tol, tol_h = token_scores(few, 1.0)
+    at = np.arange(R) % 24
+    _close(_np(lp), wl[at, np.arange(R) % 7], tol[at, np.arange(R) % 7], "given")
+    _close(_np(H), wh[at], tol_h[at], "entropy")
+    if k:
+        assert np.array_equal(tt.cpu().numpy(), order[at, :k])
+        _close(_np(tl), np.take_along_axis(wl, order[:, :k], 1)[at], np.take_along_axis(tol, order[:, :k], 1)[at], "alternatives")
+
+
 @pytest.mark.parametrize("temperature", [0.05, 0.7, 1.5, 40.0])
 def test_scores_with_a_temperature(temperature):
     g = torch.Generator().manual_seed(5)

@@ -150,10 +150,10 @@ def test_binding_refuses_rows_that_are_not_evenly_spaced():
     with pytest.raises(ValueError):
         ac.acache_token_scores(2, 4, torch.zeros(4, 2).T)
     # a slice of a wider projection is evenly spaced
-    qkv = torch.zeros(2, 3, 8, 128, dtype=torch.bfloat16)
+    qkv = torch.zeros(2, 5, 8, 128, dtype=torch.bfloat16)
     assert _lib._row_stride(qkv[:, :, :4], 4, 128) == 1024
     assert _lib._row_stride(qkv[:1, :1, :4], 4, 128) == 512           # a single row has no next one
-    assert _lib._row_stride(qkv[:, 1:2, :4], 4, 128) == 3072
+    assert _lib._row_stride(qkv[:, 1:2, :4], 4, 128) == 5120
 
 
 # ------------------------------------------------------------------------------------- rotary descriptors

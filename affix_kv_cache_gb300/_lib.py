@@ -561,7 +561,12 @@ def acache_token_scores(rows, vocab, logits, tokens=None, token_logprob=None, en
     if logits.dim() < 1 or (vocab > 1 and logits.stride(-1) != 1):
         raise ValueError("the logits of a row have to follow one another")
     dev = _current_device()
-    stride = vocab if logits.is_contiguous() else _row_stride(logits.unsqueeze(-2), 1, vocab)
+    if logits.is_contiguous():
+        stride = vocab
+    elif logits.dim() == 2:
+        stride = logits.stride(0) if logits.shape[0] > 1 else vocab
+    else:
+        stride = _row_stride(logits.unsqueeze(-2), 1, vocab)
     if k is None:
         k = 0 if top_tokens is None else top_tokens.shape[-1]
     st = lib().acache_token_scores(dtype, rows, vocab, _on(dev, logits), stride, temperature, _on(dev, tokens),

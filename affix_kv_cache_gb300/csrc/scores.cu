@@ -14,7 +14,7 @@
 // each by its best logit, is a bound that k elements reach, so only threads whose best reaches it are looked at again, a
 // warp to the pieces of one, for the elements that do; these -- few more than k -- are ranked by comparing all
 // with all.
-// Measured: 4,100 rows of 100,003 in bf16 149 us with 5 alternatives (0.81 of the copy bandwidth; 138 without, 200 with 32); 128 rows
+// Measured: 4,100 rows of 100,003 in bf16 146 us with 5 alternatives (0.82 of the copy bandwidth; 138 without, 200 with 32); 128 rows
 // of 126,464 13 us on the device (launch, two dependent loads, five barriers and a merge beside 5 us of
 // reading); one row of 32,000 in float32 with 20 alternatives 7.5 us.
 #include <algorithm>

@@ -14,7 +14,9 @@
 //   warp 8     issues the MMAs of both (S = Q K^T from shared memory, O += P V with P from TMEM), A's and B's in turn
 //   warps 10-15  TMA producers of a 3-stage K ring and a 2-stage V ring: a tile of 128 consecutive slots is tiled
 //              box loads of the pool, any other gather4 loads of four rows each.
-// A block left with one Q tile splits its keys between the two chains and merges them at the end.
+// A block left with one Q tile splits its keys between the two chains and merges them at the end.  Where blocks leave SMs idle, a
+// cluster of up to 8 CTAs shares a block's keys; each leaves its unnormalised sums, references and sums of weights in shared memory and
+// merges D / cs columns of all rows out of its peers'.
 // The CTA streams only keys from the first that one of its rows sees to the last: the window [min lo, max hi),
 // which need not start at a whole tile.  Inside it a row's range is a bit mask per 32 keys; tiles that every row of a warp sees
 // whole skip it.  Blocks run from the last to the first, so that a causal call starts its longest first.
@@ -56,6 +58,8 @@ constexpr int kBM = 128;                    // rows of a Q tile
 constexpr int kQT = 2;                      // Q tiles to a CTA
 constexpr int kBN = 128;                    // keys of a tile
 constexpr int kKStages = 3, kVStages = 2;
+constexpr float kAgain = -1.f;              // in place of a row's sum of weights
+constexpr int kMaxParts = 8;                // CTAs to a block (a portable cluster)
 constexpr int kMmaWarp = 8, kProdWarp = 10, kProdPerRing = 3;
 constexpr int kThreads = (kProdWarp + 2 * kProdPerRing) * 32;
 // Registers: 512 threads x 128 at launch; the softmax warpgroups grow to 208, which hold a tile's scores without spilling,
@@ -98,6 +102,7 @@ struct MaskParams {
     float cap_near;       // |q.k| of a score of half the cap ...
     float cap_k[4];       // ... up to which the capped score in log2 units is q.k times this polynomial in (q.k)^2
     long long budget;
+    int cs;               // CTAs (a cluster) to a block, each with a part of its window
 };
 
 struct MaskCtl {
@@ -112,6 +117,7 @@ struct MaskCtl {
     int unlanded;         // abort path: some load issued before the abort may not have landed
     int split_ok;
     int win_lo[8], win_hi[8];
+    float missing[8];             // (split clusters) by softmax warp: a wait gave up
     float split_m[kBM], split_l[kBM];
 };
 
@@ -156,14 +162,16 @@ ACACHE_DEVFN bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_f
     }
 }
 
+ACACHE_DEVFN void st_shared_f32(uint32_t addr, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
 // bits [max(n, 0), 32), none from 32 on (the instruction clamps its shift)
 ACACHE_DEVFN uint32_t bits_from(int n) {
     uint32_t r;
     asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(r) : "r"(max(n, 0)));
     return r;
 }
-// kCap: scores are capped; kBounded: by so little that they need no maximum (then there is no bias).
-template <int D, bool kCap, bool kBounded, bool kBias>
+// kCap: scores are capped; kBounded: by so little that they need no maximum (then there is no bias); kParts: a
+// cluster of CTAs shares a block's keys.
+template <int D, bool kCap, bool kBounded, bool kBias, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
 masked_tc_kernel(const __grid_constant__ MaskParams p) {
     constexpr uint32_t kTileBytes = tile_bytes(D);
@@ -174,7 +182,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
     auto sQ = [&](int t) { return base + kTileBytes * (uint32_t)t; };
     auto sK = [&](int s) { return base + kTileBytes * (uint32_t)(kQT + s); };
     auto sV = [&](int s) { return base + kTileBytes * (uint32_t)(kQT + kKStages + s); };
-    const int hk = (int)blockIdx.x, b = (int)blockIdx.y, qb = (int)(gridDim.z - 1 - blockIdx.z);
+    const int hk = kParts ? (int)blockIdx.x / p.cs : (int)blockIdx.x, rank = kParts ? (int)blockIdx.x % p.cs : 0, b = (int)blockIdx.y, qb = (int)(gridDim.z - 1 - blockIdx.z);
     int n_rows = p.n_rows, T_len = p.T_len;
     int64_t qbase = (int64_t)b * p.n_rows, kbase = (int64_t)b * p.T_len;
     if (p.q_start) {
@@ -270,13 +278,22 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
         w_hi = max(w_hi, ctl.win_hi[x]);
     }
     if (w_lo > w_hi) w_lo = w_hi = 0;
-    const int T_win = w_hi - w_lo;
+    int T_win = w_hi - w_lo;
+    if constexpr (kParts) {                            // ... or this CTA's part of them, whole tiles
+        const int n_all = (T_win + kBN - 1) / kBN, j0 = n_all * rank / p.cs, j1 = n_all * (rank + 1) / p.cs;
+        w_lo += j0 * kBN;
+        T_win = max(min(T_win - j0 * kBN, (j1 - j0) * kBN), 0);
+    }
     const int n_kv = (T_win + kBN - 1) / kBN;
     const int32_t* rs = p.read_slot + kbase + w_lo;
     const bool split = n_qt == 1 && n_kv >= 2;
     const int n_ch = split ? 2 : n_qt;
     const KeySchedule ks{split, n_kv, split ? (n_kv + 1) / 2 : n_kv};
     const int n_vst = split ? kVStages + 1 : kVStages;
+    // (split clusters) what a CTA leaves of its part: sums in sK(0), sK(1) / sV(0), sV(1), [column / 4][row] of 4; m and l in sK(2)
+    auto part_o = [&](int t) { return t == 0 ? sK(0) : sV(0); };
+    auto part_m = [&](int t) { return sK(2) + 1024u * (uint32_t)t; };
+    auto part_l = [&](int t) { return sK(2) + 1024u * (uint32_t)t + 512u; };
     auto sVs = [&](int s) { return s < kVStages ? sV(s) : sQ(1); };
     const uint32_t tmem = ctl.tmem_base;
 
@@ -438,6 +455,10 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 mbar_wait(&ctl.fin, 0, kDrainBudget);
             }
             __syncwarp();
+        }
+        if constexpr (kParts) {
+            cluster_sync();
+            cluster_sync();
         }
     } else {
         setmaxnreg_inc<kRegSoftmax>();
@@ -668,6 +689,44 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                 m_used = m;
             }
         }
+        if constexpr (kParts) {
+            // A part of the keys: the sums of weighted V as they are, the reference and the sum of weights (kAgain: the row has to
+            // be computed again) into shared memory, where K and V were once every MMA is done.
+            if (ok && n_kv > 0 && n_ch == 2) ok = __all_sync(0xffffffffu, wait_bar(&ctl.drain[1 - t], 0, abort_flag, dev_status, budget));
+            if (!split || t == 0) {
+                bool bad = lost;
+                if (ok && n_kv > 0) {
+                    tc_fence_after();
+                    float chk = 0.f;
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(lane_base + col_o(t) + cc * 32, o);
+                        tmem_ld_wait();
+                        if (split) {
+                            uint32_t ob[32];
+                            tmem_ld32(lane_base + col_o(1) + cc * 32, ob);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                o[x] = __float_as_uint(fmaf(__uint_as_float(o[x]), w_a, __uint_as_float(ob[x]) * w_b));
+                        }
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) chk = fmaf(__uint_as_float(o[x]), 0.f, chk);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            st_shared_v4(part_o(t) + (uint32_t)((8 * cc + x) * kBM + r) * 16u, o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    }
+                    bad = bad || (chk != chk && l_sum == l_sum);
+                }
+                const bool sees = m_used != -INFINITY && mine;
+                if (ok) {                              // (then no load is in flight either)
+                    st_shared_f32(part_m(t) + 4u * r, sees ? m_used : -INFINITY);
+                    st_shared_f32(part_l(t) + 4u * r, !sees ? 0.f : bad ? kAgain : l_sum);
+                }
+                if (lane == 0) ctl.missing[warp] = ok ? 0.f : 1.f;
+            }
+        } else {
         const bool writer = !split || t == 0;
         const uint32_t stage = sQ(t);
         bool fix = false;
@@ -745,6 +804,75 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             }
         }
         }
+        }
+        if constexpr (kParts) {
+            // ---- the rows from their parts: each CTA of the cluster merges D / cs columns of all of them
+            cluster_sync();
+            if (wg < n_qt) {
+                const int t = wg, r = threadIdx.x & 127;
+                int lo, hi;
+                const bool mine = row_keys(t, r, lo, hi);
+                float w[kMaxParts], m = -INFINITY, l = 0.f;
+                bool again = false, missing = false;
+#pragma unroll
+                for (int c = 0; c < kMaxParts; ++c) {
+                    w[c] = c < p.cs ? ld_cluster_f32(mapa_shared(part_m(t) + 4u * r, (uint32_t)c)) : -INFINITY;
+                    m = fmaxf(m, w[c]);
+                }
+#pragma unroll
+                for (int c = 0; c < kMaxParts; ++c) {
+                    const float lc = c < p.cs ? ld_cluster_f32(mapa_shared(part_l(t) + 4u * r, (uint32_t)c)) : 0.f;
+                    // (a part in which the row sees no key, and a part that is none: no weight, and its sums are not looked at)
+                    w[c] = w[c] == -INFINITY ? 0.f : fast_exp2(w[c] - m);
+                    again = again || lc == kAgain;
+                    // (a wait gave up: the row stays unwritten)
+                    missing = missing || (c < p.cs && ld_cluster_f32(mapa_shared(smem_u32(&ctl.missing[warp]), (uint32_t)c)) != 0.f);
+                    l = fmaf(w[c], lc, l);
+                }
+                const bool none = m == -INFINITY;
+                const float inv_l = 1.f / l;
+                const int per = D / p.cs;
+                const int64_t row_at = ((qbase + q0 + t * qpt + r / p.g) * p.Hq + hk * p.g + r % p.g) * D;
+                for (int x = rank * per; x < (rank + 1) * per; x += 8) {
+                    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < kMaxParts; ++c) {
+                        if (c >= p.cs) continue;
+                        const uint32_t from = mapa_shared(part_o(t) + (uint32_t)((x >> 2) * kBM + r) * 16u, (uint32_t)c);
+                        const float4 u = ld_cluster_v4(from), v = ld_cluster_v4(from + kBM * 16u);
+                        if (w[c] > 0.f) {
+                            y[0] = fmaf(w[c], u.x, y[0]), y[1] = fmaf(w[c], u.y, y[1]), y[2] = fmaf(w[c], u.z, y[2]), y[3] = fmaf(w[c], u.w, y[3]);
+                            y[4] = fmaf(w[c], v.x, y[4]), y[5] = fmaf(w[c], v.y, y[5]), y[6] = fmaf(w[c], v.z, y[6]), y[7] = fmaf(w[c], v.w, y[7]);
+                        }
+                    }
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        __nv_bfloat162 two = __floats2bfloat162_rn(none ? 0.f : y[2 * e] * inv_l, none ? 0.f : y[2 * e + 1] * inv_l);
+                        o[e] = *reinterpret_cast<uint32_t*>(&two);
+                    }
+                    if (mine && !again && !missing) *reinterpret_cast<uint4*>(p.out + row_at + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                if (rank == 0) {
+                    float slope = 0.f;
+                    int64_t pos = 0;
+                    if (kBias && mine) {
+                        slope = p.slopes[hk * p.g + r % p.g] * kLog2e;
+                        pos = p.q_pos[qbase + q0 + t * qpt + r / p.g];
+                    }
+                    __syncwarp();
+                    for (uint32_t todo = __ballot_sync(0xffffffffu, mine && again && !missing); todo; todo &= todo - 1) {
+                        const int l0 = __ffs(todo) - 1;
+                        const int64_t at = __shfl_sync(0xffffffffu, row_at, l0);
+                        masked_row<bf16, D>(MaskedPool<bf16>{p.k_cache, p.v_cache, p.read_slot + kbase, p.num_slots, p.Hkv, p.drop, p.wide != 0,
+                                                             p.scale_log2, kCap ? p.cap_in : 0.f, p.cap_log2, 0.f},
+                                      p.q + at, p.out + at, __shfl_sync(0xffffffffu, lo, l0), __shfl_sync(0xffffffffu, hi, l0), hk,
+                                      __shfl_sync(0xffffffffu, slope, l0), __shfl_sync(0xffffffffu, pos, l0), lane);
+                    }
+                }
+            }
+            cluster_sync();                            // no CTA leaves while another reads its shared memory
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -757,9 +885,9 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kCap, bool kBounded, bool kBias>
+template <int D, bool kCap, bool kBounded, bool kBias, bool kParts>
 int launch(const MaskParams& prm, dim3 grid, cudaStream_t stream) {
-    auto kern = masked_tc_kernel<D, kCap, kBounded, kBias>;
+    auto kern = masked_tc_kernel<D, kCap, kBounded, kBias, kParts>;
     static std::atomic<int> prepared[64];             // per device: the launch is allowed for
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
@@ -776,15 +904,62 @@ int launch(const MaskParams& prm, dim3 grid, cudaStream_t stream) {
         if (fa.numRegs < kRegLaunch) return ACACHE_ERR_UNSUPPORTED;   // the register split assumes the launch allocation
         prepared[dev].store(1, std::memory_order_release);
     }
-    kern<<<grid, kThreads, smem_bytes(D), stream>>>(prm);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes(D);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)prm.cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kParts ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, prm) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ACACHE_ERR_CUDA;
+    }
     return launch_status();
 }
 
-template <int D>
+// Clusters of `cs` CTAs that the current device holds at once (0: unknown); every form of the kernel takes an SM to a CTA.
+int clusters_at_once(int cs) {
+    static std::atomic<int> known[64][kMaxParts + 1];  // 1 + the number
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    int n = known[dev][cs].load(std::memory_order_relaxed);
+    if (n == 0) {
+        auto kern = masked_tc_kernel<128, false, false, false, true>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)cs);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem_bytes(128);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)cs;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(128)) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        known[dev][cs].store(++n, std::memory_order_relaxed);
+    }
+    return n - 1;
+}
+
+template <int D, bool kParts>
 int dispatch(const MaskParams& prm, bool cap, bool bounded, bool bias, dim3 grid, cudaStream_t stream) {
-    if (cap && bias) return launch<D, true, false, true>(prm, grid, stream);
-    if (cap) return bounded ? launch<D, true, true, false>(prm, grid, stream) : launch<D, true, false, false>(prm, grid, stream);
-    return bias ? launch<D, false, false, true>(prm, grid, stream) : launch<D, false, false, false>(prm, grid, stream);
+    if (cap && bias) return launch<D, true, false, true, kParts>(prm, grid, stream);
+    if (cap) return bounded ? launch<D, true, true, false, kParts>(prm, grid, stream) : launch<D, true, false, false, kParts>(prm, grid, stream);
+    return bias ? launch<D, false, false, true, kParts>(prm, grid, stream) : launch<D, false, false, false, kParts>(prm, grid, stream);
 }
 
 }  // namespace
@@ -844,10 +1019,20 @@ int launch_masked_tc(const MaskedAttn& c) {
         }
     }
     prm.budget = wait_budget();
-    const dim3 grid((unsigned)c.a.hkv, (unsigned)c.B, (unsigned)n_qb);
+    // Blocks that leave SMs idle are split over clusters, as many as run at once, with more than two and a half tiles of keys to
+    // a CTA.  us, 28 heads over 4, 32 rows, causal over 3,260 keys: 3 requests 58 whole, 29 in 8 parts; 16 requests 60, 48
+    // in 2.  33 rows of 8 heads over 1, 8,000 keys: 115, 33 in 8.  A merge takes some 5 us: 64 rows over 1,408 keys 31, 29 in 2,
+    // 23 in 4; 200 rows over 600 keys 21, 23 in 2.
+    const int64_t blocks = n_qb * c.B * c.a.hkv, tiles = (c.T_len + kBN - 1) / kBN;
+    prm.cs = 1;
+    for (int cs = 2; cs <= kMaxParts && 5LL * cs < 2 * tiles && cs * blocks <= sm_count(); cs *= 2)
+        if (blocks <= clusters_at_once(cs)) prm.cs = cs;
+    const dim3 grid((unsigned)(c.a.hkv * prm.cs), (unsigned)c.B, (unsigned)n_qb);
     const bool bias = c.mask.slopes != nullptr;
     const bool bounded = cap && !bias && c.mask.softcap <= kBoundedCap;
-    return d == 64 ? dispatch<64>(prm, cap, bounded, bias, grid, c.stream) : dispatch<128>(prm, cap, bounded, bias, grid, c.stream);
+    if (prm.cs > 1)
+        return d == 64 ? dispatch<64, true>(prm, cap, bounded, bias, grid, c.stream) : dispatch<128, true>(prm, cap, bounded, bias, grid, c.stream);
+    return d == 64 ? dispatch<64, false>(prm, cap, bounded, bias, grid, c.stream) : dispatch<128, false>(prm, cap, bounded, bias, grid, c.stream);
 }
 
 }  // namespace acache

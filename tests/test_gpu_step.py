@@ -358,6 +358,88 @@ def test_masked_attention_with_a_scale_that_is_not_positive(n, scale):
     _attend_case(BF16, 4, 2, 128, 1, n, 160, "causal", cap=3.0, scale=scale, seed=4)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(7, 1, 128), (4, 2, 64)])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,n,T", [(1, 40, 700), (3, 60, 1500), (1, 33, 2700), (2, 150, 2600)])
+def test_masked_attention_of_few_blocks_over_many_keys(hq, hkv, d, kind, B, n, T):
+    """Blocks that a cluster of 2, 4 or 8 CTAs shares, each with a part of the keys; some parts hold none of a row's."""
+    _attend_case(BF16, hq, hkv, d, B, n, T, kind, seed=B)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(7, 1, 128), (16, 2, 64)])
+@pytest.mark.parametrize("kind", ["causal", "any"])
+@pytest.mark.parametrize("cap,bias,drop", [(1.5, False, False), (0.0, True, False), (80.0, True, True), (700.0, False, True)])
+@pytest.mark.parametrize("n,T", [(37, 900), (70, 2700)])
+def test_masked_attention_of_few_blocks_caps_biases_and_discarded_keys(hq, hkv, d, kind, cap, bias, drop, n, T):
+    _attend_case(BF16, hq, hkv, d, 1, n, T, kind, cap=cap, bias=bias, drop=drop, seed=5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [700, 2700])
+def test_what_one_row_sees_does_not_reach_its_neighbours_over_many_keys(d, T):
+    """NaN and infinities in keys and values of some parts of a block's keys, which some rows see and others do not."""
+    g = torch.Generator().manual_seed(T)
+    hq, hkv, n = 4, 2, 100
+    q = torch.randn((1, n, hq, d), generator=g).to(BF16)
+    kp, vp = (torch.randn((T, hkv, d), generator=g).to(BF16) for _ in range(2))
+    rs = torch.randperm(T, generator=g).to(torch.int32)[None]
+    kp[rs[0, T - 2], 0, 3] = NAN
+    vp[rs[0, T - 1], 1, 5] = INF
+    vp[rs[0, 40], 0, 7] = NAN
+    kp[rs[0, 41], 1] = INF
+    vp[rs[0, T // 2], :, 9] = -INF
+    lo, hi = torch.zeros(n, dtype=torch.int32), torch.full((n,), T, dtype=torch.int32)
+    hi[::2] = T - 2
+    lo[::3] = 42
+    hi[1::5] = T // 2
+    lo[n // 2] = hi[n // 2] = 10
+    out, st = torch.empty((1, n, hq, d), dtype=BF16, device="cuda"), _status()
+    ac.acache_slot_attention_masked(_desc(hq, hkv, d, BF16), 1, n, dev(q), T, dev(rs), dev(kp), dev(vp), T, out,
+                                    row_range=dev(torch.stack((lo, hi), -1)[None]), dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    want, tol = masked_attention(q[0], rs[0].numpy(), kp, vp, d ** -0.5, lo, hi)
+    assert np.isnan(want).any() and (want[n // 2] == 0).all()
+    got = _np(out[0])
+    fine = np.isfinite(want)
+    assert np.array_equal(np.isfinite(got), fine)
+    assert (np.abs(got[fine] - want[fine]) - tol[fine]).max(initial=0.0) <= 0
+
+
+@pytest.mark.parametrize("n,cap", [(40, 0.0), (200, 30.0)])
+def test_masked_waits_of_shared_blocks_that_run_out(n, cap):
+    """One request whose blocks are shared by clusters: no row is written that lacks a part."""
+    g = torch.Generator().manual_seed(n)
+    hq, hkv, d, T = 8, 1, 128, 2700
+    q = torch.randn((1, n, hq, d), generator=g).to(BF16)
+    kp, vp = (torch.randn((T, hkv, d), generator=g).to(BF16) for _ in range(2))
+    args = (_desc(hq, hkv, d, BF16), 1, n, dev(q), T, dev(torch.randperm(T, generator=g).to(torch.int32)[None]), dev(kp), dev(vp), T)
+
+    def call():
+        out, st = torch.full((1, n, hq, d), 7.0, dtype=BF16, device="cuda"), _status()
+        ac.acache_slot_attention_masked(*args, out, softcap=cap, dev_status=st)
+        torch.cuda.synchronize()
+        return out, st.item()
+
+    want, st = call()
+    assert st == 0
+    timed_out = 0
+    for budget in (1, 300, 1000, 2000, 4000, 8000):
+        prev = ac.acache_wait_budget(budget)
+        try:
+            out, st = call()
+        finally:
+            ac.acache_wait_budget(prev)
+        assert st in (0, _lib.DEV_TIMEOUT)
+        timed_out += st != 0
+        same = (out == want).all(-1)
+        assert (same | (out == 7.0).all(-1)).all()
+        assert st != 0 or same.all()
+    assert timed_out
+    out, st = call()
+    assert st == 0 and torch.equal(out, want)
+
+
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 128)])
 @pytest.mark.parametrize("n", [1, 5, 100, 300])
 def test_what_one_row_sees_does_not_reach_its_neighbours(dtype, d, n):

@@ -108,11 +108,13 @@ template <> struct Piece<__nv_bfloat16> {
         return fmaxf(__low2float(m[0]), __high2float(m[0]));
     }
     // Elements e, e + 1, raised to a floor below which a weight is zero all the same: two to an instruction.  The floor
-    // lies kFloor in log2 units below the reference, and by more than its rounding; 0: there is no such bf16 value.
+    // lies kFloor in log2 units below the reference, and by more than its rounding, at most 1.01 gap + |m| / 42; 0: there
+    // is no such bf16 value, or its distance in log2 units (|m| / 42 of kFloor / gap) might leave float32, and a weight
+    // of zero times that in the entropy's sum were NaN.
     using Floor = uint32_t;
     ACACHE_DEVFN static Floor floor_of(float m, float gap) {
         const float f = m - gap - fabsf(m) * 0.015625f;
-        if (!(f > -3.3e38f)) return 0u;
+        if (!(f > -3.3e38f) || fabsf(m) > gap * 1e36f) return 0u;
         const uint32_t u = __float_as_uint(f) >> 16;         // (cut: a little more for negative ones, less for others)
         return u | u << 16;
     }
@@ -246,7 +248,7 @@ scores_kernel(const ScoreParams p) {
             if (i + u * NT < z) w[u] = __ldg(w0 + i + u * NT);
         }
         if (note(W::top(w))) floor = W::floor_of(st.m, p.floor_gap);
-        if (!W::bounds(floor)) {            // (a maximum near the lowest value)
+        if (!W::bounds(floor)) {            // (a maximum near the lowest value, or far beyond the temperature)
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
                 if (i + u * NT < z) add(w[u]);

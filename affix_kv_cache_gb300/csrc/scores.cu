@@ -43,7 +43,10 @@ struct ScoreParams {
     float *token_logprob, *entropy, *top_logprob;
     int32_t *top_tokens, *dev_status;
     int vocab, k, cs;
-    float to_log2, to_ln;                   // log2e / temperature, 1 / temperature
+    float to_log2;                          // log2e / temperature
+    float half, far_log2, far_ln;           // differences of any two logits: taken of their halves (half = 1/2) where the
+                                            // temperature is above 1, as the quotient can be a number where the difference
+                                            // is not; log2e / temperature and 1 / temperature over `half`
     float head, floor_gap;                  // kHead and kFloor in logits
 };
 
@@ -70,10 +73,11 @@ template <> struct Piece<float> {
         for (int u = 1; u < B; ++u) m = fmaxf(m, top(w[u]));
         return m;
     }
-    // Elements e, e + 1; weights' exponents are bounded from below one by one.
-    struct Floor {};
-    ACACHE_DEVFN static Floor floor_of(float, float) { return {}; }
-    ACACHE_DEVFN static bool bounds(Floor) { return true; }
+    // Elements e, e + 1; weights' exponents are bounded from below one by one.  A floor only tells whether differences from
+    // the reference m stay float32 where they count.
+    using Floor = bool;
+    ACACHE_DEVFN static Floor floor_of(float m, float gap) { return m - gap > -3.3e38f; }
+    ACACHE_DEVFN static bool bounds(Floor f) { return f; }
     ACACHE_DEVFN static uint64_t pair(const uint4& w, int e, Floor) { return f2pack(at(w, e), at(w, e + 1)); }
     ACACHE_DEVFN static void bound(float& a, float& b) {
         a = max_nan(a, kLowest);
@@ -157,8 +161,8 @@ struct Stat {
     float m, s, u;
 };
 // `b` brought to the maximum m (>= b.m)
-ACACHE_DEVFN Stat moved(const Stat& b, float m, float to_log2) {
-    const float dd = max_nan((b.m - m) * to_log2, kLowest);
+ACACHE_DEVFN Stat moved(const Stat& b, float m, const ScoreParams& p) {
+    const float dd = max_nan(fmaf(b.m, p.half, -m * p.half) * p.far_log2, kLowest);
     const float a = fast_exp2(dd);
     return Stat{m, b.s * a, (b.u + b.s * dd) * a};
 }
@@ -219,7 +223,7 @@ scores_kernel(const ScoreParams p) {
     auto note = [&](float m) -> bool {
         best = fmaxf(best, m);
         const bool up = m > st.m + p.head;
-        if (up) st = moved(st, m, p.to_log2);
+        if (up) st = moved(st, m, p);
         return up;
     };
     // One piece, or what there is of it, with every weight's exponent bounded from below on its own.
@@ -227,7 +231,7 @@ scores_kernel(const ScoreParams p) {
         note(W::top(w));
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const float d = max_nan((W::at(w, e) - st.m) * p.to_log2, kLowest), q = fast_exp2(d);
+            const float d = max_nan(fmaf(W::at(w, e), p.half, -st.m * p.half) * p.far_log2, kLowest), q = fast_exp2(d);
             st.s += q;
             st.u = fmaf(q, d, st.u);
         }
@@ -248,7 +252,8 @@ scores_kernel(const ScoreParams p) {
             if (i + u * NT < z) w[u] = __ldg(w0 + i + u * NT);
         }
         if (note(W::top(w))) floor = W::floor_of(st.m, p.floor_gap);
-        if (!W::bounds(floor)) {            // (a maximum near the lowest value, or far beyond the temperature)
+        if (!W::bounds(floor)) {            // (a maximum near the lowest value, or far beyond the temperature, or next to
+                                            // nothing beside it)
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
                 if (i + u * NT < z) add(w[u]);
@@ -278,7 +283,7 @@ scores_kernel(const ScoreParams p) {
     // ---- the CTA's maximum, S and U
     {
         float m = warp_max(st.m);
-        Stat t = moved(st, m, p.to_log2);
+        Stat t = moved(st, m, p);
         t.s = warp_sum(t.s);
         t.u = warp_sum(t.u);
         if (lane == 0) sm.part[warp] = t;
@@ -293,7 +298,7 @@ scores_kernel(const ScoreParams p) {
     if (warp == 0) {
         Stat t = lane < kWarps ? sm.part[lane] : Stat{kNone, 0.f, 0.f};
         const float m = warp_max(t.m);
-        t = moved(t, m, p.to_log2);
+        t = moved(t, m, p);
         t.s = warp_sum(t.s);
         t.u = warp_sum(t.u);
         if (lane == 0) sm.stat = Stat{m, t.s, t.u};
@@ -414,7 +419,7 @@ scores_kernel(const ScoreParams p) {
                 t = Stat{ptx::ld_cluster_f32(a), ptx::ld_cluster_f32(a + 4), ptx::ld_cluster_f32(a + 8)};
             }
             const float m = warp_max(t.m);
-            t = moved(t, m, p.to_log2);
+            t = moved(t, m, p);
             all = Stat{m, warp_sum(t.s), warp_sum(t.u)};
             __syncthreads();
             for (int a = tid; a < p.cs * p.k; a += NT) {
@@ -431,7 +436,7 @@ scores_kernel(const ScoreParams p) {
     }
     if (warp != 0) return;
     const float ln_s = logf(all.s);
-    auto logprob = [&](float v) { return (v - all.m) * p.to_ln - ln_s; };
+    auto logprob = [&](float v) { return fmaf(v, p.half, -all.m * p.half) * p.far_ln - ln_s; };
     if (lane == 0) {
         if (all.s != all.s) flag(p.dev_status, ACACHE_DEV_NAN);
         if (p.entropy) p.entropy[row] = ln_s - 0.693147180559945f * (all.u / all.s);
@@ -500,7 +505,9 @@ int launch_token_scores(const ScoreCall& c) {
     p.vocab = c.vocab;
     p.k = c.k;
     p.to_log2 = kLog2e / c.temperature;
-    p.to_ln = 1.f / c.temperature;
+    p.half = c.temperature > 1.f ? 0.5f : 1.f;
+    p.far_log2 = (float)((double)kLog2e / c.temperature / p.half);
+    p.far_ln = (float)(1.0 / c.temperature / p.half);
     p.head = kHead / p.to_log2;
     p.floor_gap = kFloor / p.to_log2;
     return c.dtype == ACACHE_F32 ? dispatch<float>(p, c.rows, c.stream) : dispatch<__nv_bfloat16>(p, c.rows, c.stream);

@@ -61,3 +61,17 @@ def test_scores_of_logits_far_from_the_temperature(dtype, V, top, temperature):
         x[r, at[r, :1 + r % 3]] = top
     x[4, V // 2 + 1:] = -INF
     _check_extreme(x, min(3, V), temperature)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [8, 13, 1003, 5000, 70001])
+@pytest.mark.parametrize("temperature", [3e37, 1e38, 3.4e38])
+def test_scores_of_logits_whose_differences_leave_float32(dtype, V, temperature):
+    """Logits at both ends of float32 over a temperature of their size: the differences divided by it are small numbers."""
+    g = torch.Generator().manual_seed(V)
+    x = (torch.rand((5, V), generator=g) * 2 - 1) * 3.3e38
+    x[1] = x[1].abs() * -1.0
+    x[1, V // 2] = 3.3e38                                # one far above the others
+    x[2, ::2] = -INF
+    x[3] = torch.where(x[3] > 0, 3.3e38, -3.3e38)
+    _check_extreme(x.to(dtype), min(5, V), temperature)

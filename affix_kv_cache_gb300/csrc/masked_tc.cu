@@ -80,6 +80,10 @@ constexpr float kBoundedCap = 50.f;
 constexpr double kTanhHalf[4] = {1, -0.33328159, 0.1320536, -0.04475064};
 constexpr long long kDrainBudget = 1LL << 31, kLandBudget = 1LL << 21;   // cycles: the abort path's own waits
 
+// Log2 units by which partial sums are scaled down where they are joined: each may lie close below 2^128 (a last tile
+// whose scores jump by 100 and more raises no reference), and up to 16 of them are added.
+constexpr float kSpare = 8.f;
+
 struct MaskParams {
     CUtensorMap tm_q;     // fixed: 4-D [B][n_q][Hq][d], box {64, g, qpt, 1}; ragged: 3-D [total_q][Hq][d], box {64, g, qpt}
     CUtensorMap tm_o;     // output, laid out as tm_q
@@ -680,7 +684,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
             } else if (ok) {
                 ok = ctl.split_ok && __all_sync(0xffffffffu, wait_bar(&ctl.drain[1], 0, abort_flag, dev_status, budget));
                 const float mb = ctl.split_m[r], lb = ctl.split_l[r];
-                const float m = fmaxf(m_used, mb);
+                const float m = fmaxf(m_used, mb) + kSpare;
                 w_a = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m);
                 w_b = mb == -INFINITY ? 0.f : fast_exp2(mb - m);
                 // (a sum that is NaN stays: its weight 0 times NaN)
@@ -819,6 +823,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                     w[c] = c < p.cs ? ld_cluster_f32(mapa_shared(part_m(t) + 4u * r, (uint32_t)c)) : -INFINITY;
                     m = fmaxf(m, w[c]);
                 }
+                m += kSpare;
 #pragma unroll
                 for (int c = 0; c < kMaxParts; ++c) {
                     const float lc = c < p.cs ? ld_cluster_f32(mapa_shared(part_l(t) + 4u * r, (uint32_t)c)) : 0.f;

@@ -75,3 +75,43 @@ def test_scores_of_logits_whose_differences_leave_float32(dtype, V, temperature)
     x[2, ::2] = -INF
     x[3] = torch.where(x[3] > 0, 3.3e38, -3.3e38)
     _check_extreme(x.to(dtype), min(5, V), temperature)
+
+
+# ------------------------------------------------------------------------------------- masked attention
+def _attend(n, T, hq, k, v, q, scale, cap=0.0):
+    """All rows see all keys, slots in order."""
+    d = q.shape[-1]
+    out, st = torch.full((1, n, hq, d), 7.0, dtype=q.dtype, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    rr = torch.tensor([0, T], dtype=torch.int32).expand(1, n, 2).contiguous()
+    ac.acache_slot_attention_masked(_desc(hq, k.shape[1], d, q.dtype, scale), 1, n, dev(q), T,
+                                    dev(torch.arange(T, dtype=torch.int32)[None]), dev(k), dev(v), T, out, row_range=dev(rr),
+                                    softcap=cap, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    want, tol = masked_attention(q[0], np.arange(T), k, v, scale, [0] * n, [T] * n, cap=cap)
+    assert_attention(_np(out[0]), want, tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,T", [(40, 512), (200, 512), (40, 3328), (200, 3328)])
+@pytest.mark.parametrize("size", [0.25, 1.0, 3.0])
+def test_sums_of_weights_at_the_end_of_float32(d, n, T, size):
+    """Scores 120 powers of two above the first tile's in a tile behind which nothing raises the reference, in every chain
+    and every CTA that shares the keys: each sum of weights is below 2^128, all of them together are not."""
+    g = torch.Generator().manual_seed(T + n)
+    q = torch.zeros((1, n, 1, d))
+    q[..., 0] = 8.0
+    q[..., 1:] = 0.01 * torch.randn((1, n, 1, d - 1), generator=g)
+    k = 0.01 * torch.randn((T, 1, d), generator=g)
+    tile = torch.arange(T) // 128
+    k[:, 0, 0] = 0.0
+    parts = 8 if T == 3328 else 1
+    n_all = T // 128
+    high = []
+    for r in range(parts):                              # the last tiles of a part's chains, as the kernel lays them out
+        j0, j1 = n_all * r // parts, n_all * (r + 1) // parts
+        high += [j1 - 1] if n > 128 else [j0 + (j1 - j0 + 1) // 2 - 1, j1 - 1]
+    for j in high:
+        k[tile == j, 0, 0] = 10.4375                    # 83.5 = 120.46 ln 2
+    v = size * (1.0 + 0.5 * torch.rand((T, 1, d), generator=g))
+    _attend(n, T, 1, k.to(BF16), v.to(BF16), q.to(BF16), 1.0)

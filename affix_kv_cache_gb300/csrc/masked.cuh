@@ -28,10 +28,10 @@ ACACHE_DEVFN float capped(float dot, float cap_in, float cap_log2) {
     return fmaf(-2.f * cap_log2, fast_rcp(1.f + fast_exp2(dot * cap_in)), cap_log2);
 }
 // The same within 2^-20 of itself, for large caps: below y = 1/4 by y - y^3/3 + 2 y^5/15 - 17 y^7/315 (what follows is
-// below 62/2835 y^9).
-ACACHE_DEVFN float capped_wide(float dot, float cap_in, float cap_log2) {
+// below 62/2835 y^9), with the score itself for y: next to a cap near the end of float32 cap_in has few bits or none.
+ACACHE_DEVFN float capped_wide(float dot, float cap_in, float cap_log2, float scale_log2) {
     const float y = dot * (cap_in * 0.34657359f), z = y * y;        // ln2 / 2
-    const float near = cap_log2 * y * fmaf(z, fmaf(z, fmaf(z, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+    const float near = dot * scale_log2 * fmaf(z, fmaf(z, fmaf(z, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
     return fabsf(y) < 0.25f ? near : capped(dot, cap_in, cap_log2);
 }
 // Up to here the plain form is off by at most 2^-13, a sixteenth of a weight's rounding to bf16.
@@ -76,7 +76,7 @@ ACACHE_DEVFN void masked_row(const MaskedPool<T>& p, const T* q, T* out, int lo,
                 if (p.scale != 0.f || p.scale_log2 == 0.f)
                     s = p.cap_in > 0.f ? p.cap_in * tanhf(dot * p.scale / p.cap_in) * kLog2e : dot * p.scale * kLog2e;
                 else
-                    s = p.cap_in > 0.f ? (p.wide ? capped_wide(dot, p.cap_in, p.cap_log2) : capped(dot, p.cap_in, p.cap_log2)) : dot * p.scale_log2;
+                    s = p.cap_in > 0.f ? (p.wide ? capped_wide(dot, p.cap_in, p.cap_log2, p.scale_log2) : capped(dot, p.cap_in, p.cap_log2)) : dot * p.scale_log2;
                 if (slope_log2 != 0.f) s = fmaf(-slope_log2, fabsf((float)(pos - t)), s);
             }
         }

@@ -272,7 +272,7 @@ masked_decode_kernel(const DecParams p) {
                     float d = s[b][0][2 * k + x];
 #pragma unroll
                     for (int i = 1; i < CH; ++i) d += s[b][i][2 * k + x];
-                    float y = p.cap_in > 0.f ? (p.wide ? capped_wide(d, p.cap_in, p.cap_log2) : capped(d, p.cap_in, p.cap_log2)) : d * p.scale_log2;
+                    float y = p.cap_in > 0.f ? (p.wide ? capped_wide(d, p.cap_in, p.cap_log2, p.scale_log2) : capped(d, p.cap_in, p.cap_log2)) : d * p.scale_log2;
                     if (p.slopes) y = fmaf(-sm.slope[8 * b + 2 * t + x], fabsf((float)(sm.pos[8 * b + 2 * t + x] - key)), y);
                     const bool see = in && key >= lo[b][x] && key < hi[b][x];
                     saw |= (uint32_t)see << (2 * b + x);

@@ -540,7 +540,7 @@ masked_tc_kernel(const __grid_constant__ MaskParams p) {
                     for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
-                            v[cc][x] = __float_as_uint(capped_wide(__uint_as_float(v[cc][x]), p.cap_in, p.cap_log2));
+                            v[cc][x] = __float_as_uint(capped_wide(__uint_as_float(v[cc][x]), p.cap_in, p.cap_log2, p.scale_log2));
                 } else {
 #pragma unroll
                     for (int cc = 0; cc < 4; ++cc)

@@ -115,3 +115,14 @@ def test_sums_of_weights_at_the_end_of_float32(d, n, T, size):
         k[tile == j, 0, 0] = 10.4375                    # 83.5 = 120.46 ln 2
     v = size * (1.0 + 0.5 * torch.rand((T, 1, d), generator=g))
     _attend(n, T, 1, k.to(BF16), v.to(BF16), q.to(BF16), 1.0)
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+@pytest.mark.parametrize("scale,cap", [(2.0 ** -20, 1e38), (2.0 ** -12, 2e38), (1e-3, 1e37)])
+def test_caps_whose_quotient_with_the_scale_is_next_to_nothing(n, scale, cap):
+    """2 log2e scale / cap is a float32 number of few bits or none: the score is the uncapped one."""
+    g = torch.Generator().manual_seed(n)
+    d, T = 128, 300
+    q = (torch.randn((1, n, 2, d), generator=g) * (0.2 / scale) ** 0.5).to(BF16)
+    k, v = ((torch.randn((T, 1, d), generator=g) * s).to(BF16) for s in ((0.2 / scale) ** 0.5, 1.0))
+    _attend(n, T, 2, k, v, q, scale, cap)

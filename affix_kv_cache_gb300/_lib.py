@@ -459,6 +459,19 @@ def rope_desc_frequencies(frequencies, interleaved=False, amplitude=1.0) -> Rope
     return r
 
 
+def _step_of(shape, stride):
+    """Elements from one row to the next, where `shape` and `stride` are of the dimensions that number the rows (None: one)."""
+    step, rows = None, 1
+    for size, at in zip(reversed(shape), reversed(stride)):
+        if size != 1:
+            if step is None:
+                step = at
+            elif at != step * rows:
+                raise ValueError("the rows have to be evenly spaced")
+            rows *= size
+    return step
+
+
 def _row_stride(t, heads, d):
     """Elements from one row [heads][d] of a tensor [..., heads, d] to the next; rows must be evenly spaced."""
     if t is None or not hasattr(t, "stride") or t.is_contiguous():
@@ -469,15 +482,7 @@ def _row_stride(t, heads, d):
         return stride[1]                     # slices of a batch of fused rows
     if n < 3 or stride[-1] != 1 or (stride[-2] != shape[-1] and shape[-2] > 1):
         raise ValueError("the heads of a row have to follow one another")
-    step, rows = None, 1
-    for i in range(n - 3, -1, -1):
-        size = shape[i]
-        if size != 1:
-            if step is None:
-                step = stride[i]
-            elif stride[i] != step * rows:
-                raise ValueError("the rows have to be evenly spaced")
-            rows *= size
+    step = _step_of(shape[:-2], stride[:-2])
     return heads * d if step is None else step
 
 
@@ -553,6 +558,16 @@ def acache_slot_attention_masked_varlen(desc, batch, q_start, max_q_rows, total_
     return _check("acache_slot_attention_masked_varlen", st) if check else st
 
 
+def _logit_stride(logits, rows, vocab):
+    """Elements from one row to the next of logits of any shape [..., at least vocab]."""
+    if logits.is_contiguous() and (logits.numel() == rows * vocab or (logits.dim() == 1 and logits.numel() > rows * vocab)):
+        return vocab                         # rows that follow one another, however they are shaped
+    if logits.dim() < 1 or logits.shape[-1] < vocab or logits.numel() < rows * logits.shape[-1]:
+        raise ValueError("logits of fewer rows or tokens than are to be scored")
+    step = _step_of(logits.shape[:-1], logits.stride()[:-1])
+    return vocab if step is None else step
+
+
 def acache_token_scores(rows, vocab, logits, tokens=None, token_logprob=None, entropy=None, top_tokens=None,
                         top_logprob=None, temperature=1.0, k=None, dev_status=None, stream=None, check=True):
     """Log probabilities of given tokens, entropy and the likeliest tokens (k = the last dimension of top_tokens)
@@ -561,12 +576,10 @@ def acache_token_scores(rows, vocab, logits, tokens=None, token_logprob=None, en
     if logits.dim() < 1 or (vocab > 1 and logits.stride(-1) != 1):
         raise ValueError("the logits of a row have to follow one another")
     dev = _current_device()
-    if logits.is_contiguous():
-        stride = vocab
-    elif logits.dim() == 2:
+    if logits.dim() == 2 and logits.shape[0] >= rows and logits.shape[1] >= vocab:
         stride = logits.stride(0) if logits.shape[0] > 1 else vocab
     else:
-        stride = _row_stride(logits.unsqueeze(-2), 1, vocab)
+        stride = _logit_stride(logits, rows, vocab)
     if k is None:
         k = 0 if top_tokens is None else top_tokens.shape[-1]
     st = lib().acache_token_scores(dtype, rows, vocab, _on(dev, logits), stride, temperature, _on(dev, tokens),

@@ -24,7 +24,7 @@ def _np(t):
 
 
 # ------------------------------------------------------------------------------------- token scores
-def _check_extreme(x, k, temperature):
+def _check_extreme(x, k, temperature, on=None):
     """Scores whose log probabilities may lie beyond float32 (then they are -infinity); the given tokens are the likeliest."""
     T = float(np.float32(temperature))
     R, V = x.shape
@@ -35,7 +35,7 @@ def _check_extreme(x, k, temperature):
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     given, ent = torch.empty(R, device="cuda"), torch.empty(R, device="cuda")
     tt, tl = torch.empty((R, k), dtype=torch.int32, device="cuda"), torch.empty((R, k), device="cuda")
-    ac.acache_token_scores(R, V, dev(x), tokens=dev(torch.from_numpy(first)), token_logprob=given, entropy=ent, top_tokens=tt,
+    ac.acache_token_scores(R, V, dev(x) if on is None else on, tokens=dev(torch.from_numpy(first)), token_logprob=given, entropy=ent, top_tokens=tt,
                            top_logprob=tl, temperature=T, dev_status=st)
     torch.cuda.synchronize()
     assert st.item() == 0
@@ -126,3 +126,14 @@ def test_caps_whose_quotient_with_the_scale_is_next_to_nothing(n, scale, cap):
     q = (torch.randn((1, n, 2, d), generator=g) * (0.2 / scale) ** 0.5).to(BF16)
     k, v = ((torch.randn((T, 1, d), generator=g) * s).to(BF16) for s in ((0.2 / scale) ** 0.5, 1.0))
     _attend(n, T, 2, k, v, q, scale, cap)
+
+
+# ------------------------------------------------------------------------------------- buffers wider than the rows
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape", [(6, 1088), (2, 3, 1088), (6, 1003), (8, 1024)])
+def test_scores_of_a_padded_buffer(dtype, shape):
+    """The whole buffer of a padded LM head is handed over: its rows lie as far apart as it says."""
+    R, V = 6, 1003
+    x = torch.randn(shape, generator=torch.Generator().manual_seed(shape[-1])).to(dtype)
+    x[..., V:] = 1000.0
+    _check_extreme(x.view(-1, shape[-1])[:R, :V], 4, 0.7, on=dev(x))

@@ -9,6 +9,7 @@ module's functions fails loudly.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -166,8 +167,11 @@ def _p(t):
         return t or None
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """The handle of a call's stream; `device`: the current one, where the caller has looked it up."""
     if stream is None:
+        if device is not None:
+            return torch._C._cuda_getCurrentRawStream(device)
         # the current stream's handle, as torch.cuda.current_stream().cuda_stream gives it in 15 times the
         # time; before torch has touched CUDA that is the default stream
         if not torch.cuda.is_initialized():
@@ -472,39 +476,48 @@ def _step_of(shape, stride):
     return step
 
 
-def _row_stride(t, heads, d):
-    """Elements from one row [heads][d] of a tensor [..., heads, d] to the next; rows must be evenly spaced."""
-    if t is None or not hasattr(t, "stride") or t.is_contiguous():
+def _row_stride(t, heads, d, rows=None):
+    """Elements from one row [heads][d] of a tensor [..., heads or more, d] to the next; rows must be evenly spaced.
+    A dense tensor of another shape holds its rows one after the other."""
+    if t is None or not hasattr(t, "stride"):
+        return heads * d
+    if t.is_contiguous() and (rows is None or t.numel() == rows * heads * d):
         return heads * d
     shape, stride = t.shape, t.stride()
     n = len(shape)
-    if n == 4 and stride[3] == 1 and stride[2] == d and stride[0] == stride[1] * shape[1] and shape[1] > 1:
-        return stride[1]                     # slices of a batch of fused rows
-    if n < 3 or stride[-1] != 1 or (stride[-2] != shape[-1] and shape[-2] > 1):
-        raise ValueError("the heads of a row have to follow one another")
-    step = _step_of(shape[:-2], stride[:-2])
-    return heads * d if step is None else step
+    if n > 1 and shape[-1] == d and shape[-2] >= heads:
+        if stride[-1] != 1 or (stride[-2] != d and heads > 1):
+            raise ValueError("the heads of a row have to follow one another")
+        if n == 4 and shape[1] > 1 and stride[0] == stride[1] * shape[1]:
+            many, step = shape[0] * shape[1], stride[1]       # slices of a batch of fused rows
+        else:
+            many, step = math.prod(shape[:-2]), _step_of(shape[:-2], stride[:-2])
+        if rows is None or many >= rows:
+            return heads * d if step is None else step
+    if rows is None or not t.is_contiguous() or t.numel() < rows * heads * d or (n > 1 and shape[-1] not in (d, heads * d)):
+        raise ValueError(f"rows have to be [..., {heads}, {d}]" + ("" if rows is None else f", {rows} of them"))
+    return heads * d
 
 
 def acache_rotate_qk(desc, rope, rows, positions, q, k, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6,
                      stream=None, check=True):
     """Norm (with a weight) and rotary position of query and key rows [..., heads, d], which may be slices
-    of a wider row; rope=None rotates nothing, q or k None is left out."""
+    of a wider row (of rows with more heads the first are taken); rope=None rotates nothing, q or k None is left out."""
     dev = _current_device()
     hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
     st = lib().acache_rotate_qk(
         ctypes.byref(desc), None if rope is None else ctypes.byref(rope), rows, _on(dev, positions), _on(dev, q),
-        _row_stride(q, hq, d), _on(dev, k), _row_stride(k, hkv, d), _on(dev, q_weight), _on(dev, k_weight), eps,
-        _on(dev, q_out), _row_stride(q_out, hq, d), _on(dev, k_out), _row_stride(k_out, hkv, d), _stream(stream))
+        _row_stride(q, hq, d, rows), _on(dev, k), _row_stride(k, hkv, d, rows), _on(dev, q_weight), _on(dev, k_weight), eps,
+        _on(dev, q_out), _row_stride(q_out, hq, d, rows), _on(dev, k_out), _row_stride(k_out, hkv, d, rows), _stream(stream, dev))
     return _check("acache_rotate_qk", st) if check else st
 
 
 def _new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight, k_weight, eps, q_out, k_cache,
               v_cache):
-    hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    hq, hkv, d, n = desc.num_q_heads, desc.num_kv_heads, desc.head_dim, batch * rows
     return (ctypes.byref(desc), None if rope is None else ctypes.byref(rope), batch, rows, _on(dev, positions),
-            _on(dev, write_slot), _on(dev, q), _row_stride(q, hq, d), _on(dev, k), _row_stride(k, hkv, d), _on(dev, v),
-            _row_stride(v, hkv, d), _on(dev, q_weight), _on(dev, k_weight), eps, _on(dev, q_out), _on(dev, k_cache),
+            _on(dev, write_slot), _on(dev, q), _row_stride(q, hq, d, n), _on(dev, k), _row_stride(k, hkv, d, n), _on(dev, v),
+            _row_stride(v, hkv, d, n), _on(dev, q_weight), _on(dev, k_weight), eps, _on(dev, q_out), _on(dev, k_cache),
             _on(dev, v_cache))
 
 
@@ -515,7 +528,7 @@ def acache_rotate_store(desc, rope, batch, rows, positions, write_slot, q, k, v,
     dev = _current_device()
     st = lib().acache_rotate_store(*_new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight,
                                               k_weight, eps, q_out, k_cache, v_cache),
-                                   num_slots, private_begin, _on(dev, dev_status), _stream(stream))
+                                   num_slots, private_begin, _on(dev, dev_status), _stream(stream, dev))
     return _check("acache_rotate_store", st) if check else st
 
 
@@ -527,7 +540,7 @@ def acache_rotate_store_q8(desc, rope, batch, rows, positions, write_slot, q, k,
     st = lib().acache_rotate_store_q8(*_new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight,
                                                  k_weight, eps, q_out, k_cache, v_cache),
                                       _on(dev, kv_scale), num_slots, private_begin, _on(dev, dev_status),
-                                      _stream(stream))
+                                      _stream(stream, dev))
     return _check("acache_rotate_store_q8", st) if check else st
 
 
@@ -540,7 +553,7 @@ def acache_slot_attention_masked(desc, batch, n_q, q, seq_len, read_slot, k_cach
     mask = Mask(_on(dev, row_range), _on(dev, q_pos), _on(dev, slopes), softcap, int(bool(drop_none)))
     st = lib().acache_slot_attention_masked(ctypes.byref(desc), ctypes.byref(mask), batch, n_q, _on(dev, q), seq_len,
                                             _on(dev, read_slot), _on(dev, k_cache), _on(dev, v_cache), num_slots,
-                                            _on(dev, out), _on(dev, dev_status), _stream(stream))
+                                            _on(dev, out), _on(dev, dev_status), _stream(stream, dev))
     return _check("acache_slot_attention_masked", st) if check else st
 
 
@@ -554,7 +567,7 @@ def acache_slot_attention_masked_varlen(desc, batch, q_start, max_q_rows, total_
     st = lib().acache_slot_attention_masked_varlen(
         ctypes.byref(desc), ctypes.byref(mask), batch, _on(dev, q_start), max_q_rows, total_q_rows, _on(dev, q),
         _on(dev, kv_start), max_seq_len, _on(dev, read_slot), _on(dev, k_cache), _on(dev, v_cache), num_slots,
-        _on(dev, out), _on(dev, dev_status), _stream(stream))
+        _on(dev, out), _on(dev, dev_status), _stream(stream, dev))
     return _check("acache_slot_attention_masked_varlen", st) if check else st
 
 
@@ -562,7 +575,7 @@ def _logit_stride(logits, rows, vocab):
     """Elements from one row to the next of logits of any shape [..., at least vocab]."""
     if logits.is_contiguous() and (logits.numel() == rows * vocab or (logits.dim() == 1 and logits.numel() > rows * vocab)):
         return vocab                         # rows that follow one another, however they are shaped
-    if logits.dim() < 1 or logits.shape[-1] < vocab or logits.numel() < rows * logits.shape[-1]:
+    if logits.shape[-1] < vocab or logits.numel() < rows * logits.shape[-1]:
         raise ValueError("logits of fewer rows or tokens than are to be scored")
     step = _step_of(logits.shape[:-1], logits.stride()[:-1])
     return vocab if step is None else step
@@ -573,18 +586,19 @@ def acache_token_scores(rows, vocab, logits, tokens=None, token_logprob=None, en
     """Log probabilities of given tokens, entropy and the likeliest tokens (k = the last dimension of top_tokens)
     of logits [rows, vocab] in bf16 or float32, whose rows may lie apart."""
     dtype = {torch.float32: ACACHE_F32, torch.bfloat16: ACACHE_BF16}.get(logits.dtype, -1)
-    if logits.dim() < 1 or (vocab > 1 and logits.stride(-1) != 1):
+    shape, step = logits.shape, logits.stride()
+    if not shape or (vocab > 1 and step[-1] != 1):
         raise ValueError("the logits of a row have to follow one another")
     dev = _current_device()
-    if logits.dim() == 2 and logits.shape[0] >= rows and logits.shape[1] >= vocab:
-        stride = logits.stride(0) if logits.shape[0] > 1 else vocab
+    if len(shape) == 2 and shape[0] >= rows and shape[1] >= vocab:
+        stride = step[0] if shape[0] > 1 else vocab
     else:
         stride = _logit_stride(logits, rows, vocab)
     if k is None:
         k = 0 if top_tokens is None else top_tokens.shape[-1]
     st = lib().acache_token_scores(dtype, rows, vocab, _on(dev, logits), stride, temperature, _on(dev, tokens),
                                    _on(dev, token_logprob), _on(dev, entropy), k, _on(dev, top_tokens),
-                                   _on(dev, top_logprob), _on(dev, dev_status), _stream(stream))
+                                   _on(dev, top_logprob), _on(dev, dev_status), _stream(stream, dev))
     return _check("acache_token_scores", st) if check else st
 
 

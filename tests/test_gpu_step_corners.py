@@ -137,3 +137,26 @@ def test_scores_of_a_padded_buffer(dtype, shape):
     x = torch.randn(shape, generator=torch.Generator().manual_seed(shape[-1])).to(dtype)
     x[..., V:] = 1000.0
     _check_extreme(x.view(-1, shape[-1])[:R, :V], 4, 0.7, on=dev(x))
+
+
+def test_rotation_of_a_whole_fused_buffer():
+    """The queries of rows of queries, keys and values, unsliced: the first heads of each row."""
+    g = torch.Generator().manual_seed(3)
+    B, n, hq, hkv, d = 2, 5, 4, 2, 128
+    qkv = torch.randn((B, n, hq + 2 * hkv, d), generator=g).to(BF16).cuda()
+    q, k, v = qkv.split((hq, hkv, hkv), 2)
+    pos = torch.arange(B * n, dtype=torch.int32, device="cuda") * 100
+    rope, desc = ac.rope_desc(d), _desc(hq, hkv, d, BF16)
+    want, got = (torch.empty((B, n, hq, d), dtype=BF16, device="cuda") for _ in range(2))
+    wide = torch.full((B, n, hq + 3, d), 7.0, dtype=BF16, device="cuda")
+    ac.acache_rotate_qk(desc, rope, B * n, pos, q.contiguous(), None, want, None)
+    ac.acache_rotate_qk(desc, rope, B * n, pos, qkv, None, got, None)
+    ac.acache_rotate_qk(desc, rope, B * n, pos, q, None, wide, None)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(wide[:, :, :hq], want) and (wide[:, :, hq:] == 7).all()
+    pools = [[torch.zeros((B * n, hkv, d), dtype=BF16, device="cuda") for _ in range(2)] for _ in range(2)]
+    slots = torch.arange(B * n, dtype=torch.int32, device="cuda")
+    ac.acache_rotate_store(desc, rope, B, n, pos, slots, qkv, k, v, got, *pools[0], B * n, 0)
+    ac.acache_rotate_store(desc, rope, B, n, pos, slots, *(x.contiguous() for x in (q, k, v)), want, *pools[1], B * n, 0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(*pools))

@@ -27,6 +27,7 @@ def calls(monkeypatch):
     lib = _Recorder()
     monkeypatch.setattr(_lib, "lib", lambda: lib)
     monkeypatch.setattr(_lib, "_current_device", lambda: -1)
+    monkeypatch.setattr(_lib, "_stream", lambda *a: None)
     return lib.calls
 
 
@@ -57,4 +58,61 @@ def test_logits_that_are_slices(calls):
 def test_logits_of_too_few_rows_or_tokens_are_refused(calls, shape, rows, vocab):
     with pytest.raises(ValueError):
         ac.acache_token_scores(rows, vocab, torch.zeros(shape), entropy=torch.zeros(rows))
+    assert not calls
+
+
+# ------------------------------------------------------------------------------------- rows of heads
+HQ, HKV, D = 4, 2, 128
+
+
+def _desc():
+    return ac.attn_desc(HQ, HKV, D, 0.1, "bf16")
+
+
+def _rows(*shape):
+    return torch.zeros(shape, dtype=BF16)
+
+
+def _rotate(q, k, rows=6, q_out=None, k_out=None):
+    ac.acache_rotate_qk(_desc(), None, rows, None, q, k, _rows(rows, HQ, D) if q_out is None else q_out,
+                        _rows(rows, HKV, D) if k_out is None else k_out)
+
+
+def _strides(args):
+    """q, k, q_out, k_out of acache_rotate_qk(desc, rope, rows, positions, q, stride, k, stride, weights, eps, ...)."""
+    return args[5], args[7], args[12], args[14]
+
+
+@pytest.mark.parametrize("shape,rows,want", [
+    ((6, HQ, D), 6, 512), ((2, 3, HQ, D), 6, 512), ((6, 8, D), 6, 1024), ((2, 3, 8, D), 6, 1024), ((2, 3, 8, D), 5, 1024),
+    ((9, HQ, D), 6, 512), ((6, HQ * D), 6, 512), ((9, HQ * D), 6, 512), ((6 * HQ, D), 6, 512), ((2, 3 * HQ, D), 6, 512),
+    ((6 * HQ * D,), 6, 512), ((7 * HQ * D,), 6, 512), ((1, 2, 3, 8, D), 6, 1024)])
+def test_rows_in_a_buffer_of_more_heads(calls, shape, rows, want):
+    """A whole fused projection in place of its slice of queries, and dense rows of any shape."""
+    _rotate(_rows(*shape), None, rows)
+    assert _strides(calls[0][1])[0] == want
+    calls.clear()
+    _rotate(None, None, rows, q_out=_rows(*shape))
+    assert _strides(calls[0][1])[2] == want
+
+
+def test_rows_of_every_matrix(calls):
+    qkv, out = _rows(2, 3, HQ + 2 * HKV, D), _rows(2, 3, 2 * HQ, D)
+    q, k, v = qkv.split((HQ, HKV, HKV), 2)
+    _rotate(qkv, k, 6, out, out[:, :, HQ:HQ + HKV])
+    assert _strides(calls[0][1]) == (1024, 1024, 1024, 1024)
+    for call in (ac.acache_rotate_store, ac.acache_rotate_store_q8):
+        calls.clear()
+        pool = [_rows(9, HKV, D)] * (2 if call is ac.acache_rotate_store else 3)
+        call(_desc(), None, 2, 3, None, torch.zeros(6, dtype=torch.int32), qkv, k, _rows(6, 5, D), _rows(6, HQ, D), *pool, 9, 0)
+        a = calls[0][1]
+        assert (a[7], a[9], a[11]) == (1024, 1024, 640)
+
+
+@pytest.mark.parametrize("shape", [(6, HQ, D + 16), (6, HQ - 1, D + 8), (5, HQ, D), (2, 2, HQ, D), (5, 2 * HQ * D), (6, 2 * HQ * D)])
+def test_rows_that_are_too_few_or_lie_otherwise_are_refused(calls, shape):
+    with pytest.raises(ValueError):
+        _rotate(_rows(*shape), None)
+    with pytest.raises(ValueError):
+        _rotate(None, None, q_out=_rows(*shape))
     assert not calls

@@ -515,6 +515,8 @@ def acache_rotate_qk(desc, rope, rows, positions, q, k, q_out, k_out, q_weight=N
 def _new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight, k_weight, eps, q_out, k_cache,
               v_cache):
     hq, hkv, d, n = desc.num_q_heads, desc.num_kv_heads, desc.head_dim, batch * rows
+    if q is not None and n > 1 and _row_stride(q_out, hq, d, n) != hq * d:
+        raise ValueError("the rows of q_out have to follow one another")
     return (ctypes.byref(desc), None if rope is None else ctypes.byref(rope), batch, rows, _on(dev, positions),
             _on(dev, write_slot), _on(dev, q), _row_stride(q, hq, d, n), _on(dev, k), _row_stride(k, hkv, d, n), _on(dev, v),
             _row_stride(v, hkv, d, n), _on(dev, q_weight), _on(dev, k_weight), eps, _on(dev, q_out), _on(dev, k_cache),

@@ -116,3 +116,24 @@ def test_rows_that_are_too_few_or_lie_otherwise_are_refused(calls, shape):
     with pytest.raises(ValueError):
         _rotate(None, None, q_out=_rows(*shape))
     assert not calls
+
+
+@pytest.mark.parametrize("call", [ac.acache_rotate_store, ac.acache_rotate_store_q8])
+def test_queries_of_a_store_come_out_dense(calls, call):
+    """The stores write q_out as [rows][Hq][d]: rows that lie further apart are refused, not written in between."""
+    pool = [_rows(9, HKV, D)] * (2 if call is ac.acache_rotate_store else 3)
+
+    def store(batch, rows, q, q_out):
+        call(_desc(), None, batch, rows, None, torch.zeros(batch * rows, dtype=torch.int32), q, _rows(batch, rows, HKV, D),
+             _rows(batch, rows, HKV, D), q_out, *pool, 9, 0)
+
+    wide = _rows(2, 3, HQ + 2, D)
+    for q_out in (wide[:, :, :HQ], wide, _rows(6, HQ + 1, D), _rows(2, 6, HQ, D)[:, ::2], _rows(5, HQ, D)):
+        with pytest.raises(ValueError):
+            store(2, 3, _rows(2, 3, HQ, D), q_out)
+    assert not calls
+    for q_out in (_rows(2, 3, HQ, D), _rows(6, HQ * D), _rows(8, HQ, D)):
+        store(2, 3, _rows(2, 3, HQ, D), q_out)
+    store(1, 1, _rows(1, 1, HQ, D), wide[:1, :1, :HQ])             # a single row has no next one
+    store(2, 3, None, wide[:, :, :HQ])                             # no queries: not used
+    assert len(calls) == 5

@@ -200,6 +200,21 @@ def _on(device, t):
         return t or None
 
 
+def _dense(device, t):
+    """_on, of a tensor that a call reads or writes as one dense block: with gaps or repeats it were another one, or none."""
+    if t is None:
+        return None
+    try:
+        if not t.is_contiguous():
+            raise ValueError("a tensor that has to be contiguous is not")
+        at = t.data_ptr()
+        if at and t.get_device() != device:
+            raise ValueError(f"tensor on {t.device}, not on the current device")
+        return at or None
+    except AttributeError:       # a plain address
+        return t or None
+
+
 def _check(fn, status):
     if status != ACACHE_OK:
         raise AcacheError(fn, status)
@@ -479,20 +494,25 @@ def _step_of(shape, stride):
 def _row_stride(t, heads, d, rows=None):
     """Elements from one row [heads][d] of a tensor [..., heads or more, d] to the next; rows must be evenly spaced.
     A dense tensor of another shape holds its rows one after the other."""
-    if t is None or not hasattr(t, "stride"):
+    if t is None:
         return heads * d
-    if t.is_contiguous() and (rows is None or t.numel() == rows * heads * d):
+    try:
+        if t.is_contiguous() and (rows is None or t.numel() == rows * heads * d):
+            return heads * d
+        shape, stride = t.shape, t.stride()
+    except AttributeError:       # a plain address
         return heads * d
-    shape, stride = t.shape, t.stride()
     n = len(shape)
+    if n == 4:                               # slices of a batch of fused rows
+        a, b, h, w = shape
+        sa, sb, sh, sw = stride
+        if w == d and h >= heads and sw == 1 and sh == d and b > 1 and sa == sb * b and (rows is None or a * b >= rows):
+            return sb
     if n > 1 and shape[-1] == d and shape[-2] >= heads:
         if stride[-1] != 1 or (stride[-2] != d and heads > 1):
             raise ValueError("the heads of a row have to follow one another")
-        if n == 4 and shape[1] > 1 and stride[0] == stride[1] * shape[1]:
-            many, step = shape[0] * shape[1], stride[1]       # slices of a batch of fused rows
-        else:
-            many, step = math.prod(shape[:-2]), _step_of(shape[:-2], stride[:-2])
-        if rows is None or many >= rows:
+        step = _step_of(shape[:-2], stride[:-2])
+        if rows is None or math.prod(shape[:-2]) >= rows:
             return heads * d if step is None else step
     if rows is None or not t.is_contiguous() or t.numel() < rows * heads * d or (n > 1 and shape[-1] not in (d, heads * d)):
         raise ValueError(f"rows have to be [..., {heads}, {d}]" + ("" if rows is None else f", {rows} of them"))
@@ -506,8 +526,8 @@ def acache_rotate_qk(desc, rope, rows, positions, q, k, q_out, k_out, q_weight=N
     dev = _current_device()
     hq, hkv, d = desc.num_q_heads, desc.num_kv_heads, desc.head_dim
     st = lib().acache_rotate_qk(
-        ctypes.byref(desc), None if rope is None else ctypes.byref(rope), rows, _on(dev, positions), _on(dev, q),
-        _row_stride(q, hq, d, rows), _on(dev, k), _row_stride(k, hkv, d, rows), _on(dev, q_weight), _on(dev, k_weight), eps,
+        desc, rope, rows, _dense(dev, positions), _on(dev, q),
+        _row_stride(q, hq, d, rows), _on(dev, k), _row_stride(k, hkv, d, rows), _dense(dev, q_weight), _dense(dev, k_weight), eps,
         _on(dev, q_out), _row_stride(q_out, hq, d, rows), _on(dev, k_out), _row_stride(k_out, hkv, d, rows), _stream(stream, dev))
     return _check("acache_rotate_qk", st) if check else st
 
@@ -517,10 +537,10 @@ def _new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_we
     hq, hkv, d, n = desc.num_q_heads, desc.num_kv_heads, desc.head_dim, batch * rows
     if q is not None and n > 1 and _row_stride(q_out, hq, d, n) != hq * d:
         raise ValueError("the rows of q_out have to follow one another")
-    return (ctypes.byref(desc), None if rope is None else ctypes.byref(rope), batch, rows, _on(dev, positions),
-            _on(dev, write_slot), _on(dev, q), _row_stride(q, hq, d, n), _on(dev, k), _row_stride(k, hkv, d, n), _on(dev, v),
-            _row_stride(v, hkv, d, n), _on(dev, q_weight), _on(dev, k_weight), eps, _on(dev, q_out), _on(dev, k_cache),
-            _on(dev, v_cache))
+    return (desc, rope, batch, rows, _dense(dev, positions),
+            _dense(dev, write_slot), _on(dev, q), _row_stride(q, hq, d, n), _on(dev, k), _row_stride(k, hkv, d, n), _on(dev, v),
+            _row_stride(v, hkv, d, n), _dense(dev, q_weight), _dense(dev, k_weight), eps, _on(dev, q_out), _dense(dev, k_cache),
+            _dense(dev, v_cache))
 
 
 def acache_rotate_store(desc, rope, batch, rows, positions, write_slot, q, k, v, q_out, k_cache, v_cache, num_slots,
@@ -541,7 +561,7 @@ def acache_rotate_store_q8(desc, rope, batch, rows, positions, write_slot, q, k,
     dev = _current_device()
     st = lib().acache_rotate_store_q8(*_new_rows(dev, desc, rope, batch, rows, positions, write_slot, q, k, v, q_weight,
                                                  k_weight, eps, q_out, k_cache, v_cache),
-                                      _on(dev, kv_scale), num_slots, private_begin, _on(dev, dev_status),
+                                      _dense(dev, kv_scale), num_slots, private_begin, _on(dev, dev_status),
                                       _stream(stream, dev))
     return _check("acache_rotate_store_q8", st) if check else st
 
@@ -552,10 +572,10 @@ def acache_slot_attention_masked(desc, batch, n_q, q, seq_len, read_slot, k_cach
     """Read-slot attention whose rows see a range of keys (row_range [B, n_q, 2]), with capped scores and a
     bias of -slopes[h] * |q_pos - t|."""
     dev = _current_device()
-    mask = Mask(_on(dev, row_range), _on(dev, q_pos), _on(dev, slopes), softcap, int(bool(drop_none)))
-    st = lib().acache_slot_attention_masked(ctypes.byref(desc), ctypes.byref(mask), batch, n_q, _on(dev, q), seq_len,
-                                            _on(dev, read_slot), _on(dev, k_cache), _on(dev, v_cache), num_slots,
-                                            _on(dev, out), _on(dev, dev_status), _stream(stream, dev))
+    mask = Mask(_dense(dev, row_range), _dense(dev, q_pos), _dense(dev, slopes), softcap, int(bool(drop_none)))
+    st = lib().acache_slot_attention_masked(desc, mask, batch, n_q, _dense(dev, q), seq_len,
+                                            _dense(dev, read_slot), _dense(dev, k_cache), _dense(dev, v_cache), num_slots,
+                                            _dense(dev, out), _on(dev, dev_status), _stream(stream, dev))
     return _check("acache_slot_attention_masked", st) if check else st
 
 
@@ -565,11 +585,11 @@ def acache_slot_attention_masked_varlen(desc, batch, q_start, max_q_rows, total_
                                         check=True):
     """The same over a ragged batch (offsets as in acache_slot_attention_varlen)."""
     dev = _current_device()
-    mask = Mask(_on(dev, row_range), _on(dev, q_pos), _on(dev, slopes), softcap, int(bool(drop_none)))
+    mask = Mask(_dense(dev, row_range), _dense(dev, q_pos), _dense(dev, slopes), softcap, int(bool(drop_none)))
     st = lib().acache_slot_attention_masked_varlen(
-        ctypes.byref(desc), ctypes.byref(mask), batch, _on(dev, q_start), max_q_rows, total_q_rows, _on(dev, q),
-        _on(dev, kv_start), max_seq_len, _on(dev, read_slot), _on(dev, k_cache), _on(dev, v_cache), num_slots,
-        _on(dev, out), _on(dev, dev_status), _stream(stream, dev))
+        desc, mask, batch, _dense(dev, q_start), max_q_rows, total_q_rows, _dense(dev, q),
+        _dense(dev, kv_start), max_seq_len, _dense(dev, read_slot), _dense(dev, k_cache), _dense(dev, v_cache), num_slots,
+        _dense(dev, out), _on(dev, dev_status), _stream(stream, dev))
     return _check("acache_slot_attention_masked_varlen", st) if check else st
 
 
@@ -598,9 +618,9 @@ def acache_token_scores(rows, vocab, logits, tokens=None, token_logprob=None, en
         stride = _logit_stride(logits, rows, vocab)
     if k is None:
         k = 0 if top_tokens is None else top_tokens.shape[-1]
-    st = lib().acache_token_scores(dtype, rows, vocab, _on(dev, logits), stride, temperature, _on(dev, tokens),
-                                   _on(dev, token_logprob), _on(dev, entropy), k, _on(dev, top_tokens),
-                                   _on(dev, top_logprob), _on(dev, dev_status), _stream(stream, dev))
+    st = lib().acache_token_scores(dtype, rows, vocab, _on(dev, logits), stride, temperature, _dense(dev, tokens),
+                                   _dense(dev, token_logprob), _dense(dev, entropy), k, _dense(dev, top_tokens),
+                                   _dense(dev, top_logprob), _on(dev, dev_status), _stream(stream, dev))
     return _check("acache_token_scores", st) if check else st
 
 

@@ -137,3 +137,48 @@ def test_queries_of_a_store_come_out_dense(calls, call):
     store(1, 1, _rows(1, 1, HQ, D), wide[:1, :1, :HQ])             # a single row has no next one
     store(2, 3, None, wide[:, :, :HQ])                             # no queries: not used
     assert len(calls) == 5
+
+
+# ------------------------------------------------------------------------------------- everything else is dense
+def _apart(t):
+    """The same shape and values with gaps between the elements."""
+    return torch.stack((t, t), -1)[..., 0]
+
+
+def _calls():
+    """(name, call, arguments by name) of every call that takes tensors as one dense block."""
+    i32 = torch.int32
+    pos, slot, w = torch.zeros(6, dtype=i32), torch.zeros(6, dtype=i32), torch.zeros(D, dtype=BF16)
+    q, k, v = _rows(2, 3, HQ, D), _rows(2, 3, HKV, D), _rows(2, 3, HKV, D)
+    pool = dict(k_cache=_rows(9, HKV, D), v_cache=_rows(9, HKV, D), num_slots=9)
+    turn = dict(desc=_desc(), rope=_lib.Rope(), positions=pos, q=q, k=k, q_weight=w, k_weight=w, q_out=_rows(2, 3, HQ, D))
+    store = dict(turn, batch=2, rows=3, write_slot=slot, v=v, private_begin=0, **pool)
+    mask = dict(row_range=torch.zeros((2, 3, 2), dtype=i32), q_pos=pos, slopes=torch.zeros(HQ))
+    attend = dict(desc=_desc(), batch=2, q=q, read_slot=torch.zeros((2, 8), dtype=i32), out=_rows(2, 3, HQ, D), **pool, **mask)
+    start = torch.zeros(3, dtype=i32)
+    return [
+        (ac.acache_rotate_qk, dict(turn, rows=6, k_out=_rows(2, 3, HKV, D)), ("positions", "q_weight", "k_weight")),
+        (ac.acache_rotate_store, store, ("positions", "write_slot", "q_weight", "k_weight", "k_cache", "v_cache")),
+        (ac.acache_rotate_store_q8, dict(store, kv_scale=torch.zeros(9, HKV, 2)), ("positions", "write_slot", "k_cache", "v_cache", "kv_scale")),
+        (ac.acache_slot_attention_masked, dict(attend, n_q=3, seq_len=8),
+         ("q", "read_slot", "k_cache", "v_cache", "out", "row_range", "q_pos", "slopes")),
+        (ac.acache_slot_attention_masked_varlen, dict(attend, q_start=start, kv_start=start, max_q_rows=3, total_q_rows=6, max_seq_len=8),
+         ("q", "read_slot", "q_start", "kv_start", "k_cache", "v_cache", "out", "row_range", "q_pos", "slopes")),
+        (ac.acache_token_scores, dict(rows=6, vocab=50, logits=torch.zeros(6, 50), tokens=pos, token_logprob=torch.zeros(6),
+                                      entropy=torch.zeros(6), top_tokens=torch.zeros((6, 4), dtype=i32), top_logprob=torch.zeros(6, 4), k=4),
+         ("tokens", "token_logprob", "entropy", "top_tokens", "top_logprob"))]
+
+
+@pytest.mark.parametrize("at", range(6))
+def test_tensors_with_gaps_or_repeats_are_refused(calls, at):
+    """A column of a wider tensor, or one row's positions expanded to a batch, does not lie as the kernels read it: they would
+    take other values, or read behind its memory."""
+    call, args, names = _calls()[at]
+    call(**args)
+    assert len(calls) == 1
+    for name in names:
+        for bad in (_apart(args[name]), args[name][:1].expand(args[name].shape)):
+            with pytest.raises(ValueError):
+                call(**dict(args, **{name: bad}))
+        call(**dict(args, **{name: 1 << 40}))                       # a plain address is the caller's own
+    assert len(calls) == 1 + len(names)

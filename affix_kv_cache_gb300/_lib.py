@@ -618,6 +618,9 @@ def acache_token_scores(rows, vocab, logits, tokens=None, token_logprob=None, en
         stride = _logit_stride(logits, rows, vocab)
     if k is None:
         k = 0 if top_tokens is None else top_tokens.shape[-1]
+    for t in (top_tokens, top_logprob):
+        if t is not None and k > 0 and rows > 1 and hasattr(t, "shape") and t.shape[-1] != k and t.dim() > 1:
+            raise ValueError(f"alternatives are [rows, {k}]")
     st = lib().acache_token_scores(dtype, rows, vocab, _on(dev, logits), stride, temperature, _dense(dev, tokens),
                                    _dense(dev, token_logprob), _dense(dev, entropy), k, _dense(dev, top_tokens),
                                    _dense(dev, top_logprob), _on(dev, dev_status), _stream(stream, dev))

@@ -182,3 +182,16 @@ def test_tensors_with_gaps_or_repeats_are_refused(calls, at):
                 call(**dict(args, **{name: bad}))
         call(**dict(args, **{name: 1 << 40}))                       # a plain address is the caller's own
     assert len(calls) == 1 + len(names)
+
+
+def test_alternatives_of_another_width_are_refused(calls):
+    """The alternatives of a row follow those of the row before: k columns in each output."""
+    i32, x = torch.int32, torch.zeros(6, 50)
+    for tt, tl, k in (((6, 8), None, 4), ((6, 4), (6, 8), None), ((6, 4), (6, 2), 4), ((2, 3, 8), None, 4)):
+        with pytest.raises(ValueError):
+            ac.acache_token_scores(6, 50, x, top_tokens=torch.zeros(tt, dtype=i32), top_logprob=None if tl is None else torch.zeros(tl), k=k)
+    assert not calls
+    for tt, tl, k in (((6, 4), (6, 4), None), ((2, 3, 4), (6, 4), 4), ((24,), (24,), 4), ((8, 4), None, 4)):
+        ac.acache_token_scores(6, 50, x, top_tokens=torch.zeros(tt, dtype=i32), top_logprob=None if tl is None else torch.zeros(tl), k=k)
+    ac.acache_token_scores(1, 50, x[:1], top_tokens=torch.zeros((1, 32), dtype=i32), k=4)
+    assert [c[1][9] for c in calls] == [4] * 5

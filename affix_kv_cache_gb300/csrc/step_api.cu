@@ -41,12 +41,25 @@ bool rows_ok(const AttnArgs& a, const void* p, int64_t stride, int heads) {
     const int64_t e = a.dtype == ACACHE_F32 ? 4 : 2;
     return p && aligned16(p) && stride >= (int64_t)heads * a.d && stride * e % 16 == 0 && stride < (1LL << 40);
 }
+int64_t row_bytes(const AttnArgs& a, int heads) { return (int64_t)heads * a.d * (a.dtype == ACACHE_F32 ? 4 : 2); }
+// Bytes from the first row of one matrix to the end of its last.
+int64_t span(const AttnArgs& a, int64_t rows, int64_t stride, int heads) {
+    return (rows - 1) * stride * (a.dtype == ACACHE_F32 ? 4 : 2) + row_bytes(a, heads);
+}
+// Two matrices lie apart: one behind the other, or with the same stride each in the gaps between the other's rows.  kUnknown:
+// their rows are spaced otherwise, and the one begins before the other ends.
+enum Apart { kMeet, kApart, kUnknown };
+Apart lie(const AttnArgs& a, int64_t rows, const void* x, int64_t sx, int hx, const void* y, int64_t sy, int hy) {
+    const uintptr_t x0 = (uintptr_t)x, y0 = (uintptr_t)y;
+    if (x0 + span(a, rows, sx, hx) <= y0 || y0 + span(a, rows, sy, hy) <= x0) return kApart;
+    if (rows == 1) return kMeet;
+    if (sx != sy) return kUnknown;
+    const int64_t step = sx * (a.dtype == ACACHE_F32 ? 4 : 2), behind = ((int64_t)(y0 - x0) % step + step) % step;
+    return behind >= row_bytes(a, hx) && step - behind >= row_bytes(a, hy) ? kApart : kMeet;
+}
 // An output is its own input, or lies apart from it.
 bool apart(const AttnArgs& a, int64_t rows, const void* in, int64_t si, const void* out, int64_t so, int heads) {
-    if (in == out) return si == so;
-    const int64_t e = a.dtype == ACACHE_F32 ? 4 : 2, row = (int64_t)heads * a.d;
-    const char *i0 = (const char*)in, *o0 = (const char*)out;
-    return i0 + ((rows - 1) * si + row) * e <= o0 || o0 + ((rows - 1) * so + row) * e <= i0;
+    return in == out ? si == so : lie(a, rows, in, si, heads, out, so, heads) == kApart;
 }
 // Head counts of one call (items of a row are numbered in 32 bits) and rows whose byte offsets fit 64.
 bool sizes_fit(const AttnArgs& a, int64_t rows) {
@@ -70,6 +83,8 @@ int rotate_store(const acache_attn_desc* desc, const acache_rope* rope, int batc
         return ACACHE_ERR_INVALID_ARG;
     const int64_t row = (int64_t)a.hq * a.d;
     if (q && (!rows_ok(a, q, q_stride, a.hq) || !rows_ok(a, q_out, row, a.hq) || !apart(a, n, q, q_stride, q_out, row, a.hq)))
+        return ACACHE_ERR_INVALID_ARG;
+    if (q && (lie(a, n, k, k_stride, a.hkv, q_out, row, a.hq) == kMeet || lie(a, n, v, v_stride, a.hkv, q_out, row, a.hq) == kMeet))
         return ACACHE_ERR_INVALID_ARG;
     RotateCall c{};
     c.a = a;
@@ -210,6 +225,10 @@ int acache_rotate_qk(const acache_attn_desc* desc, const acache_rope* rope, int6
         return ACACHE_ERR_INVALID_ARG;
     if (k && (!rows_ok(a, k, k_stride, a.hkv) || !rows_ok(a, k_out, k_out_stride, a.hkv) ||
               !apart(a, rows, k, k_stride, k_out, k_out_stride, a.hkv)))
+        return ACACHE_ERR_INVALID_ARG;
+    if (q && k && (lie(a, rows, q, q_stride, a.hq, k_out, k_out_stride, a.hkv) == kMeet ||
+                   lie(a, rows, k, k_stride, a.hkv, q_out, q_out_stride, a.hq) == kMeet ||
+                   lie(a, rows, q_out, q_out_stride, a.hq, k_out, k_out_stride, a.hkv) == kMeet))
         return ACACHE_ERR_INVALID_ARG;
     RotateCall c{};
     c.a = a;

@@ -523,7 +523,8 @@ ACACHE_API int acache_rope_init_frequencies(acache_rope* out, int rotary_dim, in
  *                may be NULL: that matrix is left out
  *   q_weight, k_weight  [d] of the descriptor's dtype, or NULL: no norm
  *   q_out, k_out rows at their own strides.  An output may be its own input (same pointer and
- *                stride); otherwise it must not overlap an input
+ *                stride); otherwise it must not overlap an input or the other output (rows of the
+ *                same stride may lie in the gaps between one another's)
  * Pointers 16-byte aligned, strides >= a row and multiples of 16 bytes; eps >= 0.
  * ------------------------------------------------------------------------------- */
 ACACHE_API int acache_rotate_qk(const acache_attn_desc* a, const acache_rope* rope, int64_t rows,

@@ -160,3 +160,25 @@ def test_rotation_of_a_whole_fused_buffer():
     ac.acache_rotate_store(desc, rope, B, n, pos, slots, *(x.contiguous() for x in (q, k, v)), want, *pools[1], B * n, 0)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(*pools))
+
+
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("n", [1, 7])
+def test_rotation_into_the_gaps_between_its_rows(first, n):
+    """Rows before and after the rotation side by side in one buffer."""
+    g = torch.Generator().manual_seed(n)
+    hq, hkv, d = 4, 2, 64
+    buf = torch.randn((n, 2 * (hq + hkv), d), generator=g).to(BF16).cuda()
+    keep = buf.clone()
+    half = slice(0, hq + hkv), slice(hq + hkv, None)
+    x, y = (buf[:, half[not first]], buf[:, half[first]])
+    pos, rope, desc = torch.arange(n, dtype=torch.int32, device="cuda") + 5, ac.rope_desc(d), _desc(hq, hkv, d, BF16)
+    want = [x[:, :hq].clone(), x[:, hq:].clone()]
+    ac.acache_rotate_qk(desc, rope, n, pos, *want, *want)
+    ac.acache_rotate_qk(desc, rope, n, pos, x[:, :hq], x[:, hq:], y[:, :hq], y[:, hq:])
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, :hq], want[0]) and torch.equal(y[:, hq:], want[1])
+    assert torch.equal(x, keep[:, half[not first]])
+    if n > 1:                                            # an output that shares a head with its input
+        with pytest.raises(ac.AcacheError):
+            ac.acache_rotate_qk(desc, rope, n, pos, buf[:, 1:1 + hq], None, buf[:, :hq], None)

@@ -472,8 +472,9 @@ ACACHE_API int acache_rerotate_keys(const acache_attn_desc* a, int64_t rows, con
  * `amplitude`; elements from rotary_dim on pass unchanged.  Pairs as in acache_rerotate_keys
  * (interleaved = 0: (x_i, x_{i + rotary_dim/2}); 1: (x_{2i}, x_{2i+1})).  phase[i] is f_i / 2 pi
  * modulo one turn in units of 2^-64 turns: the product with a 32-bit position is exact modulo
- * whole turns, so far positions lose nothing (the angle is off by at most 2^-33 turns from the
- * frequency's own rounding, and by 2^-24 of itself, taken within half a turn, in float32).
+ * whole turns, so far positions lose nothing.  The angle of the double f_i is off by at most 2^-34
+ * turns (with a turn or more per position also by 2^-52 of its turns, f_i / 2 pi being rounded to
+ * double there), and by 2^-24 of itself, taken within half a turn, in float32.
  *
  * acache_rope_init fills one with f_i = theta^(-2i/rotary_dim), changed for long contexts by
  *   ACACHE_ROPE_NONE    nothing

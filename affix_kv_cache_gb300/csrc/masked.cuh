@@ -22,19 +22,23 @@ ACACHE_DEVFN float fast_rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// c tanh(s / c) in log2 units from the product q.k: tanh y = 1 - 2 / (1 + e^2y), within 2^-22 c of it
+// c tanh(s / c) in log2 units from the product q.k: tanh y = 1 - 2 / (1 + e^2y), within 11 x 2^-24 c of it
 // (infinities of e^2y give the limits).  cap_in = 2 log2e scale / c, cap_log2 = c log2e.
+// In units of 2^-24 c, with E = e^2y: 16 |y| E / (1 + E)^2 from the four roundings of the exponent, 8 E / (1 + E)^2 from exp2
+// (2^-22 of itself), 2 / (1 + E) from the sum, 4 / (1 + E) from the reciprocal (2^-23 of itself), 3 |tanh y| from the last
+// product and the two of cap_log2.  Their sum is largest at y = -1.08: 10.1.
 ACACHE_DEVFN float capped(float dot, float cap_in, float cap_log2) {
     return fmaf(-2.f * cap_log2, fast_rcp(1.f + fast_exp2(dot * cap_in)), cap_log2);
 }
-// The same within 2^-20 of itself, for large caps: below y = 1/4 by y - y^3/3 + 2 y^5/15 - 17 y^7/315 (what follows is
+// The same within 2^-19 of itself, for large caps (2^-20 below y = 1/4; from there on as above, worst at y = -1/4 with
+// 7.3 x 2^-24 c of c / 4.08): below y = 1/4 by y - y^3/3 + 2 y^5/15 - 17 y^7/315 (what follows is
 // below 62/2835 y^9), with the score itself for y: next to a cap near the end of float32 cap_in has few bits or none.
 ACACHE_DEVFN float capped_wide(float dot, float cap_in, float cap_log2, float scale_log2) {
     const float y = dot * (cap_in * 0.34657359f), z = y * y;        // ln2 / 2
     const float near = dot * scale_log2 * fmaf(z, fmaf(z, fmaf(z, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
     return fabsf(y) < 0.25f ? near : capped(dot, cap_in, cap_log2);
 }
-// Up to here the plain form is off by at most 2^-13, a sixteenth of a weight's rounding to bf16.
+// Up to here the plain form is off by at most 2^-11.6, a sixth of a weight's rounding to bf16.
 constexpr float kWideCap = 512.f;
 
 template <typename T>

@@ -585,9 +585,10 @@ ACACHE_API int acache_rotate_store_q8(const acache_attn_desc* a, const acache_ro
  * Tensor cores: bf16 (head dim 64 and 128) with a positive scale; otherwise CUDA cores.
  * Limits: B <= 65,535, pools below 2^31 rows (slots x heads), T <= 2^31 - 1024,
  * n_q * Hq / Hkv <= 65,535 * 64; more is ACACHE_ERR_INVALID_ARG.
- * Roundings: logits, maxima, sums and O are float32 (exponentials to 2^-22, a capped
- * score to 2^-22 of the cap, or from a cap of 512 on to 2^-20 of itself); in a bf16 call the weights are rounded to bf16 before the product with V, not in
- * their sum.
+ * Roundings: logits, maxima, sums and O are float32 (exponentials to 2^-22; a capped score, next
+ * to that of its float32 product q.k, to 11 x 2^-24 of the cap, or with a cap above 512 to 2^-19 of
+ * itself); in a bf16 call the weights are rounded to bf16 before the product with V, not in their
+ * sum.
  * ------------------------------------------------------------------------------- */
 typedef struct {
     const int32_t* row_range;

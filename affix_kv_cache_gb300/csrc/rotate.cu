@@ -128,7 +128,6 @@ rotate_kernel(const __grid_constant__ RotateParams p) {
     __shared__ __align__(16) float s_cos[kWarps][64], s_sin[kWarps][64];   // of a warp's row
     __shared__ __align__(16) float s_w[2][D];                              // 4 elements of each piece after 4 of each (no bank conflicts)
     __shared__ float s_head[kLayout == kHalfAny ? kWarps * HPW * D : 1];
-    if (kMode != kRotate) ptx::grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPH, j = lane % LPH;
     // the lane's two pieces of a head
     const int hp = kLayout == kHalfPieces ? p.half / N : 0;            // pieces in the first half

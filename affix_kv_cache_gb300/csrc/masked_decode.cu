@@ -468,10 +468,29 @@ masked_decode_kernel(const DecParams p) {
     cluster_sync();                // no CTA may leave while another still reads its shared memory
 }
 
-std::atomic<int> g_prepared[6][64];   // the kernel's shared memory is allowed for, per device and variant
+std::atomic<int> g_clusters[6][kMaxCluster + 1][64];   // per variant, size and device: 1 + the clusters that run at once
+
+// Clusters of `cs` CTAs of a variant that the device holds at once.  A cluster stays within a group of SMs, whose places the
+// larger sizes leave unused (of 304: 296 in use at 4 to a cluster, 288 at 8, 247 at 13, 196 at 14); 0: the size cannot be launched.
+template <int D, int NB>
+int clusters_at_once(cudaLaunchConfig_t cfg, cudaLaunchAttribute attr, int cs, int dev) {
+    std::atomic<int>& known = g_clusters[(D == 128 ? 3 : 0) + NB / 2][cs][dev];
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cfg.gridDim = dim3((unsigned)cs);
+        attr.val.clusterDim.x = (unsigned)cs;
+        cfg.attrs = &attr;
+        if (cudaOccupancyMaxActiveClusters(&n, masked_decode_kernel<D, NB>, &cfg) != cudaSuccess || n < 0) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        known.store(++n, std::memory_order_relaxed);
+    }
+    return n - 1;
+}
 
 template <int D, int NB>
-int launch(const DecParams& prm, dim3 grid, cudaStream_t stream) {
+int launch(DecParams prm, const MaskedAttn& c) {
     auto kern = masked_decode_kernel<D, NB>;
     constexpr int smem = (int)sizeof(Smem<D, 8 * NB>);
     int dev = 0;
@@ -479,26 +498,50 @@ int launch(const DecParams& prm, dim3 grid, cudaStream_t stream) {
         (void)cudaGetLastError();
         return ACACHE_ERR_CUDA;
     }
-    std::atomic<int>& st = g_prepared[(D == 128 ? 3 : 0) + NB / 2][dev];
-    if (!st.load(std::memory_order_acquire)) {
+    static std::atomic<int> prepared[64];             // the kernel's shared memory and clusters are allowed for, per device
+    if (!prepared[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
             cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
             (void)cudaGetLastError();
             return ACACHE_ERR_CUDA;
         }
-        st.store(1, std::memory_order_release);
+        prepared[dev].store(1, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
+    cfg.stream = c.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)prm.cs;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // Parts of the key range, in chunks of a warp: kFix is what a CTA costs besides its keys, kMerge a merge
+    // over the cluster.  A fixed batch runs in waves of as many clusters as run at once.  Of a ragged batch the host knows
+    // the longest request only: parts until that one no longer outlasts the others, taken as an eighth as long.
+    constexpr int kFix = 6, kMerge = 2;
+    const int n_ch = (c.T_len + kChunk - 1) / kChunk;
+    const int64_t units = (int64_t)c.B * prm.Hkv;
+    prm.cs = 1;
+    int64_t best = 0;
+    for (int cs = 1; cs <= kMaxCluster && cs <= n_ch; ++cs) {
+        int64_t clusters = clusters_at_once<D, NB>(cfg, attr[0], cs, dev);
+        if (clusters == 0) {
+            if (cs > 1) continue;
+            clusters = (int64_t)sm_count() * kCtasPerSm;
+        }
+        const int64_t per = (n_ch + cs * kWarps - 1) / (cs * kWarps) + kFix + (cs > 1 ? kMerge : 0);
+        int64_t est = ((units + clusters - 1) / clusters) * per;
+        if (c.q_start)
+            est = std::max(per, (units * (n_ch / (8 * kWarps) + kFix + (cs > 1 ? kMerge : 0)) + clusters * cs - 1) / (clusters * cs));
+        if (cs == 1 || est < best) {
+            best = est;
+            prm.cs = cs;
+        }
+    }
+    cfg.gridDim = dim3((unsigned)(prm.Hkv * prm.cs), (unsigned)c.B, 1);
+    attr[0].val.clusterDim.x = (unsigned)prm.cs;
     cfg.numAttrs = prm.cs > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kern, prm) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -508,10 +551,11 @@ int launch(const DecParams& prm, dim3 grid, cudaStream_t stream) {
 }
 
 template <int D>
-int dispatch(const DecParams& prm, int rows, dim3 grid, cudaStream_t stream) {
-    if (rows <= 8) return launch<D, 1>(prm, grid, stream);
-    if (rows <= 16) return launch<D, 2>(prm, grid, stream);
-    return launch<D, 4>(prm, grid, stream);
+int dispatch(const DecParams& prm, const MaskedAttn& c) {
+    const int rows = c.n_q * prm.g;
+    if (rows <= 8) return launch<D, 1>(prm, c);
+    if (rows <= 16) return launch<D, 2>(prm, c);
+    return launch<D, 4>(prm, c);
 }
 
 }  // namespace
@@ -548,25 +592,7 @@ int launch_masked_decode(const MaskedAttn& c) {
         prm.cap_log2 = c.mask.softcap * kLog2e;
         prm.wide = c.mask.softcap > kWideCap;
     }
-    // Parts of the key range, in chunks of a warp: kFix is what a CTA costs besides its keys, kMerge a merge
-    // over the cluster.  A fixed batch runs in waves of equal CTAs.  Of a ragged batch the host knows the longest
-    // request only: parts until that one no longer outlasts the others, taken as an eighth as long.
-    constexpr int kFix = 6, kMerge = 2;
-    const int n_ch = (c.T_len + kChunk - 1) / kChunk;
-    const int64_t units = (int64_t)c.B * hkv, slots = (int64_t)sm_count() * kCtasPerSm;
-    prm.cs = 1;
-    int64_t best = 0;
-    for (int cs = 1; cs <= kMaxCluster && cs <= n_ch; ++cs) {
-        const int64_t per = (n_ch + cs * kWarps - 1) / (cs * kWarps) + kFix + (cs > 1 ? kMerge : 0);
-        int64_t est = ((units * cs + slots - 1) / slots) * per;
-        if (c.q_start) est = std::max(per, (units * (n_ch / (8 * kWarps) + kFix + (cs > 1 ? kMerge : 0)) + slots - 1) / slots);
-        if (cs == 1 || est < best) {
-            best = est;
-            prm.cs = cs;
-        }
-    }
-    const dim3 grid((unsigned)(hkv * prm.cs), (unsigned)c.B, 1);
-    return c.a.d == 128 ? dispatch<128>(prm, c.n_q * g, grid, c.stream) : dispatch<64>(prm, c.n_q * g, grid, c.stream);
+    return c.a.d == 128 ? dispatch<128>(prm, c) : dispatch<64>(prm, c);
 }
 
 }  // namespace acache

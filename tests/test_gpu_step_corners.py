@@ -182,3 +182,26 @@ def test_rotation_into_the_gaps_between_its_rows(first, n):
     if n > 1:                                            # an output that shares a head with its input
         with pytest.raises(ac.AcacheError):
             ac.acache_rotate_qk(desc, rope, n, pos, buf[:, 1:1 + hq], None, buf[:, :hq], None)
+
+
+# ------------------------------------------------------------------------------------- few rows over many keys
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,hkv", [(2, 8), (17, 1), (10, 2), (21, 1), (3, 8), (4, 8), (5, 8), (1, 3)])
+def test_single_tokens_split_over_clusters_of_any_size(d, B, hkv):
+    """From 3 to 40 (request, KV head) units over 1,500 keys: clusters of 6 to 16 CTAs, as many as run at once."""
+    g = torch.Generator().manual_seed(B + hkv)
+    T, hq = 1500, 2 * hkv
+    ns = B * T
+    q = torch.randn((B, 1, hq, d), generator=g).to(BF16)
+    k, v = (torch.randn((ns, hkv, d), generator=g).to(BF16) for _ in range(2))
+    rs = torch.randperm(ns, generator=g).to(torch.int32).view(B, T)
+    lo = torch.randint(0, 700, (B,), generator=g)
+    hi = torch.randint(600, T + 1, (B,), generator=g)
+    out, st = torch.full((B, 1, hq, d), 7.0, dtype=BF16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ac.acache_slot_attention_masked(_desc(hq, hkv, d, BF16), B, 1, dev(q), T, dev(rs), dev(k), dev(v), ns, out,
+                                    row_range=dev(torch.stack((lo, hi), -1).to(torch.int32)[:, None]), dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for b in range(B):
+        want, tol = masked_attention(q[b], rs[b].numpy(), k, v, d ** -0.5, lo[b:b + 1], hi[b:b + 1])
+        assert_attention(_np(out[b]), want, tol, f"request {b}")

@@ -519,7 +519,11 @@ int launch(DecParams prm, const MaskedAttn& c) {
     cfg.numAttrs = 1;
     // Parts of the key range, in chunks of a warp: kFix is what a CTA costs besides its keys, kMerge a merge
     // over the cluster.  A fixed batch runs in waves of as many clusters as run at once.  Of a ragged batch the host knows
-    // the longest request only: parts until that one no longer outlasts the others, taken as an eighth as long.
+    // the longest request only: its time, or that of the waves of all of them with an eighth of its keys each, whichever is
+    // longer.  us, single tokens of 32 heads over 8, as chosen here and with the best and the worst of 1 to 16 parts.  Lengths
+    // even over their logarithm: 16 requests up to 2,000 keys 16.7 (16.7, 54.7), up to 8,000 34.7 (34.7, 143), 32 up to 8,000
+    // 68.9 (68.9, 144).  Even up to 8,000: 16 requests 81.9 (78.4, 147).  All 8,000: 4 requests 42.2 (30.1, 144), 16 107 (96.3, 163).
+    // All but one short: 32 requests up to 16,000 keys 77.6 (51.6, 282), the furthest that was found.
     constexpr int kFix = 6, kMerge = 2;
     const int n_ch = (c.T_len + kChunk - 1) / kChunk;
     const int64_t units = (int64_t)c.B * prm.Hkv;
@@ -531,10 +535,9 @@ int launch(DecParams prm, const MaskedAttn& c) {
             if (cs > 1) continue;
             clusters = (int64_t)sm_count() * kCtasPerSm;
         }
-        const int64_t per = (n_ch + cs * kWarps - 1) / (cs * kWarps) + kFix + (cs > 1 ? kMerge : 0);
-        int64_t est = ((units + clusters - 1) / clusters) * per;
-        if (c.q_start)
-            est = std::max(per, (units * (n_ch / (8 * kWarps) + kFix + (cs > 1 ? kMerge : 0)) + clusters * cs - 1) / (clusters * cs));
+        const int64_t waves = (units + clusters - 1) / clusters;
+        auto takes = [&](int64_t chunks) { return (chunks + cs * kWarps - 1) / (cs * kWarps) + kFix + (cs > 1 ? kMerge : 0); };
+        const int64_t est = c.q_start ? std::max(takes(n_ch), waves * takes(n_ch / 8)) : waves * takes(n_ch);
         if (cs == 1 || est < best) {
             best = est;
             prm.cs = cs;

@@ -205,3 +205,24 @@ def test_single_tokens_split_over_clusters_of_any_size(d, B, hkv):
     for b in range(B):
         want, tol = masked_attention(q[b], rs[b].numpy(), k, v, d ** -0.5, lo[b:b + 1], hi[b:b + 1])
         assert_attention(_np(out[b]), want, tol, f"request {b}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,hkv", [(4, 8), (16, 4), (33, 8)])
+def test_ragged_single_tokens_split_over_clusters(d, B, hkv):
+    g = torch.Generator().manual_seed(B)
+    hq = 2 * hkv
+    keys = [2000] + [int(2000 ** x) for x in torch.rand(B - 1, generator=g).tolist()]
+    ks = np.concatenate(([0], np.cumsum(keys))).astype(np.int32)
+    ns = int(ks[-1])
+    q = torch.randn((B, hq, d), generator=g).to(BF16)
+    k, v = (torch.randn((ns, hkv, d), generator=g).to(BF16) for _ in range(2))
+    rs = torch.randperm(ns, generator=g).to(torch.int32)
+    out, st = torch.full((B, hq, d), 7.0, dtype=BF16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ac.acache_slot_attention_masked_varlen(_desc(hq, hkv, d, BF16), B, dev(torch.arange(B + 1, dtype=torch.int32)), 1, B, dev(q),
+                                           dev(torch.from_numpy(ks)), 2000, dev(rs), dev(k), dev(v), ns, out, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    for b in range(B):
+        want, tol = masked_attention(q[b:b + 1], rs[ks[b]:ks[b + 1]].numpy(), k, v, d ** -0.5, [0], [keys[b]])
+        assert_attention(_np(out[b:b + 1]), want, tol, f"request {b}")

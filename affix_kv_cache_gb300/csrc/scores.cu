@@ -33,8 +33,9 @@ constexpr float kNone = -3.402823466e38f;   // maximum before any logit (lowest 
 constexpr float kLowest = -200.f;           // d from here on down is a weight of zero
 constexpr float kHead = 6.f, kFloor = 300.f;   // log2 units: how far a logit may pass the reference; where a floor under it lies
 constexpr int kBatch = 4;                   // pieces in flight
-// CTAs to an SM: 1,536 threads (40 registers), at most 32 CTAs
-constexpr int ctas(int nt) { return nt >= 48 ? 1536 / nt : 32; }
+// CTAs to an SM: 1,536 threads (40 registers); of 64 and 32 threads 22, as many as their 9 KB of shared memory, most of it the
+// list, let in (1,408 and 704 threads)
+constexpr int ctas(int nt) { return nt >= 128 ? 1536 / nt : 22; }
 
 struct ScoreParams {
     const void* logits;
@@ -48,6 +49,7 @@ struct ScoreParams {
                                             // temperature is above 1, as the quotient can be a number where the difference
                                             // is not; log2e / temperature and 1 / temperature over `half`
     float head, floor_gap;                  // kHead and kFloor in logits
+    bool far;                               // a weight that counts may lie further than the end of float32 from the largest
 };
 
 ACACHE_DEVFN float max_nan(float a, float b) {
@@ -73,11 +75,10 @@ template <> struct Piece<float> {
         for (int u = 1; u < B; ++u) m = fmaxf(m, top(w[u]));
         return m;
     }
-    // Elements e, e + 1; weights' exponents are bounded from below one by one.  A floor only tells whether differences from
-    // the reference m stay float32 where they count.
-    using Floor = bool;
-    ACACHE_DEVFN static Floor floor_of(float m, float gap) { return m - gap > -3.3e38f; }
-    ACACHE_DEVFN static bool bounds(Floor f) { return f; }
+    // Elements e, e + 1; weights' exponents are bounded from below one by one (far: differences that count may leave float32).
+    struct Floor {};
+    ACACHE_DEVFN static Floor floor_of(float, float) { return {}; }
+    ACACHE_DEVFN static bool bounds(Floor, bool far) { return !far; }
     ACACHE_DEVFN static uint64_t pair(const uint4& w, int e, Floor) { return f2pack(at(w, e), at(w, e + 1)); }
     ACACHE_DEVFN static void bound(float& a, float& b) {
         a = max_nan(a, kLowest);
@@ -122,7 +123,7 @@ template <> struct Piece<__nv_bfloat16> {
         const uint32_t u = __float_as_uint(f) >> 16;         // (cut: a little more for negative ones, less for others)
         return u | u << 16;
     }
-    ACACHE_DEVFN static bool bounds(Floor f) { return f != 0u; }
+    ACACHE_DEVFN static bool bounds(Floor f, bool) { return f != 0u; }
     ACACHE_DEVFN static uint64_t pair(const uint4& w, int e, Floor f) {
         uint32_t v = e == 0 ? w.x : e == 2 ? w.y : e == 4 ? w.z : w.w;
         const __nv_bfloat162 h = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&f));
@@ -252,7 +253,7 @@ scores_kernel(const ScoreParams p) {
             if (i + u * NT < z) w[u] = __ldg(w0 + i + u * NT);
         }
         if (note(W::top(w))) floor = W::floor_of(st.m, p.floor_gap);
-        if (!W::bounds(floor)) {            // (a maximum near the lowest value, or far beyond the temperature, or next to
+        if (!W::bounds(floor, p.far)) {            // (a maximum near the lowest value, or far beyond the temperature, or next to
                                             // nothing beside it)
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
@@ -510,6 +511,7 @@ int launch_token_scores(const ScoreCall& c) {
     p.far_ln = (float)(1.0 / c.temperature / p.half);
     p.head = kHead / p.to_log2;
     p.floor_gap = kFloor / p.to_log2;
+    p.far = p.floor_gap > 1.7e38f;
     return c.dtype == ACACHE_F32 ? dispatch<float>(p, c.rows, c.stream) : dispatch<__nv_bfloat16>(p, c.rows, c.stream);
 }
 

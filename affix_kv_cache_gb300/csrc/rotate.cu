@@ -15,8 +15,9 @@
 // angle is exact modulo one turn: position times a frequency held in 2^-64 turns, in integers; only what is
 // left within an eighth of a turn becomes a float.
 // Measured (bf16, d = 128): 16 x 1,562 rows of 28 + 4 heads, half of each rotated, 68 us, 0.88 of the copy bandwidth; the normed
-// store of 16 x 1,205 rows 66 us, 0.79 (issue: norm and rotation take some 270 instructions for 4 heads); 8,191 rows into an 8-bit
-// pool with their read-back 48 us, 0.72.  With the angles read from shared memory for every head 92 and 72 us (LDS
+// store of 16 x 1,205 rows 66 us, 0.79 (latency: a warp loads two steps of a row, turns them and only then loads again; issue is
+// active 47 % of the time, and most stalls wait for loads); 8,191 rows into an 8-bit pool with their read-back 48 us, 0.72 (the
+// same).  float32: 138 us, 0.87, and 133 us, 0.79.  With the angles read from shared memory for every head 92 and 72 us (LDS
 // wavefronts); a CTA to 8 rows behind one barrier 80 and 78 us.
 #include <algorithm>
 

@@ -526,7 +526,8 @@ ACACHE_API int acache_rope_init_frequencies(acache_rope* out, int rotary_dim, in
  *   q_out, k_out rows at their own strides.  An output may be its own input (same pointer and
  *                stride); otherwise it must not overlap an input or the other output (rows of the
  *                same stride may lie in the gaps between one another's)
- * Pointers 16-byte aligned, strides >= a row and multiples of 16 bytes; eps >= 0.
+ * Pointers 16-byte aligned, strides >= a row, multiples of 16 bytes and below 2^40 elements;
+ * eps >= 0; at most 2^31 rows and 2^20 heads.
  * ------------------------------------------------------------------------------- */
 ACACHE_API int acache_rotate_qk(const acache_attn_desc* a, const acache_rope* rope, int64_t rows,
                         const int32_t* positions, const void* q, int64_t q_stride, const void* k,
@@ -585,6 +586,9 @@ ACACHE_API int acache_rotate_store_q8(const acache_attn_desc* a, const acache_ro
  * Tensor cores: bf16 (head dim 64 and 128) with a positive scale; otherwise CUDA cores.
  * Limits: B <= 65,535, pools below 2^31 rows (slots x heads), T <= 2^31 - 1024,
  * n_q * Hq / Hkv <= 65,535 * 64; more is ACACHE_ERR_INVALID_ARG.
+ * Rows whose neighbours see a V that is not finite where they do not, and rows without cap and bias
+ * whose scores rise by more than 88 (127 ln 2) from the 128 keys before to the next, are computed
+ * again one by one: right, but slow (a row of 4,096 keys takes 1.6 ms).
  * Roundings: logits, maxima, sums and O are float32 (exponentials to 2^-22; a capped score, next
  * to that of its float32 product q.k, to 11 x 2^-24 of the cap, or with a cap above 512 to 2^-19 of
  * itself); in a bf16 call the weights are rounded to bf16 before the product with V, not in their
@@ -617,8 +621,9 @@ ACACHE_API int acache_slot_attention_masked_varlen(const acache_attn_desc* a, co
  *   top_tokens [rows][k] int32, top_logprob [rows][k] float (or NULL): the k largest logits in
  *                 descending order, ties to the lower token; -0.0 counts as +0.0, NaN ranks below
  *                 every number
- * 0 <= k <= min(vocab, ACACHE_MAX_ALTERNATIVES); dtype is that of the logits, row_stride (>= vocab)
- * counts elements; rows need no alignment beyond their element's.  Logits of -infinity are tokens
+ * 0 <= k <= min(vocab, ACACHE_MAX_ALTERNATIVES); dtype is that of the logits, row_stride (>= vocab,
+ * below 2^40) counts elements; rows need no alignment beyond their element's; at most 2^28 - 1 rows.
+ * temperature is positive and finite, and log2e / temperature within float32.  Logits of -infinity are tokens
  * that cannot be chosen.  A row with a NaN or +infinity has NaN as every log probability and
  * entropy and flags ACACHE_DEV_NAN; one that is -infinity throughout has NaN too, unflagged.
  * Logits are read once (a few candidates' again); sums are float32, in a fixed order.
